@@ -29,6 +29,10 @@ EXPORTED = ["rece_plan", "rece_plan_destroy", "rece_workspace_bytes", "rece_forw
             "rece_forward_static", "rece_backward", "rece_export", "rece_export_bytes", "rece_check",
             "rece_profile_enable", "rece_profile_read",
             "rece_full_ce_workspace_bytes", "rece_full_ce_forward", "rece_full_ce_backward", "rece_auto_size",
+            "rece_embed_forward", "rece_embed_workspace_bytes", "rece_embed_backward",
+            "rece_logprob_workspace_bytes", "rece_logprob_forward", "rece_logprob_backward",
+            "rece_policy_workspace_bytes", "rece_policy_loss",
+            "rece_preference_workspace_bytes", "rece_preference_loss",
             "rece_status_string", "rece_last_error", "rece_version"]
 PHASES = ["project", "sort", "select", "loss", "bwd_dx", "bwd_dy", "bwd_sort", "other"]
 
@@ -79,6 +83,18 @@ def lib() -> ctypes.CDLL:
         L.rece_auto_size.argtypes = [i64, i64, i32, ctypes.c_double, i32, ctypes.POINTER(ctypes.c_int32),
                                      ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                                      ctypes.POINTER(ctypes.c_double)]
+        i32t, u32t, f32t = ctypes.c_int32, ctypes.c_uint32, ctypes.c_float
+        L.rece_embed_forward.argtypes = [vp, i64, i64, i32t, i32t, f32t, vp, vp, vp]
+        L.rece_embed_workspace_bytes.argtypes = [i64, i64, i32t, sz]
+        L.rece_embed_backward.argtypes = [vp, i64, i64, i32t, i32t, f32t, u32t, vp, vp, vp, ctypes.c_size_t, vp]
+        L.rece_logprob_workspace_bytes.argtypes = [i64, i64, i32t, i32t, u32t, sz]
+        L.rece_logprob_forward.argtypes = [vp, i64, i64, i32t, i32t, f32t, u32t, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+        L.rece_logprob_backward.argtypes = [vp, i64, i64, i32t, i32t, f32t, u32t, vp, vp, vp, vp, ctypes.c_size_t, vp,
+                                            vp, vp, vp]
+        L.rece_policy_workspace_bytes.argtypes = [vp, sz]
+        L.rece_policy_loss.argtypes = [vp] * 11 + [ctypes.c_size_t] + [vp] * 4
+        L.rece_preference_workspace_bytes.argtypes = [vp, sz]
+        L.rece_preference_loss.argtypes = [vp] * 9 + [ctypes.c_size_t] + [vp] * 4
         L.rece_status_string.argtypes = [i32]
         L.rece_status_string.restype = ctypes.c_char_p
         L.rece_last_error.restype = ctypes.c_char_p
@@ -86,7 +102,11 @@ def lib() -> ctypes.CDLL:
         for name in ("rece_plan", "rece_plan_destroy", "rece_workspace_bytes", "rece_forward",
                      "rece_forward_static", "rece_backward", "rece_export", "rece_export_bytes", "rece_check",
                      "rece_profile_enable", "rece_profile_read", "rece_full_ce_workspace_bytes",
-                     "rece_full_ce_forward", "rece_full_ce_backward", "rece_auto_size"):
+                     "rece_full_ce_forward", "rece_full_ce_backward", "rece_auto_size",
+                     "rece_embed_forward", "rece_embed_workspace_bytes", "rece_embed_backward",
+                     "rece_logprob_workspace_bytes", "rece_logprob_forward", "rece_logprob_backward",
+                     "rece_policy_workspace_bytes", "rece_policy_loss",
+                     "rece_preference_workspace_bytes", "rece_preference_loss"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -393,3 +413,9 @@ class FullCE:
 
 def version() -> str:
     return lib().rece_version().decode()
+
+
+from .ops import (  # noqa: E402,F401  (the operators around the losses use the names above)
+    FLAG_ACCUMULATE, FLAG_ENTROPY, FLAG_NO_GRAD, ItemEmbedding, LogProb, PolicyConfig, PolicyLoss, PreferenceConfig,
+    PreferenceLoss, embed, log_probs, policy_loss, preference_loss,
+)

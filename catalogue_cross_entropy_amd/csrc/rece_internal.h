@@ -186,6 +186,30 @@ size_t dy_area_bytes(int64_t E, int d);
 // Every row of dY from the sorted records (K, V, *ntot of them); E bounds *ntot.
 hipError_t launch_dy(bool is_bf16, int d, const BwdArgs& a, const int32_t* K, const int32_t* V, const uint32_t* ntot,
                      int64_t E, void* area, hipStream_t st);
+// Item embedding (k_embed.hip).
+size_t embed_workspace_bytes(int64_t n, int64_t C, int d);
+hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, const void* table, const int32_t* ids,
+                         void* out, hipStream_t st);
+hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, bool grad_bf16, bool accumulate,
+                          const int32_t* ids, const void* dout, void* ws, void* dtable, hipStream_t st);
+// Log-probabilities over the catalogue (k_logprob.hip).
+size_t logprob_workspace_bytes(bool bf16v, int64_t s, int64_t C, int d, uint32_t flags);
+hipError_t logprob_forward(bool bf16v, int64_t s, int64_t C, int d, float temperature, uint32_t flags, const void* X,
+                           const void* Y, const int32_t* ids, void* ws, float* logp, float* entropy, hipStream_t st);
+hipError_t logprob_backward(bool bf16v, int64_t s, int64_t C, int d, float temperature, uint32_t flags, const void* X,
+                            const void* Y, const int32_t* ids, void* ws, const float* dlogp, const float* dentropy,
+                            void* dX, void* dY, hipStream_t st);
+// Losses on log-probabilities (k_policy.hip).
+size_t policy_workspace_bytes(const rece_policy_config& c);
+hipError_t policy_loss(const rece_policy_config& c, const void* logp, const void* old, const void* ref,
+                       const void* entropy, const float* adv, const int32_t* offsets, const uint8_t* mask,
+                       const float* dloss, void* ws, float* loss, float* stats, void* dlogp, void* dentropy,
+                       hipStream_t st);
+size_t preference_workspace_bytes(const rece_preference_config& c);
+hipError_t preference_loss(const rece_preference_config& c, const void* logp, const void* ref, const int32_t* offsets,
+                           const int32_t* group_offsets, const uint8_t* mask, const float* dloss, void* ws, float* loss,
+                           float* loss_pg, float* rewards, void* dlogp, hipStream_t st);
+
 // Bucket (SCE) variant.
 // Per bucket column of a listed selection (k_col_pass / k_col_thresh): the
 // histogram coordinate of a float32 score v is x = med3(v * sc + nlsc, 0, 32 -)

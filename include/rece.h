@@ -225,6 +225,140 @@ rece_status rece_full_ce_backward(void* stream, int64_t s, int64_t C, int32_t d,
                                   const void* Y, const int32_t* pos, void* workspace, size_t workspace_bytes,
                                   const float* dloss, const float* dloss_pp, float* dX, float* dY);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the losses: what a next-item model needs before the loss (its
+ * input rows, read from the same item table) and for training on preferences or
+ * rewards (log-probabilities over the whole catalogue and the losses on them).
+ * The conventions above hold; every call only enqueues kernels on `stream`, keeps
+ * no state and can be captured into a HIP graph.  Two calls in flight at once need
+ * their own workspaces.  Results are deterministic: sums have a fixed order, no
+ * float atomics.
+ * ------------------------------------------------------------------------- */
+
+#define RECE_FLAG_ACCUMULATE 16u   /* rece_embed_backward adds to dtable instead of overwriting it */
+#define RECE_FLAG_NO_GRAD 32u      /* rece_logprob_*: no backward call will follow (smaller workspace) */
+#define RECE_FLAG_ENTROPY 64u      /* rece_logprob_*: entropies too, and their gradient */
+
+/* Rows of an item table as a model's inputs:
+ *   out_i = scale * table[ids[i]]     (float32 product, rounded once to dtype)
+ *   n rows, n <= 2^31 - 1 (n = 0: nothing is done); C >= 1; d a multiple of 8, at most 8192
+ *   table [C][d], out [n][d] dtype;  ids [n] int32
+ * An id outside [0, C) is padding: its output row is zero and it has no gradient. */
+rece_status rece_embed_forward(void* stream, int64_t n, int64_t C, int32_t d, int32_t dtype, float scale,
+                               const void* table, const int32_t* ids, void* out);
+
+/* Gradient of the table: dtable_j = scale * sum over i with ids[i] = j of dout_i, from
+ * the ids sorted (stable), each row summed in float32 in the order of i within
+ * fixed pieces, so that two calls give identical bits.
+ *   dout [n][d] dtype;  dtable [C][d] float32 (bf16 with RECE_FLAG_BF16_GRADS)
+ * Every row of dtable is written (zero where no id names it).  With
+ * RECE_FLAG_ACCUMULATE (float32 only) the sums are added to dtable and other rows
+ * are left alone: a table shared with the loss adds to the loss's dY this way.
+ *   workspace  rece_embed_workspace_bytes bytes, temporary */
+rece_status rece_embed_workspace_bytes(int64_t n, int64_t C, int32_t d, size_t* bytes);
+rece_status rece_embed_backward(void* stream, int64_t n, int64_t C, int32_t d, int32_t dtype, float scale,
+                                uint32_t flags, const int32_t* ids, const void* dout, void* workspace,
+                                size_t workspace_bytes, void* dtable);
+
+/* Log-probability of one item per position under the softmax over the whole
+ * catalogue, and the entropy of that softmax; no array of size s x C exists:
+ *   x_ij = X_i . Y_j / temperature,  lse_i = log sum_j exp(x_ij),  p_ij = exp(x_ij - lse_i)
+ *   logp_i = x_i,ids(i) - lse_i          entropy_i = lse_i - sum_j p_ij x_ij
+ *   X [s][d], Y [C][d] dtype, d in {32, 64, 128, 256}; ids [s] int32; temperature > 0
+ *   logp [s] float32; entropy [s] float32 (RECE_FLAG_ENTROPY, else NULL)
+ * An id outside [0, C) is padding: logp and entropy are 0, the row of X is not
+ * read into any result (it may hold anything) and gets a zero gradient.
+ *   workspace  rece_logprob_workspace_bytes bytes (same sizes, dtype, flags); unless
+ *   RECE_FLAG_NO_GRAD is given it feeds the backward call and stays untouched between.
+ * Backward (same X, Y, ids, temperature, flags as the forward call that filled the workspace):
+ *   dlogp [s], dentropy [s] (or NULL: zero; needs RECE_FLAG_ENTROPY)  float32 upstream gradients
+ *   G_ij = (dlogp_i ([j = ids(i)] - p_ij) - dentropy_i p_ij (log p_ij + entropy_i)) / temperature
+ *   dX = G Y [s][d], dY = G^T X [C][d]   float32 (bf16 with RECE_FLAG_BF16_GRADS), overwritten */
+rece_status rece_logprob_workspace_bytes(int64_t s, int64_t C, int32_t d, int32_t dtype, uint32_t flags, size_t* bytes);
+rece_status rece_logprob_forward(void* stream, int64_t s, int64_t C, int32_t d, int32_t dtype, float temperature,
+                                 uint32_t flags, const void* X, const void* Y, const int32_t* ids, void* workspace,
+                                 size_t workspace_bytes, float* logp, float* entropy);
+rece_status rece_logprob_backward(void* stream, int64_t s, int64_t C, int32_t d, int32_t dtype, float temperature,
+                                  uint32_t flags, const void* X, const void* Y, const int32_t* ids, void* workspace,
+                                  size_t workspace_bytes, const float* dlogp, const float* dentropy, void* dX,
+                                  void* dY);
+
+/* Clipped policy loss with a KL and an entropy term over ragged sequences of tokens.
+ * Token t of sequence i (offsets[i] <= t < offsets[i + 1]) with mask[t] != 0 counts; over those
+ *   r_t = exp(logp_t - old_t),  A_t = adv[t] or adv[i]
+ *   pg_t = -min(r_t A_t, clip(r_t, 1 - clip_low, 1 + clip_high) A_t)
+ *   kl_t = exp(u) - u - 1 with u = ref_t - logp_t   (0 without ref)
+ *   loss = sum_t w_t (pg_t + kl_coef kl_t - entropy_coef entropy_t)
+ * with w_t = 1 / (tokens that count) (RECE_MEAN_TOKEN) or 1 / (tokens that count in
+ * sequence i * sequences with such a token) (RECE_MEAN_SEQUENCE); loss 0 if none counts.
+ *   n tokens (0 <= n <= 2^31 - 1), n_seq >= 1 sequences, offsets [n_seq + 1] int32
+ *   non-decreasing (values outside [0, n] are clamped; tokens before the first or
+ *   behind the last sequence do not count)
+ *   logp, old, ref (or NULL), entropy (or NULL) [n] dtype; mask [n] uint8 (or NULL: all count);
+ *   adv float32, [n] if token_adv, else [n_seq].  What a token that does not count holds is not used.
+ *   dloss [1] float32 upstream gradient (or NULL: 1)
+ *   loss [1], stats [6] float32: means over the tokens that count of pg, kl, entropy,
+ *   [clipped], r, and their number; [clipped]: A > 0 and r > 1 + clip_high, or A < 0 and r < 1 - clip_low
+ *   dlogp [n] dtype (or NULL), dentropy [n] dtype (or NULL): gradients times dloss,
+ *   written for every token (0 where it does not count)
+ *   workspace  rece_policy_workspace_bytes bytes, temporary */
+#define RECE_MEAN_TOKEN 0
+#define RECE_MEAN_SEQUENCE 1
+typedef struct {
+  int64_t n;
+  int64_t n_seq;
+  int32_t dtype;        /* rece_dtype of logp, old, ref, entropy, dlogp, dentropy */
+  int32_t reduction;    /* RECE_MEAN_TOKEN or RECE_MEAN_SEQUENCE */
+  int32_t token_adv;    /* 1: one advantage per token, 0: per sequence */
+  float clip_low;       /* 0 <= clip_low <= 1 */
+  float clip_high;      /* >= 0 */
+  float kl_coef;        /* not NaN; 0 with ref = NULL */
+  float entropy_coef;   /* 0 with entropy = NULL */
+} rece_policy_config;
+rece_status rece_policy_workspace_bytes(const rece_policy_config* cfg, size_t* bytes);
+rece_status rece_policy_loss(const rece_policy_config* cfg, void* stream, const void* logp, const void* old,
+                             const void* ref, const void* entropy, const float* adv, const int32_t* offsets,
+                             const uint8_t* mask, const float* dloss, void* workspace, size_t workspace_bytes,
+                             float* loss, float* stats, void* dlogp, void* dentropy);
+
+/* Preference loss over groups of sequences: the first sequence of a group is the
+ * preferred one (c), the others are not (k = 1 .. K).  With the tokens of sequence i
+ * that count (mask), h_i = sum_t (logp_t - ref_t) (divided by their number with
+ * average), ref = 0 if NULL, and z_k = beta (h_c - h_k) - margin:
+ *   RECE_PREF_SIGMOID  loss_g = mean_k ((1 - smoothing) softplus(-z_k) + smoothing softplus(z_k))
+ *   RECE_PREF_IPO      loss_g = mean_k (z_k / beta - 1 / (2 beta))^2
+ *   RECE_PREF_HINGE    loss_g = mean_k max(0, 1 - z_k)
+ *   RECE_PREF_SOFTMAX  loss_g = log(1 + sum_k exp(-z_k))      (sigmoid with one k)
+ *   loss = mean of loss_g over the n_group groups (a group without a second sequence has loss 0)
+ *   n tokens, n_seq sequences (offsets as above), n_group >= 1 groups: group g holds
+ *   sequences group_offsets[g] .. group_offsets[g + 1] - 1, [n_group + 1] int32
+ *   non-decreasing (values outside [0, n_seq] are clamped)
+ *   logp, ref [n] dtype;  dloss [1] float32 (or NULL: 1)
+ *   loss [1], loss_pg [n_group], rewards [n_seq] = beta h_i (of every sequence) float32
+ *   dlogp [n] dtype (or NULL): gradient times dloss, written for every token (0 where
+ *   it does not count or its sequence is in no group)
+ *   workspace  rece_preference_workspace_bytes bytes, temporary */
+#define RECE_PREF_SIGMOID 0
+#define RECE_PREF_IPO 1
+#define RECE_PREF_HINGE 2
+#define RECE_PREF_SOFTMAX 3
+typedef struct {
+  int64_t n;
+  int64_t n_seq;
+  int64_t n_group;
+  int32_t dtype;
+  int32_t kind;         /* RECE_PREF_* */
+  int32_t average;      /* 1: h_i is the mean over the sequence's tokens instead of their sum */
+  float beta;           /* > 0 */
+  float margin;         /* 0: none */
+  float smoothing;      /* RECE_PREF_SIGMOID: 0 <= smoothing < 1; otherwise 0 */
+} rece_preference_config;
+rece_status rece_preference_workspace_bytes(const rece_preference_config* cfg, size_t* bytes);
+rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream, const void* logp, const void* ref,
+                                 const int32_t* offsets, const int32_t* group_offsets, const uint8_t* mask,
+                                 const float* dloss, void* workspace, size_t workspace_bytes, float* loss,
+                                 float* loss_pg, float* rewards, void* dlogp);
+
 /* Intermediate results kept in `saved` (the steps of Algorithm 1, RECE page,
  * Section 3), copied asynchronously into the caller's `dst`. */
 typedef enum {
