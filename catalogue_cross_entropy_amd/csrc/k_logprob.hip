@@ -39,11 +39,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float LP_REF_LIMIT = 1.0995116e12f;   // 2^40: a block sum beyond it moves the reference
+constexpr float LP_REF_LIMIT = 1.1529215e18f;   // 2^60: a sum beyond it is taken again with a better reference
 constexpr float LP_NEVER = 1e30f;               // lse2 of a row that has no weight: exp2(x2 - 1e30) = 0
 constexpr int LP_ROW_PAD = 256;                 // packed rows are padded with zero rows to a multiple of this
 
-enum LpMode { LP_LSE = 0, LP_DX = 1, LP_DY = 2 };
+enum LpMode { LP_LSE = 0, LP_LSEO = 1, LP_DX = 2, LP_DY = 3 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -60,18 +60,19 @@ struct LpArgs {
   int own_is_pos;         // the owners are the packed positions (else the streamed side is)
   int splits;
   float c2;               // log2(e) / temperature
-  float *m, *z, *t;       // LP_LSE: [splits][own_pad] reference, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m)
+  float *m, *z, *t;       // LP_LSE(O): [parts][own_pad] reference, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m)
   int64_t own_pad;
-  const LpRow* rows;      // gradients: of the packed positions
-  const int32_t* idc;     // gradients: ids of the packed positions
-  float* out;             // gradients: [splits][own_pad][D]
+  const LpRow* rows;      // LP_DX, LP_DY: of the packed positions
+  const int32_t* idc;     // ids of the packed positions
+  float* out;             // LP_LSEO, LP_DX, LP_DY: [parts][own_pad][D]
+  int terms;              // bf16 terms of a weight in the products
 };
 
 // Geometry of a streamed tile: TI rows of RB bytes; 16-byte chunk c of row n is stored at
 // chunk c ^ (n & SWM), which spreads the 32 rows a fragment read touches over the banks.
 template <class E, int D, int NWS> struct LpTile {
   static constexpr int RB = D * (int)sizeof(E);
-  static constexpr int TI = NWS > 1 ? 32 * NWS : (RB <= 256 ? 64 : 32);
+  static constexpr int TI = NWS > 1 ? 32 * NWS : (RB <= 128 ? 128 : RB <= 256 ? 64 : 32);
   static constexpr int CPR = RB / 16;
   static constexpr int SWM = (CPR < 8 ? CPR : 8) - 1;
   static constexpr int BYTES = TI * RB;
@@ -100,394 +101,511 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// acc[nb] += G[32 owners][32 streamed] . rows[32 streamed][D], lane l holding G[owner l % 32]
-// [streamed 8 (v / 4) + 4 (l / 32) + v % 4] in g[v].  bf16: G as the sum of NS bf16 terms (1: rounded
-// once, for results that are themselves rounded to bf16; 3: all 24 bits).
-template <class E, int D, int NWS, int NS>
-__device__ __forceinline__ void lp_accumulate(f32x16 (&acc)[D / 32], const float (&g)[16], const char* tile, int rb) {
+// LDS by byte offset: a per-lane offset and a constant that becomes the instruction's.
+template <class T>
+__device__ __forceinline__ T lds_at(uint32_t off) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>((uintptr_t)off);
+}
+__device__ __forceinline__ s16x4 lds_tr4(uint32_t off) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)off);
+}
+
+// Row of value v of a 32 x 32 block (less 4 h for the lane half h).
+__device__ __forceinline__ constexpr int lp_row(int v) { return 8 * (v >> 2) + (v & 3); }
+
+// Per-lane LDS offsets of a wave's fragment reads inside a tile.  The swizzle only mixes the low bits of
+// a chunk's number, so a few offsets serve all reads, with constants added.
+template <class E, int D, int NWS> struct LpLds {
   using T = LpTile<E, D, NWS>;
-  const int l = lane_id(), h = l >> 5;
-  if constexpr (sizeof(E) == 2) {
+  static constexpr int KC = T::RB / 32;
+  static constexpr int NX = KC < (T::SWM + 1) / 2 ? KC : (T::SWM + 1) / 2;
+  static constexpr int NY = sizeof(E) == 2 ? (D / 32 < 2 ? 1 : 2) : 4;
+  uint32_t x[NX], y[NY];
+  __device__ __forceinline__ void init() {
+    const int l = lane_id(), h = l >> 5, r = l & 31;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 part[NS];
-      float r[8];
+    for (int k = 0; k < NX; ++k) x[k] = r * T::RB + (((2 * k + h) ^ (r & T::SWM)) << 4);
+    if constexpr (sizeof(E) == 2) {
+      // rows 4 h + j / 4, coordinates 16 ((l / 16) % 2) + 4 (j % 4) .. + 3 of each 32: within a 16-lane
+      // group the transpose read hands lane i coordinate i of the group's four rows
+      const int j = l & 15, half = (l >> 4) & 1, row = 4 * h + (j >> 2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = g[8 * kk + e];
+      for (int q = 0; q < NY; ++q)
+        y[q] = row * T::RB + (((4 * q + 2 * half + ((j & 3) >> 1)) ^ (row & T::SWM)) << 4) + (j & 1) * 8;
+    } else {
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const uint32_t w = pack_bf16(r[e], r[e + 1]);
-          part[s][e / 2] = w;
-          if (s + 1 < NS) {
-            r[e] -= lo_f32(w);
-            r[e + 1] -= hi_f32(w);
-          }
-        }
-      // rows rb * 32 + 16 kk + 4 h + 0 .. 3 and + 8 .. 11, coordinates 32 nb + l % 32: within each
-      // 16-lane group, source lane j names 4 coordinates of row j / 4
-      const int j = l & 15, half = (l >> 4) & 1;
-      const int row0 = rb * 32 + 16 * kk + 4 * h + (j >> 2), row1 = row0 + 8;
-#pragma unroll
-      for (int nb = 0; nb < D / 32; ++nb) {
-        const int dim = 32 * nb + 16 * half + 4 * (j & 3);
-        const char* a0 = tile + row0 * T::RB + (((dim >> 3) ^ (row0 & T::SWM)) << 4) + ((dim >> 2) & 1) * 8;
-        const char* a1 = tile + row1 * T::RB + (((dim >> 3) ^ (row1 & T::SWM)) << 4) + ((dim >> 2) & 1) * 8;
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const s16x4 b[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a0),
-                            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a1)};
-        const u32x4 bw = __builtin_bit_cast(u32x4, b);
-#pragma unroll
-        for (int s = 0; s < NS; ++s) acc[nb] = LpMma<bf16>::run(part[s], bw, acc[nb]);
+      for (int q = 0; q < NY; ++q) {
+        const int row = 4 * h + q;
+        y[q] = row * T::RB + (((r >> 2) ^ (row & T::SWM)) << 4) + 4 * (r & 3);
       }
+    }
+  }
+  // 16-byte chunk 2 k + h of row l % 32
+  static __device__ __forceinline__ u32x4 frag(const LpLds& o, uint32_t base, int k) {
+    return lds_at<u32x4>(o.x[k % NX] + base + (k / NX) * (NX * 32));
+  }
+};
+
+// acc[ob][nb] += G[32 owners][32 streamed] . rows[32 streamed][D], lane l holding G[owner l % 32]
+// [streamed lp_row(v) + 4 (l / 32)] in g[ob][v].  bf16: `terms` products, each with the bf16
+// rounding of what the ones before left of G (1: rounded once, 3: all 24 bits).
+template <class E, int D, int NWS, int OB>
+__device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g)[OB], int terms, const LpLds<E, D, NWS>& o,
+                                           uint32_t base) {
+  using T = LpTile<E, D, NWS>;
+  if constexpr (sizeof(E) == 2) {
+#pragma unroll 1
+    while (true) {
+      u32x4 part[OB][2];
+#pragma unroll
+      for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[ob][e / 4][e % 4] = pack_bf16(g[ob][2 * e], g[ob][2 * e + 1]);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int nb = 0; nb < D / 32; ++nb) {
+          const uint32_t at = o.y[nb % o.NY] + base + (nb / o.NY) * 128 + 16 * kk * T::RB;
+          const s16x4 b[2] = {lds_tr4(at), lds_tr4(at + 8 * T::RB)};
+          const u32x4 bw = __builtin_bit_cast(u32x4, b);
+#pragma unroll
+          for (int ob = 0; ob < OB; ++ob) acc[ob][nb] = LpMma<bf16>::run(part[ob][kk], bw, acc[ob][nb]);
+        }
+      if (--terms <= 0) break;
+#pragma unroll
+      for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          g[ob][2 * e] -= lo_f32(part[ob][e / 4][e % 4]);
+          g[ob][2 * e + 1] -= hi_f32(part[ob][e / 4][e % 4]);
+        }
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int row = rb * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+    for (int v = 0; v < 16; ++v)
 #pragma unroll
       for (int nb = 0; nb < D / 32; ++nb) {
-        const int dim = 32 * nb + (l & 31);
-        const float b = *reinterpret_cast<const float*>(tile + row * T::RB + (((dim >> 2) ^ (row & T::SWM)) << 4) + 4 * (dim & 3));
-        acc[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(g[v], b, acc[nb], 0, 0, 0);
+        const float b = lds_at<float>(o.y[v & 3] + base + 8 * (v >> 2) * T::RB + nb * 128);
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob) acc[ob][nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(g[ob][v], b, acc[ob][nb], 0, 0, 0);
       }
-    }
   }
 }
 
 // NWO waves along the owners x NWS waves along a tile's rows; OB blocks of 32 owners per wave.
-template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int NS>
-__global__ __launch_bounds__(64 * NWO * NWS) void k_lp_sweep(LpArgs a) {
+template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int MINW>
+__global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   using T = LpTile<E, D, NWS>;
+  using L = LpLds<E, D, NWS>;
   constexpr int TI = T::TI, RB = T::RB, NT = 64 * NWO * NWS;
-  constexpr int KC = RB / 32;              // 32-byte steps of a row: one chunk per lane half
+  constexpr int KC = L::KC;
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile
-  static_assert(T::BYTES % (16 * NT) == 0, "whole chunks per thread");
+  constexpr bool ACC = MODE != LP_LSE, LSE = MODE == LP_LSE || MODE == LP_LSEO, DY = MODE == LP_DY;
+  static_assert(T::BYTES % (16 * NT) == 0 && TI <= NT, "whole chunks per thread");
   extern __shared__ __attribute__((aligned(16))) char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
   const int tid = threadIdx.x, w = tid >> 6, l = lane_id(), h = l >> 5, r = l & 31;
   const int wo = w % NWO, ws = w / NWO;
-  const int64_t nv = *a.nv;
-  const int64_t n_own = a.own_is_pos ? nv : a.n_own, n_str = a.own_is_pos ? a.n_str : nv;
-  const int64_t blk0 = (int64_t)blockIdx.x * (32 * OB * NWO), o0 = blk0 + wo * (32 * OB);
+  // row numbers in 32 bits without a sign: at most 2^31 - 1 rows and a tile
+  const uint32_t nv = (uint32_t)*a.nv;
+  const uint32_t n_own = a.own_is_pos ? nv : (uint32_t)a.n_own, n_str = a.own_is_pos ? (uint32_t)a.n_str : nv;
+  const uint32_t blk0 = blockIdx.x * (32 * OB * NWO), o0 = blk0 + wo * (32 * OB);
   const int split = blockIdx.y;
   if (blk0 >= n_own) return;
-  const int64_t ntiles = (n_str + TI - 1) / TI, per = (ntiles + a.splits - 1) / a.splits;
-  const int64_t tb = min(ntiles, (int64_t)split * per), te = min(ntiles, tb + per);
+  const uint32_t ntiles = (n_str + TI - 1) / TI, per = (ntiles + a.splits - 1) / a.splits;
+  const uint32_t tb = min(ntiles, split * per), te = min(ntiles, tb + per);
 
+  L lo;
+  lo.init();
   u32x4 bown[OB][KC];
+  float olse[OB], oa[OB], obt[OB], og[OB];   // LP_DX: the owner's constants
+  uint32_t opos[OB];                         // its own item
 #pragma unroll
   for (int ob = 0; ob < OB; ++ob) {
-    const int64_t o = min(o0 + 32 * ob + r, n_own - 1);
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.own) + o * RB);
+    const uint32_t o = min(o0 + 32 * ob + r, n_own - 1);
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.own) + (int64_t)o * RB);
 #pragma unroll
     for (int t = 0; t < KC; ++t) bown[ob][t] = p[2 * t + h];
-  }
-  LpRow orow[OB];        // LP_DX
-  int opos[OB];
-  if constexpr (MODE == LP_DX) {
-#pragma unroll
-    for (int ob = 0; ob < OB; ++ob) {
-      const int64_t o = min(o0 + 32 * ob + r, n_own - 1);
-      orow[ob] = a.rows[o];
-      opos[ob] = a.idc[o];
+    opos[ob] = 0;
+    if constexpr (MODE == LP_DX || MODE == LP_LSEO) opos[ob] = (uint32_t)a.idc[o];
+    if constexpr (MODE == LP_DX) {
+      const LpRow c = a.rows[o];
+      olse[ob] = c.lse2;
+      oa[ob] = c.a;
+      obt[ob] = c.b;
+      og[ob] = c.g;
     }
   }
-  float m[OB], z[OB], tt[OB];
-  f32x16 acc[MODE == LP_LSE ? 1 : OB][D / 32];
+  float m[OB], z[OB], tt[OB];   // LP_LSE(O): reference and sums
+  f32x16 acc[ACC ? OB : 1][D / 32];
+  auto clear = [&]() {
 #pragma unroll
-  for (int ob = 0; ob < OB; ++ob) {
-    m[ob] = NEG_INF;
-    z[ob] = tt[ob] = 0.0f;
-  }
-  if constexpr (MODE != LP_LSE) {
+    for (int ob = 0; ob < OB; ++ob) {
+      z[ob] = tt[ob] = 0.0f;
+      if constexpr (ACC)
 #pragma unroll
-    for (int ob = 0; ob < OB; ++ob)
+        for (int nb = 0; nb < D / 32; ++nb)
 #pragma unroll
-      for (int nb = 0; nb < D / 32; ++nb)
+          for (int v = 0; v < 16; ++v) acc[ob][nb][v] = 0.0f;
+    }
+  };
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[ob][nb][v] = 0.0f;
-  }
+  for (int ob = 0; ob < OB; ++ob) m[ob] = NEG_INF;
+  clear();
+  const float c2 = a.c2;
+  // a logit that weighs nothing, finite after the factor c2
+  const float far = fmaxf(-1e30f / c2, -3e38f);
 
-  char* const bufs = smem;
-  // streamed positions' constants and ids of a tile (LP_DY), behind the two tile buffers
-  LpRow* const srow = reinterpret_cast<LpRow*>(smem + 2 * T::BYTES);
-  int32_t* const sid = reinterpret_cast<int32_t*>(smem + 2 * T::BYTES + 2 * TI * sizeof(LpRow));
+  // behind the two tile buffers (LP_DY): the rows' constants, [2][5][TI] words: lse2, a, b, g, id
+  constexpr int PB = 5 * TI * 4;
+  const uint32_t par0 = lds0 + 2 * T::BYTES;
   u32x4 nxt[PT];
   u32x4 nrow = u32x4{0u, 0u, 0u, 0u};
   int nid = -1;
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](uint32_t t) {
+    const char* src = static_cast<const char*>(a.str) + (int64_t)t * T::BYTES;
+    const uint32_t last = min((uint32_t)TI, n_str - t * TI) - 1;
 #pragma unroll
     for (int q = 0; q < PT; ++q) {
-      const int ch = q * NT + tid;
-      const int64_t row = min(t * TI + ch / T::CPR, n_str - 1);
-      nxt[q] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.str) + row * RB + (ch % T::CPR) * 16);
+      const uint32_t ch = q * NT + tid;
+      nxt[q] = *reinterpret_cast<const u32x4*>(src + (min(ch / T::CPR, last) * RB + (ch % T::CPR) * 16));
     }
-    if constexpr (MODE == LP_DY) {
+    if constexpr (DY) {
       if (tid < TI) {   // packed rows are padded with rows of no weight to whole tiles
-        nrow = *reinterpret_cast<const u32x4*>(a.rows + t * TI + tid);
-        nid = a.idc[t * TI + tid];
+        nrow = *reinterpret_cast<const u32x4*>(a.rows + ((int64_t)t * TI + tid));
+        nid = a.idc[(int64_t)t * TI + tid];
       }
     }
   };
-  auto stash = [&](int64_t t) {
-    char* buf = bufs + (t & 1) * T::BYTES;
+  auto stash = [&](uint32_t t) {
+    const uint32_t buf = lds0 + (t & 1) * T::BYTES;
 #pragma unroll
     for (int q = 0; q < PT; ++q) {
-      const int ch = q * NT + tid, row = ch / T::CPR, c = ch % T::CPR;
-      *reinterpret_cast<u32x4*>(buf + row * RB + ((c ^ (row & T::SWM)) << 4)) = nxt[q];
+      const uint32_t ch = q * NT + tid, row = ch / T::CPR, c = ch % T::CPR;
+      *reinterpret_cast<__attribute__((address_space(3))) u32x4*>((uintptr_t)(buf + row * RB + ((c ^ (row & T::SWM)) << 4))) = nxt[q];
     }
-    if constexpr (MODE == LP_DY) {
+    if constexpr (DY) {
       if (tid < TI) {
-        *reinterpret_cast<u32x4*>(srow + (t & 1) * TI + tid) = nrow;
-        sid[(t & 1) * TI + tid] = nid;
+        const uint32_t par = par0 + (t & 1) * PB + 4 * tid;
+#pragma unroll
+        for (int q = 0; q < 5; ++q)
+          *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>((uintptr_t)(par + q * TI * 4)) = q < 4 ? nrow[q < 4 ? q : 0] : (uint32_t)nid;
       }
     }
   };
-  if (tb < te) {
-    fetch(tb);
-    stash(tb);
-  }
-  for (int64_t t = tb; t < te; ++t) {
-    __syncthreads();
-    if (t + 1 < te) fetch(t + 1);
-    const char* tile = bufs + (t & 1) * T::BYTES;
-#pragma unroll 1
-    for (int rb = ws; rb < TI / 32; rb += NWS) {
-      const int64_t q0 = t * TI + rb * 32;
-      const int lim = (int)min((int64_t)32, n_str - q0);   // rows of the block that exist (<= 0: none)
-      f32x16 x[OB];
+
+  f32x16 x[OB];
+  // logits of 32 streamed rows (first one q0, at LDS offset base) against the wave's owners
+  auto logits = [&](uint32_t base, uint32_t q0) {
+    const f32x16 zero = {};
 #pragma unroll
-      for (int ob = 0; ob < OB; ++ob)
+    for (int k = 0; k < KC; ++k) {
+      const u32x4 f = L::frag(lo, base, k);
 #pragma unroll
-        for (int v = 0; v < 16; ++v) x[ob][v] = 0.0f;
-      const int row = rb * 32 + r;
+      for (int ob = 0; ob < OB; ++ob) x[ob] = LpMma<E>::run(f, bown[ob][k], k == 0 ? zero : x[ob]);
+    }
+    if constexpr (!DY) {
+      if (q0 + 32 > n_str) {   // the last tile's rows beyond the end
+        const int lim = (int)(n_str - q0) - 4 * h;
 #pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        const u32x4 f = *reinterpret_cast<const u32x4*>(tile + row * RB + (((2 * k + h) ^ (row & T::SWM)) << 4));
+        for (int ob = 0; ob < OB; ++ob)
 #pragma unroll
-        for (int ob = 0; ob < OB; ++ob) x[ob] = LpMma<E>::run(f, bown[ob][k], x[ob]);
-      }
-      if constexpr (MODE == LP_LSE) {
-#pragma unroll
-        for (int ob = 0; ob < OB; ++ob) {
-          float e[16], d[16];
-          auto sums = [&](float& s, float& st) {
-            s = st = 0.0f;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const int n = 8 * (v >> 2) + 4 * h + (v & 3);
-              d[v] = fmaf(x[ob][v], a.c2, -m[ob]);
-              e[v] = exp2_fast(d[v]);
-              if (lim < 32 && n >= lim) e[v] = d[v] = 0.0f;
-              s += e[v];
-              if constexpr (ENT) st = fmaf(e[v], d[v], st);
-            }
-          };
-          float s, st;
-          sums(s, st);
-          // the reference m is the first block's maximum and moves only when a block's sum
-          // would pass 2^40 (exp2 has the range); NaN logits end here too, and stay NaN
-          if (ballot(!(s < LP_REF_LIMIT))) {
-            float bm = NEG_INF;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const int n = 8 * (v >> 2) + 4 * h + (v & 3);
-              if (lim >= 32 || n < lim) bm = fmaxf(bm, x[ob][v] * a.c2);
-            }
-            if (bm > m[ob]) {
-              const float f = z[ob] > 0.0f ? exp2_fast(m[ob] - bm) : 0.0f;
-              if constexpr (ENT) tt[ob] = z[ob] > 0.0f ? (tt[ob] + z[ob] * (m[ob] - bm)) * f : 0.0f;
-              z[ob] *= f;
-              m[ob] = bm;
-            }
-            sums(s, st);
-          }
-          if (m[ob] != NEG_INF) {
-            z[ob] += s;
-            if constexpr (ENT) tt[ob] += st;
-          }
-        }
-      } else {
-        bool hit = false;
-        if constexpr (MODE == LP_DX) {
-#pragma unroll
-          for (int ob = 0; ob < OB; ++ob) hit = hit || (opos[ob] >= q0 && opos[ob] < q0 + 32);
-        } else {
-          const int id = sid[(t & 1) * TI + row];
-          hit = id >= o0 && id < o0 + 32 * OB;
-        }
-        const bool any = ballot(hit) != 0;
-#pragma unroll
-        for (int ob = 0; ob < OB; ++ob) {
-          float g[16];
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int n = 8 * (v >> 2) + 4 * h + (v & 3);
-            LpRow c;
-            if constexpr (MODE == LP_DX)
-              c = orow[ob];
-            else
-              c = srow[(t & 1) * TI + rb * 32 + n];
-            const float d = fmaf(x[ob][v], a.c2, -c.lse2);
-            const float wgt = ENT ? fmaf(c.b, d, c.a) : c.a;
-            g[v] = -exp2_fast(d) * wgt;
-            if (lim < 32 && n >= lim) g[v] = 0.0f;
-            if (any) {
-              bool on;
-              if constexpr (MODE == LP_DX)
-                on = q0 + n == opos[ob];
-              else
-                on = (int64_t)sid[(t & 1) * TI + rb * 32 + n] == o0 + 32 * ob + r;
-              if (on) g[v] += c.g;
-            }
-          }
-          // a block that holds some row's own item: 1 - p would lose its digits in one bf16 term
-          if (any)
-            lp_accumulate<E, D, NWS, 3>(acc[ob], g, tile, rb);
-          else
-            lp_accumulate<E, D, NWS, NS>(acc[ob], g, tile, rb);
-        }
+          for (int v = 0; v < 16; ++v)
+            if (lp_row(v) >= lim) x[ob][v] = far;
       }
     }
-    if (t + 1 < te) stash(t + 1);
-  }
-
-  if constexpr (MODE == LP_LSE) {
+  };
+  // m = max(m, the block's logits), the same in both lane halves of an owner
+  auto raise = [&]() {
 #pragma unroll
     for (int ob = 0; ob < OB; ++ob) {
-      // the two lane halves hold different rows of the same owner
-      const float om = __shfl_xor(m[ob], 32), oz = __shfl_xor(z[ob], 32), ot = __shfl_xor(tt[ob], 32);
-      const float mm = fmaxf(m[ob], om);
-      const float f0 = m[ob] == NEG_INF ? 0.0f : exp2_fast(m[ob] - mm), f1 = om == NEG_INF ? 0.0f : exp2_fast(om - mm);
-      const float zz = z[ob] * f0 + oz * f1;
-      const float t0 = m[ob] == NEG_INF ? 0.0f : (tt[ob] + z[ob] * (m[ob] - mm)) * f0;
-      const float t1 = om == NEG_INF ? 0.0f : (ot + oz * (om - mm)) * f1;
-      const int64_t o = o0 + 32 * ob + r;
+      float bm = m[ob];
+#pragma unroll
+      for (int v = 0; v < 16; ++v) bm = fmaxf(bm, x[ob][v] * c2);
+      m[ob] = fmaxf(bm, __shfl_xor(bm, 32));
+    }
+  };
+  // One block; own: the tile holds an owner's own item (LP_DY: a row whose item is an owner).
+  auto block = [&](bool own, uint32_t base, uint32_t par, uint32_t q0) {
+    logits(base, q0);
+    if constexpr (LSE) {
+#pragma unroll
+      for (int ob = 0; ob < OB; ++ob) {
+        float s = 0.0f, st = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const float d = fmaf(x[ob][v], c2, -m[ob]);
+          x[ob][v] = exp2_fast(d);
+          s += x[ob][v];
+          if constexpr (ENT) st = fmaf(x[ob][v], d, st);
+        }
+        z[ob] += s;
+        if constexpr (ENT) tt[ob] += st;
+      }
+      if constexpr (MODE == LP_LSEO) {
+        if (own) {   // the owner's own item stays out of the sum of rows
+#pragma unroll
+          for (int ob = 0; ob < OB; ++ob) {
+            const uint32_t at = opos[ob] - q0 - 4 * h;
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              if (lp_row(v) == at) x[ob][v] = 0.0f;
+          }
+        }
+        lp_product<E, D, NWS, OB>(acc, x, a.terms, lo, base);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 pl, pa, pb;
+        if constexpr (DY) {
+          const uint32_t at = par + 32 * q + 16 * h;
+          pl = lds_at<f32x4>(at);
+          pa = lds_at<f32x4>(at + TI * 4);
+          if constexpr (ENT) pb = lds_at<f32x4>(at + 2 * TI * 4);
+        }
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int v = 4 * q + e;
+            const float d = fmaf(x[ob][v], c2, DY ? -pl[e] : -olse[ob]);
+            const float wgt = ENT ? fmaf(DY ? pb[e] : obt[ob], d, DY ? pa[e] : oa[ob]) : (DY ? pa[e] : oa[ob]);
+            x[ob][v] = -exp2_fast(d) * wgt;
+          }
+      }
+      if (own) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 pg;
+          u32x4 pid;
+          if constexpr (DY) {
+            const uint32_t at = par + 32 * q + 16 * h;
+            pg = lds_at<f32x4>(at + 3 * TI * 4);
+            pid = lds_at<u32x4>(at + 4 * TI * 4);
+          }
+#pragma unroll
+          for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int v = 4 * q + e;
+              const bool on = DY ? pid[e] == o0 + 32 * ob + r : q0 + lp_row(v) + 4 * h == opos[ob];
+              if (on) x[ob][v] += DY ? pg[e] : og[ob];
+            }
+        }
+      }
+      // the own item's weight, g (1 - p), is most of its row's result: it enters with all its bits
+      lp_product<E, D, NWS, OB>(acc, x, own ? 3 : a.terms, lo, base);
+    }
+  };
+  // All tiles of the split through f(tile, LDS offset of the wave's first block, of its constants, first row).
+  auto sweep = [&](auto f) {
+    if (tb < te) {
+      fetch(tb);
+      stash(tb);
+    }
+    for (uint32_t t = tb; t < te; ++t) {
+      __syncthreads();
+      if (t + 1 < te) fetch(t + 1);
+      f(t, lds0 + (t & 1) * T::BYTES + ws * (32 * RB), par0 + (t & 1) * PB + ws * 128, t * TI + ws * 32);
+      if (t + 1 < te) stash(t + 1);
+    }
+  };
+  auto main_pass = [&](bool fresh) {
+    sweep([&](uint32_t t, uint32_t base, uint32_t par, uint32_t q0) {
+      if constexpr (LSE) {
+        if (fresh && t == tb) {   // the first block's largest logit is the reference of the sums
+          logits(base, q0);
+          raise();
+        }
+      }
+      bool hit = false;
+      if constexpr (MODE == LP_DX || MODE == LP_LSEO) {
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob) hit = hit || opos[ob] - t * TI < TI;
+      } else if constexpr (DY) {
+#pragma unroll
+        for (int q = 0; q < TI; q += WAVE) {
+          const uint32_t id = lds_at<uint32_t>(par0 + (t & 1) * PB + 4 * TI * 4 + 4 * (q + (TI < WAVE ? r : l)));
+          hit = hit || id - o0 < 32 * OB;
+        }
+      }
+      const bool own = MODE != LP_LSE && ballot(hit) != 0;
+#pragma unroll 1
+      for (int i = 0; i < TI / 32 / NWS; ++i)
+        block(own, base + i * (NWS * 32 * RB), par + i * NWS * 128, q0 + i * NWS * 32);
+    });
+  };
+  main_pass(true);
+  if constexpr (LSE) {
+    // exp2 has the range for logits up to 2^60 times the reference's; beyond (or with NaN among
+    // them) the references become the split's true maxima and the sums are taken again
+    bool over = false;
+#pragma unroll
+    for (int ob = 0; ob < OB; ++ob) over = over || !(z[ob] < LP_REF_LIMIT);
+    if (__syncthreads_or(over)) {
+      sweep([&](uint32_t, uint32_t base, uint32_t, uint32_t q0) {
+#pragma unroll 1
+        for (int i = 0; i < TI / 32 / NWS; ++i) {
+          logits(base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
+          raise();
+        }
+      });
+      __syncthreads();
+      clear();
+      main_pass(false);
+    }
+  }
+
+  const int64_t part = (int64_t)split * NWS + ws;
+  if constexpr (LSE) {
+#pragma unroll
+    for (int ob = 0; ob < OB; ++ob) {
+      // the two lane halves hold different rows of the same owner, against one reference
+      const float zz = z[ob] + __shfl_xor(z[ob], 32), t0 = tt[ob] + __shfl_xor(tt[ob], 32);
+      const uint32_t o = o0 + 32 * ob + r;
       if (h == 0 && o < n_own) {
-        const int64_t at = ((int64_t)split * NWS + ws) * a.own_pad + o;
-        a.m[at] = mm;
-        a.z[at] = zz;
-        if constexpr (ENT) a.t[at] = t0 + t1;
+        a.m[part * a.own_pad + o] = m[ob];
+        a.z[part * a.own_pad + o] = zz;
+        if constexpr (ENT) a.t[part * a.own_pad + o] = t0;
       }
     }
-  } else {
-    float* out = a.out + ((int64_t)split * NWS + ws) * a.own_pad * D;
+  }
+  if constexpr (ACC) {
+    float* out = a.out + part * a.own_pad * D;
 #pragma unroll
     for (int ob = 0; ob < OB; ++ob)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int64_t o = o0 + 32 * ob + 8 * (v >> 2) + 4 * h + (v & 3);
+        const uint32_t o = o0 + 32 * ob + lp_row(v) + 4 * h;
         if (o < n_own)
 #pragma unroll
-          for (int nb = 0; nb < D / 32; ++nb) out[o * D + 32 * nb + r] = acc[ob][nb][v];
+          for (int nb = 0; nb < D / 32; ++nb) out[(int64_t)o * D + 32 * nb + r] = acc[ob][nb][v];
       }
   }
 }
 
 // ------------------------------------------------------------------ packing
-// One workgroup: the positions with an id in [0, C), in order.  inv[i] is position i's
-// place among them, or -1.
-constexpr int PACK_THREADS = 1024;
-__global__ __launch_bounds__(PACK_THREADS) void k_lp_list(const int32_t* __restrict__ ids, int64_t s, int64_t C,
-                                                          int32_t* __restrict__ nv, int32_t* __restrict__ list,
-                                                          int32_t* __restrict__ inv) {
-  constexpr int PER = 8;   // ids per thread and step, loaded before the step's prefix sum
-  __shared__ int32_t wsum[PACK_THREADS / WAVE];
+// Workgroup b takes ids [b per, (b + 1) per): it counts the ids before them that lie in
+// [0, C) itself (an L2-resident read of 4 bytes a position, in place of a scan's further
+// launches), then writes the list of its own, the packed rows and ids, and the base-2
+// logit of each row's own item.  The last workgroup adds zero rows up to the padding.
+constexpr int PACK_THREADS = 512;
+constexpr int64_t PACK_BLOCKS = 256;
+
+template <class E, int D>
+__global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ X, const E* __restrict__ Y,
+                                                          const int32_t* __restrict__ ids, int64_t s, int64_t C,
+                                                          int64_t per, int64_t pad, float c2, int32_t* __restrict__ nv,
+                                                          int32_t* __restrict__ list, int32_t* __restrict__ inv,
+                                                          E* __restrict__ Xc, int32_t* __restrict__ idc,
+                                                          float* __restrict__ own2) {
+  constexpr int EPL = 16 / (int)sizeof(E), LPR = D / EPL, NW = PACK_THREADS / WAVE, RPB = PACK_THREADS / LPR;
+  __shared__ int32_t wsum[NW];
+  __shared__ int32_t src[PACK_THREADS];
   const int tid = threadIdx.x, w = tid >> 6, l = lane_id();
+  const int64_t i0 = (int64_t)blockIdx.x * per, i1 = min(s, i0 + per);
+  auto good = [&](int64_t i, int64_t end) {
+    const int id = i < end ? ids[i] : -1;
+    return id >= 0 && id < C;
+  };
+  int before = 0;
+#pragma unroll 8
+  for (int64_t i = tid; i < i0; i += PACK_THREADS) before += good(i, i0) ? 1 : 0;
+  before = wave_sum(before);
+  if (l == 0) wsum[w] = before;
+  __syncthreads();
   int64_t done = 0;
-  for (int64_t b = 0; b < s; b += PACK_THREADS * PER) {
-    const int64_t i0 = b + (int64_t)tid * PER;
-    uint32_t ok = 0;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int id = i0 + q < s ? ids[i0 + q] : -1;
-      ok |= id >= 0 && id < C ? 1u << q : 0u;
+  for (int q = 0; q < NW; ++q) done += wsum[q];
+  const int sub = tid % LPR;
+  // one packed row per lane group: list entry q of src, or (q beyond n) zeros
+  auto put_row = [&](int64_t row, int64_t i) {
+    u32x4 x = u32x4{0u, 0u, 0u, 0u};
+    int id = -1;
+    float dot = 0.0f;
+    if (i >= 0) {
+      id = ids[i];
+      x = reinterpret_cast<const u32x4*>(X + i * D)[sub];
+      const u32x4 y = reinterpret_cast<const u32x4*>(Y + (int64_t)id * D)[sub];
+      const E* xe = reinterpret_cast<const E*>(&x);
+      const E* ye = reinterpret_cast<const E*>(&y);
+#pragma unroll
+      for (int t = 0; t < EPL; ++t) dot = fmaf(to_f32(xe[t]), to_f32(ye[t]), dot);
     }
-    const int mine = __popc(ok);
-    const int incl = (int)wave_prefix_incl((uint32_t)mine);
-    __syncthreads();
-    if (l == WAVE - 1) wsum[w] = incl;
-    __syncthreads();
-    int64_t at = done + incl - mine;
-    int tot = 0;
 #pragma unroll
-    for (int q = 0; q < PACK_THREADS / WAVE; ++q) {
+    for (int o = LPR / 2; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
+    reinterpret_cast<u32x4*>(Xc + row * D)[sub] = x;
+    if (sub == 0) {
+      idc[row] = id;
+      own2[row] = dot * c2;
+    }
+  };
+  for (int64_t b = i0; b < i1; b += PACK_THREADS) {
+    const int64_t i = b + tid;
+    const bool on = good(i, i1);
+    const uint64_t mask = ballot(on);
+    __syncthreads();   // wsum and src of the step before are read
+    if (l == 0) wsum[w] = popc(mask);
+    __syncthreads();
+    int at = popc(mask & lanemask_lt()), tot = 0;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
       if (q < w) at += wsum[q];
       tot += wsum[q];
     }
-    done += tot;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      if (i0 + q >= s) break;
-      const bool on = (ok >> q) & 1u;
-      inv[i0 + q] = on ? (int32_t)at : -1;
-      if (on) list[at++] = (int32_t)(i0 + q);
+    if (i < i1) inv[i] = on ? (int32_t)(done + at) : -1;
+    if (on) {
+      list[done + at] = (int32_t)i;
+      src[at] = (int32_t)i;
     }
+    __syncthreads();
+    for (int q = tid / LPR; q < tot; q += RPB) put_row(done + q, src[q]);
+    done += tot;
   }
-  if (tid == 0) *nv = (int32_t)done;
-}
-
-// Packed rows and ids (zero rows up to the padding), and the base-2 logit of each row's
-// own item.  One lane group of D / (16 / sizeof(E)) lanes per row.
-template <class E, int D>
-__global__ __launch_bounds__(256) void k_lp_pack(const E* __restrict__ X, const E* __restrict__ Y,
-                                                 const int32_t* __restrict__ ids, const int32_t* __restrict__ nv_p,
-                                                 const int32_t* __restrict__ list, int64_t pad, float c2,
-                                                 E* __restrict__ Xc, int32_t* __restrict__ idc, float* __restrict__ own2) {
-  constexpr int EPL = 16 / (int)sizeof(E), LPR = D / EPL;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-  const int sub = threadIdx.x % LPR;
-  const int64_t nv = *nv_p;
-  if (row >= min(pad, (nv + LP_ROW_PAD - 1) / LP_ROW_PAD * LP_ROW_PAD)) return;
-  u32x4 x = u32x4{0u, 0u, 0u, 0u};
-  int id = -1;
-  float dot = 0.0f;
-  if (row < nv) {
-    const int64_t i = list[row];
-    id = ids[i];
-    x = reinterpret_cast<const u32x4*>(X + i * D)[sub];
-    const u32x4 y = reinterpret_cast<const u32x4*>(Y + (int64_t)id * D)[sub];
-    const E* xe = reinterpret_cast<const E*>(&x);
-    const E* ye = reinterpret_cast<const E*>(&y);
-#pragma unroll
-    for (int t = 0; t < EPL; ++t) dot = fmaf(to_f32(xe[t]), to_f32(ye[t]), dot);
-  }
-#pragma unroll
-  for (int o = LPR / 2; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
-  reinterpret_cast<u32x4*>(Xc + row * D)[sub] = x;
-  if (sub == 0) {
-    idc[row] = id;
-    own2[row] = dot * c2;
+  if (blockIdx.x + 1 == gridDim.x) {
+    const int64_t end = min(pad, (done + LP_ROW_PAD - 1) / LP_ROW_PAD * LP_ROW_PAD);
+    for (int64_t q = done + tid / LPR; q < end; q += RPB) put_row(q, -1);
+    if (tid == 0) *nv = (int32_t)done;
   }
 }
 
 // ------------------------------------------------------------------ joins
-// Per position: the parts of its sum, in order -> log-sum-exp, log-probability, entropy.
+// One wave per position: the parts of its sum -> log-sum-exp, log-probability, entropy.
 __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ inv, int64_t s, int parts, int64_t pad,
                                                    const float* __restrict__ m, const float* __restrict__ z,
                                                    const float* __restrict__ t, const float* __restrict__ own2,
                                                    float* __restrict__ lse2, float* __restrict__ ent_c,
                                                    float* __restrict__ logp, float* __restrict__ entropy) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int l = lane_id();
   if (i >= s) return;
   const int64_t r = inv[i];
   if (r < 0) {
-    logp[i] = 0.0f;
-    if (entropy) entropy[i] = 0.0f;
+    if (l == 0) {
+      logp[i] = 0.0f;
+      if (entropy) entropy[i] = 0.0f;
+    }
     return;
   }
-  float mm = NEG_INF;
-  for (int p = 0; p < parts; ++p) mm = fmaxf(mm, m[(int64_t)p * pad + r]);
-  float zz = 0.0f, tt = 0.0f;
-  for (int p = 0; p < parts; ++p) {
+  float mm = NEG_INF, zz = 0.0f, tt = 0.0f;
+  for (int p = l; p < parts; p += WAVE) {
     const float mp = m[(int64_t)p * pad + r], zp = z[(int64_t)p * pad + r];
+    const float tp = entropy ? t[(int64_t)p * pad + r] : 0.0f;
     if (mp == NEG_INF) continue;
-    const float f = exp2_fast(mp - mm);
-    zz = fmaf(zp, f, zz);
-    if (entropy) tt += (t[(int64_t)p * pad + r] + zp * (mp - mm)) * f;
+    const float mn = fmaxf(mm, mp);
+    const float f0 = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn), f1 = exp2_fast(mp - mn);
+    tt = (mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f0) + (tp + zp * (mp - mn)) * f1;
+    zz = zz * f0 + zp * f1;
+    mm = mn;
   }
-  const float lz = log2f(zz), l2 = mm + lz;
+  const float mn = wave_max(mm);
+  const float f = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn);
+  tt = wave_sumf(mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f);
+  zz = wave_sumf(zz * f);
+  if (l != 0) return;
+  const float lz = log2f(zz), l2 = mn + lz;
   lse2[r] = l2;
   logp[i] = (own2[r] - l2) * LN2;
   if (entropy) {
@@ -516,10 +634,20 @@ __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_
   rows[r] = c;
 }
 
+__device__ __forceinline__ void put4(void* out, int64_t at, float4 v, bool b16) {
+  if (b16) {
+    uint2 o;
+    o.x = pack_bf16(v.x, v.y);
+    o.y = pack_bf16(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = o;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  }
+}
+
 // out row = sum of the parts' rows, in order; inv: row of the parts for each output row (or -1: zeros).
-template <bool B16>
 __global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part, int parts, int64_t pad, int d,
-                                                 const int32_t* __restrict__ inv, int64_t n, void* __restrict__ out) {
+                                                 const int32_t* __restrict__ inv, int64_t n, void* __restrict__ out, int b16) {
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = d / 4;
   if (q >= n * per) return;
@@ -528,19 +656,44 @@ __global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part,
   const int64_t r = inv ? inv[i] : i;
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
+#pragma unroll 4
     for (int p = 0; p < parts; ++p) {
       const float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
       v = float4{v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w};
     }
   }
-  if constexpr (B16) {
-    uint2 o;
-    o.x = pack_bf16(v.x, v.y);
-    o.y = pack_bf16(v.z, v.w);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i * d + c) = o;
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + i * d + c) = v;
+  put4(out, i * d + c, v, b16 != 0);
+}
+
+// dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j over the
+// items but the row's own:  dX_i = g_i ((1 - p_i) y_own - sum of the parts of O 2^(m - lse2)).
+template <class E>
+__global__ __launch_bounds__(256) void k_lp_dx(const float* __restrict__ part, const float* __restrict__ m, int parts,
+                                               int64_t pad, int d, const int32_t* __restrict__ inv, int64_t s,
+                                               const E* __restrict__ Y, const int32_t* __restrict__ idc,
+                                               const float* __restrict__ own2, const float* __restrict__ lse2,
+                                               const float* __restrict__ dlogp, float inv_t, void* __restrict__ out,
+                                               int b16) {
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = d / 4;
+  if (q >= s * per) return;
+  const int64_t i = q / per;
+  const int c = (int)(q % per) * 4;
+  const int64_t r = inv[i];
+  float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (r >= 0) {
+    const float l2 = lse2[r], g = dlogp[i] * inv_t;
+    const float rest = -expm1f((own2[r] - l2) * LN2);
+    for (int p = 0; p < parts; ++p) {
+      const float f = exp2_fast(m[(int64_t)p * pad + r] - l2);
+      const float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
+      v = float4{fmaf(f, w.x, v.x), fmaf(f, w.y, v.y), fmaf(f, w.z, v.z), fmaf(f, w.w, v.w)};
+    }
+    const E* y = Y + (int64_t)idc[r] * d + c;
+    v = float4{g * fmaf(rest, to_f32(y[0]), -v.x), g * fmaf(rest, to_f32(y[1]), -v.y),
+               g * fmaf(rest, to_f32(y[2]), -v.z), g * fmaf(rest, to_f32(y[3]), -v.w)};
   }
+  put4(out, i * d + c, v, b16 != 0);
 }
 
 // ------------------------------------------------------------------ host side
@@ -560,15 +713,20 @@ int lp_splits(int64_t n_own, int64_t own_block, int64_t n_str, int64_t ti, int64
   return (int)std::max<int64_t>(1, std::min<int64_t>(sp, 4096));
 }
 
+// Launch shapes: blocks of 32 owners per wave (more: fewer LDS reads per product; fewer: more waves
+// per SIMD to overlap the exponentials with the products) and waves per SIMD.
 template <class E, int D> struct LpShape {
-  static constexpr int OB_LSE = sizeof(E) == 2 && D <= 128 ? 2 : 1;
-  static constexpr int OB_GRAD = 1;
+  static constexpr bool B = sizeof(E) == 2;
   static constexpr int NWO = 4;
+  static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
+  static constexpr int MW_LSE = B ? 2 : (D <= 128 ? 2 : 1);
+  static constexpr int OB_GRAD = B && D <= 64 ? 2 : 1;
+  static constexpr int MW_GRAD = B ? 2 : (D <= 64 ? 2 : 1);
 };
 
 struct LpLayout {
   int64_t pad;
-  size_t nv, list, inv, idc, own2, lse2, ent, rows, xc, m, z, t, dx, dy, bytes;
+  size_t nv, list, inv, idc, own2, lse2, ent, rows, xc, m, z, t, o, dx, dy, bytes;
   int sp_lse, sp_dx, sp_dy;
 };
 
@@ -576,9 +734,13 @@ template <class E, int D>
 LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   using S = LpShape<E, D>;
   using T = LpTile<E, D, 1>;
+  const bool grad = !(flags & RECE_FLAG_NO_GRAD), ent = flags & RECE_FLAG_ENTROPY;
   LpLayout y{};
   y.pad = ceil_div(s, LP_ROW_PAD) * LP_ROW_PAD;
-  y.sp_lse = lp_splits(s, 32 * S::OB_LSE * S::NWO, C, T::TI, 12 * y.pad);
+  // without entropies the forward pass of a gradient takes the sums of item rows along
+  const bool fused = grad && !ent;
+  y.sp_lse = fused ? lp_splits(s, 32 * S::OB_GRAD * S::NWO, C, T::TI, y.pad * D * 4)
+                   : lp_splits(s, 32 * S::OB_LSE * S::NWO, C, T::TI, 12 * y.pad);
   y.sp_dx = lp_splits(s, 32 * S::OB_GRAD * S::NWO, C, T::TI, y.pad * D * 4);
   y.sp_dy = lp_splits(C, 32 * S::OB_GRAD * S::NWO, s, T::TI, C * D * 4);
   size_t off = 0;
@@ -593,30 +755,35 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   y.idc = take(y.pad * 4);
   y.own2 = take(y.pad * 4);
   y.lse2 = take(y.pad * 4);
-  y.ent = take(flags & RECE_FLAG_ENTROPY ? y.pad * 4 : 0);
+  y.ent = take(ent ? y.pad * 4 : 0);
   y.xc = take((size_t)y.pad * D * sizeof(E));
-  // what one call alone uses: the forward pass's parts, the backward pass's rows and parts
-  const size_t base = off;
   const size_t parts = (size_t)y.sp_lse * y.pad * 4;
+  size_t base = off;
   y.m = take(parts);
+  if (fused) {
+    y.o = take((size_t)y.sp_lse * y.pad * D * 4);
+    base = off;
+  }
+  // what one call alone uses: the forward pass's parts, the backward pass's rows and parts
   y.z = take(parts);
-  y.t = take(flags & RECE_FLAG_ENTROPY ? parts : 0);
+  y.t = take(ent ? parts : 0);
   const size_t fwd = off;
   off = base;
-  if (!(flags & RECE_FLAG_NO_GRAD)) {
+  if (grad) {
     y.rows = take(y.pad * sizeof(LpRow));
     // dX is finished before the dY sweep starts
-    y.dx = y.dy = take(std::max((size_t)y.sp_dx * y.pad * D * 4, (size_t)y.sp_dy * C * D * 4));
+    y.dx = y.dy = take(std::max(ent ? (size_t)y.sp_dx * y.pad * D * 4 : 0, (size_t)y.sp_dy * C * D * 4));
   }
   y.bytes = std::max(fwd, off);
   return y;
 }
 
-template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int NS>
+template <class E, int D, int OB, int MODE, bool ENT, int MINW>
 hipError_t lp_launch(const LpArgs& a, int64_t n_own, hipStream_t st) {
+  constexpr int NWO = LpShape<E, D>::NWO, NWS = 1;
   using T = LpTile<E, D, NWS>;
   const size_t lds = 2 * (size_t)T::BYTES + (MODE == LP_DY ? 2 * T::TI * (sizeof(LpRow) + 4) : 0);
-  auto kern = k_lp_sweep<E, D, OB, NWO, NWS, MODE, ENT, NS>;
+  auto kern = k_lp_sweep<E, D, OB, NWO, NWS, MODE, ENT, MINW>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
@@ -624,6 +791,9 @@ hipError_t lp_launch(const LpArgs& a, int64_t n_own, hipStream_t st) {
   hipLaunchKernelGGL(kern, grid, dim3(64 * NWO * NWS), lds, st, a);
   return hipGetLastError();
 }
+
+// bf16 results take one bf16 term of a weight, float32 results all of its bits.
+template <class E> int lp_terms(uint32_t flags) { return sizeof(E) == 2 && !(flags & RECE_FLAG_BF16_GRADS) ? 3 : 1; }
 
 #define LP_TRY(call)                     \
   do {                                   \
@@ -639,13 +809,11 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
   using S = LpShape<E, D>;
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
   const float c2 = LOG2E / temperature;
-  hipLaunchKernelGGL(k_lp_list, dim3(1), dim3(PACK_THREADS), 0, st, ids, s, C, at<int32_t>(ws, y.nv),
-                     at<int32_t>(ws, y.list), at<int32_t>(ws, y.inv));
-  LP_TRY(hipGetLastError());
-  const int64_t lanes = y.pad * (D * (int)sizeof(E) / 16);
-  hipLaunchKernelGGL((k_lp_pack<E, D>), dim3((unsigned)ceil_div(lanes, 256)), dim3(256), 0, st,
-                     static_cast<const E*>(X), static_cast<const E*>(Y), ids, at<int32_t>(ws, y.nv),
-                     at<int32_t>(ws, y.list), y.pad, c2, at<E>(ws, y.xc), at<int32_t>(ws, y.idc), at<float>(ws, y.own2));
+  const int64_t per = std::max<int64_t>(PACK_THREADS, ceil_div(s, PACK_BLOCKS));
+  hipLaunchKernelGGL((k_lp_pack<E, D>), dim3((unsigned)ceil_div(s, per)), dim3(PACK_THREADS), 0, st,
+                     static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad, c2,
+                     at<int32_t>(ws, y.nv), at<int32_t>(ws, y.list), at<int32_t>(ws, y.inv), at<E>(ws, y.xc),
+                     at<int32_t>(ws, y.idc), at<float>(ws, y.own2));
   LP_TRY(hipGetLastError());
   LpArgs a{};
   a.own = at<E>(ws, y.xc);
@@ -660,48 +828,60 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
   a.z = at<float>(ws, y.z);
   a.t = at<float>(ws, y.t);
   a.own_pad = y.pad;
+  a.idc = at<int32_t>(ws, y.idc);
+  a.out = at<float>(ws, y.o);
+  a.terms = lp_terms<E>(flags);
   if (entropy)
-    LP_TRY((lp_launch<E, D, S::OB_LSE, S::NWO, 1, LP_LSE, true, 1>(a, s, st)));
+    LP_TRY((lp_launch<E, D, S::OB_LSE, LP_LSE, true, S::MW_LSE>(a, s, st)));
+  else if (flags & RECE_FLAG_NO_GRAD)
+    LP_TRY((lp_launch<E, D, S::OB_LSE, LP_LSE, false, S::MW_LSE>(a, s, st)));
   else
-    LP_TRY((lp_launch<E, D, S::OB_LSE, S::NWO, 1, LP_LSE, false, 1>(a, s, st)));
-  hipLaunchKernelGGL(k_lp_finish, dim3((unsigned)ceil_div(s, 256)), dim3(256), 0, st, at<int32_t>(ws, y.inv), s, y.sp_lse,
+    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_LSEO, false, S::MW_GRAD>(a, s, st)));
+  hipLaunchKernelGGL(k_lp_finish, dim3((unsigned)ceil_div(s, 4)), dim3(256), 0, st, at<int32_t>(ws, y.inv), s, y.sp_lse,
                      y.pad, a.m, a.z, a.t, at<float>(ws, y.own2), at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
                      entropy);
   return hipGetLastError();
 }
 
-template <class E, int D, bool ENT, int NS>
-hipError_t lp_backward_g(int64_t s, int64_t C, float temperature, uint32_t flags, const void* Y, void* ws,
+template <class E, int D>
+hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags, const void* Y, void* ws,
                          const float* dlogp, const float* dent, void* dX, void* dY, hipStream_t st) {
   using S = LpShape<E, D>;
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
+  const float inv_t = 1.0f / temperature;
+  const int b16 = flags & RECE_FLAG_BF16_GRADS ? 1 : 0;
   hipLaunchKernelGGL(k_lp_coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, at<int32_t>(ws, y.nv),
-                     at<int32_t>(ws, y.list), y.pad, at<float>(ws, y.lse2), at<float>(ws, y.ent), dlogp, dent,
-                     1.0f / temperature, at<LpRow>(ws, y.rows));
+                     at<int32_t>(ws, y.list), y.pad, at<float>(ws, y.lse2), at<float>(ws, y.ent), dlogp, dent, inv_t,
+                     at<LpRow>(ws, y.rows));
   LP_TRY(hipGetLastError());
   LpArgs a{};
   a.nv = at<int32_t>(ws, y.nv);
   a.c2 = LOG2E / temperature;
   a.rows = at<LpRow>(ws, y.rows);
+  a.terms = lp_terms<E>(flags);
   a.idc = at<int32_t>(ws, y.idc);
   auto join = [&](const int32_t* inv, int64_t n, void* out) {
-    const dim3 grid((unsigned)ceil_div(n * (D / 4), 256));
-    if (flags & RECE_FLAG_BF16_GRADS)
-      hipLaunchKernelGGL((k_lp_join<true>), grid, dim3(256), 0, st, a.out, a.splits, a.own_pad, D, inv, n, out);
-    else
-      hipLaunchKernelGGL((k_lp_join<false>), grid, dim3(256), 0, st, a.out, a.splits, a.own_pad, D, inv, n, out);
+    hipLaunchKernelGGL(k_lp_join, dim3((unsigned)ceil_div(n * (D / 4), 256)), dim3(256), 0, st, a.out, a.splits,
+                       a.own_pad, D, inv, n, out, b16);
     return hipGetLastError();
   };
-  a.own = at<E>(ws, y.xc);
-  a.str = Y;
-  a.n_own = s;
-  a.n_str = C;
-  a.own_is_pos = 1;
-  a.splits = y.sp_dx;
-  a.own_pad = y.pad;
-  a.out = at<float>(ws, y.dx);
-  LP_TRY((lp_launch<E, D, S::OB_GRAD, S::NWO, 1, LP_DX, ENT, NS>(a, s, st)));
-  LP_TRY(join(at<int32_t>(ws, y.inv), s, dX));
+  if (flags & RECE_FLAG_ENTROPY) {
+    a.own = at<E>(ws, y.xc);
+    a.str = Y;
+    a.n_own = s;
+    a.n_str = C;
+    a.own_is_pos = 1;
+    a.splits = y.sp_dx;
+    a.own_pad = y.pad;
+    a.out = at<float>(ws, y.dx);
+    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DX, true, S::MW_GRAD>(a, s, st)));
+    LP_TRY(join(at<int32_t>(ws, y.inv), s, dX));
+  } else {
+    hipLaunchKernelGGL((k_lp_dx<E>), dim3((unsigned)ceil_div(s * (D / 4), 256)), dim3(256), 0, st, at<float>(ws, y.o),
+                       at<float>(ws, y.m), y.sp_lse, y.pad, D, at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y),
+                       at<int32_t>(ws, y.idc), at<float>(ws, y.own2), at<float>(ws, y.lse2), dlogp, inv_t, dX, b16);
+    LP_TRY(hipGetLastError());
+  }
   a.own = Y;
   a.str = at<E>(ws, y.xc);
   a.n_own = C;
@@ -710,21 +890,11 @@ hipError_t lp_backward_g(int64_t s, int64_t C, float temperature, uint32_t flags
   a.splits = y.sp_dy;
   a.own_pad = C;
   a.out = at<float>(ws, y.dy);
-  LP_TRY((lp_launch<E, D, S::OB_GRAD, S::NWO, 1, LP_DY, ENT, NS>(a, C, st)));
+  if (dent)
+    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DY, true, S::MW_GRAD>(a, C, st)));
+  else
+    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DY, false, S::MW_GRAD>(a, C, st)));
   return join(nullptr, C, dY);
-}
-
-template <class E, int D>
-hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags, const void* Y, void* ws,
-                         const float* dlogp, const float* dent, void* dX, void* dY, hipStream_t st) {
-  // bf16 results take one bf16 term of G, float32 results all of its bits
-  const bool one = flags & RECE_FLAG_BF16_GRADS;
-  if (dent) {
-    if (one) return lp_backward_g<E, D, true, 1>(s, C, temperature, flags, Y, ws, dlogp, dent, dX, dY, st);
-    return lp_backward_g<E, D, true, 3>(s, C, temperature, flags, Y, ws, dlogp, dent, dX, dY, st);
-  }
-  if (one) return lp_backward_g<E, D, false, 1>(s, C, temperature, flags, Y, ws, dlogp, dent, dX, dY, st);
-  return lp_backward_g<E, D, false, 3>(s, C, temperature, flags, Y, ws, dlogp, dent, dX, dY, st);
 }
 
 }  // namespace
