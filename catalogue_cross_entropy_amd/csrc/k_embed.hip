@@ -95,6 +95,11 @@ struct EmbGrad {
   const int32_t* V;        // their rows (bit 31 set)
   const uint32_t* ntot;    // records
   const void* dout;
+  const float* weight;     // per row, every wstride-th, or NULL
+  int wstride;
+  const float* parts;      // [nparts][pstride] rows added first, or NULL
+  int nparts;
+  int64_t pstride;
   float* partial;          // [pieces][2][d]: the piece's part of a run that began earlier, and of one that goes on
   void* dtable;
   int d;
@@ -108,6 +113,24 @@ __device__ __forceinline__ void put_row(const EmbGrad& a, int64_t j, int col, fl
 #pragma unroll
   for (int t = 0; t < EPL; ++t) v[t] *= a.scale;
   const int64_t off = j * a.d + col;
+  if (a.parts) {
+    float base[EPL];
+#pragma unroll
+    for (int t = 0; t < EPL; ++t) base[t] = 0.0f;
+    for (int p = 0; p < a.nparts; ++p) {
+      const float4* h = reinterpret_cast<const float4*>(a.parts + p * a.pstride + off);
+#pragma unroll
+      for (int t = 0; t < EPL / 4; ++t) {
+        const float4 w = h[t];
+        base[4 * t] += w.x;
+        base[4 * t + 1] += w.y;
+        base[4 * t + 2] += w.z;
+        base[4 * t + 3] += w.w;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < EPL; ++t) v[t] += base[t];
+  }
   if (a.b16) {
     uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.dtable) + off);
 #pragma unroll
@@ -159,17 +182,23 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_pieces(EmbGrad a) {
   for (int64_t tb = t0; tb < t1; tb += UNR) {
     int key[UNR];
     u32x4 raw[UNR];
+    float wgt[UNR];
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
       const int64_t t = min(tb + u, t1 - 1);
+      const int64_t i = a.V[t] & 0x7FFFFFFF;
       key[u] = a.K[t];
-      raw[u] = *reinterpret_cast<const u32x4*>(dout + (int64_t)(a.V[t] & 0x7FFFFFFF) * a.d + col);
+      raw[u] = *reinterpret_cast<const u32x4*>(dout + i * a.d + col);
+      wgt[u] = a.weight ? a.weight[i * a.wstride] : 1.0f;
     }
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
       if (tb + u >= t1) break;
       float v[EPL];
       unpack16(raw[u], v);
+      if (a.weight)
+#pragma unroll
+        for (int t = 0; t < EPL; ++t) v[t] *= wgt[u];
       if (key[u] != cur) {
         if (cur >= 0) flush(tb + u);
         cur = key[u];
@@ -292,11 +321,13 @@ int64_t piece_count(int64_t n) { return (n + EMB_PIECE - 1) / EMB_PIECE; }
 
 }  // namespace
 
-size_t embed_workspace_bytes(int64_t n, int64_t C, int d) {
+size_t row_sums_bytes(int64_t n, int64_t C, int d) {
   if (n == 0) return 16;
   return align256(pair_sort_geom(n, C).scratch_bytes) + 4 * align256((size_t)n * 4) +
          align256((size_t)piece_count(n) * 2 * d * 4);
 }
+
+size_t embed_workspace_bytes(int64_t n, int64_t C, int d) { return row_sums_bytes(n, C, d); }
 
 hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, const void* table, const int32_t* ids,
                          void* out, hipStream_t st) {
@@ -313,8 +344,23 @@ hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  RowSums r{};
+  r.bf16v = bf16v;
+  r.n = n;
+  r.C = C;
+  r.d = d;
+  r.scale = scale;
+  r.grad_bf16 = grad_bf16;
+  r.accumulate = accumulate;
+  r.ids = ids;
+  r.rows = dout;
+  return row_sums(r, ws, dtable, st);
+}
+
+hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st) {
+  const int64_t n = r.n;
   if (n == 0) return hipSuccess;
-  const PairSortGeom g = pair_sort_geom(n, C);
+  const PairSortGeom g = pair_sort_geom(n, r.C);
   char* p = static_cast<char*>(ws);
   void* scratch = p;
   p += align256(g.scratch_bytes);
@@ -322,17 +368,22 @@ hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, 
   for (int q = 0; q < 4; ++q, p += align256((size_t)n * 4)) buf[q] = reinterpret_cast<int32_t*>(p);
   EmbGrad a{};
   // no list entries: the records are the positions' ids alone
-  hipError_t e = launch_pair_sort(g, ids, 0, 1, n, ids, C, scratch, buf[0], buf[1], buf[2], buf[3], &a.K, &a.V, &a.ntot, st);
+  hipError_t e = launch_pair_sort(g, r.ids, 0, 1, n, r.ids, r.C, scratch, buf[0], buf[1], buf[2], buf[3], &a.K, &a.V, &a.ntot, st);
   if (e != hipSuccess) return e;
-  a.dout = dout;
+  a.dout = r.rows;
+  a.weight = r.weight;
+  a.wstride = r.wstride;
+  a.parts = r.parts;
+  a.nparts = r.nparts;
+  a.pstride = r.pstride;
   a.partial = reinterpret_cast<float*>(p);
-  a.dtable = dtable;
-  a.d = d;
-  a.scale = scale;
-  a.b16 = grad_bf16;
-  a.acc = accumulate;
+  a.dtable = out;
+  a.d = r.d;
+  a.scale = r.scale;
+  a.b16 = r.grad_bf16;
+  a.acc = r.accumulate;
   const int64_t np = piece_count(n);
-  e = bf16v ? pieces_t<bf16>(a, np, st) : pieces_t<float>(a, np, st);
+  e = r.bf16v ? pieces_t<bf16>(a, np, st) : pieces_t<float>(a, np, st);
   if (e != hipSuccess) return e;
   return join(a, np, st);
 }

@@ -28,6 +28,12 @@
 #include "rece_device.h"
 #include "rece_internal.h"
 
+#ifndef VTI
+#define VTI 128
+#endif
+#ifndef VFR
+#define VFR 4
+#endif
 namespace rece {
 
 namespace {
@@ -41,6 +47,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LP_REF_LIMIT = 1.1529215e18f;   // 2^60: a sum beyond it is taken again with a better reference
 constexpr float LP_NEVER = 1e30f;               // lse2 of a row that has no weight: exp2(x2 - 1e30) = 0
+constexpr int LP_FRAGS = VFR;                     // fragments of a row read ahead of their products
 constexpr int LP_ROW_PAD = 256;                 // packed rows are padded with zero rows to a multiple of this
 
 enum LpMode { LP_LSE = 0, LP_LSEO = 1, LP_DX = 2, LP_DY = 3 };
@@ -72,7 +79,7 @@ struct LpArgs {
 // chunk c ^ (n & SWM), which spreads the 32 rows a fragment read touches over the banks.
 template <class E, int D, int NWS> struct LpTile {
   static constexpr int RB = D * (int)sizeof(E);
-  static constexpr int TI = NWS > 1 ? 32 * NWS : (RB <= 128 ? 128 : RB <= 256 ? 64 : 32);
+  static constexpr int TI = NWS > 1 ? 32 * NWS : (RB <= 128 ? VTI : RB <= 256 ? 64 : 32);
   static constexpr int CPR = RB / 16;
   static constexpr int SWM = (CPR < 8 ? CPR : 8) - 1;
   static constexpr int BYTES = TI * RB;
@@ -109,6 +116,17 @@ __device__ __forceinline__ T lds_at(uint32_t off) {
 __device__ __forceinline__ s16x4 lds_tr4(uint32_t off) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)off);
+}
+
+template <class T>
+__device__ __forceinline__ void lds_put(uint32_t off, T v) {
+  *reinterpret_cast<__attribute__((address_space(3))) T*>((uintptr_t)off) = v;
+}
+
+// Gradient by a logit (less [own] g): -p (a + b d) with d = x2 - lse2, p = 2^d.
+template <bool ENT>
+__device__ __forceinline__ float lp_weight(float d, float a, float b) {
+  return -exp2_fast(d) * (ENT ? fmaf(b, d, a) : a);
 }
 
 // Row of value v of a 32 x 32 block (less 4 h for the lane half h).
@@ -193,20 +211,27 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
   }
 }
 
+// What of a weight went into the products: all of it, or (one bf16 term) its rounding.
+__device__ __forceinline__ float lp_taken(float g, int terms, bool b16) { return b16 && terms == 1 ? lo_f32(pack_bf16(g, 0.0f)) : g; }
+
 // NWO waves along the owners x NWS waves along a tile's rows; OB blocks of 32 owners per wave.
+// A row's own item enters LP_LSEO, LP_DX and LP_DY (bf16) with the others, as -p (..); the joins add what is
+// missing of g - p (..) in float32 (1 - p would lose its digits in a bf16 term), knowing what went in: the
+// own logits come from the same products, so the same bits.  LP_DY (float32) adds g here.
 template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int MINW>
 __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   using T = LpTile<E, D, NWS>;
   using L = LpLds<E, D, NWS>;
-  constexpr int TI = T::TI, RB = T::RB, NT = 64 * NWO * NWS;
+  constexpr int TI = T::TI, RB = T::RB, CPR = T::CPR, NT = 64 * NWO * NWS;
   constexpr int KC = L::KC;
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile
   constexpr bool ACC = MODE != LP_LSE, LSE = MODE == LP_LSE || MODE == LP_LSEO, DY = MODE == LP_DY;
+  constexpr bool OWN = DY && sizeof(E) == 4;
   static_assert(T::BYTES % (16 * NT) == 0 && TI <= NT, "whole chunks per thread");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-  const int tid = threadIdx.x, w = tid >> 6, l = lane_id(), h = l >> 5, r = l & 31;
-  const int wo = w % NWO, ws = w / NWO;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
+  const int wo = w % NWO, ws = w / NWO;   // in scalar registers, and so is what follows from them
   // row numbers in 32 bits without a sign: at most 2^31 - 1 rows and a tile
   const uint32_t nv = (uint32_t)*a.nv;
   const uint32_t n_own = a.own_is_pos ? nv : (uint32_t)a.n_own, n_str = a.own_is_pos ? (uint32_t)a.n_str : nv;
@@ -219,40 +244,22 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   L lo;
   lo.init();
   u32x4 bown[OB][KC];
-  float olse[OB], oa[OB], obt[OB], og[OB];   // LP_DX: the owner's constants
-  uint32_t opos[OB];                         // its own item
+  float olse[OB], oa[OB], obt[OB];   // LP_DX: the owner's constants
 #pragma unroll
   for (int ob = 0; ob < OB; ++ob) {
     const uint32_t o = min(o0 + 32 * ob + r, n_own - 1);
     const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.own) + (int64_t)o * RB);
 #pragma unroll
     for (int t = 0; t < KC; ++t) bown[ob][t] = p[2 * t + h];
-    opos[ob] = 0;
-    if constexpr (MODE == LP_DX || MODE == LP_LSEO) opos[ob] = (uint32_t)a.idc[o];
     if constexpr (MODE == LP_DX) {
       const LpRow c = a.rows[o];
       olse[ob] = c.lse2;
       oa[ob] = c.a;
       obt[ob] = c.b;
-      og[ob] = c.g;
     }
   }
   float m[OB], z[OB], tt[OB];   // LP_LSE(O): reference and sums
   f32x16 acc[ACC ? OB : 1][D / 32];
-  auto clear = [&]() {
-#pragma unroll
-    for (int ob = 0; ob < OB; ++ob) {
-      z[ob] = tt[ob] = 0.0f;
-      if constexpr (ACC)
-#pragma unroll
-        for (int nb = 0; nb < D / 32; ++nb)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[ob][nb][v] = 0.0f;
-    }
-  };
-#pragma unroll
-  for (int ob = 0; ob < OB; ++ob) m[ob] = NEG_INF;
-  clear();
   const float c2 = a.c2;
   // a logit that weighs nothing, finite after the factor c2
   const float far = fmaxf(-1e30f / c2, -3e38f);
@@ -262,35 +269,39 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   const uint32_t par0 = lds0 + 2 * T::BYTES;
   u32x4 nxt[PT];
   u32x4 nrow = u32x4{0u, 0u, 0u, 0u};
-  int nid = -1;
+  uint32_t nid = 0;
+  // Chunk q NT + tid of a tile: row q (NT / CPR) + tid / CPR.  One lane offset serves all q, beside
+  // scalar ones; the swizzle repeats every 8 rows.
+  constexpr int RPQ = NT / CPR;
+  static_assert(RPQ % 8 == 0 || RPQ == 4, "rows per copy step");
+  const uint32_t crow = tid / CPR, ccol = tid % CPR;
+  const uint32_t st0 = crow * RB + ((ccol ^ (crow & T::SWM)) << 4), st1 = RPQ == 4 ? st0 ^ 64u : st0;
   auto fetch = [&](uint32_t t) {
     const char* src = static_cast<const char*>(a.str) + (int64_t)t * T::BYTES;
-    const uint32_t last = min((uint32_t)TI, n_str - t * TI) - 1;
+    if ((t + 1) * TI <= n_str) {
 #pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      const uint32_t ch = q * NT + tid;
-      nxt[q] = *reinterpret_cast<const u32x4*>(src + (min(ch / T::CPR, last) * RB + (ch % T::CPR) * 16));
+      for (int q = 0; q < PT; ++q) nxt[q] = *reinterpret_cast<const u32x4*>(src + q * (NT * 16) + (uint32_t)tid * 16);
+    } else {   // rows beyond the end repeat the last one
+      const uint32_t last = n_str - t * TI - 1;
+#pragma unroll
+      for (int q = 0; q < PT; ++q) nxt[q] = *reinterpret_cast<const u32x4*>(src + (min(crow + q * RPQ, last) * RB + ccol * 16));
     }
     if constexpr (DY) {
       if (tid < TI) {   // packed rows are padded with rows of no weight to whole tiles
         nrow = *reinterpret_cast<const u32x4*>(a.rows + ((int64_t)t * TI + tid));
-        nid = a.idc[(int64_t)t * TI + tid];
+        if constexpr (OWN) nid = (uint32_t)a.idc[(int64_t)t * TI + tid];
       }
     }
   };
   auto stash = [&](uint32_t t) {
     const uint32_t buf = lds0 + (t & 1) * T::BYTES;
 #pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      const uint32_t ch = q * NT + tid, row = ch / T::CPR, c = ch % T::CPR;
-      *reinterpret_cast<__attribute__((address_space(3))) u32x4*>((uintptr_t)(buf + row * RB + ((c ^ (row & T::SWM)) << 4))) = nxt[q];
-    }
+    for (int q = 0; q < PT; ++q) lds_put(((q & 1) ? st1 : st0) + buf + q * (NT * 16), nxt[q]);
     if constexpr (DY) {
       if (tid < TI) {
         const uint32_t par = par0 + (t & 1) * PB + 4 * tid;
 #pragma unroll
-        for (int q = 0; q < 5; ++q)
-          *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>((uintptr_t)(par + q * TI * 4)) = q < 4 ? nrow[q < 4 ? q : 0] : (uint32_t)nid;
+        for (int q = 0; q < (OWN ? 5 : 3); ++q) lds_put(par + q * TI * 4, q < 4 ? nrow[q < 4 ? q : 0] : nid);
       }
     }
   };
@@ -299,11 +310,16 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   // logits of 32 streamed rows (first one q0, at LDS offset base) against the wave's owners
   auto logits = [&](uint32_t base, uint32_t q0) {
     const f32x16 zero = {};
+    constexpr int KG = KC < LP_FRAGS ? KC : LP_FRAGS;   // fragments in flight
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      const u32x4 f = L::frag(lo, base, k);
+    for (int k0 = 0; k0 < KC; k0 += KG) {
+      u32x4 f[KG];
 #pragma unroll
-      for (int ob = 0; ob < OB; ++ob) x[ob] = LpMma<E>::run(f, bown[ob][k], k == 0 ? zero : x[ob]);
+      for (int k = 0; k < KG; ++k) f[k] = L::frag(lo, base, k0 + k);
+#pragma unroll
+      for (int k = 0; k < KG; ++k)
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob) x[ob] = LpMma<E>::run(f[k], bown[ob][k0 + k], k0 + k == 0 ? zero : x[ob]);
     }
     if constexpr (!DY) {
       if (q0 + 32 > n_str) {   // the last tile's rows beyond the end
@@ -326,8 +342,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
       m[ob] = fmaxf(bm, __shfl_xor(bm, 32));
     }
   };
-  // One block; own: the tile holds an owner's own item (LP_DY: a row whose item is an owner).
-  auto block = [&](bool own, uint32_t base, uint32_t par, uint32_t q0) {
+  auto block = [&](uint32_t base, uint32_t par, uint32_t q0) {
     logits(base, q0);
     if constexpr (LSE) {
 #pragma unroll
@@ -342,18 +357,6 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
         }
         z[ob] += s;
         if constexpr (ENT) tt[ob] += st;
-      }
-      if constexpr (MODE == LP_LSEO) {
-        if (own) {   // the owner's own item stays out of the sum of rows
-#pragma unroll
-          for (int ob = 0; ob < OB; ++ob) {
-            const uint32_t at = opos[ob] - q0 - 4 * h;
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-              if (lp_row(v) == at) x[ob][v] = 0.0f;
-          }
-        }
-        lp_product<E, D, NWS, OB>(acc, x, a.terms, lo, base);
       }
     } else {
 #pragma unroll
@@ -371,91 +374,82 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
           for (int e = 0; e < 4; ++e) {
             const int v = 4 * q + e;
             const float d = fmaf(x[ob][v], c2, DY ? -pl[e] : -olse[ob]);
-            const float wgt = ENT ? fmaf(DY ? pb[e] : obt[ob], d, DY ? pa[e] : oa[ob]) : (DY ? pa[e] : oa[ob]);
-            x[ob][v] = -exp2_fast(d) * wgt;
+            x[ob][v] = lp_weight<ENT>(d, DY ? pa[e] : oa[ob], DY ? pb[e] : obt[ob]);
           }
       }
-      if (own) {
+      if constexpr (OWN) {
+        if (ballot(lds_at<uint32_t>(par + 4 * TI * 4 + 4 * r) - o0 < 32 * OB)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f32x4 pg;
-          u32x4 pid;
-          if constexpr (DY) {
-            const uint32_t at = par + 32 * q + 16 * h;
-            pg = lds_at<f32x4>(at + 3 * TI * 4);
-            pid = lds_at<u32x4>(at + 4 * TI * 4);
+          for (int v = 0; v < 16; ++v) {
+            const uint32_t at = par + 4 * (lp_row(v) + 4 * h);
+            const uint32_t id = lds_at<uint32_t>(at + 4 * TI * 4);
+            const float g = lds_at<float>(at + 3 * TI * 4);
+#pragma unroll
+            for (int ob = 0; ob < OB; ++ob) x[ob][v] += id == o0 + 32 * ob + r ? g : 0.0f;
           }
-#pragma unroll
-          for (int ob = 0; ob < OB; ++ob)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int v = 4 * q + e;
-              const bool on = DY ? pid[e] == o0 + 32 * ob + r : q0 + lp_row(v) + 4 * h == opos[ob];
-              if (on) x[ob][v] += DY ? pg[e] : og[ob];
-            }
         }
       }
-      // the own item's weight, g (1 - p), is most of its row's result: it enters with all its bits
-      lp_product<E, D, NWS, OB>(acc, x, own ? 3 : a.terms, lo, base);
     }
+    if constexpr (ACC) lp_product<E, D, NWS, OB>(acc, x, a.terms, lo, base);
   };
-  // All tiles of the split through f(tile, LDS offset of the wave's first block, of its constants, first row).
+  // All tiles of the split through f(LDS offset of the wave's first block, of its constants, its first row).
   auto sweep = [&](auto f) {
     if (tb < te) {
       fetch(tb);
       stash(tb);
     }
+#pragma unroll 1
     for (uint32_t t = tb; t < te; ++t) {
       __syncthreads();
       if (t + 1 < te) fetch(t + 1);
-      f(t, lds0 + (t & 1) * T::BYTES + ws * (32 * RB), par0 + (t & 1) * PB + ws * 128, t * TI + ws * 32);
+      const uint32_t base = lds0 + (t & 1) * T::BYTES + ws * (32 * RB), par = par0 + (t & 1) * PB + ws * 128;
+#pragma unroll 1
+      for (int i = 0; i < TI / 32 / NWS; ++i) f(base + i * (NWS * 32 * RB), par + i * (NWS * 128), t * TI + (ws + i * NWS) * 32);
       if (t + 1 < te) stash(t + 1);
     }
+    __syncthreads();   // the buffers may be filled again
   };
-  auto main_pass = [&](bool fresh) {
-    sweep([&](uint32_t t, uint32_t base, uint32_t par, uint32_t q0) {
-      if constexpr (LSE) {
-        if (fresh && t == tb) {   // the first block's largest logit is the reference of the sums
+#pragma unroll
+  for (int ob = 0; ob < OB; ++ob) m[ob] = NEG_INF;
+  if constexpr (LSE) {
+    // the largest logit of the wave's first block is the reference of the sums
+    if (tb < te) {
+      fetch(tb);
+      stash(tb);
+    }
+    __syncthreads();
+    if (tb < te) {
+      logits(lds0 + (tb & 1) * T::BYTES + ws * (32 * RB), tb * TI + ws * 32);
+      raise();
+    }
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (bool again = false;; again = true) {
+    if constexpr (LSE) {
+      if (again)   // true maxima of the split
+        sweep([&](uint32_t base, uint32_t, uint32_t q0) {
           logits(base, q0);
           raise();
-        }
-      }
-      bool hit = false;
-      if constexpr (MODE == LP_DX || MODE == LP_LSEO) {
+        });
+    }
 #pragma unroll
-        for (int ob = 0; ob < OB; ++ob) hit = hit || opos[ob] - t * TI < TI;
-      } else if constexpr (DY) {
+    for (int ob = 0; ob < OB; ++ob) {
+      z[ob] = tt[ob] = 0.0f;
+      if constexpr (ACC)
 #pragma unroll
-        for (int q = 0; q < TI; q += WAVE) {
-          const uint32_t id = lds_at<uint32_t>(par0 + (t & 1) * PB + 4 * TI * 4 + 4 * (q + (TI < WAVE ? r : l)));
-          hit = hit || id - o0 < 32 * OB;
-        }
-      }
-      const bool own = MODE != LP_LSE && ballot(hit) != 0;
-#pragma unroll 1
-      for (int i = 0; i < TI / 32 / NWS; ++i)
-        block(own, base + i * (NWS * 32 * RB), par + i * NWS * 128, q0 + i * NWS * 32);
-    });
-  };
-  main_pass(true);
-  if constexpr (LSE) {
-    // exp2 has the range for logits up to 2^60 times the reference's; beyond (or with NaN among
-    // them) the references become the split's true maxima and the sums are taken again
+        for (int nb = 0; nb < D / 32; ++nb)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[ob][nb][v] = 0.0f;
+    }
+    sweep(block);
+    if constexpr (!LSE) break;
+    // exp2 has the range for logits up to 60 (base 2) beyond the reference; further (or with NaN among
+    // them) the references become the split's true maxima and the sums are taken once more
     bool over = false;
 #pragma unroll
     for (int ob = 0; ob < OB; ++ob) over = over || !(z[ob] < LP_REF_LIMIT);
-    if (__syncthreads_or(over)) {
-      sweep([&](uint32_t, uint32_t base, uint32_t, uint32_t q0) {
-#pragma unroll 1
-        for (int i = 0; i < TI / 32 / NWS; ++i) {
-          logits(base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
-          raise();
-        }
-      });
-      __syncthreads();
-      clear();
-      main_pass(false);
-    }
+    if (again || !__syncthreads_or(over)) break;
   }
 
   const int64_t part = (int64_t)split * NWS + ws;
@@ -489,22 +483,23 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
 // ------------------------------------------------------------------ packing
 // Workgroup b takes ids [b per, (b + 1) per): it counts the ids before them that lie in
 // [0, C) itself (an L2-resident read of 4 bytes a position, in place of a scan's further
-// launches), then writes the list of its own, the packed rows and ids, and the base-2
-// logit of each row's own item.  The last workgroup adds zero rows up to the padding.
+// launches), then writes the list of its own, the packed rows and ids, and the (unscaled)
+// logit of each row's own item, the diagonal of a 32 x 32 product, so that it has the
+// same bits as in the sweeps.  The last workgroup fills the padding with zero rows.
 constexpr int PACK_THREADS = 512;
 constexpr int64_t PACK_BLOCKS = 256;
 
 template <class E, int D>
 __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ X, const E* __restrict__ Y,
                                                           const int32_t* __restrict__ ids, int64_t s, int64_t C,
-                                                          int64_t per, int64_t pad, float c2, int32_t* __restrict__ nv,
+                                                          int64_t per, int64_t pad, int32_t* __restrict__ nv,
                                                           int32_t* __restrict__ list, int32_t* __restrict__ inv,
                                                           E* __restrict__ Xc, int32_t* __restrict__ idc,
-                                                          float* __restrict__ own2) {
-  constexpr int EPL = 16 / (int)sizeof(E), LPR = D / EPL, NW = PACK_THREADS / WAVE, RPB = PACK_THREADS / LPR;
+                                                          float* __restrict__ own) {
+  constexpr int RB = D * (int)sizeof(E), KC = RB / 32, NW = PACK_THREADS / WAVE;
   __shared__ int32_t wsum[NW];
   __shared__ int32_t src[PACK_THREADS];
-  const int tid = threadIdx.x, w = tid >> 6, l = lane_id();
+  const int tid = threadIdx.x, w = tid >> 6, l = lane_id(), h = l >> 5, r = l & 31;
   const int64_t i0 = (int64_t)blockIdx.x * per, i1 = min(s, i0 + per);
   auto good = [&](int64_t i, int64_t end) {
     const int id = i < end ? ids[i] : -1;
@@ -519,29 +514,6 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
   int64_t done = 0;
 #pragma unroll
   for (int q = 0; q < NW; ++q) done += wsum[q];
-  const int sub = tid % LPR;
-  // one packed row per lane group: list entry q of src, or (q beyond n) zeros
-  auto put_row = [&](int64_t row, int64_t i) {
-    u32x4 x = u32x4{0u, 0u, 0u, 0u};
-    int id = -1;
-    float dot = 0.0f;
-    if (i >= 0) {
-      id = ids[i];
-      x = reinterpret_cast<const u32x4*>(X + i * D)[sub];
-      const u32x4 y = reinterpret_cast<const u32x4*>(Y + (int64_t)id * D)[sub];
-      const E* xe = reinterpret_cast<const E*>(&x);
-      const E* ye = reinterpret_cast<const E*>(&y);
-#pragma unroll
-      for (int t = 0; t < EPL; ++t) dot = fmaf(to_f32(xe[t]), to_f32(ye[t]), dot);
-    }
-#pragma unroll
-    for (int o = LPR / 2; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
-    reinterpret_cast<u32x4*>(Xc + row * D)[sub] = x;
-    if (sub == 0) {
-      idc[row] = id;
-      own2[row] = dot * c2;
-    }
-  };
   for (int64_t b = i0; b < i1; b += PACK_THREADS) {
     const int64_t i = b + tid;
     const bool on = good(i, i1);
@@ -561,12 +533,39 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
       src[at] = (int32_t)i;
     }
     __syncthreads();
-    for (int q = tid / LPR; q < tot; q += RPB) put_row(done + q, src[q]);
+    for (int q = w * 32; q < tot; q += NW * 32) {   // 32 rows per wave
+      const int64_t pos = src[min(q + r, tot - 1)];
+      const int32_t id = ids[pos];
+      const u32x4* px = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(X) + pos * RB);
+      const u32x4* py = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(Y) + (int64_t)id * RB);
+      u32x4* pc = reinterpret_cast<u32x4*>(reinterpret_cast<char*>(Xc) + (done + q + r) * RB);
+      f32x16 x = {};
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const u32x4 fx = px[2 * k + h], fy = py[2 * k + h];
+        x = LpMma<E>::run(fy, fx, x);
+        if (q + r < tot) pc[2 * k + h] = fx;
+      }
+      float d = 0.0f;
+      bool mine = false;
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        if (lp_row(v) + 4 * h == r) {
+          d = x[v];
+          mine = true;
+        }
+      if (mine && q + r < tot) {
+        own[done + q + r] = d;
+        idc[done + q + r] = id;
+      }
+    }
     done += tot;
   }
   if (blockIdx.x + 1 == gridDim.x) {
     const int64_t end = min(pad, (done + LP_ROW_PAD - 1) / LP_ROW_PAD * LP_ROW_PAD);
-    for (int64_t q = done + tid / LPR; q < end; q += RPB) put_row(q, -1);
+    for (int64_t q = done * (RB / 16) + tid; q < end * (RB / 16); q += PACK_THREADS)
+      reinterpret_cast<u32x4*>(Xc)[q] = u32x4{0u, 0u, 0u, 0u};
+    for (int64_t q = done + tid; q < pad; q += PACK_THREADS) idc[q] = -1;
     if (tid == 0) *nv = (int32_t)done;
   }
 }
@@ -575,7 +574,7 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
 // One wave per position: the parts of its sum -> log-sum-exp, log-probability, entropy.
 __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ inv, int64_t s, int parts, int64_t pad,
                                                    const float* __restrict__ m, const float* __restrict__ z,
-                                                   const float* __restrict__ t, const float* __restrict__ own2,
+                                                   const float* __restrict__ t, const float* __restrict__ own, float c2,
                                                    float* __restrict__ lse2, float* __restrict__ ent_c,
                                                    float* __restrict__ logp, float* __restrict__ entropy) {
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -607,7 +606,7 @@ __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ i
   if (l != 0) return;
   const float lz = log2f(zz), l2 = mn + lz;
   lse2[r] = l2;
-  logp[i] = (own2[r] - l2) * LN2;
+  logp[i] = fmaf(own[r], c2, -l2) * LN2;
   if (entropy) {
     const float H = (lz - tt / zz) * LN2;
     entropy[i] = H;
@@ -615,21 +614,25 @@ __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ i
   }
 }
 
-// Constants of the gradient per packed row; rows of no weight up to the padding.
+// Constants of the gradient per packed row; rows of no weight up to the padding.  own: the row's own
+// logit; rows' g: what the sweep over the items leaves of the own item's g - p (..) (float32: all of g).
+template <bool ENT>
 __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_p, const int32_t* __restrict__ list,
                                                  int64_t pad, const float* __restrict__ lse2,
-                                                 const float* __restrict__ ent_c, const float* __restrict__ dlogp,
-                                                 const float* __restrict__ dent, float inv_t, LpRow* __restrict__ rows) {
+                                                 const float* __restrict__ ent_c, const float* __restrict__ own, float c2,
+                                                 const float* __restrict__ dlogp, const float* __restrict__ dent,
+                                                 float inv_t, int terms, int b16, LpRow* __restrict__ rows) {
   const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (r >= pad) return;
   LpRow c{LP_NEVER, 0.0f, 0.0f, 0.0f};
   if (r < *nv_p) {
     const int64_t i = list[r];
-    const float g = dlogp[i] * inv_t, h = dent ? dent[i] * inv_t : 0.0f;
+    const float g = dlogp[i] * inv_t, h = ENT ? dent[i] * inv_t : 0.0f;
     c.lse2 = lse2[r];
-    c.g = g;
-    c.a = dent ? fmaf(h, ent_c[r], g) : g;
+    c.a = ENT ? fmaf(h, ent_c[r], g) : g;
     c.b = h * LN2;
+    const float w = lp_weight<ENT>(fmaf(own[r], c2, -c.lse2), c.a, c.b);
+    c.g = b16 ? g + (w - lp_taken(w, terms, true)) : g;
   }
   rows[r] = c;
 }
@@ -645,9 +648,13 @@ __device__ __forceinline__ void put4(void* out, int64_t at, float4 v, bool b16) 
   }
 }
 
-// out row = sum of the parts' rows, in order; inv: row of the parts for each output row (or -1: zeros).
+// out row = sum of the parts' rows, in order.  inv (dX): the row of the parts for each output row (or -1: zeros),
+// whose own item's row of Y is added g times.
+template <class E>
 __global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part, int parts, int64_t pad, int d,
-                                                 const int32_t* __restrict__ inv, int64_t n, void* __restrict__ out, int b16) {
+                                                 const int32_t* __restrict__ inv, const LpRow* __restrict__ rows,
+                                                 const int32_t* __restrict__ idc, const E* __restrict__ Y, int64_t n,
+                                                 void* __restrict__ out, int b16) {
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = d / 4;
   if (q >= n * per) return;
@@ -661,19 +668,26 @@ __global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part,
       const float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
       v = float4{v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w};
     }
+    if (inv) {
+      const float g = rows[r].g;
+      const E* y = Y + (int64_t)idc[r] * d + c;
+      v = float4{fmaf(g, to_f32(y[0]), v.x), fmaf(g, to_f32(y[1]), v.y), fmaf(g, to_f32(y[2]), v.z), fmaf(g, to_f32(y[3]), v.w)};
+    }
   }
   put4(out, i * d + c, v, b16 != 0);
 }
 
-// dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j over the
-// items but the row's own:  dX_i = g_i ((1 - p_i) y_own - sum of the parts of O 2^(m - lse2)).
+// dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j:
+//   dX_i = g_i (y_own - sum over the parts of O 2^(m - lse2))
+// with the own item's share of the sum taken out and 1 - p_own in its place, so that nothing is lost where
+// p_own is near 1.  own_part: part that holds item id (tile id / ti, split of `per` tiles).
 template <class E>
 __global__ __launch_bounds__(256) void k_lp_dx(const float* __restrict__ part, const float* __restrict__ m, int parts,
-                                               int64_t pad, int d, const int32_t* __restrict__ inv, int64_t s,
-                                               const E* __restrict__ Y, const int32_t* __restrict__ idc,
-                                               const float* __restrict__ own2, const float* __restrict__ lse2,
-                                               const float* __restrict__ dlogp, float inv_t, void* __restrict__ out,
-                                               int b16) {
+                                               int64_t pad, int d, int64_t split_rows, const int32_t* __restrict__ inv,
+                                               int64_t s, const E* __restrict__ Y, const int32_t* __restrict__ idc,
+                                               const float* __restrict__ own, float c2, const float* __restrict__ lse2,
+                                               const float* __restrict__ dlogp, float inv_t, int terms,
+                                               void* __restrict__ out, int b16) {
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = d / 4;
   if (q >= s * per) return;
@@ -682,16 +696,22 @@ __global__ __launch_bounds__(256) void k_lp_dx(const float* __restrict__ part, c
   const int64_t r = inv[i];
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
-    const float l2 = lse2[r], g = dlogp[i] * inv_t;
-    const float rest = -expm1f((own2[r] - l2) * LN2);
+    const float l2 = lse2[r], g = dlogp[i] * inv_t, o = own[r];
+    const int64_t id = idc[r];
+    const E* yp = Y + id * d + c;
+    const float4 y = float4{to_f32(yp[0]), to_f32(yp[1]), to_f32(yp[2]), to_f32(yp[3])};
+    const int home = (int)(id / split_rows);
     for (int p = 0; p < parts; ++p) {
-      const float f = exp2_fast(m[(int64_t)p * pad + r] - l2);
-      const float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
+      const float mp = m[(int64_t)p * pad + r], f = exp2_fast(mp - l2);
+      float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
+      if (p == home) {
+        const float e = lp_taken(exp2_fast(fmaf(o, c2, -mp)), terms, sizeof(E) == 2);
+        w = float4{fmaf(-e, y.x, w.x), fmaf(-e, y.y, w.y), fmaf(-e, y.z, w.z), fmaf(-e, y.w, w.w)};
+      }
       v = float4{fmaf(f, w.x, v.x), fmaf(f, w.y, v.y), fmaf(f, w.z, v.z), fmaf(f, w.w, v.w)};
     }
-    const E* y = Y + (int64_t)idc[r] * d + c;
-    v = float4{g * fmaf(rest, to_f32(y[0]), -v.x), g * fmaf(rest, to_f32(y[1]), -v.y),
-               g * fmaf(rest, to_f32(y[2]), -v.z), g * fmaf(rest, to_f32(y[3]), -v.w)};
+    const float rest = -expm1f(fmaf(o, c2, -l2) * LN2);
+    v = float4{g * fmaf(rest, y.x, -v.x), g * fmaf(rest, y.y, -v.y), g * fmaf(rest, y.z, -v.z), g * fmaf(rest, y.w, -v.w)};
   }
   put4(out, i * d + c, v, b16 != 0);
 }
@@ -720,13 +740,31 @@ template <class E, int D> struct LpShape {
   static constexpr int NWO = 4;
   static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
   static constexpr int MW_LSE = B ? 2 : (D <= 128 ? 2 : 1);
-  static constexpr int OB_GRAD = B && D <= 64 ? 2 : 1;
-  static constexpr int MW_GRAD = B ? 2 : (D <= 64 ? 2 : 1);
+  #ifndef VOB
+#define VOB 2
+#endif
+#ifndef VMW
+#define VMW 2
+#endif
+#ifndef VOB1
+#define VOB1 1
+#endif
+#ifndef VMW1
+#define VMW1 2
+#endif
+#ifndef VOB2
+#define VOB2 1
+#endif
+#ifndef VMW2
+#define VMW2 2
+#endif
+  static constexpr int OB_GRAD = !B ? 1 : D <= 64 ? VOB : D == 128 ? VOB1 : VOB2;
+  static constexpr int MW_GRAD = !B ? (D <= 64 ? 2 : 1) : D <= 64 ? VMW : D == 128 ? VMW1 : VMW2;
 };
 
 struct LpLayout {
   int64_t pad;
-  size_t nv, list, inv, idc, own2, lse2, ent, rows, xc, m, z, t, o, dx, dy, bytes;
+  size_t nv, list, inv, idc, own, lse2, ent, rows, xc, m, z, t, o, dx, dy, sums, bytes;
   int sp_lse, sp_dx, sp_dy;
 };
 
@@ -753,7 +791,7 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   y.list = take(y.pad * 4);
   y.inv = take(y.pad * 4);
   y.idc = take(y.pad * 4);
-  y.own2 = take(y.pad * 4);
+  y.own = take(y.pad * 4);
   y.lse2 = take(y.pad * 4);
   y.ent = take(ent ? y.pad * 4 : 0);
   y.xc = take((size_t)y.pad * D * sizeof(E));
@@ -773,6 +811,7 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
     y.rows = take(y.pad * sizeof(LpRow));
     // dX is finished before the dY sweep starts
     y.dx = y.dy = take(std::max(ent ? (size_t)y.sp_dx * y.pad * D * 4 : 0, (size_t)y.sp_dy * C * D * 4));
+    if (sizeof(E) == 2) y.sums = take(row_sums_bytes(y.pad, C, D));
   }
   y.bytes = std::max(fwd, off);
   return y;
@@ -811,9 +850,9 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
   const float c2 = LOG2E / temperature;
   const int64_t per = std::max<int64_t>(PACK_THREADS, ceil_div(s, PACK_BLOCKS));
   hipLaunchKernelGGL((k_lp_pack<E, D>), dim3((unsigned)ceil_div(s, per)), dim3(PACK_THREADS), 0, st,
-                     static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad, c2,
+                     static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad,
                      at<int32_t>(ws, y.nv), at<int32_t>(ws, y.list), at<int32_t>(ws, y.inv), at<E>(ws, y.xc),
-                     at<int32_t>(ws, y.idc), at<float>(ws, y.own2));
+                     at<int32_t>(ws, y.idc), at<float>(ws, y.own));
   LP_TRY(hipGetLastError());
   LpArgs a{};
   a.own = at<E>(ws, y.xc);
@@ -838,7 +877,7 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
   else
     LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_LSEO, false, S::MW_GRAD>(a, s, st)));
   hipLaunchKernelGGL(k_lp_finish, dim3((unsigned)ceil_div(s, 4)), dim3(256), 0, st, at<int32_t>(ws, y.inv), s, y.sp_lse,
-                     y.pad, a.m, a.z, a.t, at<float>(ws, y.own2), at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
+                     y.pad, a.m, a.z, a.t, at<float>(ws, y.own), c2, at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
                      entropy);
   return hipGetLastError();
 }
@@ -848,21 +887,22 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
                          const float* dlogp, const float* dent, void* dX, void* dY, hipStream_t st) {
   using S = LpShape<E, D>;
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
-  const float inv_t = 1.0f / temperature;
-  const int b16 = flags & RECE_FLAG_BF16_GRADS ? 1 : 0;
-  hipLaunchKernelGGL(k_lp_coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, at<int32_t>(ws, y.nv),
-                     at<int32_t>(ws, y.list), y.pad, at<float>(ws, y.lse2), at<float>(ws, y.ent), dlogp, dent, inv_t,
-                     at<LpRow>(ws, y.rows));
+  const float inv_t = 1.0f / temperature, c2 = LOG2E / temperature;
+  const int b16 = flags & RECE_FLAG_BF16_GRADS ? 1 : 0, terms = lp_terms<E>(flags);
+  auto coef = dent ? k_lp_coef<true> : k_lp_coef<false>;
+  hipLaunchKernelGGL(coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, at<int32_t>(ws, y.nv),
+                     at<int32_t>(ws, y.list), y.pad, at<float>(ws, y.lse2), at<float>(ws, y.ent), at<float>(ws, y.own), c2,
+                     dlogp, dent, inv_t, terms, sizeof(E) == 2 ? 1 : 0, at<LpRow>(ws, y.rows));
   LP_TRY(hipGetLastError());
   LpArgs a{};
   a.nv = at<int32_t>(ws, y.nv);
-  a.c2 = LOG2E / temperature;
+  a.c2 = c2;
   a.rows = at<LpRow>(ws, y.rows);
-  a.terms = lp_terms<E>(flags);
+  a.terms = terms;
   a.idc = at<int32_t>(ws, y.idc);
   auto join = [&](const int32_t* inv, int64_t n, void* out) {
-    hipLaunchKernelGGL(k_lp_join, dim3((unsigned)ceil_div(n * (D / 4), 256)), dim3(256), 0, st, a.out, a.splits,
-                       a.own_pad, D, inv, n, out, b16);
+    hipLaunchKernelGGL((k_lp_join<E>), dim3((unsigned)ceil_div(n * (D / 4), 256)), dim3(256), 0, st, a.out, a.splits,
+                       a.own_pad, D, inv, a.rows, a.idc, static_cast<const E*>(Y), n, out, b16);
     return hipGetLastError();
   };
   if (flags & RECE_FLAG_ENTROPY) {
@@ -874,12 +914,17 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
     a.splits = y.sp_dx;
     a.own_pad = y.pad;
     a.out = at<float>(ws, y.dx);
-    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DX, true, S::MW_GRAD>(a, s, st)));
+    if (dent)
+      LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DX, true, S::MW_GRAD>(a, s, st)));
+    else
+      LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DX, false, S::MW_GRAD>(a, s, st)));
     LP_TRY(join(at<int32_t>(ws, y.inv), s, dX));
   } else {
+    constexpr int64_t TI = LpTile<E, D, 1>::TI;
     hipLaunchKernelGGL((k_lp_dx<E>), dim3((unsigned)ceil_div(s * (D / 4), 256)), dim3(256), 0, st, at<float>(ws, y.o),
-                       at<float>(ws, y.m), y.sp_lse, y.pad, D, at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y),
-                       at<int32_t>(ws, y.idc), at<float>(ws, y.own2), at<float>(ws, y.lse2), dlogp, inv_t, dX, b16);
+                       at<float>(ws, y.m), y.sp_lse, y.pad, D, ceil_div(ceil_div(C, TI), y.sp_lse) * TI,
+                       at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y), a.idc, at<float>(ws, y.own), c2,
+                       at<float>(ws, y.lse2), dlogp, inv_t, terms, dX, b16);
     LP_TRY(hipGetLastError());
   }
   a.own = Y;
@@ -894,7 +939,24 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
     LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DY, true, S::MW_GRAD>(a, C, st)));
   else
     LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DY, false, S::MW_GRAD>(a, C, st)));
-  return join(nullptr, C, dY);
+  LP_TRY(join(nullptr, C, dY));
+  if (sizeof(E) == 4) return hipSuccess;
+  // the items that are some position's own: their rows once more, with what the sweep left of g
+  RowSums r{};
+  r.bf16v = true;
+  r.n = y.pad;
+  r.C = C;
+  r.d = D;
+  r.scale = 1.0f;
+  r.grad_bf16 = b16 != 0;
+  r.ids = a.idc;
+  r.rows = a.str;
+  r.weight = &a.rows[0].g;
+  r.wstride = sizeof(LpRow) / 4;
+  r.parts = a.out;
+  r.nparts = a.splits;
+  r.pstride = C * D;
+  return row_sums(r, at<void>(ws, y.sums), dY, st);
 }
 
 }  // namespace
