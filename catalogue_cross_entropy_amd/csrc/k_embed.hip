@@ -11,13 +11,14 @@
 
 #include "rece_device.h"
 #include "rece_internal.h"
+#include "rece_parts.h"
 
 namespace rece {
 
 namespace {
 
 constexpr int EMB_THREADS = 256;
-constexpr int EMB_PIECE = 32;   // sorted records per piece
+constexpr int EMB_PIECE = 8;    // sorted records per piece
 
 template <class E> struct Piece16 {
   static constexpr int EPL = 16 / (int)sizeof(E);
@@ -97,9 +98,7 @@ struct EmbGrad {
   const void* dout;
   const float* weight;     // per row, every wstride-th, or NULL
   int wstride;
-  const float* parts;      // [nparts][pstride] rows added first, or NULL
-  int nparts;
-  int64_t pstride;
+  SweepParts parts;        // partial rows added first (rows NULL: none)
   float* partial;          // [pieces][2][d]: the piece's part of a run that began earlier, and of one that goes on
   void* dtable;
   int d;
@@ -113,12 +112,12 @@ __device__ __forceinline__ void put_row(const EmbGrad& a, int64_t j, int col, fl
 #pragma unroll
   for (int t = 0; t < EPL; ++t) v[t] *= a.scale;
   const int64_t off = j * a.d + col;
-  if (a.parts) {
+  if (a.parts.rows) {
     float base[EPL];
 #pragma unroll
     for (int t = 0; t < EPL; ++t) base[t] = 0.0f;
-    for (int p = 0; p < a.nparts; ++p) {
-      const float4* h = reinterpret_cast<const float4*>(a.parts + p * a.pstride + off);
+    a.parts.each(j, [&](int64_t at) {
+      const float4* h = reinterpret_cast<const float4*>(a.parts.rows + at * a.d + col);
 #pragma unroll
       for (int t = 0; t < EPL / 4; ++t) {
         const float4 w = h[t];
@@ -127,7 +126,7 @@ __device__ __forceinline__ void put_row(const EmbGrad& a, int64_t j, int col, fl
         base[4 * t + 2] += w.z;
         base[4 * t + 3] += w.w;
       }
-    }
+    });
 #pragma unroll
     for (int t = 0; t < EPL; ++t) v[t] += base[t];
   }
@@ -373,9 +372,7 @@ hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st) {
   a.dout = r.rows;
   a.weight = r.weight;
   a.wstride = r.wstride;
-  a.parts = r.parts;
-  a.nparts = r.nparts;
-  a.pstride = r.pstride;
+  if (r.parts) a.parts = *r.parts;
   a.partial = reinterpret_cast<float*>(p);
   a.dtable = out;
   a.d = r.d;

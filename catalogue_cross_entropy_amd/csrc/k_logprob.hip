@@ -27,7 +27,20 @@
 
 #include "rece_device.h"
 #include "rece_internal.h"
+#include "rece_parts.h"
 
+#ifndef VPIPE
+#define VPIPE 1
+#endif
+#ifndef VPIPED
+#define VPIPED 64
+#endif
+#ifndef LP_SCHED
+#define LP_SCHED
+#endif
+#ifndef VFR2
+#define VFR2 2
+#endif
 #ifndef VTI
 #define VTI 128
 #endif
@@ -46,6 +59,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LP_REF_LIMIT = 1.1529215e18f;   // 2^60: a sum beyond it is taken again with a better reference
+constexpr float LP_FLOOR = -1e28f;              // a reference where no logit is: those beyond the end lie at -1e30
 constexpr float LP_NEVER = 1e30f;               // lse2 of a row that has no weight: exp2(x2 - 1e30) = 0
 constexpr int LP_FRAGS = VFR;                     // fragments of a row read ahead of their products
 constexpr int LP_ROW_PAD = 256;                 // packed rows are padded with zero rows to a multiple of this
@@ -62,16 +76,12 @@ struct LpRow {
 struct LpArgs {
   const void* own;        // owner vectors [n_own][D]
   const void* str;        // streamed vectors [n_str][D]
-  int64_t n_own, n_str;   // upper bounds; the positions' side is *nv
-  const int32_t* nv;      // packed positions
-  int own_is_pos;         // the owners are the packed positions (else the streamed side is)
-  int splits;
+  SweepParts parts;       // sizes, workgroups, and where parts lie
   float c2;               // log2(e) / temperature
-  float *m, *z, *t;       // LP_LSE(O): [parts][own_pad] reference, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m)
-  int64_t own_pad;
+  float *m, *z, *t;       // LP_LSE(O): parts of the reference, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m)
   const LpRow* rows;      // LP_DX, LP_DY: of the packed positions
   const int32_t* idc;     // ids of the packed positions
-  float* out;             // LP_LSEO, LP_DX, LP_DY: [parts][own_pad][D]
+  float* out;             // LP_LSEO, LP_DX, LP_DY: parts.rows
   int terms;              // bf16 terms of a weight in the products
 };
 
@@ -166,22 +176,20 @@ template <class E, int D, int NWS> struct LpLds {
 };
 
 // acc[ob][nb] += G[32 owners][32 streamed] . rows[32 streamed][D], lane l holding G[owner l % 32]
-// [streamed lp_row(v) + 4 (l / 32)] in g[ob][v].  bf16: `terms` products, each with the bf16
+// [streamed lp_row(v) + 4 (l / 32)] in g[ob][v].  bf16: TERMS products, each with the bf16
 // rounding of what the ones before left of G (1: rounded once, 3: all 24 bits).
-template <class E, int D, int NWS, int OB>
-__device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g)[OB], int terms, const LpLds<E, D, NWS>& o,
+template <class E, int D, int NWS, int OB, int TERMS>
+__device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g)[OB], const LpLds<E, D, NWS>& o,
                                            uint32_t base) {
   using T = LpTile<E, D, NWS>;
   if constexpr (sizeof(E) == 2) {
-#pragma unroll 1
-    while (true) {
-      u32x4 part[OB][2];
+    auto term = [&](u32x4 (&part)[OB][2]) {
 #pragma unroll
-      for (int ob = 0; ob < OB; ++ob)
+      for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) part[ob][e / 4][e % 4] = pack_bf16(g[ob][2 * e], g[ob][2 * e + 1]);
+        for (int ob = 0; ob < OB; ++ob)
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+          for (int e = 0; e < 4; ++e) part[ob][kk][e] = pack_bf16(g[ob][8 * kk + 2 * e], g[ob][8 * kk + 2 * e + 1]);
 #pragma unroll
         for (int nb = 0; nb < D / 32; ++nb) {
           const uint32_t at = o.y[nb % o.NY] + base + (nb / o.NY) * 128 + 16 * kk * T::RB;
@@ -190,14 +198,23 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
 #pragma unroll
           for (int ob = 0; ob < OB; ++ob) acc[ob][nb] = LpMma<bf16>::run(part[ob][kk], bw, acc[ob][nb]);
         }
-      if (--terms <= 0) break;
+      }
+    };
+    u32x4 part[OB][2];
+    if constexpr (TERMS == 1) {
+      term(part);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < TERMS; ++t) {
+        term(part);
 #pragma unroll
-      for (int ob = 0; ob < OB; ++ob)
+        for (int ob = 0; ob < OB; ++ob)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          g[ob][2 * e] -= lo_f32(part[ob][e / 4][e % 4]);
-          g[ob][2 * e + 1] -= hi_f32(part[ob][e / 4][e % 4]);
-        }
+          for (int e = 0; e < 8; ++e) {
+            g[ob][2 * e] -= lo_f32(part[ob][e / 4][e % 4]);
+            g[ob][2 * e + 1] -= hi_f32(part[ob][e / 4][e % 4]);
+          }
+      }
     }
   } else {
 #pragma unroll
@@ -218,7 +235,7 @@ __device__ __forceinline__ float lp_taken(float g, int terms, bool b16) { return
 // A row's own item enters LP_LSEO, LP_DX and LP_DY (bf16) with the others, as -p (..); the joins add what is
 // missing of g - p (..) in float32 (1 - p would lose its digits in a bf16 term), knowing what went in: the
 // own logits come from the same products, so the same bits.  LP_DY (float32) adds g here.
-template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int MINW>
+template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int TERMS, int MINW>
 __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   using T = LpTile<E, D, NWS>;
   using L = LpLds<E, D, NWS>;
@@ -227,37 +244,38 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile
   constexpr bool ACC = MODE != LP_LSE, LSE = MODE == LP_LSE || MODE == LP_LSEO, DY = MODE == LP_DY;
   constexpr bool OWN = DY && sizeof(E) == 4;
+  constexpr bool PIPE = VPIPE && DY && sizeof(E) == 2 && TERMS == 1 && D <= VPIPED;
   static_assert(T::BYTES % (16 * NT) == 0 && TI <= NT, "whole chunks per thread");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
   const int wo = w % NWO, ws = w / NWO;   // in scalar registers, and so is what follows from them
   // row numbers in 32 bits without a sign: at most 2^31 - 1 rows and a tile
-  const uint32_t nv = (uint32_t)*a.nv;
-  const uint32_t n_own = a.own_is_pos ? nv : (uint32_t)a.n_own, n_str = a.own_is_pos ? (uint32_t)a.n_str : nv;
-  const uint32_t blk0 = blockIdx.x * (32 * OB * NWO), o0 = blk0 + wo * (32 * OB);
-  const int split = blockIdx.y;
-  if (blk0 >= n_own) return;
-  const uint32_t ntiles = (n_str + TI - 1) / TI, per = (ntiles + a.splits - 1) / a.splits;
-  const uint32_t tb = min(ntiles, split * per), te = min(ntiles, tb + per);
+  const uint32_t n_own = a.parts.owners(), n_str = a.parts.streamed();
+  const SweepWork work = a.parts.work();
+  const uint32_t ntiles = work.nt;
 
   L lo;
   lo.init();
+  uint32_t o0 = 0, tb = 0, te = 0;   // the wave's first owner, the run's tiles of its block
   u32x4 bown[OB][KC];
   float olse[OB], oa[OB], obt[OB];   // LP_DX: the owner's constants
+  auto load_owners = [&]() {
+    const uint32_t rr = settled(r), hh = settled(h);
 #pragma unroll
-  for (int ob = 0; ob < OB; ++ob) {
-    const uint32_t o = min(o0 + 32 * ob + r, n_own - 1);
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.own) + (int64_t)o * RB);
+    for (int ob = 0; ob < OB; ++ob) {
+      const uint32_t o = min(o0 + 32 * ob + rr, n_own - 1);
+      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.own) + (int64_t)o * RB) + hh;
 #pragma unroll
-    for (int t = 0; t < KC; ++t) bown[ob][t] = p[2 * t + h];
-    if constexpr (MODE == LP_DX) {
-      const LpRow c = a.rows[o];
-      olse[ob] = c.lse2;
-      oa[ob] = c.a;
-      obt[ob] = c.b;
+      for (int t = 0; t < KC; ++t) bown[ob][t] = p[2 * t];
+      if constexpr (MODE == LP_DX) {
+        const LpRow c = a.rows[o];
+        olse[ob] = c.lse2;
+        oa[ob] = c.a;
+        obt[ob] = c.b;
+      }
     }
-  }
+  };
   float m[OB], z[OB], tt[OB];   // LP_LSE(O): reference and sums
   f32x16 acc[ACC ? OB : 1][D / 32];
   const float c2 = a.c2;
@@ -306,11 +324,10 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     }
   };
 
-  f32x16 x[OB];
   // logits of 32 streamed rows (first one q0, at LDS offset base) against the wave's owners
-  auto logits = [&](uint32_t base, uint32_t q0) {
+  auto logits = [&](f32x16 (&x)[OB], uint32_t base, uint32_t q0) {
     const f32x16 zero = {};
-    constexpr int KG = KC < LP_FRAGS ? KC : LP_FRAGS;   // fragments in flight
+    constexpr int KG = KC < LP_FRAGS ? KC : (D == 256 ? VFR2 : LP_FRAGS);   // fragments in flight
 #pragma unroll
     for (int k0 = 0; k0 < KC; k0 += KG) {
       u32x4 f[KG];
@@ -333,7 +350,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     }
   };
   // m = max(m, the block's logits), the same in both lane halves of an owner
-  auto raise = [&]() {
+  auto raise = [&](f32x16 (&x)[OB]) {
 #pragma unroll
     for (int ob = 0; ob < OB; ++ob) {
       float bm = m[ob];
@@ -342,8 +359,8 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
       m[ob] = fmaxf(bm, __shfl_xor(bm, 32));
     }
   };
-  auto block = [&](uint32_t base, uint32_t par, uint32_t q0) {
-    logits(base, q0);
+  // the block's logits become weights, and join the sums
+  auto weigh = [&](f32x16 (&x)[OB], uint32_t par) {
     if constexpr (LSE) {
 #pragma unroll
       for (int ob = 0; ob < OB; ++ob) {
@@ -390,93 +407,124 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
         }
       }
     }
-    if constexpr (ACC) lp_product<E, D, NWS, OB>(acc, x, a.terms, lo, base);
   };
+  constexpr int NB = TI / 32 / NWS;   // blocks of a tile per wave
   // All tiles of the split through f(LDS offset of the wave's first block, of its constants, its first row).
   auto sweep = [&](auto f) {
-    if (tb < te) {
-      fetch(tb);
-      stash(tb);
-    }
+    fetch(tb);
+    stash(tb);
 #pragma unroll 1
     for (uint32_t t = tb; t < te; ++t) {
       __syncthreads();
       if (t + 1 < te) fetch(t + 1);
-      const uint32_t base = lds0 + (t & 1) * T::BYTES + ws * (32 * RB), par = par0 + (t & 1) * PB + ws * 128;
-#pragma unroll 1
-      for (int i = 0; i < TI / 32 / NWS; ++i) f(base + i * (NWS * 32 * RB), par + i * (NWS * 128), t * TI + (ws + i * NWS) * 32);
+      f(lds0 + (t & 1) * T::BYTES + ws * (32 * RB), par0 + (t & 1) * PB + ws * 128, t * TI + ws * 32);
       if (t + 1 < te) stash(t + 1);
     }
     __syncthreads();   // the buffers may be filled again
   };
+  auto main_tile = [&](uint32_t base, uint32_t par, uint32_t q0) {
+    if constexpr (PIPE) {
+      // the next block's logits are on the matrix cores while this block's weights are computed
+      f32x16 x[2][OB];
+      logits(x[0], base, q0);
 #pragma unroll
-  for (int ob = 0; ob < OB; ++ob) m[ob] = NEG_INF;
-  if constexpr (LSE) {
-    // the largest logit of the wave's first block is the reference of the sums
-    if (tb < te) {
+      for (int i = 0; i < NB; ++i) {
+        if (i + 1 < NB) logits(x[(i + 1) & 1], base + (i + 1) * (NWS * 32 * RB), q0 + (i + 1) * NWS * 32);
+        weigh(x[i & 1], par + i * (NWS * 128));
+        if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x[i & 1], lo, base + i * (NWS * 32 * RB));
+        LP_SCHED
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < NB; ++i) {
+        f32x16 x[OB];
+        logits(x, base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
+        weigh(x, par + i * (NWS * 128));
+        if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x, lo, base + i * (NWS * 32 * RB));
+      }
+    }
+  };
+  auto run = [&]() {
+#pragma unroll
+    for (int ob = 0; ob < OB; ++ob) m[ob] = LP_FLOOR;
+    if constexpr (LSE) {
+      // the largest logit of the wave's first block is the reference of the sums
       fetch(tb);
       stash(tb);
+      __syncthreads();
+      f32x16 x[OB];
+      logits(x, lds0 + (tb & 1) * T::BYTES + ws * (32 * RB), tb * TI + ws * 32);
+      raise(x);
+      __syncthreads();
     }
-    __syncthreads();
-    if (tb < te) {
-      logits(lds0 + (tb & 1) * T::BYTES + ws * (32 * RB), tb * TI + ws * 32);
-      raise();
-    }
-    __syncthreads();
-  }
 #pragma unroll 1
-  for (bool again = false;; again = true) {
-    if constexpr (LSE) {
-      if (again)   // true maxima of the split
-        sweep([&](uint32_t base, uint32_t, uint32_t q0) {
-          logits(base, q0);
-          raise();
-        });
+    for (bool again = false;; again = true) {
+      if constexpr (LSE) {
+        if (again)   // true maxima of the run's tiles
+          sweep([&](uint32_t base, uint32_t, uint32_t q0) {
+#pragma unroll 1
+            for (int i = 0; i < NB; ++i) {
+              f32x16 x[OB];
+              logits(x, base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
+              raise(x);
+            }
+          });
+      }
+#pragma unroll
+      for (int ob = 0; ob < OB; ++ob) {
+        z[ob] = tt[ob] = 0.0f;
+        if constexpr (ACC)
+#pragma unroll
+          for (int nb = 0; nb < D / 32; ++nb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[ob][nb][v] = 0.0f;
+      }
+      sweep(main_tile);
+      if constexpr (!LSE) break;
+      // exp2 has the range for logits up to 60 (base 2) beyond the reference; further (or with NaN among
+      // them) the references become the true maxima and the sums are taken once more
+      bool over = false;
+#pragma unroll
+      for (int ob = 0; ob < OB; ++ob) over = over || !(z[ob] < LP_REF_LIMIT);
+      if (again || !__syncthreads_or(over)) break;
     }
-#pragma unroll
-    for (int ob = 0; ob < OB; ++ob) {
-      z[ob] = tt[ob] = 0.0f;
-      if constexpr (ACC)
-#pragma unroll
-        for (int nb = 0; nb < D / 32; ++nb)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[ob][nb][v] = 0.0f;
-    }
-    sweep(block);
-    if constexpr (!LSE) break;
-    // exp2 has the range for logits up to 60 (base 2) beyond the reference; further (or with NaN among
-    // them) the references become the split's true maxima and the sums are taken once more
-    bool over = false;
-#pragma unroll
-    for (int ob = 0; ob < OB; ++ob) over = over || !(z[ob] < LP_REF_LIMIT);
-    if (again || !__syncthreads_or(over)) break;
-  }
+  };
 
-  const int64_t part = (int64_t)split * NWS + ws;
-  if constexpr (LSE) {
+  const uint64_t u1 = min(work.total, (uint64_t)(blockIdx.x + 1) * work.per);
+#pragma unroll 1
+  for (uint64_t u = (uint64_t)blockIdx.x * work.per; u < u1; u += te - tb) {
+    const uint32_t b = (uint32_t)div_u64(u, ntiles);
+    tb = (uint32_t)(u - (uint64_t)b * ntiles);
+    te = (uint32_t)min((uint64_t)ntiles, tb + (u1 - u));
+    o0 = b * (32 * OB * NWO) + wo * (32 * OB);
+    load_owners();
+    run();
+    // part [slot b + blockIdx.x][ws][owner of the block]; settled(): the lanes' offsets are formed here, not
+    // kept in registers through the sweep
+    const int64_t part = (((int64_t)b + blockIdx.x) * NWS + ws) * (32 * OB * NWO) + wo * (32 * OB);
+    const int rr = settled(r), hh = settled(h);
+    if constexpr (LSE) {
 #pragma unroll
-    for (int ob = 0; ob < OB; ++ob) {
-      // the two lane halves hold different rows of the same owner, against one reference
-      const float zz = z[ob] + __shfl_xor(z[ob], 32), t0 = tt[ob] + __shfl_xor(tt[ob], 32);
-      const uint32_t o = o0 + 32 * ob + r;
-      if (h == 0 && o < n_own) {
-        a.m[part * a.own_pad + o] = m[ob];
-        a.z[part * a.own_pad + o] = zz;
-        if constexpr (ENT) a.t[part * a.own_pad + o] = t0;
+      for (int ob = 0; ob < OB; ++ob) {
+        // the two lane halves hold different rows of the same owner, against one reference
+        const float zz = z[ob] + __shfl_xor(z[ob], 32), t0 = tt[ob] + __shfl_xor(tt[ob], 32);
+        if (hh == 0) {
+          a.m[part + 32 * ob + rr] = m[ob];
+          a.z[part + 32 * ob + rr] = zz;
+          if constexpr (ENT) a.t[part + 32 * ob + rr] = t0;
+        }
       }
     }
-  }
-  if constexpr (ACC) {
-    float* out = a.out + part * a.own_pad * D;
+    if constexpr (ACC) {   // whole blocks: rows beyond the last owner hold values that nothing reads
+      float* out = a.out + part * D;
+      const uint32_t lane = 4 * hh * D + rr;
 #pragma unroll
-    for (int ob = 0; ob < OB; ++ob)
+      for (int ob = 0; ob < OB; ++ob)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const uint32_t o = o0 + 32 * ob + lp_row(v) + 4 * h;
-        if (o < n_own)
+        for (int v = 0; v < 16; ++v)
 #pragma unroll
-          for (int nb = 0; nb < D / 32; ++nb) out[(int64_t)o * D + 32 * nb + r] = acc[ob][nb][v];
-      }
+          for (int nb = 0; nb < D / 32; ++nb) out[(32 * ob + lp_row(v)) * D + 32 * nb + lane] = acc[ob][nb][v];
+    }
   }
 }
 
@@ -571,14 +619,15 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
 }
 
 // ------------------------------------------------------------------ joins
-// One wave per position: the parts of its sum -> log-sum-exp, log-probability, entropy.
-__global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ inv, int64_t s, int parts, int64_t pad,
+// L lanes per position: the parts of its sum -> log-sum-exp, log-probability, entropy.
+template <int L>
+__global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ inv, int64_t s, SweepParts parts,
                                                    const float* __restrict__ m, const float* __restrict__ z,
                                                    const float* __restrict__ t, const float* __restrict__ own, float c2,
                                                    float* __restrict__ lse2, float* __restrict__ ent_c,
                                                    float* __restrict__ logp, float* __restrict__ entropy) {
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int l = lane_id();
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+  const int l = threadIdx.x % L;
   if (i >= s) return;
   const int64_t r = inv[i];
   if (r < 0) {
@@ -588,23 +637,28 @@ __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ i
     }
     return;
   }
+  const SweepWork w = parts.work();
+  const uint32_t b = (uint32_t)r / parts.block, in = (uint32_t)r % parts.block;
+  const int64_t p0 = ((int64_t)b + w.first(b)) * parts.nws, p1 = ((int64_t)b + w.last(b) + 1) * parts.nws;
   float mm = NEG_INF, zz = 0.0f, tt = 0.0f;
-  for (int p = l; p < parts; p += WAVE) {
-    const float mp = m[(int64_t)p * pad + r], zp = z[(int64_t)p * pad + r];
-    const float tp = entropy ? t[(int64_t)p * pad + r] : 0.0f;
-    if (mp == NEG_INF) continue;
+  for (int64_t p = p0 + l; p < p1; p += L) {
+    const int64_t at = p * parts.block + in;
+    const float mp = m[at], zp = z[at], tp = entropy ? t[at] : 0.0f;
     const float mn = fmaxf(mm, mp);
     const float f0 = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn), f1 = exp2_fast(mp - mn);
     tt = (mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f0) + (tp + zp * (mp - mn)) * f1;
     zz = zz * f0 + zp * f1;
     mm = mn;
   }
-  const float mn = wave_max(mm);
-  const float f = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn);
-  tt = wave_sumf(mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f);
-  zz = wave_sumf(zz * f);
-  if (l != 0) return;
-  const float lz = log2f(zz), l2 = mn + lz;
+  if constexpr (L > 1) {
+    const float mn = wave_max(mm);
+    const float f = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn);
+    tt = wave_sumf(mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f);
+    zz = wave_sumf(zz * f);
+    mm = mn;
+    if (l != 0) return;
+  }
+  const float lz = log2f(zz), l2 = mm + lz;
   lse2[r] = l2;
   logp[i] = fmaf(own[r], c2, -l2) * LN2;
   if (entropy) {
@@ -651,10 +705,9 @@ __device__ __forceinline__ void put4(void* out, int64_t at, float4 v, bool b16) 
 // out row = sum of the parts' rows, in order.  inv (dX): the row of the parts for each output row (or -1: zeros),
 // whose own item's row of Y is added g times.
 template <class E>
-__global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part, int parts, int64_t pad, int d,
-                                                 const int32_t* __restrict__ inv, const LpRow* __restrict__ rows,
-                                                 const int32_t* __restrict__ idc, const E* __restrict__ Y, int64_t n,
-                                                 void* __restrict__ out, int b16) {
+__global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, const int32_t* __restrict__ inv,
+                                                 const LpRow* __restrict__ rows, const int32_t* __restrict__ idc,
+                                                 const E* __restrict__ Y, int64_t n, void* __restrict__ out, int b16) {
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = d / 4;
   if (q >= n * per) return;
@@ -663,11 +716,10 @@ __global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part,
   const int64_t r = inv ? inv[i] : i;
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
+    parts.each(r, [&](int64_t at) {
+      const float4 w = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       v = float4{v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w};
-    }
+    });
     if (inv) {
       const float g = rows[r].g;
       const E* y = Y + (int64_t)idc[r] * d + c;
@@ -680,14 +732,13 @@ __global__ __launch_bounds__(256) void k_lp_join(const float* __restrict__ part,
 // dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j:
 //   dX_i = g_i (y_own - sum over the parts of O 2^(m - lse2))
 // with the own item's share of the sum taken out and 1 - p_own in its place, so that nothing is lost where
-// p_own is near 1.  own_part: part that holds item id (tile id / ti, split of `per` tiles).
+// p_own is near 1.
 template <class E>
-__global__ __launch_bounds__(256) void k_lp_dx(const float* __restrict__ part, const float* __restrict__ m, int parts,
-                                               int64_t pad, int d, int64_t split_rows, const int32_t* __restrict__ inv,
-                                               int64_t s, const E* __restrict__ Y, const int32_t* __restrict__ idc,
-                                               const float* __restrict__ own, float c2, const float* __restrict__ lse2,
-                                               const float* __restrict__ dlogp, float inv_t, int terms,
-                                               void* __restrict__ out, int b16) {
+__global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float* __restrict__ m, int d,
+                                               const int32_t* __restrict__ inv, int64_t s, const E* __restrict__ Y,
+                                               const int32_t* __restrict__ idc, const float* __restrict__ own, float c2,
+                                               const float* __restrict__ lse2, const float* __restrict__ dlogp,
+                                               float inv_t, int terms, void* __restrict__ out, int b16) {
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = d / 4;
   if (q >= s * per) return;
@@ -697,19 +748,23 @@ __global__ __launch_bounds__(256) void k_lp_dx(const float* __restrict__ part, c
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
     const float l2 = lse2[r], g = dlogp[i] * inv_t, o = own[r];
-    const int64_t id = idc[r];
-    const E* yp = Y + id * d + c;
+    const uint32_t id = (uint32_t)idc[r];
+    const E* yp = Y + (int64_t)id * d + c;
     const float4 y = float4{to_f32(yp[0]), to_f32(yp[1]), to_f32(yp[2]), to_f32(yp[3])};
-    const int home = (int)(id / split_rows);
-    for (int p = 0; p < parts; ++p) {
-      const float mp = m[(int64_t)p * pad + r], f = exp2_fast(mp - l2);
-      float4 w = *reinterpret_cast<const float4*>(part + ((int64_t)p * pad + r) * d + c);
-      if (p == home) {
+    // the part that holds the own item: workgroup of its tile, wave of its block of 32 rows
+    const SweepWork w = parts.work();
+    const uint32_t b = (uint32_t)r / parts.block;
+    const int64_t g_own = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
+    const int64_t home = ((b + g_own) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + (uint32_t)r % parts.block;
+    parts.each(r, [&](int64_t at) {
+      const float mp = m[at], f = exp2_fast(mp - l2);
+      float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
+      if (at == home) {
         const float e = lp_taken(exp2_fast(fmaf(o, c2, -mp)), terms, sizeof(E) == 2);
-        w = float4{fmaf(-e, y.x, w.x), fmaf(-e, y.y, w.y), fmaf(-e, y.z, w.z), fmaf(-e, y.w, w.w)};
+        x = float4{fmaf(-e, y.x, x.x), fmaf(-e, y.y, x.y), fmaf(-e, y.z, x.z), fmaf(-e, y.w, x.w)};
       }
-      v = float4{fmaf(f, w.x, v.x), fmaf(f, w.y, v.y), fmaf(f, w.z, v.z), fmaf(f, w.w, v.w)};
-    }
+      v = float4{fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w)};
+    });
     const float rest = -expm1f(fmaf(o, c2, -l2) * LN2);
     v = float4{g * fmaf(rest, y.x, -v.x), g * fmaf(rest, y.y, -v.y), g * fmaf(rest, y.z, -v.z), g * fmaf(rest, y.w, -v.w)};
   }
@@ -720,67 +775,63 @@ __global__ __launch_bounds__(256) void k_lp_dx(const float* __restrict__ part, c
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Splits of the streamed side: enough workgroups to fill the card (256 CUs, a few each),
-// no split shorter than a few tiles, and the parts within 256 MB.
-constexpr int64_t LP_TARGET_BLOCKS = 1024;
-constexpr int64_t LP_MIN_TILES = 4;
-constexpr int64_t LP_PART_BYTES = (int64_t)256 << 20;
-int lp_splits(int64_t n_own, int64_t own_block, int64_t n_str, int64_t ti, int64_t part_bytes) {
-  const int64_t nb = ceil_div(n_own, own_block);
-  int64_t sp = LP_TARGET_BLOCKS / nb;
-  sp = std::min(sp, ceil_div(n_str, ti) / LP_MIN_TILES);
-  sp = std::min(sp, LP_PART_BYTES / std::max<int64_t>(part_bytes, 1));
-  return (int)std::max<int64_t>(1, std::min<int64_t>(sp, 4096));
-}
+constexpr int LP_CUS = 256;
 
 // Launch shapes: blocks of 32 owners per wave (more: fewer LDS reads per product; fewer: more waves
-// per SIMD to overlap the exponentials with the products) and waves per SIMD.
+// per SIMD to overlap the exponentials with the products), workgroups per CU that the registers
+// allow (the grid: every CU filled once), and the rows up to which the waves of a workgroup share their owners
+// and split each tile's rows instead (a block of owners that is mostly empty costs as much as a full one).
 template <class E, int D> struct LpShape {
   static constexpr bool B = sizeof(E) == 2;
-  static constexpr int NWO = 4;
-  static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
-  static constexpr int MW_LSE = B ? 2 : (D <= 128 ? 2 : 1);
-  #ifndef VOB
+#ifndef VOB
 #define VOB 2
 #endif
 #ifndef VMW
 #define VMW 2
 #endif
-#ifndef VOB1
-#define VOB1 1
+#ifndef VWL
+#define VWL 3
 #endif
-#ifndef VMW1
-#define VMW1 2
-#endif
-#ifndef VOB2
-#define VOB2 1
-#endif
-#ifndef VMW2
-#define VMW2 2
-#endif
-  static constexpr int OB_GRAD = !B ? 1 : D <= 64 ? VOB : D == 128 ? VOB1 : VOB2;
-  static constexpr int MW_GRAD = !B ? (D <= 64 ? 2 : 1) : D <= 64 ? VMW : D == 128 ? VMW1 : VMW2;
+  static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
+  static constexpr int MW_LSE = B ? VWL : (D <= 128 ? 3 : 2);
+  static constexpr int OB_GRAD = B && D <= 64 ? VOB : 1;
+  static constexpr int MW_GRAD = B ? VMW : (D <= 64 ? 2 : 1);
+  static constexpr int NWS_FEW = D * (int)sizeof(E) <= 256 ? 4 : 1;
 };
+
+struct LpSweep {   // one sweep's shape
+  int ob, nwo, nws, ti;
+  uint32_t grid;
+  int64_t slots(int64_t n_own) const { return (ceil_div(n_own, 32 * ob * nwo) + grid) * nws; }   // parts of a block each
+  int64_t block() const { return 32 * (int64_t)ob * nwo; }
+};
+
+template <class E, int D>
+LpSweep lp_shape(int mode, int64_t n_own, int64_t n_str) {
+  using S = LpShape<E, D>;
+  LpSweep p{};
+  p.ob = mode == LP_LSE ? S::OB_LSE : S::OB_GRAD;
+  const bool few = mode != LP_DY && S::NWS_FEW > 1 && n_own <= 32 * p.ob;
+  p.nwo = few ? 1 : 4;
+  p.nws = few ? S::NWS_FEW : 1;
+  p.ti = few ? LpTile<E, D, S::NWS_FEW>::TI : LpTile<E, D, 1>::TI;
+  const int64_t units = ceil_div(n_own, p.block()) * ceil_div(n_str, p.ti);
+  p.grid = (uint32_t)std::min<int64_t>(LP_CUS * (mode == LP_LSE ? S::MW_LSE : S::MW_GRAD), units);
+  return p;
+}
 
 struct LpLayout {
   int64_t pad;
-  size_t nv, list, inv, idc, own, lse2, ent, rows, xc, m, z, t, o, dx, dy, sums, bytes;
-  int sp_lse, sp_dx, sp_dy;
+  size_t nv, list, inv, idc, own, lse2, ent, rows, xc, m, z, t, o, dx, sums, bytes;
 };
 
 template <class E, int D>
 LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
-  using S = LpShape<E, D>;
-  using T = LpTile<E, D, 1>;
   const bool grad = !(flags & RECE_FLAG_NO_GRAD), ent = flags & RECE_FLAG_ENTROPY;
   LpLayout y{};
   y.pad = ceil_div(s, LP_ROW_PAD) * LP_ROW_PAD;
   // without entropies the forward pass of a gradient takes the sums of item rows along
   const bool fused = grad && !ent;
-  y.sp_lse = fused ? lp_splits(s, 32 * S::OB_GRAD * S::NWO, C, T::TI, y.pad * D * 4)
-                   : lp_splits(s, 32 * S::OB_LSE * S::NWO, C, T::TI, 12 * y.pad);
-  y.sp_dx = lp_splits(s, 32 * S::OB_GRAD * S::NWO, C, T::TI, y.pad * D * 4);
-  y.sp_dy = lp_splits(C, 32 * S::OB_GRAD * S::NWO, s, T::TI, C * D * 4);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -795,11 +846,12 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   y.lse2 = take(y.pad * 4);
   y.ent = take(ent ? y.pad * 4 : 0);
   y.xc = take((size_t)y.pad * D * sizeof(E));
-  const size_t parts = (size_t)y.sp_lse * y.pad * 4;
+  const LpSweep f = lp_shape<E, D>(fused ? LP_LSEO : LP_LSE, s, C);
+  const size_t parts = (size_t)f.slots(s) * f.block() * 4;
   size_t base = off;
   y.m = take(parts);
   if (fused) {
-    y.o = take((size_t)y.sp_lse * y.pad * D * 4);
+    y.o = take(parts * D);
     base = off;
   }
   // what one call alone uses: the forward pass's parts, the backward pass's rows and parts
@@ -808,27 +860,43 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   const size_t fwd = off;
   off = base;
   if (grad) {
+    const LpSweep x = lp_shape<E, D>(LP_DX, s, C), v = lp_shape<E, D>(LP_DY, C, s);
     y.rows = take(y.pad * sizeof(LpRow));
     // dX is finished before the dY sweep starts
-    y.dx = y.dy = take(std::max(ent ? (size_t)y.sp_dx * y.pad * D * 4 : 0, (size_t)y.sp_dy * C * D * 4));
+    y.dx = take(std::max(ent ? (size_t)x.slots(s) * x.block() : 0, (size_t)v.slots(C) * v.block()) * D * 4);
     if (sizeof(E) == 2) y.sums = take(row_sums_bytes(y.pad, C, D));
   }
   y.bytes = std::max(fwd, off);
   return y;
 }
 
-template <class E, int D, int OB, int MODE, bool ENT, int MINW>
-hipError_t lp_launch(const LpArgs& a, int64_t n_own, hipStream_t st) {
-  constexpr int NWO = LpShape<E, D>::NWO, NWS = 1;
+template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int TERMS, int MINW>
+hipError_t lp_launch_t(const LpArgs& a, hipStream_t st) {
   using T = LpTile<E, D, NWS>;
   const size_t lds = 2 * (size_t)T::BYTES + (MODE == LP_DY ? 2 * T::TI * (sizeof(LpRow) + 4) : 0);
-  auto kern = k_lp_sweep<E, D, OB, NWO, NWS, MODE, ENT, MINW>;
+  auto kern = k_lp_sweep<E, D, OB, NWO, NWS, MODE, ENT, TERMS, MINW>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)ceil_div(n_own, 32 * OB * NWO), (unsigned)a.splits);
-  hipLaunchKernelGGL(kern, grid, dim3(64 * NWO * NWS), lds, st, a);
+  hipLaunchKernelGGL(kern, dim3(a.parts.grid), dim3(64 * NWO * NWS), lds, st, a);
   return hipGetLastError();
+}
+
+template <class E, int D, int MODE, bool ENT>
+hipError_t lp_launch(const LpArgs& a, hipStream_t st) {
+  using S = LpShape<E, D>;
+  constexpr int OB = MODE == LP_LSE ? S::OB_LSE : S::OB_GRAD, MINW = MODE == LP_LSE ? S::MW_LSE : S::MW_GRAD;
+  constexpr bool THREE = sizeof(E) == 2 && MODE != LP_LSE;
+  if constexpr (MODE != LP_DY && S::NWS_FEW > 1) {
+    if (a.parts.nws > 1) {
+      if constexpr (THREE)
+        if (a.terms != 1) return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 3, MINW>(a, st);
+      return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 1, MINW>(a, st);
+    }
+  }
+  if constexpr (THREE)
+    if (a.terms != 1) return lp_launch_t<E, D, OB, 4, 1, MODE, ENT, 3, MINW>(a, st);
+  return lp_launch_t<E, D, OB, 4, 1, MODE, ENT, 1, MINW>(a, st);
 }
 
 // bf16 results take one bf16 term of a weight, float32 results all of its bits.
@@ -843,41 +911,54 @@ template <class E> int lp_terms(uint32_t flags) { return sizeof(E) == 2 && !(fla
 template <class T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
 template <class E, int D>
+SweepParts lp_parts(int mode, int64_t n_own, int64_t n_str, const int32_t* nv, const float* rows) {
+  const LpSweep f = lp_shape<E, D>(mode, n_own, n_str);
+  SweepParts p{};
+  p.nv = nv;
+  p.n_own = n_own;
+  p.n_str = n_str;
+  p.own_is_pos = mode != LP_DY;
+  p.block = (uint32_t)f.block();
+  p.tile = (uint32_t)f.ti;
+  p.grid = f.grid;
+  p.nws = f.nws;
+  p.rows = rows;
+  return p;
+}
+
+template <class E, int D>
 hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags, const void* X, const void* Y,
                         const int32_t* ids, void* ws, float* logp, float* entropy, hipStream_t st) {
-  using S = LpShape<E, D>;
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
   const float c2 = LOG2E / temperature;
   const int64_t per = std::max<int64_t>(PACK_THREADS, ceil_div(s, PACK_BLOCKS));
   hipLaunchKernelGGL((k_lp_pack<E, D>), dim3((unsigned)ceil_div(s, per)), dim3(PACK_THREADS), 0, st,
-                     static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad,
-                     at<int32_t>(ws, y.nv), at<int32_t>(ws, y.list), at<int32_t>(ws, y.inv), at<E>(ws, y.xc),
-                     at<int32_t>(ws, y.idc), at<float>(ws, y.own));
+                     static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad, at<int32_t>(ws, y.nv),
+                     at<int32_t>(ws, y.list), at<int32_t>(ws, y.inv), at<E>(ws, y.xc), at<int32_t>(ws, y.idc),
+                     at<float>(ws, y.own));
   LP_TRY(hipGetLastError());
+  const bool fused = !entropy && !(flags & RECE_FLAG_NO_GRAD);
   LpArgs a{};
   a.own = at<E>(ws, y.xc);
   a.str = Y;
-  a.n_own = s;
-  a.n_str = C;
-  a.nv = at<int32_t>(ws, y.nv);
-  a.own_is_pos = 1;
-  a.splits = y.sp_lse;
+  a.parts = lp_parts<E, D>(fused ? LP_LSEO : LP_LSE, s, C, at<int32_t>(ws, y.nv), nullptr);
   a.c2 = c2;
   a.m = at<float>(ws, y.m);
   a.z = at<float>(ws, y.z);
   a.t = at<float>(ws, y.t);
-  a.own_pad = y.pad;
-  a.idc = at<int32_t>(ws, y.idc);
   a.out = at<float>(ws, y.o);
   a.terms = lp_terms<E>(flags);
-  if (entropy)
-    LP_TRY((lp_launch<E, D, S::OB_LSE, LP_LSE, true, S::MW_LSE>(a, s, st)));
-  else if (flags & RECE_FLAG_NO_GRAD)
-    LP_TRY((lp_launch<E, D, S::OB_LSE, LP_LSE, false, S::MW_LSE>(a, s, st)));
+  if (fused)
+    LP_TRY((lp_launch<E, D, LP_LSEO, false>(a, st)));
+  else if (entropy)
+    LP_TRY((lp_launch<E, D, LP_LSE, true>(a, st)));
   else
-    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_LSEO, false, S::MW_GRAD>(a, s, st)));
-  hipLaunchKernelGGL(k_lp_finish, dim3((unsigned)ceil_div(s, 4)), dim3(256), 0, st, at<int32_t>(ws, y.inv), s, y.sp_lse,
-                     y.pad, a.m, a.z, a.t, at<float>(ws, y.own), c2, at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
+    LP_TRY((lp_launch<E, D, LP_LSE, false>(a, st)));
+  // few positions have many parts each: a wave for each; many have few
+  const int lanes = s <= 8192 ? WAVE : 1;
+  auto finish = lanes == WAVE ? k_lp_finish<WAVE> : k_lp_finish<1>;
+  hipLaunchKernelGGL(finish, dim3((unsigned)ceil_div(s * lanes, 256)), dim3(256), 0, st, at<int32_t>(ws, y.inv), s,
+                     a.parts, a.m, a.z, a.t, at<float>(ws, y.own), c2, at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
                      entropy);
   return hipGetLastError();
 }
@@ -885,60 +966,50 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
 template <class E, int D>
 hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags, const void* Y, void* ws,
                          const float* dlogp, const float* dent, void* dX, void* dY, hipStream_t st) {
-  using S = LpShape<E, D>;
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
   const float inv_t = 1.0f / temperature, c2 = LOG2E / temperature;
   const int b16 = flags & RECE_FLAG_BF16_GRADS ? 1 : 0, terms = lp_terms<E>(flags);
+  const int32_t* nv = at<int32_t>(ws, y.nv);
   auto coef = dent ? k_lp_coef<true> : k_lp_coef<false>;
-  hipLaunchKernelGGL(coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, at<int32_t>(ws, y.nv),
-                     at<int32_t>(ws, y.list), y.pad, at<float>(ws, y.lse2), at<float>(ws, y.ent), at<float>(ws, y.own), c2,
-                     dlogp, dent, inv_t, terms, sizeof(E) == 2 ? 1 : 0, at<LpRow>(ws, y.rows));
+  hipLaunchKernelGGL(coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, nv, at<int32_t>(ws, y.list), y.pad,
+                     at<float>(ws, y.lse2), at<float>(ws, y.ent), at<float>(ws, y.own), c2, dlogp, dent, inv_t, terms,
+                     sizeof(E) == 2 ? 1 : 0, at<LpRow>(ws, y.rows));
   LP_TRY(hipGetLastError());
   LpArgs a{};
-  a.nv = at<int32_t>(ws, y.nv);
   a.c2 = c2;
   a.rows = at<LpRow>(ws, y.rows);
   a.terms = terms;
   a.idc = at<int32_t>(ws, y.idc);
   auto join = [&](const int32_t* inv, int64_t n, void* out) {
-    hipLaunchKernelGGL((k_lp_join<E>), dim3((unsigned)ceil_div(n * (D / 4), 256)), dim3(256), 0, st, a.out, a.splits,
-                       a.own_pad, D, inv, a.rows, a.idc, static_cast<const E*>(Y), n, out, b16);
+    hipLaunchKernelGGL((k_lp_join<E>), dim3((unsigned)ceil_div(n * (D / 4), 256)), dim3(256), 0, st, a.parts, D, inv,
+                       a.rows, a.idc, static_cast<const E*>(Y), n, out, b16);
     return hipGetLastError();
   };
   if (flags & RECE_FLAG_ENTROPY) {
     a.own = at<E>(ws, y.xc);
     a.str = Y;
-    a.n_own = s;
-    a.n_str = C;
-    a.own_is_pos = 1;
-    a.splits = y.sp_dx;
-    a.own_pad = y.pad;
     a.out = at<float>(ws, y.dx);
+    a.parts = lp_parts<E, D>(LP_DX, s, C, nv, a.out);
     if (dent)
-      LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DX, true, S::MW_GRAD>(a, s, st)));
+      LP_TRY((lp_launch<E, D, LP_DX, true>(a, st)));
     else
-      LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DX, false, S::MW_GRAD>(a, s, st)));
+      LP_TRY((lp_launch<E, D, LP_DX, false>(a, st)));
     LP_TRY(join(at<int32_t>(ws, y.inv), s, dX));
   } else {
-    constexpr int64_t TI = LpTile<E, D, 1>::TI;
-    hipLaunchKernelGGL((k_lp_dx<E>), dim3((unsigned)ceil_div(s * (D / 4), 256)), dim3(256), 0, st, at<float>(ws, y.o),
-                       at<float>(ws, y.m), y.sp_lse, y.pad, D, ceil_div(ceil_div(C, TI), y.sp_lse) * TI,
+    hipLaunchKernelGGL((k_lp_dx<E>), dim3((unsigned)ceil_div(s * (D / 4), 256)), dim3(256), 0, st,
+                       lp_parts<E, D>(LP_LSEO, s, C, nv, at<float>(ws, y.o)), at<float>(ws, y.m), D,
                        at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y), a.idc, at<float>(ws, y.own), c2,
                        at<float>(ws, y.lse2), dlogp, inv_t, terms, dX, b16);
     LP_TRY(hipGetLastError());
   }
   a.own = Y;
   a.str = at<E>(ws, y.xc);
-  a.n_own = C;
-  a.n_str = s;
-  a.own_is_pos = 0;
-  a.splits = y.sp_dy;
-  a.own_pad = C;
-  a.out = at<float>(ws, y.dy);
+  a.out = at<float>(ws, y.dx);
+  a.parts = lp_parts<E, D>(LP_DY, C, s, nv, a.out);
   if (dent)
-    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DY, true, S::MW_GRAD>(a, C, st)));
+    LP_TRY((lp_launch<E, D, LP_DY, true>(a, st)));
   else
-    LP_TRY((lp_launch<E, D, S::OB_GRAD, LP_DY, false, S::MW_GRAD>(a, C, st)));
+    LP_TRY((lp_launch<E, D, LP_DY, false>(a, st)));
   LP_TRY(join(nullptr, C, dY));
   if (sizeof(E) == 4) return hipSuccess;
   // the items that are some position's own: their rows once more, with what the sweep left of g
@@ -953,9 +1024,7 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
   r.rows = a.str;
   r.weight = &a.rows[0].g;
   r.wstride = sizeof(LpRow) / 4;
-  r.parts = a.out;
-  r.nparts = a.splits;
-  r.pstride = C * D;
+  r.parts = &a.parts;
   return row_sums(r, at<void>(ws, y.sums), dY, st);
 }
 

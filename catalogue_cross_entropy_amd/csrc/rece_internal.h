@@ -192,6 +192,7 @@ hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, c
                          void* out, hipStream_t st);
 hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, bool grad_bf16, bool accumulate,
                           const int32_t* ids, const void* dout, void* ws, void* dtable, hipStream_t st);
+struct SweepParts;
 // Sums of rows by id, out_j = scale * sum over i with ids[i] = j of weight_i rows_i (+ parts), in a fixed
 // order: the embedding's gradient, and the own items' share of the log-probabilities' dY.
 struct RowSums {
@@ -205,9 +206,7 @@ struct RowSums {
   const void* rows;       // [n][d]
   const float* weight;    // weight of row i at weight[i * wstride], or NULL: 1
   int wstride;
-  const float* parts;     // [nparts][pstride] float32 rows [C][d] that are summed first, or NULL
-  int nparts;
-  int64_t pstride;
+  const SweepParts* parts;   // a sweep's partial rows of out that are summed first, or NULL
 };
 size_t row_sums_bytes(int64_t n, int64_t C, int d);
 // Writes the rows of out that some id names; the others stay.
