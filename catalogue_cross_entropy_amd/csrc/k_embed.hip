@@ -18,6 +18,11 @@ namespace rece {
 namespace {
 
 constexpr int EMB_THREADS = 256;
+constexpr int ORD_THREADS = 1024;
+constexpr int ORD_TILE = 4096;      // records per workgroup of the sort
+constexpr int ORD_BITS = 10;        // largest digit
+constexpr int ORD_BINS = 1 << ORD_BITS;
+constexpr int64_t ORD_TILES = 64;   // beyond these the library's longer sort, with a scan of its own, takes over
 constexpr int EMB_PIECE = 8;    // sorted records per piece
 
 template <class E> struct Piece16 {
@@ -86,14 +91,231 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_rows(const E* __restrict_
 }
 
 // ------------------------------------------------------------------ backward
-__global__ __launch_bounds__(EMB_THREADS) void k_embed_clear(u32x4* __restrict__ p, int64_t n16) {
-  const int64_t step = (int64_t)gridDim.x * EMB_THREADS;
-  for (int64_t t = (int64_t)blockIdx.x * EMB_THREADS + threadIdx.x; t < n16; t += step) p[t] = u32x4{0u, 0u, 0u, 0u};
+// Share `part` of `parts` of a region cleared by the `n` workgroups given (1024 threads each).
+struct ClearArgs {
+  u32x4* p;
+  int64_t n16;   // 16-byte pieces of the region
+};
+__device__ __forceinline__ void clear_share(const ClearArgs& c, int part, int parts, int64_t b, int64_t n) {
+  const int64_t lo = c.n16 * part / parts, hi = c.n16 * (part + 1) / parts;
+  constexpr int UNR = 4;
+  for (int64_t t = lo + b * (ORD_THREADS * UNR) + threadIdx.x; t < hi; t += n * (ORD_THREADS * UNR))
+#pragma unroll
+    for (int u = 0; u < UNR; ++u)
+      if (t + u * ORD_THREADS < hi) __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, c.p + t + u * ORD_THREADS);
+}
+
+__global__ __launch_bounds__(ORD_THREADS) void k_embed_clear(ClearArgs c) { clear_share(c, 0, 1, blockIdx.x, gridDim.x); }
+
+// ------------------------------------------------------------------ rows in the order of their ids
+// Stable counting sort of the records (id, row) by digits of up to 10 bits, over tiles of 4096 records.
+//   k_order_hist     per tile, the count of every value of a digit;
+//   k_order_scatter  per tile: every workgroup forms the digits' starting slots from all tiles' counts by
+//                    itself (at most 64 tiles: 256 KB that lie in the L2; a scan of its own would be three
+//                    more launches of a few us each), ranks its records in input order and writes them out.
+// Integer atomics in LDS only, so the order is the same on every run.  Further workgroups of these launches
+// clear the gradient meanwhile (the sort is latency, the clearing bandwidth).
+struct OrderArgs {
+  const int32_t* ids;      // first pass
+  const int32_t *kin, *vin;
+  int32_t *kout, *vout;
+  int64_t n, C;
+  int tiles, shift, bits;
+  uint32_t* counts;        // [tiles][ORD_BINS] of this digit
+  uint32_t* ntot;
+  ClearArgs clear;
+  int part, parts;
+};
+
+// Record t of a pass (id -1: none).
+template <bool FIRST>
+__device__ __forceinline__ int order_key(const OrderArgs& a, int64_t t, int64_t n) {
+  if (t >= n) return -1;
+  if constexpr (!FIRST) return a.kin[t];
+  const int k = a.ids[t];
+  return k < a.C ? k : -1;
+}
+
+template <bool FIRST>
+__global__ __launch_bounds__(ORD_THREADS) void k_order_hist(OrderArgs a) {
+  __shared__ uint32_t hist[ORD_BINS];
+  const int tid = threadIdx.x, tile = blockIdx.x;
+  if (tile >= a.tiles) {
+    clear_share(a.clear, a.part, a.parts, tile - a.tiles, (int64_t)gridDim.x - a.tiles);
+    return;
+  }
+  const int64_t n = FIRST ? a.n : (int64_t)*a.ntot;
+  hist[tid] = 0u;
+  int key[ORD_TILE / ORD_THREADS];
+#pragma unroll
+  for (int u = 0; u < ORD_TILE / ORD_THREADS; ++u) key[u] = order_key<FIRST>(a, (int64_t)tile * ORD_TILE + u * ORD_THREADS + tid, n);
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < ORD_TILE / ORD_THREADS; ++u) {
+    // one add for a wave of equal digits (popular ids after the first pass); others one by one
+    const int dig = key[u] >= 0 ? (int)((uint32_t)key[u] >> a.shift & ((1u << a.bits) - 1u)) : -1;
+    const int first = __builtin_amdgcn_readfirstlane(dig);
+    if (ballot(dig == first) == ~0ull) {
+      if (lane_id() == 0 && first >= 0) atomicAdd(&hist[first], (uint32_t)WAVE);
+    } else if (dig >= 0) {
+      atomicAdd(&hist[dig], 1u);
+    }
+  }
+  __syncthreads();
+  a.counts[(int64_t)tile * ORD_BINS + tid] = hist[tid];
+}
+
+// Exclusive prefix over the workgroup's threads (sh: one word per wave).
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sh, uint32_t* total) {
+  const int w = threadIdx.x / WAVE;
+  const uint32_t incl = wave_prefix_incl(v);
+  __syncthreads();
+  if (lane_id() == WAVE - 1) sh[w] = incl;
+  __syncthreads();
+  uint32_t pre = 0, tot = 0;
+#pragma unroll
+  for (int q = 0; q < ORD_THREADS / WAVE; ++q) {
+    if (q < w) pre += sh[q];
+    tot += sh[q];
+  }
+  *total = tot;
+  return pre + incl - v;
+}
+
+// Ranks 4 x 64 consecutive records per wave among the tile's records with the same digit: cnt[wave][digit]
+// becomes the number in earlier waves, at[q] the number in the wave before record q.
+__device__ __forceinline__ void order_rank(uint16_t (*cnt)[ORD_BINS], const int (&dig)[4], int bits, uint32_t (&at)[4],
+                                           uint32_t* tot) {
+  const int tid = threadIdx.x, w = tid / WAVE;
+#pragma unroll
+  for (int q = 0; q < ORD_THREADS / WAVE; ++q) cnt[q][tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const bool on = dig[q] >= 0;
+    uint64_t same = ballot(on);
+    for (int bit = 0; bit < bits; ++bit) {
+      const bool one = (dig[q] >> bit) & 1;
+      const uint64_t m = ballot(one);
+      same &= one ? m : ~m;
+    }
+    const uint32_t rank = popc(same & lanemask_lt());
+    const uint32_t base = on ? cnt[w][dig[q]] : 0u;
+    wave_sync();
+    if (on && rank == 0) cnt[w][dig[q]] = (uint16_t)(base + popc(same));
+    wave_sync();
+    at[q] = base + rank;
+  }
+  __syncthreads();
+  uint32_t run = 0;
+#pragma unroll
+  for (int q = 0; q < ORD_THREADS / WAVE; ++q) {
+    const uint32_t c = cnt[q][tid];
+    cnt[q][tid] = (uint16_t)run;
+    run += c;
+  }
+  *tot = run;   // of digit tid
+}
+
+template <bool FIRST>
+__global__ __launch_bounds__(ORD_THREADS) void k_order_scatter(OrderArgs a) {
+  __shared__ uint16_t cnt[ORD_THREADS / WAVE][ORD_BINS];
+  __shared__ uint32_t start[ORD_BINS];
+  __shared__ uint32_t sh[ORD_THREADS / WAVE];
+  const int tid = threadIdx.x, w = tid / WAVE, l = lane_id(), tile = blockIdx.x;
+  if (tile >= a.tiles) {
+    clear_share(a.clear, a.part, a.parts, tile - a.tiles, (int64_t)gridDim.x - a.tiles);
+    return;
+  }
+  const int64_t n = FIRST ? a.n : (int64_t)*a.ntot;
+  int key[4], val[4], dig[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t t = (int64_t)tile * ORD_TILE + (w * 4 + q) * WAVE + l;
+    key[q] = order_key<FIRST>(a, t, n);
+    val[q] = FIRST ? (int)t : (t < n ? a.vin[t] : 0);
+  }
+  uint32_t before = 0, all = 0;   // records of digit tid: in earlier tiles, in all
+#pragma unroll 8
+  for (int t = 0; t < a.tiles; ++t) {
+    const uint32_t c = a.counts[(int64_t)t * ORD_BINS + tid];
+    before += t < tile ? c : 0u;
+    all += c;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    dig[q] = key[q] >= 0 ? (int)((uint32_t)key[q] >> a.shift & ((1u << a.bits) - 1u)) : -1;
+  uint32_t total, at[4], in_tile;
+  start[tid] = block_prefix(all, sh, &total) + before;
+  if (FIRST && tile == 0 && tid == 0) *a.ntot = total;
+  order_rank(cnt, dig, a.bits, at, &in_tile);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (dig[q] < 0) continue;
+    const uint32_t slot = start[dig[q]] + cnt[w][dig[q]] + at[q];
+    a.kout[slot] = key[q];
+    a.vout[slot] = val[q];
+  }
+}
+
+// Up to one tile: all digits in one workgroup, the records between passes in LDS.
+__global__ __launch_bounds__(ORD_THREADS) void k_order_small(OrderArgs a, int key_bits) {
+  __shared__ uint16_t cnt[ORD_THREADS / WAVE][ORD_BINS];
+  __shared__ uint32_t start[ORD_BINS];
+  __shared__ uint32_t sh[ORD_THREADS / WAVE];
+  __shared__ int32_t sk[ORD_TILE], sv[ORD_TILE];
+  const int tid = threadIdx.x, w = tid / WAVE, l = lane_id();
+  if (blockIdx.x > 0) {
+    clear_share(a.clear, 0, 1, (int64_t)blockIdx.x - 1, (int64_t)gridDim.x - 1);
+    return;
+  }
+  int key[4], val[4], dig[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int t = (w * 4 + q) * WAVE + l;
+    key[q] = order_key<true>(a, t, a.n);
+    val[q] = t;
+  }
+  uint32_t total = 0;
+  for (int shift = 0;;) {
+    const int passes = (key_bits - shift + ORD_BITS - 1) / ORD_BITS, bits = (key_bits - shift + passes - 1) / passes;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dig[q] = key[q] >= 0 ? (int)((uint32_t)key[q] >> shift & ((1u << bits) - 1u)) : -1;
+    uint32_t at[4], in_tile;
+    order_rank(cnt, dig, bits, at, &in_tile);
+    start[tid] = block_prefix(in_tile, sh, &total);
+    __syncthreads();
+    shift += bits;
+    const bool last = shift >= key_bits;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (dig[q] < 0) continue;
+      const uint32_t slot = start[dig[q]] + cnt[w][dig[q]] + at[q];
+      if (last) {
+        a.kout[slot] = key[q];
+        a.vout[slot] = val[q];
+      } else {
+        sk[slot] = key[q];
+        sv[slot] = val[q];
+      }
+    }
+    if (last) break;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t t = (w * 4 + q) * WAVE + l;
+      key[q] = t < total ? sk[t] : -1;
+      val[q] = t < total ? sv[t] : 0;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) *a.ntot = total;
 }
 
 struct EmbGrad {
   const int32_t* K;        // sorted ids
-  const int32_t* V;        // their rows (bit 31 set)
+  const int32_t* V;        // their rows (bit 31 may be set)
   const uint32_t* ntot;    // records
   const void* dout;
   const float* weight;     // per row, every wstride-th, or NULL
@@ -108,7 +330,7 @@ struct EmbGrad {
 
 // EPL values of row j: written, or added (accumulate: the only writer of the row in this call).
 template <int EPL>
-__device__ __forceinline__ void put_row(const EmbGrad& a, int64_t j, int col, float (&v)[EPL]) {
+__device__ __forceinline__ void put_row(const EmbGrad& a, const SweepWork& w, int64_t j, int col, float (&v)[EPL]) {
 #pragma unroll
   for (int t = 0; t < EPL; ++t) v[t] *= a.scale;
   const int64_t off = j * a.d + col;
@@ -116,15 +338,15 @@ __device__ __forceinline__ void put_row(const EmbGrad& a, int64_t j, int col, fl
     float base[EPL];
 #pragma unroll
     for (int t = 0; t < EPL; ++t) base[t] = 0.0f;
-    a.parts.each(j, [&](int64_t at) {
+    a.parts.each(w, j, [&](int64_t at) {
       const float4* h = reinterpret_cast<const float4*>(a.parts.rows + at * a.d + col);
 #pragma unroll
       for (int t = 0; t < EPL / 4; ++t) {
-        const float4 w = h[t];
-        base[4 * t] += w.x;
-        base[4 * t + 1] += w.y;
-        base[4 * t + 2] += w.z;
-        base[4 * t + 3] += w.w;
+        const float4 x = h[t];
+        base[4 * t] += x.x;
+        base[4 * t + 1] += x.y;
+        base[4 * t + 2] += x.z;
+        base[4 * t + 3] += x.w;
       }
     });
 #pragma unroll
@@ -168,13 +390,14 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_pieces(EmbGrad a) {
   const int64_t t1 = min(n, t0 + EMB_PIECE);
   const int prev = t0 > 0 ? a.K[t0 - 1] : -1, next = t1 < n ? a.K[t1] : -1;
   const E* __restrict__ dout = static_cast<const E*>(a.dout);
+  const SweepWork work = a.parts.rows ? a.parts.work() : SweepWork{};
   int cur = -1;
   int64_t start = t0;
   float sum[EPL];
   auto flush = [&](int64_t end) {
     const bool head = start == t0 && cur == prev, tail = end == t1 && cur == next;
     if (!head && !tail)
-      put_row<EPL>(a, cur, col, sum);
+      put_row<EPL>(a, work, cur, col, sum);
     else
       put_partial<EPL>(a.partial + (piece * 2 + (head ? 0 : 1)) * a.d + col, sum);
   };
@@ -237,6 +460,7 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_join(EmbGrad a) {
 #pragma unroll
   for (int t = 0; t < EPL; ++t) sum[t] = 0.0f;
   if (col < a.d) {
+#pragma unroll 4
     for (int64_t p = piece + g; p <= last; p += NG) {
       const float4* h = reinterpret_cast<const float4*>(a.partial + (p * 2 + (p == piece ? 1 : 0)) * a.d + col);
 #pragma unroll
@@ -257,7 +481,7 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_join(EmbGrad a) {
   for (int o = 1; o < used; ++o)
 #pragma unroll
     for (int t = 0; t < EPL; ++t) sum[t] += sh[o][sub * EPL + t];
-  put_row<EPL>(a, j, col, sum);
+  put_row<EPL>(a, a.parts.rows ? a.parts.work() : SweepWork{}, j, col, sum);
 }
 
 // Lanes per row: the power of two that holds a row's 16-byte pieces, at most a wave
@@ -320,54 +544,100 @@ int64_t piece_count(int64_t n) { return (n + EMB_PIECE - 1) / EMB_PIECE; }
 
 }  // namespace
 
-size_t row_sums_bytes(int64_t n, int64_t C, int d) {
-  if (n == 0) return 16;
-  return align256(pair_sort_geom(n, C).scratch_bytes) + 4 * align256((size_t)n * 4) +
-         align256((size_t)piece_count(n) * 2 * d * 4);
+namespace {
+
+int key_bits(int64_t C) {
+  int b = 1;
+  while (((int64_t)1 << b) < C) ++b;
+  return b;
+}
+int order_passes(int64_t C) { return (key_bits(C) + ORD_BITS - 1) / ORD_BITS; }
+int64_t order_tiles(int64_t n) { return (n + ORD_TILE - 1) / ORD_TILE; }
+
+// Scratch of the sort: the count matrices and the number of records, or the library's pair sort's.
+size_t order_bytes(int64_t n, int64_t C) {
+  if (order_tiles(n) > ORD_TILES) return align256(pair_sort_geom(n, C).scratch_bytes);
+  return align256((size_t)order_tiles(n) * ORD_BINS * 4 + 16);
 }
 
-size_t embed_workspace_bytes(int64_t n, int64_t C, int d) { return row_sums_bytes(n, C, d); }
-
-hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, const void* table, const int32_t* ids,
-                         void* out, hipStream_t st) {
-  return bf16v ? forward_t<bf16>(n, C, d, scale, table, ids, out, st)
-               : forward_t<float>(n, C, d, scale, table, ids, out, st);
+hipError_t clear_only(const ClearArgs& c, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>((c.n16 + 4 * ORD_THREADS - 1) / (4 * ORD_THREADS), 65536);
+  hipLaunchKernelGGL(k_embed_clear, dim3((unsigned)blocks), dim3(ORD_THREADS), 0, st, c);
+  return hipGetLastError();
 }
 
-hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, bool grad_bf16, bool accumulate,
-                          const int32_t* ids, const void* dout, void* ws, void* dtable, hipStream_t st) {
-  if (!accumulate) {
-    const int64_t n16 = C * d * (grad_bf16 ? 2 : 4) / 16;
-    const int64_t blocks = std::min<int64_t>((n16 + EMB_THREADS - 1) / EMB_THREADS, 4096);
-    hipLaunchKernelGGL(k_embed_clear, dim3((unsigned)blocks), dim3(EMB_THREADS), 0, st, static_cast<u32x4*>(dtable), n16);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+// ids -> (K, V, ntot): ids in [0, C) in ascending order with their rows, equal ids in the order of their rows.
+hipError_t order_rows(const int32_t* ids, int64_t n, int64_t C, const ClearArgs& clear, void* scratch, int32_t* const (&buf)[4],
+                      EmbGrad& g, hipStream_t st) {
+  const int64_t tiles = order_tiles(n);
+  if (tiles > ORD_TILES) {
+    if (clear.n16 > 0) {
+      const hipError_t e = clear_only(clear, st);
+      if (e != hipSuccess) return e;
+    }
+    // no list entries: the records are the rows' ids alone
+    return launch_pair_sort(pair_sort_geom(n, C), ids, 0, 1, n, ids, C, scratch, buf[0], buf[1], buf[2], buf[3], &g.K,
+                            &g.V, &g.ntot, st);
   }
-  RowSums r{};
-  r.bf16v = bf16v;
-  r.n = n;
-  r.C = C;
-  r.d = d;
-  r.scale = scale;
-  r.grad_bf16 = grad_bf16;
-  r.accumulate = accumulate;
-  r.ids = ids;
-  r.rows = dout;
-  return row_sums(r, ws, dtable, st);
+  const int kb = key_bits(C), passes = order_passes(C);
+  uint32_t* counts = static_cast<uint32_t*>(scratch);
+  OrderArgs a{};
+  a.ids = ids;
+  a.n = n;
+  a.C = C;
+  a.tiles = (int)tiles;
+  a.counts = counts;
+  a.ntot = counts + tiles * ORD_BINS;
+  a.clear = clear;
+  a.parts = 2 * passes;
+  // workgroups that clear, per launch
+  const int64_t share = clear.n16 / (tiles == 1 ? 1 : a.parts);
+  const int64_t extra = std::min<int64_t>((share + 4 * ORD_THREADS - 1) / (4 * ORD_THREADS), 16384);
+  if (tiles == 1) {
+    a.kout = buf[0];
+    a.vout = buf[1];
+    hipLaunchKernelGGL(k_order_small, dim3((unsigned)(1 + extra)), dim3(ORD_THREADS), 0, st, a, kb);
+    g.K = buf[0];
+    g.V = buf[1];
+    g.ntot = a.ntot;
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)(tiles + extra));
+  int shift = 0;
+  for (int p = 0; p < passes; ++p) {
+    const int left = passes - p, bits = (kb - shift + left - 1) / left;
+    a.shift = shift;
+    a.bits = bits;
+    a.kout = buf[2 * (p & 1)];
+    a.vout = buf[2 * (p & 1) + 1];
+    for (int half = 0; half < 2; ++half) {
+      a.part = 2 * p + half;
+      auto kern = half == 0 ? (p == 0 ? k_order_hist<true> : k_order_hist<false>)
+                            : (p == 0 ? k_order_scatter<true> : k_order_scatter<false>);
+      hipLaunchKernelGGL(kern, grid, dim3(ORD_THREADS), 0, st, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    a.kin = a.kout;
+    a.vin = a.vout;
+    shift += bits;
+  }
+  g.K = a.kout;
+  g.V = a.vout;
+  g.ntot = a.ntot;
+  return hipSuccess;
 }
 
-hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st) {
+hipError_t row_sums_clear(const RowSums& r, const ClearArgs& clear, void* ws, void* out, hipStream_t st) {
   const int64_t n = r.n;
-  if (n == 0) return hipSuccess;
-  const PairSortGeom g = pair_sort_geom(n, r.C);
+  if (n == 0) return clear.n16 > 0 ? clear_only(clear, st) : hipSuccess;
   char* p = static_cast<char*>(ws);
   void* scratch = p;
-  p += align256(g.scratch_bytes);
+  p += order_bytes(n, r.C);
   int32_t* buf[4];
   for (int q = 0; q < 4; ++q, p += align256((size_t)n * 4)) buf[q] = reinterpret_cast<int32_t*>(p);
   EmbGrad a{};
-  // no list entries: the records are the positions' ids alone
-  hipError_t e = launch_pair_sort(g, r.ids, 0, 1, n, r.ids, r.C, scratch, buf[0], buf[1], buf[2], buf[3], &a.K, &a.V, &a.ntot, st);
+  hipError_t e = order_rows(r.ids, n, r.C, clear, scratch, buf, a, st);
   if (e != hipSuccess) return e;
   a.dout = r.rows;
   a.weight = r.weight;
@@ -383,6 +653,42 @@ hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st) {
   e = r.bf16v ? pieces_t<bf16>(a, np, st) : pieces_t<float>(a, np, st);
   if (e != hipSuccess) return e;
   return join(a, np, st);
+}
+
+}  // namespace
+
+size_t row_sums_bytes(int64_t n, int64_t C, int d) {
+  if (n == 0) return 16;
+  return order_bytes(n, C) + 4 * align256((size_t)n * 4) + align256((size_t)piece_count(n) * 2 * d * 4);
+}
+
+hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st) {
+  return row_sums_clear(r, ClearArgs{}, ws, out, st);
+}
+
+size_t embed_workspace_bytes(int64_t n, int64_t C, int d) { return row_sums_bytes(n, C, d); }
+
+hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, const void* table, const int32_t* ids,
+                         void* out, hipStream_t st) {
+  return bf16v ? forward_t<bf16>(n, C, d, scale, table, ids, out, st)
+               : forward_t<float>(n, C, d, scale, table, ids, out, st);
+}
+
+hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, bool grad_bf16, bool accumulate,
+                          const int32_t* ids, const void* dout, void* ws, void* dtable, hipStream_t st) {
+  ClearArgs clear{};
+  if (!accumulate) clear = ClearArgs{static_cast<u32x4*>(dtable), C * d * (grad_bf16 ? 2 : 4) / 16};
+  RowSums r{};
+  r.bf16v = bf16v;
+  r.n = n;
+  r.C = C;
+  r.d = d;
+  r.scale = scale;
+  r.grad_bf16 = grad_bf16;
+  r.accumulate = accumulate;
+  r.ids = ids;
+  r.rows = dout;
+  return row_sums_clear(r, clear, ws, dtable, st);
 }
 
 }  // namespace rece

@@ -29,24 +29,6 @@
 #include "rece_internal.h"
 #include "rece_parts.h"
 
-#ifndef VPIPE
-#define VPIPE 1
-#endif
-#ifndef VPIPED
-#define VPIPED 64
-#endif
-#ifndef LP_SCHED
-#define LP_SCHED
-#endif
-#ifndef VFR2
-#define VFR2 2
-#endif
-#ifndef VTI
-#define VTI 128
-#endif
-#ifndef VFR
-#define VFR 4
-#endif
 namespace rece {
 
 namespace {
@@ -61,7 +43,7 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr float LP_REF_LIMIT = 1.1529215e18f;   // 2^60: a sum beyond it is taken again with a better reference
 constexpr float LP_FLOOR = -1e28f;              // a reference where no logit is: those beyond the end lie at -1e30
 constexpr float LP_NEVER = 1e30f;               // lse2 of a row that has no weight: exp2(x2 - 1e30) = 0
-constexpr int LP_FRAGS = VFR;                     // fragments of a row read ahead of their products
+constexpr int LP_FRAGS = 4;                     // fragments of a row read ahead of their products
 constexpr int LP_ROW_PAD = 256;                 // packed rows are padded with zero rows to a multiple of this
 
 enum LpMode { LP_LSE = 0, LP_LSEO = 1, LP_DX = 2, LP_DY = 3 };
@@ -89,7 +71,7 @@ struct LpArgs {
 // chunk c ^ (n & SWM), which spreads the 32 rows a fragment read touches over the banks.
 template <class E, int D, int NWS> struct LpTile {
   static constexpr int RB = D * (int)sizeof(E);
-  static constexpr int TI = NWS > 1 ? 32 * NWS : (RB <= 128 ? VTI : RB <= 256 ? 64 : 32);
+  static constexpr int TI = NWS > 1 ? 32 * NWS : (RB <= 128 ? 128 : RB <= 256 ? 64 : 32);
   static constexpr int CPR = RB / 16;
   static constexpr int SWM = (CPR < 8 ? CPR : 8) - 1;
   static constexpr int BYTES = TI * RB;
@@ -244,7 +226,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile
   constexpr bool ACC = MODE != LP_LSE, LSE = MODE == LP_LSE || MODE == LP_LSEO, DY = MODE == LP_DY;
   constexpr bool OWN = DY && sizeof(E) == 4;
-  constexpr bool PIPE = VPIPE && DY && sizeof(E) == 2 && TERMS == 1 && D <= VPIPED;
+  constexpr bool PIPE = DY && sizeof(E) == 2 && TERMS == 1 && D <= 64;   // needs a second block's registers
   static_assert(T::BYTES % (16 * NT) == 0 && TI <= NT, "whole chunks per thread");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -327,7 +309,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   // logits of 32 streamed rows (first one q0, at LDS offset base) against the wave's owners
   auto logits = [&](f32x16 (&x)[OB], uint32_t base, uint32_t q0) {
     const f32x16 zero = {};
-    constexpr int KG = KC < LP_FRAGS ? KC : (D == 256 ? VFR2 : LP_FRAGS);   // fragments in flight
+    constexpr int KG = KC < LP_FRAGS ? KC : (D == 256 ? 2 : LP_FRAGS);   // fragments in flight
 #pragma unroll
     for (int k0 = 0; k0 < KC; k0 += KG) {
       u32x4 f[KG];
@@ -432,7 +414,6 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
         if (i + 1 < NB) logits(x[(i + 1) & 1], base + (i + 1) * (NWS * 32 * RB), q0 + (i + 1) * NWS * 32);
         weigh(x[i & 1], par + i * (NWS * 128));
         if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x[i & 1], lo, base + i * (NWS * 32 * RB));
-        LP_SCHED
       }
     } else {
 #pragma unroll 1
@@ -534,7 +515,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
 // launches), then writes the list of its own, the packed rows and ids, and the (unscaled)
 // logit of each row's own item, the diagonal of a 32 x 32 product, so that it has the
 // same bits as in the sweeps.  The last workgroup fills the padding with zero rows.
-constexpr int PACK_THREADS = 512;
+constexpr int PACK_THREADS = 256;
 constexpr int64_t PACK_BLOCKS = 256;
 
 template <class E, int D>
@@ -554,8 +535,18 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
     return id >= 0 && id < C;
   };
   int before = 0;
+  int64_t from = 0;
+  if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
+    const uint32_t last = (uint32_t)(C - 1);
 #pragma unroll 8
-  for (int64_t i = tid; i < i0; i += PACK_THREADS) before += good(i, i0) ? 1 : 0;
+    for (int64_t q = tid; q < i0 / 4; q += PACK_THREADS) {
+      const u32x4 v = reinterpret_cast<const u32x4*>(ids)[q];
+      before += (v[0] <= last) + (v[1] <= last) + (v[2] <= last) + (v[3] <= last);
+    }
+    from = i0 / 4 * 4;
+  }
+#pragma unroll 8
+  for (int64_t i = from + tid; i < i0; i += PACK_THREADS) before += good(i, i0) ? 1 : 0;
   before = wave_sum(before);
   if (l == 0) wsum[w] = before;
   __syncthreads();
@@ -716,7 +707,7 @@ __global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, const 
   const int64_t r = inv ? inv[i] : i;
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
-    parts.each(r, [&](int64_t at) {
+    parts.each(parts.work(), r, [&](int64_t at) {
       const float4 w = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       v = float4{v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w};
     });
@@ -756,7 +747,7 @@ __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float* __
     const uint32_t b = (uint32_t)r / parts.block;
     const int64_t g_own = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
     const int64_t home = ((b + g_own) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + (uint32_t)r % parts.block;
-    parts.each(r, [&](int64_t at) {
+    parts.each(w, r, [&](int64_t at) {
       const float mp = m[at], f = exp2_fast(mp - l2);
       float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       if (at == home) {
@@ -783,20 +774,13 @@ constexpr int LP_CUS = 256;
 // and split each tile's rows instead (a block of owners that is mostly empty costs as much as a full one).
 template <class E, int D> struct LpShape {
   static constexpr bool B = sizeof(E) == 2;
-#ifndef VOB
-#define VOB 2
-#endif
-#ifndef VMW
-#define VMW 2
-#endif
-#ifndef VWL
-#define VWL 3
-#endif
   static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
-  static constexpr int MW_LSE = B ? VWL : (D <= 128 ? 3 : 2);
-  static constexpr int OB_GRAD = B && D <= 64 ? VOB : 1;
-  static constexpr int MW_GRAD = B ? VMW : (D <= 64 ? 2 : 1);
+  static constexpr int MW_LSE = B ? 3 : (D <= 128 ? 3 : 2);
+  static constexpr int OB_GRAD = B && D <= 64 ? 2 : 1;
+  static constexpr int MW_GRAD = !B ? (D <= 64 ? 2 : 1) : D == 128 ? 3 : 2;
+  static constexpr int NWO_GRAD = B && D == 256 ? 8 : 4;
   static constexpr int NWS_FEW = D * (int)sizeof(E) <= 256 ? 4 : 1;
+  static constexpr int MW_FEW = D * (int)sizeof(E) <= 128 ? 3 : 2;
 };
 
 struct LpSweep {   // one sweep's shape
@@ -812,11 +796,13 @@ LpSweep lp_shape(int mode, int64_t n_own, int64_t n_str) {
   LpSweep p{};
   p.ob = mode == LP_LSE ? S::OB_LSE : S::OB_GRAD;
   const bool few = mode != LP_DY && S::NWS_FEW > 1 && n_own <= 32 * p.ob;
-  p.nwo = few ? 1 : 4;
+  p.nwo = few ? 1 : mode == LP_LSE ? 4 : S::NWO_GRAD;
   p.nws = few ? S::NWS_FEW : 1;
   p.ti = few ? LpTile<E, D, S::NWS_FEW>::TI : LpTile<E, D, 1>::TI;
   const int64_t units = ceil_div(n_own, p.block()) * ceil_div(n_str, p.ti);
-  p.grid = (uint32_t)std::min<int64_t>(LP_CUS * (mode == LP_LSE ? S::MW_LSE : S::MW_GRAD), units);
+  int waves = mode == LP_LSE ? S::MW_LSE : S::MW_GRAD;   // per SIMD
+  if (few) waves = std::min<int>(waves, S::MW_FEW);
+  p.grid = (uint32_t)std::min<int64_t>(LP_CUS * waves * 4 / (p.nwo * p.nws), units);
   return p;
 }
 
@@ -885,18 +871,20 @@ hipError_t lp_launch_t(const LpArgs& a, hipStream_t st) {
 template <class E, int D, int MODE, bool ENT>
 hipError_t lp_launch(const LpArgs& a, hipStream_t st) {
   using S = LpShape<E, D>;
+  constexpr int NWO = MODE == LP_LSE ? 4 : S::NWO_GRAD;
   constexpr int OB = MODE == LP_LSE ? S::OB_LSE : S::OB_GRAD, MINW = MODE == LP_LSE ? S::MW_LSE : S::MW_GRAD;
   constexpr bool THREE = sizeof(E) == 2 && MODE != LP_LSE;
   if constexpr (MODE != LP_DY && S::NWS_FEW > 1) {
+    constexpr int FEW = MINW < S::MW_FEW ? MINW : S::MW_FEW;
     if (a.parts.nws > 1) {
       if constexpr (THREE)
-        if (a.terms != 1) return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 3, MINW>(a, st);
-      return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 1, MINW>(a, st);
+        if (a.terms != 1) return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 3, FEW>(a, st);
+      return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 1, FEW>(a, st);
     }
   }
   if constexpr (THREE)
-    if (a.terms != 1) return lp_launch_t<E, D, OB, 4, 1, MODE, ENT, 3, MINW>(a, st);
-  return lp_launch_t<E, D, OB, 4, 1, MODE, ENT, 1, MINW>(a, st);
+    if (a.terms != 1) return lp_launch_t<E, D, OB, NWO, 1, MODE, ENT, 3, MINW>(a, st);
+  return lp_launch_t<E, D, OB, NWO, 1, MODE, ENT, 1, MINW>(a, st);
 }
 
 // bf16 results take one bf16 term of a weight, float32 results all of its bits.

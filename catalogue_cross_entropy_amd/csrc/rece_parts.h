@@ -45,8 +45,7 @@ struct SweepParts {
   }
   // f(index of a partial result) for every part of row r, in order; results are indexed [slots][nws][block].
   template <class F>
-  __device__ __forceinline__ void each(int64_t r, F f) const {
-    const SweepWork w = work();
+  __device__ __forceinline__ void each(const SweepWork& w, int64_t r, F f) const {
     const uint32_t b = (uint32_t)r / block, at = (uint32_t)r % block;
     const int64_t g0 = w.first(b), g1 = w.last(b);
 #pragma unroll 4
