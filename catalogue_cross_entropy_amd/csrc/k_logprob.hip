@@ -480,9 +480,9 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     o0 = b * (32 * OB * NWO) + wo * (32 * OB);
     load_owners();
     run();
-    // part [slot b + blockIdx.x][ws][owner of the block]; settled(): the lanes' offsets are formed here, not
+    // part [slot][ws][owner of the block]; settled(): the lanes' offsets are formed here, not
     // kept in registers through the sweep
-    const int64_t part = (((int64_t)b + blockIdx.x) * NWS + ws) * (32 * OB * NWO) + wo * (32 * OB);
+    const int64_t part = (work.slot(b, blockIdx.x) * NWS + ws) * (32 * OB * NWO) + wo * (32 * OB);
     const int rr = settled(r), hh = settled(h);
     if constexpr (LSE) {
 #pragma unroll
@@ -630,7 +630,7 @@ __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ i
   }
   const SweepWork w = parts.work();
   const uint32_t b = (uint32_t)r / parts.block, in = (uint32_t)r % parts.block;
-  const int64_t p0 = ((int64_t)b + w.first(b)) * parts.nws, p1 = ((int64_t)b + w.last(b) + 1) * parts.nws;
+  const int64_t p0 = w.slot(b, w.first(b)) * parts.nws, p1 = (w.slot(b, w.last(b)) + 1) * parts.nws;
   float mm = NEG_INF, zz = 0.0f, tt = 0.0f;
   for (int64_t p = p0 + l; p < p1; p += L) {
     const int64_t at = p * parts.block + in;
@@ -746,7 +746,7 @@ __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float* __
     const SweepWork w = parts.work();
     const uint32_t b = (uint32_t)r / parts.block;
     const int64_t g_own = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
-    const int64_t home = ((b + g_own) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + (uint32_t)r % parts.block;
+    const int64_t home = (w.slot(b, g_own) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + (uint32_t)r % parts.block;
     parts.each(w, r, [&](int64_t at) {
       const float mp = m[at], f = exp2_fast(mp - l2);
       float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
@@ -786,7 +786,8 @@ template <class E, int D> struct LpShape {
 struct LpSweep {   // one sweep's shape
   int ob, nwo, nws, ti;
   uint32_t grid;
-  int64_t slots(int64_t n_own) const { return (ceil_div(n_own, 32 * ob * nwo) + grid) * nws; }   // parts of a block each
+  bool whole;
+  int64_t slots(int64_t n_own) const { return (ceil_div(n_own, block()) + (whole ? 0 : grid)) * nws; }   // parts of a block each
   int64_t block() const { return 32 * (int64_t)ob * nwo; }
 };
 
@@ -803,6 +804,9 @@ LpSweep lp_shape(int mode, int64_t n_own, int64_t n_str) {
   int waves = mode == LP_LSE ? S::MW_LSE : S::MW_GRAD;   // per SIMD
   if (few) waves = std::min<int>(waves, S::MW_FEW);
   p.grid = (uint32_t)std::min<int64_t>(LP_CUS * waves * 4 / (p.nwo * p.nws), units);
+  // items as owners (their number is known here): whole blocks where that leaves at most 1/16 of the grid's work idle
+  const int64_t nb = ceil_div(n_own, p.block());
+  p.whole = mode == LP_DY && (ceil_div(nb, p.grid) * p.grid - nb) * 16 <= nb;
   return p;
 }
 
@@ -910,6 +914,7 @@ SweepParts lp_parts(int mode, int64_t n_own, int64_t n_str, const int32_t* nv, c
   p.tile = (uint32_t)f.ti;
   p.grid = f.grid;
   p.nws = f.nws;
+  p.whole = f.whole;
   p.rows = rows;
   return p;
 }

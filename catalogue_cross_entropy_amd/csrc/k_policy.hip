@@ -76,6 +76,9 @@ constexpr int POL_TILE = 4096;      // tokens per workgroup
 constexpr int POL_SMALL_N = 8192;   // one workgroup takes the whole call up to this many tokens ...
 constexpr int POL_SMALL_SEQ = 2048; // ... and sequences (their offsets and counts lie in LDS)
 constexpr int POL_SUMS = 7;         // loss, pg, kl, entropy, clipped, ratio, tokens
+constexpr int POL_COUNTERS = 1024;  // workgroups that count, one partial count each (atomics on one word take
+                                    // 10 ns apiece: 40 us for the waves of four million tokens)
+constexpr int POL_LDS_SEQ = 1024;   // sequences of a tile whose offsets lie in LDS
 
 struct PolArgs {
   rece_policy_config c;
@@ -86,46 +89,90 @@ struct PolArgs {
   const float* dloss;
   float *loss, *stats;
   void *dlogp, *dentropy;
-  int32_t* head;        // [2] tokens that count, sequences with such a token
+  int32_t* part;        // [counters][2] tokens that count, sequences with such a token
+  int counters;         // 0: the offsets tell (no mask, token mean)
   int32_t* cnt;         // [n_seq] tokens that count (sequence mean)
   double* partial;      // [blocks][8]
 };
 
-struct PolSums {
-  double v[POL_SUMS];
+// The values of one token.
+struct PolToken {
+  float lp, old, ref, H;
+};
+// What it adds to the sums, and its gradients by logp and entropy (without dloss).
+struct PolTerm {
+  float loss, pg, kl, H, r;
+  bool clipped;
+  float dlp, dent;
 };
 
-// One token that counts: its weight w, advantage A; returns the gradients by logp and entropy (without dloss).
-template <class E>
-__device__ __forceinline__ void pol_token(const PolArgs& a, int64_t t, float w, float A, PolSums& s, float& dlp, float& dent) {
-  const float lp = to_f32(static_cast<const E*>(a.logp)[t]);
-  const float r = expf(lp - to_f32(static_cast<const E*>(a.old)[t]));
-  const float lo = 1.0f - a.c.clip_low, hi = 1.0f + a.c.clip_high;
-  const bool clipped = (A > 0.0f && r > hi) || (A < 0.0f && r < lo);
-  const float pg = clipped ? -A * (A > 0.0f ? hi : lo) : -A * r;
-  float g = clipped ? 0.0f : -A * r;
-  float kl = 0.0f, H = 0.0f;
-  if (a.ref) {
-    const float u = to_f32(static_cast<const E*>(a.ref)[t]) - lp;
-    const float eu = expf(u);
-    kl = eu - u - 1.0f;
-    if (a.c.kl_coef != 0.0f) g = fmaf(a.c.kl_coef, 1.0f - eu, g);
-  }
-  if (a.entropy) H = to_f32(static_cast<const E*>(a.entropy)[t]);
-  // without a coefficient a term is no part of the loss, whatever its value
-  float total = pg;
-  if (a.c.kl_coef != 0.0f) total = fmaf(a.c.kl_coef, kl, total);
-  if (a.c.entropy_coef != 0.0f) total = fmaf(-a.c.entropy_coef, H, total);
-  s.v[0] += (double)w * (double)total;
-  s.v[1] += pg;
-  s.v[2] += kl;
-  s.v[3] += H;
-  s.v[4] += clipped ? 1.0 : 0.0;
-  s.v[5] += r;
-  s.v[6] += 1.0;
-  dlp = w * g;
-  dent = -a.c.entropy_coef * w;
+// e^x to about an ulp: 2^y with y = x log2(e) rounded, times 1 + the rounding's share (y alone would leave |x| ulps).
+__device__ __forceinline__ float exp_near(float x) {
+  constexpr float L = 1.44269504088896341f, LLO = 1.92596299112661746e-8f;   // log2(e) and what its rounding left
+  const float y = x * L;
+  const float rest = fmaf(x, LLO, fmaf(x, L, -y)) * 0.693147180559945309f;
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fabsf(y) < 200.0f ? fmaf(e, rest, e) : e;   // beyond: 0, infinity or NaN as it is
 }
+
+// One token of weight w and advantage A.
+__device__ __forceinline__ PolTerm pol_token(const PolArgs& a, const PolToken& k, float w, float A) {
+  PolTerm o;
+  const float lo = 1.0f - a.c.clip_low, hi = 1.0f + a.c.clip_high;
+  o.r = exp_near(k.lp - k.old);
+  const float bound = A > 0.0f ? hi : lo;
+  o.clipped = (A > 0.0f && o.r > hi) || (A < 0.0f && o.r < lo);
+  o.pg = -A * (o.clipped ? bound : o.r);
+  float g = o.clipped ? 0.0f : o.pg;
+  o.kl = 0.0f;
+  o.H = 0.0f;
+  // without a coefficient a term is no part of the loss, whatever its value
+  o.loss = o.pg;
+  if (a.ref) {
+    const float u = k.ref - k.lp;
+    const float eu = exp_near(u);
+    o.kl = eu - u - 1.0f;
+    if (a.c.kl_coef != 0.0f) {
+      g = fmaf(a.c.kl_coef, 1.0f - eu, g);
+      o.loss = fmaf(a.c.kl_coef, o.kl, o.loss);
+    }
+  }
+  if (a.entropy) {
+    o.H = k.H;
+    if (a.c.entropy_coef != 0.0f) o.loss = fmaf(-a.c.entropy_coef, o.H, o.loss);
+  }
+  o.loss *= w;
+  o.dlp = w * g;
+  o.dent = -a.c.entropy_coef * w;
+  return o;
+}
+
+// Sums of a thread's tokens.  Up to four are added in float32 first (their terms carry a float32 rounding each
+// as it is; a float64 addition of each costs as much as the rest of the token), then in float64.
+struct PolSums {
+  double v[5] = {};   // loss, pg, kl, entropy, ratio
+  float f[5] = {};
+  int clipped = 0, tokens = 0;
+  __device__ __forceinline__ void add(const PolTerm& o, bool on) {
+    f[0] += on ? o.loss : 0.0f;
+    f[1] += on ? o.pg : 0.0f;
+    f[2] += on ? o.kl : 0.0f;
+    f[3] += on ? o.H : 0.0f;
+    f[4] += on ? o.r : 0.0f;
+    clipped += on && o.clipped ? 1 : 0;
+    tokens += on ? 1 : 0;
+  }
+  __device__ __forceinline__ void flush() {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      v[k] += f[k];
+      f[k] = 0.0f;
+    }
+  }
+  __device__ __forceinline__ void get(double (&o)[POL_SUMS]) const {
+    o[0] = v[0], o[1] = v[1], o[2] = v[2], o[3] = v[3], o[4] = clipped, o[5] = v[4], o[6] = tokens;
+  }
+};
 
 __global__ __launch_bounds__(POL_THREADS) void k_pol_clear(int32_t* __restrict__ p, int64_t n) {
   const int64_t t = (int64_t)blockIdx.x * POL_THREADS + threadIdx.x;
@@ -135,83 +182,60 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_clear(int32_t* __restrict__
 // Tokens that count: all (token mean) or per sequence, and the sequences that have one.
 __global__ __launch_bounds__(POL_THREADS) void k_pol_count(PolArgs a) {
   constexpr int PER = POL_TILE / POL_THREADS;
+  __shared__ int sh[2][POL_THREADS / WAVE];
   const int64_t n = a.c.n, ns = a.c.n_seq;
-  const int64_t base = (int64_t)blockIdx.x * POL_TILE, t0 = base + (int64_t)threadIdx.x * PER;
-  const int64_t lo = max(offset_at(a.offs, 0, n), t0), hi = min(offset_at(a.offs, ns, n), min(n, t0 + PER));
+  const int64_t first = offset_at(a.offs, 0, n), end = offset_at(a.offs, ns, n);
   const bool per_seq = a.c.reduction == RECE_MEAN_SEQUENCE;
-  uint32_t bits = 0;
-  if (lo < hi) {
-    if (!a.mask) {
-      bits = ((1u << (hi - t0)) - 1u) & ~((1u << (lo - t0)) - 1u);
-    } else if (hi - t0 == PER && (reinterpret_cast<uintptr_t>(a.mask) & 15) == 0) {
-      const u32x4 m = *reinterpret_cast<const u32x4*>(a.mask + t0);
+  int tokens = 0, with = 0;
+  auto add = [&](int64_t s, int c) { with += atomicAdd(&a.cnt[s], c) == 0 ? 1 : 0; };   // whoever finds 0 counts the sequence
+  for (int64_t base = (int64_t)blockIdx.x * POL_TILE; base < n; base += (int64_t)gridDim.x * POL_TILE) {
+    const int64_t t0 = base + (int64_t)threadIdx.x * PER;
+    const int64_t lo = max(first, t0), hi = min(end, min(n, t0 + PER));
+    uint32_t bits = 0;
+    if (lo < hi) {
+      if (!a.mask) {
+        bits = ((1u << (hi - t0)) - 1u) & ~((1u << (lo - t0)) - 1u);
+      } else if (hi - t0 == PER && (reinterpret_cast<uintptr_t>(a.mask) & 15) == 0) {
+        const u32x4 m = *reinterpret_cast<const u32x4*>(a.mask + t0);
 #pragma unroll
-      for (int q = 0; q < PER; ++q) bits |= ((m[q / 4] >> (8 * (q % 4))) & 0xFFu) ? 1u << q : 0u;
-      bits &= ~((1u << (lo - t0)) - 1u);
-    } else {
-      for (int64_t t = lo; t < hi; ++t) bits |= a.mask[t] ? 1u << (t - t0) : 0u;
+        for (int q = 0; q < PER; ++q) bits |= ((m[q / 4] >> (8 * (q % 4))) & 0xFFu) ? 1u << q : 0u;
+        bits &= ~((1u << (lo - t0)) - 1u);
+      } else {
+        for (int64_t t = lo; t < hi; ++t) bits |= a.mask[t] ? 1u << (t - t0) : 0u;
+      }
+    }
+    tokens += __popc(bits);
+    if (!per_seq) continue;
+    const int64_t wave0 = base + (int64_t)(threadIdx.x & ~(WAVE - 1)) * PER;
+    if (wave0 >= n) continue;   // whole waves
+    const int64_t s0 = seq_of_wave(a.offs, 0, ns - 1, wave0);
+    const int64_t s1 = seq_of_wave(a.offs, s0, ns - 1, min(n, wave0 + WAVE * PER) - 1);
+    if (s0 == s1) {
+      const int c = wave_sum(__popc(bits));
+      if (lane_id() == 0 && c) add(s0, c);
+      continue;
+    }
+    int64_t t = lo;
+    while (t < hi) {
+      const int64_t s = seq_of(a.offs, s0, s1, t);
+      const int64_t e = max(t + 1, min(hi, offset_at(a.offs, s + 1, n)));
+      const uint32_t part = bits & ~((1u << (t - t0)) - 1u) & (e - t0 >= 32 ? ~0u : (1u << (e - t0)) - 1u);
+      if (part) add(s, __popc(part));
+      t = e;
     }
   }
-  if (!per_seq) {
-    const int c = wave_sum(__popc(bits));
-    if (lane_id() == 0 && c) atomicAdd(&a.head[0], c);   // integers: any order gives the same sum
-    return;
+  tokens = wave_sum(tokens);
+  with = wave_sum(with);
+  if (lane_id() == 0) {
+    sh[0][threadIdx.x / WAVE] = tokens;
+    sh[1][threadIdx.x / WAVE] = with;
   }
-  const int64_t wave0 = base + (int64_t)(threadIdx.x & ~(WAVE - 1)) * PER;
-  if (wave0 >= n) return;   // whole waves
-  const int64_t s0 = seq_of_wave(a.offs, 0, ns - 1, wave0);
-  const int64_t s1 = seq_of_wave(a.offs, s0, ns - 1, min(n, wave0 + WAVE * PER) - 1);
-  auto add = [&](int64_t s, int c) {
-    if (atomicAdd(&a.cnt[s], c) == 0) atomicAdd(&a.head[1], 1);
-  };
-  if (s0 == s1) {
-    const int c = wave_sum(__popc(bits));
-    if (lane_id() == 0 && c) add(s0, c);
-    return;
-  }
-  int64_t t = lo;
-  while (t < hi) {
-    const int64_t s = seq_of(a.offs, s0, s1, t);
-    const int64_t e = max(t + 1, min(hi, s + 1 <= ns ? offset_at(a.offs, s + 1, n) : hi));
-    const uint32_t part = bits & ~((1u << (t - t0)) - 1u) & (e - t0 >= 32 ? ~0u : (1u << (e - t0)) - 1u);
-    if (part) add(s, __popc(part));
-    t = e;
-  }
-}
-
-template <class E>
-__global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
-  __shared__ double sh[POL_THREADS / WAVE];
-  const int64_t n = a.c.n, ns = a.c.n_seq;
-  const int64_t lo = offset_at(a.offs, 0, n), hi = offset_at(a.offs, ns, n);
-  const int64_t base = (int64_t)blockIdx.x * POL_TILE;
-  const bool per_seq = a.c.reduction == RECE_MEAN_SEQUENCE, need_seq = per_seq || !a.c.token_adv;
-  const int64_t tokens = a.head ? (int64_t)a.head[0] : hi - lo;
-  const float up = a.dloss ? a.dloss[0] : 1.0f;
-  const float wt = 1.0f / (float)max(tokens, (int64_t)1);
-  const float nonempty = per_seq ? (float)max(a.head[1], 1) : 1.0f;
-  PolSums s{};
-  int64_t s0 = 0, s1 = 0;
-  if (need_seq) {
-    s0 = seq_of_wave(a.offs, 0, ns - 1, base);
-    s1 = seq_of_wave(a.offs, s0, ns - 1, min(n, base + POL_TILE) - 1);
-  }
-  for (int q = 0; q < POL_TILE / POL_THREADS; ++q) {
-    const int64_t t = base + q * POL_THREADS + threadIdx.x;
-    if (t >= n) break;
-    float dlp = 0.0f, dent = 0.0f;
-    if (t >= lo && t < hi && (!a.mask || a.mask[t])) {
-      const int64_t sq = need_seq ? seq_of(a.offs, s0, s1, t) : 0;
-      const float w = per_seq ? 1.0f / ((float)max(a.cnt[sq], 1) * nonempty) : wt;
-      pol_token<E>(a, t, w, a.adv[a.c.token_adv ? t : sq], s, dlp, dent);
-    }
-    if (a.dlogp) put(static_cast<E*>(a.dlogp), t, up * dlp);
-    if (a.dentropy) put(static_cast<E*>(a.dentropy), t, up * dent);
-  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    int c = 0;
 #pragma unroll
-  for (int k = 0; k < POL_SUMS; ++k) {
-    const double v = block_sum_d<POL_THREADS>(s.v[k], sh);
-    if (threadIdx.x == 0) a.partial[(int64_t)blockIdx.x * 8 + k] = v;
+    for (int w = 0; w < POL_THREADS / WAVE; ++w) c += sh[threadIdx.x][w];
+    a.part[blockIdx.x * 2 + threadIdx.x] = c;
   }
 }
 
@@ -223,16 +247,248 @@ __device__ __forceinline__ void pol_write(const PolArgs& a, const double (&v)[PO
   a.stats[5] = (float)v[6];
 }
 
+// Sums of v over the workgroup in a fixed order, in thread 0.
+template <int NT>
+__device__ __forceinline__ void pol_reduce(double (&v)[POL_SUMS], double (*sh)[POL_SUMS]) {
+#pragma unroll
+  for (int k = 0; k < POL_SUMS; ++k) v[k] = wave_sum_d(v[k]);
+  __syncthreads();
+  if (lane_id() == 0)
+#pragma unroll
+    for (int k = 0; k < POL_SUMS; ++k) sh[threadIdx.x / WAVE][k] = v[k];
+  __syncthreads();
+  if (threadIdx.x == 0)
+#pragma unroll
+    for (int k = 0; k < POL_SUMS; ++k) {
+      v[k] = 0.0;
+      for (int w = 0; w < NT / WAVE; ++w) v[k] += sh[w][k];
+    }
+}
+
+// W consecutive values of a token array, W = 4 with one load or store (the array and t aligned to it).
+template <int W>
+__device__ __forceinline__ void load_tokens(const float* p, int64_t t, float (&v)[W]) {
+  if constexpr (W == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p + t);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+    v[0] = p[t];
+  }
+}
+template <int W>
+__device__ __forceinline__ void load_tokens(const bf16* p, int64_t t, float (&v)[W]) {
+  if constexpr (W == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p + t);
+    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+  } else {
+    v[0] = to_f32(p[t]);
+  }
+}
+// 0x80 in byte e: token t + e counts.
+template <int W>
+__device__ __forceinline__ uint32_t load_mask(const uint8_t* p, int64_t t) {
+  if constexpr (W == 4) {
+    if (!p) return 0x80808080u;
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(p + t);
+    return (((m & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | m) & 0x80808080u;
+  } else {
+    return !p || p[t] ? 0x80u : 0u;
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_tokens(float* p, int64_t t, const float (&v)[W]) {
+  if constexpr (W == 4)
+    *reinterpret_cast<float4*>(p + t) = float4{v[0], v[1], v[2], v[3]};
+  else
+    p[t] = v[0];
+}
+template <int W>
+__device__ __forceinline__ void store_tokens(bf16* p, int64_t t, const float (&v)[W]) {
+  if constexpr (W == 4)
+    *reinterpret_cast<uint2*>(p + t) = uint2{bf16_of(v[0]) | (bf16_of(v[1]) << 16), bf16_of(v[2]) | (bf16_of(v[3]) << 16)};
+  else
+    p[t].bits = (uint16_t)bf16_of(v[0]);
+}
+
+// A tile of tokens per workgroup, W consecutive ones per thread and step; the tile's values are requested before
+// anything waits for counts or offsets, and what a token needs of its sequence lies in LDS.
+template <class E, int W>
+__global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
+  constexpr int STEPS = POL_TILE / POL_THREADS / W;
+  constexpr int GROUP = 4;   // steps whose values are in flight together
+  static_assert(STEPS % GROUP == 0, "tile");
+  __shared__ double sh[POL_THREADS / WAVE][POL_SUMS];
+  __shared__ int32_t soff[POL_LDS_SEQ + 1];
+  __shared__ float sadv[POL_LDS_SEQ], sw[POL_LDS_SEQ];
+  __shared__ int64_t srange[2];
+  __shared__ int scount[2][POL_THREADS / WAVE];
+  const uint32_t n = (uint32_t)a.c.n, ns = (uint32_t)a.c.n_seq;   // below 2^31: a tile beyond fits in 32 bits
+  const uint32_t lo = (uint32_t)offset_at(a.offs, 0, n), hi = (uint32_t)offset_at(a.offs, ns, n);
+  const uint32_t base = blockIdx.x * POL_TILE;
+  const int tid = threadIdx.x, wave = tid / WAVE;
+  const bool per_seq = a.c.reduction == RECE_MEAN_SEQUENCE, seq_adv = !a.c.token_adv, need_seq = per_seq || seq_adv;
+  float lp[GROUP][W], old[GROUP][W], ref[GROUP][W], ent[GROUP][W];
+  uint32_t on[GROUP];
+  const bool inside = lo <= base && base + POL_TILE <= hi;   // every token of the tile lies in a sequence
+  auto load = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < GROUP; ++u) {
+      const uint32_t t = base + ((g + u) * POL_THREADS + tid) * W;
+      on[u] = 0;
+#pragma unroll
+      for (int e = 0; e < W; ++e) lp[u][e] = old[u][e] = ref[u][e] = ent[u][e] = 0.0f;
+      if (t + W <= n) {
+        load_tokens<W>(static_cast<const E*>(a.logp), t, lp[u]);
+        load_tokens<W>(static_cast<const E*>(a.old), t, old[u]);
+        if (a.ref) load_tokens<W>(static_cast<const E*>(a.ref), t, ref[u]);
+        if (a.entropy) load_tokens<W>(static_cast<const E*>(a.entropy), t, ent[u]);
+        on[u] = load_mask<W>(a.mask, t);
+      } else if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (t + e < n) {
+            lp[u][e] = to_f32(static_cast<const E*>(a.logp)[t + e]);
+            old[u][e] = to_f32(static_cast<const E*>(a.old)[t + e]);
+            if (a.ref) ref[u][e] = to_f32(static_cast<const E*>(a.ref)[t + e]);
+            if (a.entropy) ent[u][e] = to_f32(static_cast<const E*>(a.entropy)[t + e]);
+            on[u] |= load_mask<1>(a.mask, t + e) << (8 * e);
+          }
+      }
+      if (!inside)
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (t + e < lo || t + e >= hi) on[u] &= ~(0x80u << (8 * e));
+    }
+  };
+  load(0);
+  const float up = a.dloss ? a.dloss[0] : 1.0f;
+  if (a.counters) {
+    int c0 = 0, c1 = 0;
+    for (int q = tid; q < a.counters; q += POL_THREADS) {
+      const int2 c = reinterpret_cast<const int2*>(a.part)[q];
+      c0 += c.x;
+      c1 += c.y;
+    }
+    c0 = wave_sum(c0);
+    c1 = wave_sum(c1);
+    if (lane_id() == 0) {
+      scount[0][wave] = c0;
+      scount[1][wave] = c1;
+    }
+  }
+  if (need_seq && wave < 2) {   // the sequences of the tile's first and last token
+    const int64_t s = seq_of_wave(a.offs, 0, (int64_t)ns - 1, wave == 0 ? base : min(n, base + POL_TILE) - 1);
+    if (lane_id() == 0) srange[wave] = s;
+  }
+  __syncthreads();
+  int tokens = hi > lo ? (int)(hi - lo) : 0, with = 0;
+  if (a.counters) {
+    tokens = 0;
+#pragma unroll
+    for (int w = 0; w < POL_THREADS / WAVE; ++w) {
+      tokens += scount[0][w];
+      with += scount[1][w];
+    }
+  }
+  const float wt = 1.0f / (float)max(tokens, 1), nonempty = (float)max(with, 1);
+  const uint32_t s0 = need_seq ? (uint32_t)srange[0] : 0, s1 = need_seq ? max(s0, (uint32_t)srange[1]) : 0;
+  const bool in_lds = s1 - s0 < POL_LDS_SEQ;
+  auto weight_of = [&](uint32_t sq) { return per_seq ? 1.0f / ((float)max(a.cnt[sq], 1) * nonempty) : wt; };
+  if (need_seq && in_lds)
+    for (uint32_t q = tid; q <= s1 - s0 + 1; q += POL_THREADS) {
+      soff[q] = a.offs[s0 + q];
+      if (q <= s1 - s0) {
+        sadv[q] = seq_adv ? a.adv[s0 + q] : 0.0f;
+        sw[q] = weight_of(s0 + q);
+      }
+    }
+  __syncthreads();
+  PolSums s;
+#pragma unroll 1
+  for (int g = 0; g < STEPS; g += GROUP) {
+    if (g > 0) load(g);
+#pragma unroll
+    for (int u = 0; u < GROUP; ++u) {
+      const uint32_t t = base + ((g + u) * POL_THREADS + tid) * W;
+      if (t >= n) continue;
+      float dlp[W], dent[W], A[W], w[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        A[e] = 0.0f;
+        w[e] = wt;
+      }
+      if (need_seq) {
+        int64_t until = 0;   // the end of the sequence before
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (e > 0) {
+            A[e] = A[e - 1];
+            w[e] = w[e - 1];
+          }
+          const uint32_t te = t + e;
+          if (e > 0 && (int64_t)te < until) continue;
+          if (in_lds) {
+            int l = 0, h = (int)(s1 - s0);
+            while (l < h) {
+              const int m = (l + h + 1) / 2;
+              if (soff[m] <= (int)te) l = m; else h = m - 1;
+            }
+            until = soff[l + 1];
+            A[e] = sadv[l];
+            w[e] = sw[l];
+          } else {
+            const int64_t sq = seq_of(a.offs, s0, s1, te);
+            until = a.offs[sq + 1];
+            if (seq_adv) A[e] = a.adv[sq];
+            w[e] = weight_of((uint32_t)sq);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const bool live = (on[u] >> (8 * e)) & 0x80u;
+        if (!seq_adv) A[e] = live ? a.adv[t + e] : 0.0f;
+        const PolTerm o = pol_token(a, PolToken{lp[u][e], old[u][e], ref[u][e], ent[u][e]}, w[e], A[e]);
+        s.add(o, live);   // what lies at a token that does not count is selected away, NaN included
+        dlp[e] = live ? up * o.dlp : 0.0f;
+        dent[e] = live ? up * o.dent : 0.0f;
+      }
+      if (W > 1) s.flush();
+      if (t + W <= n) {
+        if (a.dlogp) store_tokens<W>(static_cast<E*>(a.dlogp), t, dlp);
+        if (a.dentropy) store_tokens<W>(static_cast<E*>(a.dentropy), t, dent);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (t + e < n) {
+            if (a.dlogp) put(static_cast<E*>(a.dlogp), t + e, dlp[e]);
+            if (a.dentropy) put(static_cast<E*>(a.dentropy), t + e, dent[e]);
+          }
+      }
+    }
+    s.flush();
+  }
+  double v[POL_SUMS];
+  s.get(v);
+  pol_reduce<POL_THREADS>(v, sh);
+  if (tid == 0) {
+#pragma unroll
+    for (int k = 0; k < POL_SUMS; ++k) a.partial[(int64_t)blockIdx.x * 8 + k] = v[k];
+  }
+}
+
+// The workgroups' sums, in their order.
 __global__ __launch_bounds__(POL_THREADS) void k_pol_final(PolArgs a, int64_t blocks) {
-  __shared__ double sh[POL_THREADS / WAVE];
+  __shared__ double sh[POL_THREADS / WAVE][POL_SUMS];
   double v[POL_SUMS];
 #pragma unroll
   for (int k = 0; k < POL_SUMS; ++k) v[k] = 0.0;
+#pragma unroll 4
   for (int64_t b = threadIdx.x; b < blocks; b += POL_THREADS)
 #pragma unroll
     for (int k = 0; k < POL_SUMS; ++k) v[k] += a.partial[b * 8 + k];
-#pragma unroll
-  for (int k = 0; k < POL_SUMS; ++k) v[k] = block_sum_d<POL_THREADS>(v[k], sh);
+  pol_reduce<POL_THREADS>(v, sh);
   if (threadIdx.x == 0) pol_write(a, v);
 }
 
@@ -244,26 +500,45 @@ __global__ __launch_bounds__(POL_SMALL_THREADS) void k_pol_small(PolArgs a) {
   __shared__ int32_t offs[POL_SMALL_SEQ + 1];
   __shared__ int32_t cnt[POL_SMALL_SEQ];
   __shared__ double sh[POL_SMALL_THREADS / WAVE];
+  __shared__ double sums[POL_SMALL_THREADS / WAVE][POL_SUMS];
   const int n = (int)a.c.n, ns = (int)a.c.n_seq;
   const bool per_seq = a.c.reduction == RECE_MEAN_SEQUENCE;
   for (int i = threadIdx.x; i <= ns; i += POL_SMALL_THREADS) {
     offs[i] = (int32_t)offset_at(a.offs, i, n);
     if (i < ns) cnt[i] = 0;
   }
+  // every value is requested before the first is used
+  PolToken k[PER];
+  bool in[PER];
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int t = q * POL_SMALL_THREADS + (int)threadIdx.x;
+    in[q] = t < n && (!a.mask || a.mask[t < n ? t : 0]);
+    k[q] = PolToken{};
+    if (t < n) {
+      k[q].lp = to_f32(static_cast<const E*>(a.logp)[t]);
+      k[q].old = to_f32(static_cast<const E*>(a.old)[t]);
+      if (a.ref) k[q].ref = to_f32(static_cast<const E*>(a.ref)[t]);
+      if (a.entropy) k[q].H = to_f32(static_cast<const E*>(a.entropy)[t]);
+    }
+  }
   __syncthreads();
   int sq[PER];
+  float A[PER];
   int mine = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int t = q * POL_SMALL_THREADS + (int)threadIdx.x;
     sq[q] = -1;
-    if (t >= offs[0] && t < offs[ns] && (!a.mask || a.mask[t])) {
+    A[q] = 0.0f;
+    if (in[q] && t >= offs[0] && t < offs[ns]) {
       int lo = 0, hi = ns - 1;
       while (lo < hi) {
         const int m = (lo + hi + 1) / 2;
         if (offs[m] <= t) lo = m; else hi = m - 1;
       }
       sq[q] = lo;
+      A[q] = a.adv[a.c.token_adv ? t : lo];
       ++mine;
       if (per_seq) atomicAdd(&cnt[lo], 1);
     }
@@ -276,7 +551,7 @@ __global__ __launch_bounds__(POL_SMALL_THREADS) void k_pol_small(PolArgs a) {
   }
   const float wt = 1.0f / (float)fmax(tokens, 1.0), nonempty = (float)fmax(with, 1.0);
   const float up = a.dloss ? a.dloss[0] : 1.0f;
-  PolSums s{};
+  PolSums s;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int t = q * POL_SMALL_THREADS + (int)threadIdx.x;
@@ -284,14 +559,18 @@ __global__ __launch_bounds__(POL_SMALL_THREADS) void k_pol_small(PolArgs a) {
     float dlp = 0.0f, dent = 0.0f;
     if (sq[q] >= 0) {
       const float w = per_seq ? 1.0f / ((float)cnt[sq[q]] * nonempty) : wt;
-      pol_token<E>(a, t, w, a.adv[a.c.token_adv ? t : sq[q]], s, dlp, dent);
+      const PolTerm o = pol_token(a, k[q], w, A[q]);
+      s.add(o, true);
+      s.flush();
+      dlp = o.dlp;
+      dent = o.dent;
     }
     if (a.dlogp) put(static_cast<E*>(a.dlogp), t, up * dlp);
     if (a.dentropy) put(static_cast<E*>(a.dentropy), t, up * dent);
   }
   double v[POL_SUMS];
-#pragma unroll
-  for (int k = 0; k < POL_SUMS; ++k) v[k] = block_sum_d<POL_SMALL_THREADS>(s.v[k], sh);
+  s.get(v);
+  pol_reduce<POL_SMALL_THREADS>(v, sums);
   if (threadIdx.x == 0) pol_write(a, v);
 }
 
@@ -308,33 +587,110 @@ struct PrefArgs {
   void* dlogp;
 };
 
-// h of sequence i by L lanes (all of them get it).
-template <class E, int L>
-__device__ __forceinline__ double pref_sum(const PrefArgs& a, int64_t i, int sub, float& share) {
-  const int64_t lo = offset_at(a.offs, i, a.c.n), hi = max(lo, offset_at(a.offs, i + 1, a.c.n));
-  const E* lp = static_cast<const E*>(a.logp);
-  const E* rf = static_cast<const E*>(a.ref);
-  double s = 0.0;
-  int c = 0;
-  for (int64_t t = lo + sub; t < hi; t += L) {
-    if (a.mask && !a.mask[t]) continue;
-    s += (double)(rf ? to_f32(lp[t]) - to_f32(rf[t]) : to_f32(lp[t]));
-    ++c;
-  }
-#pragma unroll
-  for (int o = L / 2; o >= 1; o >>= 1) {
-    s += __shfl_xor(s, o);
-    c += __shfl_xor(c, o);
-  }
-  share = a.c.average ? 1.0f / (float)max(c, 1) : 1.0f;
-  return a.c.average ? s / (double)max(c, 1) : s;
+// Tokens [lo, hi) of a sequence; tokens are below 2^31, so a step beyond fits in 32 bits.
+struct PrefSeq {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ PrefSeq pref_seq(const int32_t* offs, int64_t i, int64_t n) {
+  const uint32_t lo = (uint32_t)offset_at(offs, i, n), hi = (uint32_t)offset_at(offs, i + 1, n);
+  return PrefSeq{lo, max(lo, hi)};
 }
 
-// Gradient of sequence i's tokens: v where they count, else 0.
-template <class E, int L>
-__device__ __forceinline__ void pref_grad(const PrefArgs& a, int64_t i, int sub, float v) {
-  const int64_t lo = offset_at(a.offs, i, a.c.n), hi = max(lo, offset_at(a.offs, i + 1, a.c.n));
-  for (int64_t t = lo + sub; t < hi; t += L) put(static_cast<E*>(a.dlogp), t, a.mask && !a.mask[t] ? 0.0f : v);
+// 0x80 in byte e: token t + e lies in the sequence (t in [lo / W * W, hi)).
+template <int W>
+__device__ __forceinline__ uint32_t pref_in(PrefSeq q, uint32_t t) {
+  if constexpr (W == 1) return 0x80u;
+  uint32_t in = 0x80808080u;
+  if (t < q.lo) in &= ~0u << (8 * (q.lo - t));
+  if (q.hi - t < 4) in &= ~0u >> (8 * (4 - (q.hi - t)));
+  return in;
+}
+
+// h of K sequences by L lanes (all of them get them); the K sequences' tokens are requested together.
+template <class E, int L, int W, int K>
+__device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)[K], int sub, double (&s)[K], float (&share)[K]) {
+  const E* lp = static_cast<const E*>(a.logp);
+  const E* rf = static_cast<const E*>(a.ref);
+  const uint32_t n = (uint32_t)a.c.n;
+  int c[K];
+  uint32_t t[K];
+  bool more = false;
+#pragma unroll
+  for (int q = 0; q < K; ++q) {
+    s[q] = 0.0;
+    c[q] = 0;
+    t[q] = seq[q].lo / W * W + sub * W;
+    more |= t[q] < seq[q].hi;
+  }
+  while (more) {
+    float x[K][W], y[K][W];
+    uint32_t on[K];
+#pragma unroll
+    for (int q = 0; q < K; ++q) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) x[q][e] = y[q][e] = 0.0f;
+      on[q] = 0;
+      if (t[q] >= seq[q].hi) continue;
+      if (t[q] + W <= n) {
+        load_tokens<W>(lp, t[q], x[q]);
+        if (rf) load_tokens<W>(rf, t[q], y[q]);
+        on[q] = load_mask<W>(a.mask, t[q]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (t[q] + e < n) {
+            x[q][e] = to_f32(lp[t[q] + e]);
+            if (rf) y[q][e] = to_f32(rf[t[q] + e]);
+            on[q] |= load_mask<1>(a.mask, t[q] + e) << (8 * e);
+          }
+      }
+    }
+    more = false;
+#pragma unroll
+    for (int q = 0; q < K; ++q) {
+      if (t[q] >= seq[q].hi) continue;
+      on[q] &= pref_in<W>(seq[q], t[q]);
+#pragma unroll
+      for (int e = 0; e < W; ++e) s[q] += (double)((on[q] >> (8 * e)) & 0x80u ? x[q][e] - y[q][e] : 0.0f);
+      c[q] += __popc(on[q]);
+      t[q] += L * W;
+      more |= t[q] < seq[q].hi;
+    }
+  }
+#pragma unroll
+  for (int o = L / 2; o >= 1; o >>= 1)
+#pragma unroll
+    for (int q = 0; q < K; ++q) s[q] += __shfl_xor(s[q], o);
+#pragma unroll
+  for (int q = 0; q < K; ++q) {
+    share[q] = 1.0f;
+    if (a.c.average) {
+#pragma unroll
+      for (int o = L / 2; o >= 1; o >>= 1) c[q] += __shfl_xor(c[q], o);
+      share[q] = 1.0f / (float)max(c[q], 1);
+      s[q] /= (double)max(c[q], 1);
+    }
+  }
+}
+
+// Gradient of a sequence's tokens: v where they count, else 0.
+template <class E, int L, int W>
+__device__ __forceinline__ void pref_grad(const PrefArgs& a, PrefSeq seq, int sub, float v) {
+  E* out = static_cast<E*>(a.dlogp);
+  for (uint32_t t = seq.lo / W * W + sub * W; t < seq.hi; t += L * W) {
+    const uint32_t in = pref_in<W>(seq, t);
+    if (W == 1 || in == 0x80808080u) {   // inside the sequence, so inside the array
+      const uint32_t on = load_mask<W>(a.mask, t);
+      float x[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) x[e] = (on >> (8 * e)) & 0x80u ? v : 0.0f;
+      store_tokens<W>(out, t, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if ((in >> (8 * e)) & 0x80u) put(out, t + e, load_mask<1>(a.mask, t + e) ? v : 0.0f);
+    }
+  }
 }
 
 __device__ __forceinline__ double softplus_d(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
@@ -356,27 +712,32 @@ __device__ __forceinline__ double pair_loss(const rece_preference_config& c, dou
 }
 
 constexpr int PREF_LDS = 512;   // sequences of a group whose h lies in LDS
+constexpr int PREF_EXTRA = 1024; // workgroups for what lies in no group
 
-// Workgroups 0 .. n_group - 1: one group each.  The others: the sequences in no group, and
-// the tokens in no sequence.
-template <class E, int L, int NT>
+// The last n_group workgroups: one group each.  Those before: the sequences in no group, and the tokens in no
+// sequence.
+template <class E, int L, int W, int NT>
 __global__ __launch_bounds__(NT) void k_pref(PrefArgs a) {
   constexpr int NS = NT / L;   // sequences at a time
   __shared__ double sh_h[PREF_LDS];
   __shared__ float sh_share[PREF_LDS];
+  __shared__ int32_t sh_offs[PREF_LDS + 1];
   const int64_t G = a.c.n_group, nseq = a.c.n_seq;
   const int q = threadIdx.x / L, sub = threadIdx.x % L;
   const float beta = a.c.beta;
-  if ((int64_t)blockIdx.x >= G) {
+  const int64_t extra = (int64_t)gridDim.x - G;
+  if ((int64_t)blockIdx.x < extra) {
     const int64_t first = offset_at(a.goffs, 0, nseq), end = offset_at(a.goffs, G, nseq);
-    const int64_t extra = (int64_t)gridDim.x - G, b = (int64_t)blockIdx.x - G;
+    const int64_t b = blockIdx.x;
     for (int64_t k = b * NS + q; k < first + (nseq - end); k += extra * NS) {
       const int64_t i = k < first ? k : end + (k - first);
       if (i >= nseq) break;
-      float share;
-      const double h = pref_sum<E, L>(a, i, sub, share);
-      if (sub == 0) a.rewards[i] = (float)((double)beta * h);
-      if (a.dlogp) pref_grad<E, L>(a, i, sub, 0.0f);
+      const PrefSeq seq[1] = {pref_seq(a.offs, i, a.c.n)};
+      double h[1];
+      float share[1];
+      pref_sum<E, L, W, 1>(a, seq, sub, h, share);
+      if (sub == 0) a.rewards[i] = (float)((double)beta * h[0]);
+      if (a.dlogp) pref_grad<E, L, W>(a, seq[0], sub, 0.0f);
     }
     if (a.dlogp) {
       const int64_t lo = offset_at(a.offs, 0, a.c.n), hi = max(lo, offset_at(a.offs, nseq, a.c.n));
@@ -385,78 +746,88 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a) {
     }
     return;
   }
-  const int64_t g = blockIdx.x;
+  const int64_t g = (int64_t)blockIdx.x - extra;
   const int64_t s0 = offset_at(a.goffs, g, nseq), s1 = max(s0, offset_at(a.goffs, g + 1, nseq));
   const int64_t m = s1 - s0;
   const bool in_lds = m <= PREF_LDS;
-  for (int64_t k = q; k < m; k += NS) {
-    float share;
-    const double h = pref_sum<E, L>(a, s0 + k, sub, share);
-    if (sub == 0) {
-      a.rewards[s0 + k] = (float)((double)beta * h);
+  if (in_lds) {
+    for (int64_t k = threadIdx.x; k <= m; k += NT) sh_offs[k] = a.offs[s0 + k];
+    __syncthreads();
+  }
+  auto seq_at = [&](int64_t k) { return in_lds ? pref_seq(sh_offs, k, a.c.n) : pref_seq(a.offs, s0 + k, a.c.n); };
+  for (int64_t k = q; k < m; k += 2 * NS) {
+    const PrefSeq seq[2] = {seq_at(k), k + NS < m ? seq_at(k + NS) : PrefSeq{0, 0}};
+    double h[2];
+    float share[2];
+    pref_sum<E, L, W, 2>(a, seq, sub, h, share);
+    if (sub != 0) continue;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t i = k + u * NS;
+      if (i >= m) break;
+      a.rewards[s0 + i] = (float)((double)beta * h[u]);
       if (in_lds) {
-        sh_h[k] = h;
-        sh_share[k] = share;
+        sh_h[i] = h[u];
+        sh_share[i] = share[u];
       } else {
-        a.h[s0 + k] = h;
-        a.share[s0 + k] = share;
+        a.h[s0 + i] = h[u];
+        a.share[s0 + i] = share[u];
       }
     }
   }
   __syncthreads();
-  auto h_at = [&](int64_t k) { return in_lds ? sh_h[k] : a.h[s0 + k]; };
-  auto share_at = [&](int64_t k) { return in_lds ? sh_share[k] : a.share[s0 + k]; };
-  // every wave takes the group's loss by itself
-  const int l = lane_id();
-  const bool soft = a.c.kind == RECE_PREF_SOFTMAX;
-  double loss = 0.0, dc = 0.0, top = 0.0, tot = 1.0, per = 0.0;
-  if (m >= 2) {
-    const double hc = h_at(0);
-    auto z_of = [&](int64_t k) { return (double)beta * (hc - h_at(k)) - (double)a.c.margin; };
-    per = 1.0 / (double)(m - 1);
-    if (soft) {
-      for (int64_t k = 1 + l; k < m; k += WAVE) top = fmax(top, -z_of(k));
-      top = wave_max_d(top);
-      tot = 0.0;
-      for (int64_t k = 1 + l; k < m; k += WAVE) tot += exp(-z_of(k) - top);
-      const double others = wave_sum_d(tot);
-      tot = others + exp(-top);
-      loss = top + log(tot);
-      dc = -others / tot;
-    } else {
-      for (int64_t k = 1 + l; k < m; k += WAVE) {
-        double dz;
-        loss += pair_loss(a.c, z_of(k), dz);
-        dc += dz;
-      }
-      loss = wave_sum_d(loss) * per;
-      dc = wave_sum_d(dc) * per;
-    }
-  }
-  if (threadIdx.x == 0) a.loss_pg[g] = (float)loss;
-  if (!a.dlogp) return;
-  const double up = (double)beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G;
-  for (int64_t k = q; k < m; k += NS) {
-    double dh = dc;
-    if (k > 0) {
-      const double z = (double)beta * (h_at(0) - h_at(k)) - (double)a.c.margin;
-      if (soft) {
-        dh = exp(-z - top) / tot;
+  // The first wave takes the group's loss, a member per lane, and leaves the derivatives by h where the h were.
+  double* hs = in_lds ? sh_h : a.h + s0;
+  const float* shares = in_lds ? sh_share : a.share + s0;
+  if (threadIdx.x < WAVE) {
+    const int l = lane_id();
+    double loss = 0.0, dc = 0.0;
+    if (m >= 2) {
+      const double hc = hs[0], per = 1.0 / (double)(m - 1);
+      auto z_of = [&](int64_t k) { return (double)beta * (hc - hs[k]) - (double)a.c.margin; };
+      if (a.c.kind == RECE_PREF_SOFTMAX) {
+        double top = 0.0, others = 0.0;
+        for (int64_t k = 1 + l; k < m; k += WAVE) top = fmax(top, -z_of(k));
+        top = wave_max_d(top);
+        for (int64_t k = 1 + l; k < m; k += WAVE) {
+          const double e = exp(-z_of(k) - top);
+          others += e;
+          hs[k] = e;
+        }
+        others = wave_sum_d(others);
+        const double tot = others + exp(-top);
+        for (int64_t k = 1 + l; k < m; k += WAVE) hs[k] = hs[k] / tot;
+        loss = top + log(tot);
+        dc = -others / tot;
       } else {
-        double dz;
-        pair_loss(a.c, z, dz);
-        dh = -dz * per;
+        for (int64_t k = 1 + l; k < m; k += WAVE) {
+          double dz;
+          loss += pair_loss(a.c, z_of(k), dz);
+          dc += dz;
+          hs[k] = -dz * per;
+        }
+        loss = wave_sum_d(loss) * per;
+        dc = wave_sum_d(dc) * per;
       }
     }
-    pref_grad<E, L>(a, s0 + k, sub, (float)(dh * up * (double)share_at(k)));
+    if (l == 0) {
+      a.loss_pg[g] = (float)loss;
+      if (m > 0) hs[0] = dc;
+    }
   }
+  if (!a.dlogp) return;
+  __syncthreads();
+  const double up = (double)beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G;
+  for (int64_t k = q; k < m; k += NS) pref_grad<E, L, W>(a, seq_at(k), sub, (float)(hs[k] * up * (double)shares[k]));
 }
 
-__global__ __launch_bounds__(256) void k_pref_mean(PrefArgs a) {
-  __shared__ double sh[256 / WAVE];
+constexpr int PREF_MEAN_THREADS = 1024;
+__global__ __launch_bounds__(PREF_MEAN_THREADS) void k_pref_mean(PrefArgs a) {
+  __shared__ double sh[PREF_MEAN_THREADS / WAVE];
   double v = 0.0;
-  for (int64_t g = threadIdx.x; g < a.c.n_group; g += 256) v += a.loss_pg[g];
-  v = block_sum_d<256>(v, sh);
+#pragma unroll 4
+  for (int64_t g = threadIdx.x; g < a.c.n_group; g += PREF_MEAN_THREADS) v += a.loss_pg[g];
+  v = block_sum_d<PREF_MEAN_THREADS>(v, sh);
   if (threadIdx.x == 0) a.loss[0] = (float)(v / (double)a.c.n_group);
 }
 
@@ -473,50 +844,61 @@ hipError_t policy_t(PolArgs& a, void* ws, hipStream_t st) {
   const int64_t blocks = pol_blocks(c.n);
   const bool per_seq = c.reduction == RECE_MEAN_SEQUENCE;
   a.partial = static_cast<double*>(ws);
-  if (per_seq || a.mask) {   // else the number of tokens is known from the offsets
-    a.head = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align256((size_t)blocks * 64));
-    a.cnt = a.head + 2;
-    const int64_t words = 2 + (per_seq ? c.n_seq : 0);
-    hipLaunchKernelGGL(k_pol_clear, dim3((unsigned)((words + POL_THREADS - 1) / POL_THREADS)), dim3(POL_THREADS), 0, st,
-                       a.head, words);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_pol_count, dim3((unsigned)blocks), dim3(POL_THREADS), 0, st, a);
+  a.part = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align256((size_t)blocks * 64));
+  a.cnt = a.part + 2 * POL_COUNTERS;
+  a.counters = per_seq || a.mask ? (int)std::min<int64_t>(blocks, POL_COUNTERS) : 0;
+  hipError_t e;
+  if (per_seq) {
+    hipLaunchKernelGGL(k_pol_clear, dim3((unsigned)((c.n_seq + POL_THREADS - 1) / POL_THREADS)), dim3(POL_THREADS), 0, st,
+                       a.cnt, c.n_seq);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_pol_main<E>, dim3((unsigned)blocks), dim3(POL_THREADS), 0, st, a);
-  const hipError_t e = hipGetLastError();
+  if (a.counters) {
+    hipLaunchKernelGGL(k_pol_count, dim3((unsigned)a.counters), dim3(POL_THREADS), 0, st, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // four tokens at a time where every array allows it (slices of a longer batch may not)
+  uintptr_t tok = 0;
+  for (const void* p : {a.logp, a.old, a.ref, a.entropy, static_cast<const void*>(a.dlogp), static_cast<const void*>(a.dentropy)})
+    tok |= reinterpret_cast<uintptr_t>(p);
+  const bool wide = tok % (4 * sizeof(E)) == 0 && reinterpret_cast<uintptr_t>(a.mask) % 4 == 0;
+  auto kern = wide ? k_pol_main<E, 4> : k_pol_main<E, 1>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(POL_THREADS), 0, st, a);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_pol_final, dim3(1), dim3(POL_THREADS), 0, st, a, blocks);
   return hipGetLastError();
 }
 
-template <class E, int L, int NT>
+template <class E, int L, int W, int NT>
 hipError_t pref_launch(const PrefArgs& a, hipStream_t st) {
-  const int64_t extra = std::min<int64_t>((a.c.n_seq + NT / L - 1) / (NT / L), 1024);
-  hipLaunchKernelGGL((k_pref<E, L, NT>), dim3((unsigned)(a.c.n_group + extra)), dim3(NT), 0, st, a);
+  const int64_t extra = std::min<int64_t>((a.c.n_seq + NT / L - 1) / (NT / L), PREF_EXTRA);
+  hipLaunchKernelGGL((k_pref<E, L, W, NT>), dim3((unsigned)(a.c.n_group + extra)), dim3(NT), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_pref_mean, dim3(1), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_pref_mean, dim3(1), dim3(PREF_MEAN_THREADS), 0, st, a);
   return hipGetLastError();
 }
 
 template <class E>
 hipError_t preference_t(const PrefArgs& a, hipStream_t st) {
   const int64_t len = a.c.n / a.c.n_seq, group = a.c.n / a.c.n_group;
-  if (len >= 32) return pref_launch<E, 64, 256>(a, st);
-  if (len >= 4 && group >= 256) return pref_launch<E, 8, 256>(a, st);
-  if (len >= 4) return pref_launch<E, 8, 64>(a, st);
-  return pref_launch<E, 1, 64>(a, st);
+  const uintptr_t tok = reinterpret_cast<uintptr_t>(a.logp) | reinterpret_cast<uintptr_t>(a.ref) | reinterpret_cast<uintptr_t>(a.dlogp);
+  const bool wide = tok % (4 * sizeof(E)) == 0 && reinterpret_cast<uintptr_t>(a.mask) % 4 == 0;
+  if (len >= 64) return wide ? pref_launch<E, 64, 4, 256>(a, st) : pref_launch<E, 64, 1, 256>(a, st);
+  if (len < 4) return pref_launch<E, 1, 1, 64>(a, st);
+  if (group >= 256) return wide ? pref_launch<E, 8, 4, 256>(a, st) : pref_launch<E, 8, 1, 256>(a, st);
+  return wide ? pref_launch<E, 8, 4, 64>(a, st) : pref_launch<E, 8, 1, 64>(a, st);
 }
 
 }  // namespace
 
 size_t policy_workspace_bytes(const rece_policy_config& c) {
   if (c.n <= POL_SMALL_N && c.n_seq <= POL_SMALL_SEQ) return 16;
-  return align256((size_t)pol_blocks(c.n) * 64) +
-         align256((size_t)(2 + (c.reduction == RECE_MEAN_SEQUENCE ? c.n_seq : 0)) * 4);
+  return align256((size_t)pol_blocks(c.n) * 64) + (size_t)POL_COUNTERS * 8 +
+         align256((size_t)(c.reduction == RECE_MEAN_SEQUENCE ? c.n_seq : 0) * 4);
 }
 
 hipError_t policy_loss(const rece_policy_config& c, const void* logp, const void* old, const void* ref,
@@ -541,6 +923,7 @@ hipError_t policy_loss(const rece_policy_config& c, const void* logp, const void
 }
 
 size_t preference_workspace_bytes(const rece_preference_config& c) {
+  if (c.n_seq <= PREF_LDS) return 16;   // every group's values fit into LDS
   return align256((size_t)c.n_seq * 8) + align256((size_t)c.n_seq * 4);
 }
 

@@ -4,6 +4,7 @@
 // `per` units, one workgroup g each, so every workgroup does the same work whatever the number of
 // owner blocks; a run may end inside an owner block.  Workgroup g's part of block b lies in slot b + g
 // (the pairs that occur form a staircase, so the slots are distinct and at most blocks + workgroups).
+// With `whole`, the runs are rounded up to whole owner blocks: block b has one part, in slot b.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -19,6 +20,9 @@ __device__ __forceinline__ uint64_t div_u64(uint64_t a, uint64_t b) {
 struct SweepWork {
   uint32_t nb, nt;   // owner blocks, tiles
   uint64_t total, per;
+  bool whole;
+  // where workgroup g's part of block b lies
+  __device__ __forceinline__ int64_t slot(int64_t b, int64_t g) const { return whole ? b : b + g; }
   // workgroups that hold parts of block b (first > last: none)
   __device__ __forceinline__ int64_t first(uint64_t b) const { return nt == 0 ? 1 : (int64_t)div_u64(b * nt, per); }
   __device__ __forceinline__ int64_t last(uint64_t b) const { return nt == 0 ? 0 : (int64_t)div_u64((b + 1) * nt - 1, per); }
@@ -31,6 +35,7 @@ struct SweepParts {
   uint32_t block, tile;   // owners of a block, rows of a tile
   uint32_t grid;          // workgroups
   int nws;                // parts of a workgroup (waves along a tile)
+  int whole;              // whole owner blocks per workgroup
   const float* rows;      // [slots][nws][block][d] partial rows
   __device__ __forceinline__ uint32_t owners() const { return own_is_pos ? (uint32_t)*nv : (uint32_t)n_own; }
   __device__ __forceinline__ uint32_t streamed() const { return own_is_pos ? (uint32_t)n_str : (uint32_t)*nv; }
@@ -39,8 +44,9 @@ struct SweepParts {
     w.nb = (uint32_t)div_u64((uint64_t)owners() + block - 1, block);
     w.nt = (uint32_t)div_u64((uint64_t)streamed() + tile - 1, tile);
     w.total = (uint64_t)w.nb * w.nt;
-    w.per = div_u64(w.total + grid - 1, grid);
+    w.per = whole ? (uint64_t)div_u64((uint64_t)w.nb + grid - 1, grid) * w.nt : div_u64(w.total + grid - 1, grid);
     if (w.per == 0) w.per = 1;
+    w.whole = whole != 0;
     return w;
   }
   // f(index of a partial result) for every part of row r, in order; results are indexed [slots][nws][block].
@@ -49,7 +55,7 @@ struct SweepParts {
     const uint32_t b = (uint32_t)r / block, at = (uint32_t)r % block;
     const int64_t g0 = w.first(b), g1 = w.last(b);
 #pragma unroll 4
-    for (int64_t q = g0 * nws; q < (g1 + 1) * nws; ++q) f(((int64_t)b * nws + q) * block + at);
+    for (int64_t q = w.slot(b, g0) * nws; q < (w.slot(b, g1) + 1) * nws && g0 <= g1; ++q) f(q * block + at);
   }
 };
 

@@ -40,16 +40,17 @@ def _dtype(name: str):
 
 def _want(name, t, dtype, shape, device=None):
     """Check one tensor argument: dtype, shape, contiguity, device."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
 
 
 def _workspace(workspace, nbytes, device):
+    """The caller's workspace, or a new one."""
     import torch
     if workspace is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if (workspace.device != device or workspace.numel() * workspace.element_size() < nbytes
             or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous buffer of at least {nbytes} bytes on {device}")
@@ -59,13 +60,14 @@ def _workspace(workspace, nbytes, device):
 def _call(fn, device, stream, before, after=()):
     """fn(*before, stream, *after) with `device` current, on `stream` or the device's current one."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        s = torch.cuda.current_stream() if stream is None else stream
-        _check(fn(*before, s.cuda_stream, *after))
+    index = device.index
+    # the handle itself: torch.cuda.current_stream() makes an object around it, a third of a small call's time
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        _check(fn(*before, s, *after))
         return
     with torch.cuda.device(device):
-        s = torch.cuda.current_stream() if stream is None else stream
-        _check(fn(*before, s.cuda_stream, *after))
+        _check(fn(*before, s, *after))
 
 
 class ItemEmbedding:
@@ -218,8 +220,8 @@ class PolicyLoss:
         if dloss is not None:
             _want("dloss", dloss, torch.float32, (1,), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev)
-        out = torch.empty(7, dtype=torch.float32, device=dev)
-        loss, stats = out[:1], out[1:]
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        stats = torch.empty(6, dtype=torch.float32, device=dev)
         dlogp = torch.empty(n, dtype=self._dt, device=dev) if grads else None
         dent = torch.empty(n, dtype=self._dt, device=dev) if grads and entropy is not None else None
         _call(lib().rece_policy_loss, dev, stream, (ctypes.byref(c),),
