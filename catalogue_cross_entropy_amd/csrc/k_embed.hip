@@ -136,7 +136,7 @@ __device__ __forceinline__ int order_key(const OrderArgs& a, int64_t t, int64_t 
   return k < a.C ? k : -1;
 }
 
-template <bool FIRST>
+template <bool FIRST, int PER>
 __global__ __launch_bounds__(ORD_THREADS) void k_order_hist(OrderArgs a) {
   __shared__ uint32_t hist[ORD_BINS];
   const int tid = threadIdx.x, tile = blockIdx.x;
@@ -146,12 +146,12 @@ __global__ __launch_bounds__(ORD_THREADS) void k_order_hist(OrderArgs a) {
   }
   const int64_t n = FIRST ? a.n : (int64_t)*a.ntot;
   hist[tid] = 0u;
-  int key[ORD_TILE / ORD_THREADS];
+  int key[PER];
 #pragma unroll
-  for (int u = 0; u < ORD_TILE / ORD_THREADS; ++u) key[u] = order_key<FIRST>(a, (int64_t)tile * ORD_TILE + u * ORD_THREADS + tid, n);
+  for (int u = 0; u < PER; ++u) key[u] = order_key<FIRST>(a, (int64_t)tile * (PER * ORD_THREADS) + u * ORD_THREADS + tid, n);
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < ORD_TILE / ORD_THREADS; ++u) {
+  for (int u = 0; u < PER; ++u) {
     // one add for a wave of equal digits (popular ids after the first pass); others one by one
     const int dig = key[u] >= 0 ? (int)((uint32_t)key[u] >> a.shift & ((1u << a.bits) - 1u)) : -1;
     const int first = __builtin_amdgcn_readfirstlane(dig);
@@ -182,16 +182,17 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sh, uint3
   return pre + incl - v;
 }
 
-// Ranks 4 x 64 consecutive records per wave among the tile's records with the same digit: cnt[wave][digit]
+// Ranks PER x 64 consecutive records per wave among the tile's records with the same digit: cnt[wave][digit]
 // becomes the number in earlier waves, at[q] the number in the wave before record q.
-__device__ __forceinline__ void order_rank(uint16_t (*cnt)[ORD_BINS], const int (&dig)[4], int bits, uint32_t (&at)[4],
+template <int PER>
+__device__ __forceinline__ void order_rank(uint16_t (*cnt)[ORD_BINS], const int (&dig)[PER], int bits, uint32_t (&at)[PER],
                                            uint32_t* tot) {
   const int tid = threadIdx.x, w = tid / WAVE;
 #pragma unroll
   for (int q = 0; q < ORD_THREADS / WAVE; ++q) cnt[q][tid] = 0;
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < PER; ++q) {
     const bool on = dig[q] >= 0;
     uint64_t same = ballot(on);
     for (int bit = 0; bit < bits; ++bit) {
@@ -217,7 +218,7 @@ __device__ __forceinline__ void order_rank(uint16_t (*cnt)[ORD_BINS], const int 
   *tot = run;   // of digit tid
 }
 
-template <bool FIRST>
+template <bool FIRST, int PER>
 __global__ __launch_bounds__(ORD_THREADS) void k_order_scatter(OrderArgs a) {
   __shared__ uint16_t cnt[ORD_THREADS / WAVE][ORD_BINS];
   __shared__ uint32_t start[ORD_BINS];
@@ -228,10 +229,10 @@ __global__ __launch_bounds__(ORD_THREADS) void k_order_scatter(OrderArgs a) {
     return;
   }
   const int64_t n = FIRST ? a.n : (int64_t)*a.ntot;
-  int key[4], val[4], dig[4];
+  int key[PER], val[PER], dig[PER];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t t = (int64_t)tile * ORD_TILE + (w * 4 + q) * WAVE + l;
+  for (int q = 0; q < PER; ++q) {
+    const int64_t t = (int64_t)tile * (PER * ORD_THREADS) + (w * PER + q) * WAVE + l;
     key[q] = order_key<FIRST>(a, t, n);
     val[q] = FIRST ? (int)t : (t < n ? a.vin[t] : 0);
   }
@@ -243,15 +244,15 @@ __global__ __launch_bounds__(ORD_THREADS) void k_order_scatter(OrderArgs a) {
     all += c;
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < PER; ++q)
     dig[q] = key[q] >= 0 ? (int)((uint32_t)key[q] >> a.shift & ((1u << a.bits) - 1u)) : -1;
-  uint32_t total, at[4], in_tile;
+  uint32_t total, at[PER], in_tile;
   start[tid] = block_prefix(all, sh, &total) + before;
   if (FIRST && tile == 0 && tid == 0) *a.ntot = total;
   order_rank(cnt, dig, a.bits, at, &in_tile);
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < PER; ++q) {
     if (dig[q] < 0) continue;
     const uint32_t slot = start[dig[q]] + cnt[w][dig[q]] + at[q];
     a.kout[slot] = key[q];
@@ -448,10 +449,12 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_join(EmbGrad a) {
   if (t1 >= n) return;
   const int j = a.K[t1 - 1];
   if (a.K[t1] != j || (t0 > 0 && a.K[t0] == j && a.K[t0 - 1] == j)) return;
-  int64_t lo = t1, hi = n;   // first record beyond the run is in (lo, hi]
+  int64_t lo = t1, hi = n;   // first record beyond the run is in (lo, hi]; a wave probes 64 places at a time
   while (hi - lo > 1) {
-    const int64_t m = (lo + hi) / 2;
-    if (a.K[m] == j) lo = m; else hi = m;
+    const int64_t step = (hi - lo + WAVE) / (WAVE + 1), m = lo + step * (lane_id() + 1);
+    const int hits = popc(ballot(m < hi && a.K[m < hi ? m : lo] == j));   // sorted: the first lanes
+    hi = min(hi, lo + step * (hits + 1));
+    lo += step * hits;
   }
   const int64_t last = lo / EMB_PIECE;
   const int g = threadIdx.x / LPR, sub = threadIdx.x % LPR;
@@ -552,7 +555,16 @@ int key_bits(int64_t C) {
   return b;
 }
 int order_passes(int64_t C) { return (key_bits(C) + ORD_BITS - 1) / ORD_BITS; }
-int64_t order_tiles(int64_t n) { return (n + ORD_TILE - 1) / ORD_TILE; }
+// Records per thread of the sort's tiles: as few as 64 tiles allow, so that many CUs rank (51,200 records, both
+// digits: one per thread 23 us, two 25, four 31).
+int order_per(int64_t n) {
+  if (n <= ORD_TILE) return ORD_TILE / ORD_THREADS;   // one workgroup
+  return n <= ORD_TILES * ORD_THREADS ? 1 : n <= 2 * ORD_TILES * ORD_THREADS ? 2 : ORD_TILE / ORD_THREADS;
+}
+int64_t order_tiles(int64_t n) {
+  const int64_t tile = (int64_t)order_per(n) * ORD_THREADS;
+  return (n + tile - 1) / tile;
+}
 
 // Scratch of the sort: the count matrices and the number of records, or the library's pair sort's.
 size_t order_bytes(int64_t n, int64_t C) {
@@ -579,7 +591,7 @@ hipError_t order_rows(const int32_t* ids, int64_t n, int64_t C, const ClearArgs&
     return launch_pair_sort(pair_sort_geom(n, C), ids, 0, 1, n, ids, C, scratch, buf[0], buf[1], buf[2], buf[3], &g.K,
                             &g.V, &g.ntot, st);
   }
-  const int kb = key_bits(C), passes = order_passes(C);
+  const int kb = key_bits(C), passes = order_passes(C), per = order_per(n);
   uint32_t* counts = static_cast<uint32_t*>(scratch);
   OrderArgs a{};
   a.ids = ids;
@@ -612,8 +624,11 @@ hipError_t order_rows(const int32_t* ids, int64_t n, int64_t C, const ClearArgs&
     a.vout = buf[2 * (p & 1) + 1];
     for (int half = 0; half < 2; ++half) {
       a.part = 2 * p + half;
-      auto kern = half == 0 ? (p == 0 ? k_order_hist<true> : k_order_hist<false>)
-                            : (p == 0 ? k_order_scatter<true> : k_order_scatter<false>);
+#define ORD_KERNEL(P)                                                         \
+  (half == 0 ? (p == 0 ? k_order_hist<true, P> : k_order_hist<false, P>)      \
+             : (p == 0 ? k_order_scatter<true, P> : k_order_scatter<false, P>))
+      auto kern = per == 1 ? ORD_KERNEL(1) : per == 2 ? ORD_KERNEL(2) : ORD_KERNEL(4);
+#undef ORD_KERNEL
       hipLaunchKernelGGL(kern, grid, dim3(ORD_THREADS), 0, st, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;

@@ -60,7 +60,7 @@ struct LpArgs {
   const void* str;        // streamed vectors [n_str][D]
   SweepParts parts;       // sizes, workgroups, and where parts lie
   float c2;               // log2(e) / temperature
-  float *m, *z, *t;       // LP_LSE(O): parts of the reference, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m)
+  float4* stat;           // LP_LSE(O): parts (reference m, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m), 0)
   const LpRow* rows;      // LP_DX, LP_DY: of the packed positions
   const int32_t* idc;     // ids of the packed positions
   float* out;             // LP_LSEO, LP_DX, LP_DY: parts.rows
@@ -490,9 +490,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
         // the two lane halves hold different rows of the same owner, against one reference
         const float zz = z[ob] + __shfl_xor(z[ob], 32), t0 = tt[ob] + __shfl_xor(tt[ob], 32);
         if (hh == 0) {
-          a.m[part + 32 * ob + rr] = m[ob];
-          a.z[part + 32 * ob + rr] = zz;
-          if constexpr (ENT) a.t[part + 32 * ob + rr] = t0;
+          a.stat[part + 32 * ob + rr] = float4{m[ob], zz, ENT ? t0 : 0.0f, 0.0f};
         }
       }
     }
@@ -516,7 +514,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
 // logit of each row's own item, the diagonal of a 32 x 32 product, so that it has the
 // same bits as in the sweeps.  The last workgroup fills the padding with zero rows.
 constexpr int PACK_THREADS = 256;
-constexpr int64_t PACK_BLOCKS = 256;
+constexpr int64_t PACK_BLOCKS = 256, PACK_LEAST = 64;   // workgroups at most, ids of each at least
 
 template <class E, int D>
 __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ X, const E* __restrict__ Y,
@@ -610,14 +608,14 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
 }
 
 // ------------------------------------------------------------------ joins
-// L lanes per position: the parts of its sum -> log-sum-exp, log-probability, entropy.
+// L lanes per position (1, a wave, a workgroup): the parts of its sum -> log-sum-exp, log-probability, entropy.
+constexpr int FINISH_WIDE = 1024;
 template <int L>
-__global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ inv, int64_t s, SweepParts parts,
-                                                   const float* __restrict__ m, const float* __restrict__ z,
-                                                   const float* __restrict__ t, const float* __restrict__ own, float c2,
-                                                   float* __restrict__ lse2, float* __restrict__ ent_c,
-                                                   float* __restrict__ logp, float* __restrict__ entropy) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+__global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
+    const int32_t* __restrict__ inv, int64_t s, SweepParts parts, const float4* __restrict__ stat, const float* __restrict__ own, float c2, float* __restrict__ lse2, float* __restrict__ ent_c,
+    float* __restrict__ logp, float* __restrict__ entropy) {
+  constexpr int NT = L > WAVE ? L : 256, UNR = 4;
+  const int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) / L;
   const int l = threadIdx.x % L;
   if (i >= s) return;
   const int64_t r = inv[i];
@@ -632,21 +630,47 @@ __global__ __launch_bounds__(256) void k_lp_finish(const int32_t* __restrict__ i
   const uint32_t b = (uint32_t)r / parts.block, in = (uint32_t)r % parts.block;
   const int64_t p0 = w.slot(b, w.first(b)) * parts.nws, p1 = (w.slot(b, w.last(b)) + 1) * parts.nws;
   float mm = NEG_INF, zz = 0.0f, tt = 0.0f;
-  for (int64_t p = p0 + l; p < p1; p += L) {
-    const int64_t at = p * parts.block + in;
-    const float mp = m[at], zp = z[at], tp = entropy ? t[at] : 0.0f;
+  auto add = [&](float mp, float zp, float tp) {   // mp = NEG_INF: nothing
     const float mn = fmaxf(mm, mp);
-    const float f0 = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn), f1 = exp2_fast(mp - mn);
-    tt = (mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f0) + (tp + zp * (mp - mn)) * f1;
+    const float f0 = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn), f1 = mp == NEG_INF ? 0.0f : exp2_fast(mp - mn);
+    tt = (mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f0) + (mp == NEG_INF ? 0.0f : (tp + zp * (mp - mn)) * f1);
     zz = zz * f0 + zp * f1;
     mm = mn;
+  };
+  for (int64_t p = p0 + l; p < p1; p += UNR * L) {
+    float4 x[UNR];
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      x[u] = stat[min(p + u * L, p1 - 1) * parts.block + in];
+    }
+#pragma unroll
+    for (int u = 0; u < UNR; ++u)
+      if (p + u * L < p1) add(x[u].x, x[u].y, x[u].z);
   }
   if constexpr (L > 1) {
-    const float mn = wave_max(mm);
-    const float f = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn);
-    tt = wave_sumf(mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f);
-    zz = wave_sumf(zz * f);
-    mm = mn;
+    auto join = [&]() {
+      const float mn = wave_max(mm);
+      const float f = mm == NEG_INF ? 0.0f : exp2_fast(mm - mn);
+      tt = wave_sumf(mm == NEG_INF ? 0.0f : (tt + zz * (mm - mn)) * f);
+      zz = wave_sumf(zz * f);
+      mm = mn;
+    };
+    join();
+    if constexpr (L > WAVE) {
+      __shared__ float sm[L / WAVE], sz[L / WAVE], st[L / WAVE];
+      if (lane_id() == 0) {
+        sm[l / WAVE] = mm;
+        sz[l / WAVE] = zz;
+        st[l / WAVE] = tt;
+      }
+      __syncthreads();
+      if (l >= WAVE) return;
+      const bool one = l < L / WAVE;
+      mm = one ? sm[l] : NEG_INF;
+      zz = one ? sz[l] : 0.0f;
+      tt = one ? st[l] : 0.0f;
+      join();
+    }
     if (l != 0) return;
   }
   const float lz = log2f(zz), l2 = mm + lz;
@@ -693,31 +717,56 @@ __device__ __forceinline__ void put4(void* out, int64_t at, float4 v, bool b16) 
   }
 }
 
-// out row = sum of the parts' rows, in order.  inv (dX): the row of the parts for each output row (or -1: zeros),
+// d / 4 lanes hold a row's columns, `groups` of those share its parts: 1, or a wave's worth (256 / d, at least 1)
+// where a row has 16 parts or more, so that many loads are in flight.  (256 positions, 33 parts of 64 floats each:
+// 12 -> 5 us with 4 groups; 51,200 positions, 3 to 4 parts: 14 -> 35 us.)  Sums in a fixed order.
+struct JoinLane {
+  int64_t row;
+  int col, group, groups;
+  __device__ __forceinline__ JoinLane(int d, int n) : groups(n) {
+    const int per = d / 4, rest = (int)threadIdx.x % per;
+    const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / per;
+    row = unit / groups;
+    group = (int)(unit % groups);
+    col = rest * 4;
+  }
+  // the groups' sums, in every lane
+  __device__ __forceinline__ void sum(float4& v, int d) const {
+    for (int o = d / 4; o < d / 4 * groups; o *= 2)
+      v = float4{v.x + __shfl_xor(v.x, o), v.y + __shfl_xor(v.y, o), v.z + __shfl_xor(v.z, o), v.w + __shfl_xor(v.w, o)};
+  }
+};
+int join_groups(const SweepParts& p, int d) {
+  const int64_t nb = (p.n_own + p.block - 1) / p.block;
+  return !p.whole && (int64_t)p.grid * p.nws >= 16 * nb ? std::max(1, 256 / d) : 1;
+}
+unsigned join_grid(int64_t n, int d, int groups) { return (unsigned)((n * (d / 4) * groups + 255) / 256); }
+
+// out row = sum of the parts' rows.  inv (dX): the row of the parts for each output row (or -1: zeros),
 // whose own item's row of Y is added g times.
 template <class E>
-__global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, const int32_t* __restrict__ inv,
+__global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, int groups, const int32_t* __restrict__ inv,
                                                  const LpRow* __restrict__ rows, const int32_t* __restrict__ idc,
                                                  const E* __restrict__ Y, int64_t n, void* __restrict__ out, int b16) {
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per = d / 4;
-  if (q >= n * per) return;
-  const int64_t i = q / per;
-  const int c = (int)(q % per) * 4;
+  const JoinLane q(d, groups);
+  if (q.row >= n) return;   // a row's lanes together
+  const int64_t i = q.row;
+  const int c = q.col;
   const int64_t r = inv ? inv[i] : i;
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
     parts.each(parts.work(), r, [&](int64_t at) {
       const float4 w = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       v = float4{v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w};
-    });
+    }, q.group, q.groups);
+    q.sum(v, d);
     if (inv) {
       const float g = rows[r].g;
       const E* y = Y + (int64_t)idc[r] * d + c;
       v = float4{fmaf(g, to_f32(y[0]), v.x), fmaf(g, to_f32(y[1]), v.y), fmaf(g, to_f32(y[2]), v.z), fmaf(g, to_f32(y[3]), v.w)};
     }
   }
-  put4(out, i * d + c, v, b16 != 0);
+  if (q.group == 0) put4(out, i * d + c, v, b16 != 0);
 }
 
 // dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j:
@@ -725,16 +774,15 @@ __global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, const 
 // with the own item's share of the sum taken out and 1 - p_own in its place, so that nothing is lost where
 // p_own is near 1.
 template <class E>
-__global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float* __restrict__ m, int d,
+__global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float4* __restrict__ stat, int d, int groups,
                                                const int32_t* __restrict__ inv, int64_t s, const E* __restrict__ Y,
                                                const int32_t* __restrict__ idc, const float* __restrict__ own, float c2,
                                                const float* __restrict__ lse2, const float* __restrict__ dlogp,
                                                float inv_t, int terms, void* __restrict__ out, int b16) {
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per = d / 4;
-  if (q >= s * per) return;
-  const int64_t i = q / per;
-  const int c = (int)(q % per) * 4;
+  const JoinLane q(d, groups);
+  if (q.row >= s) return;   // a row's lanes together
+  const int64_t i = q.row;
+  const int c = q.col;
   const int64_t r = inv[i];
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
@@ -748,18 +796,19 @@ __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float* __
     const int64_t g_own = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
     const int64_t home = (w.slot(b, g_own) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + (uint32_t)r % parts.block;
     parts.each(w, r, [&](int64_t at) {
-      const float mp = m[at], f = exp2_fast(mp - l2);
+      const float mp = stat[at].x, f = exp2_fast(mp - l2);
       float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       if (at == home) {
         const float e = lp_taken(exp2_fast(fmaf(o, c2, -mp)), terms, sizeof(E) == 2);
         x = float4{fmaf(-e, y.x, x.x), fmaf(-e, y.y, x.y), fmaf(-e, y.z, x.z), fmaf(-e, y.w, x.w)};
       }
       v = float4{fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w)};
-    });
+    }, q.group, q.groups);
+    q.sum(v, d);
     const float rest = -expm1f(fmaf(o, c2, -l2) * LN2);
     v = float4{g * fmaf(rest, y.x, -v.x), g * fmaf(rest, y.y, -v.y), g * fmaf(rest, y.z, -v.z), g * fmaf(rest, y.w, -v.w)};
   }
-  put4(out, i * d + c, v, b16 != 0);
+  if (q.group == 0) put4(out, i * d + c, v, b16 != 0);
 }
 
 // ------------------------------------------------------------------ host side
@@ -812,7 +861,7 @@ LpSweep lp_shape(int mode, int64_t n_own, int64_t n_str) {
 
 struct LpLayout {
   int64_t pad;
-  size_t nv, list, inv, idc, own, lse2, ent, rows, xc, m, z, t, o, dx, sums, bytes;
+  size_t nv, list, inv, idc, own, lse2, ent, rows, xc, stat, o, dx, sums, bytes;
 };
 
 template <class E, int D>
@@ -839,14 +888,11 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   const LpSweep f = lp_shape<E, D>(fused ? LP_LSEO : LP_LSE, s, C);
   const size_t parts = (size_t)f.slots(s) * f.block() * 4;
   size_t base = off;
-  y.m = take(parts);
+  y.stat = take(parts * 4);
   if (fused) {
     y.o = take(parts * D);
     base = off;
   }
-  // what one call alone uses: the forward pass's parts, the backward pass's rows and parts
-  y.z = take(parts);
-  y.t = take(ent ? parts : 0);
   const size_t fwd = off;
   off = base;
   if (grad) {
@@ -924,7 +970,7 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
                         const int32_t* ids, void* ws, float* logp, float* entropy, hipStream_t st) {
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
   const float c2 = LOG2E / temperature;
-  const int64_t per = std::max<int64_t>(PACK_THREADS, ceil_div(s, PACK_BLOCKS));
+  const int64_t per = std::max<int64_t>(PACK_LEAST, ceil_div(s, PACK_BLOCKS));
   hipLaunchKernelGGL((k_lp_pack<E, D>), dim3((unsigned)ceil_div(s, per)), dim3(PACK_THREADS), 0, st,
                      static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad, at<int32_t>(ws, y.nv),
                      at<int32_t>(ws, y.list), at<int32_t>(ws, y.inv), at<E>(ws, y.xc), at<int32_t>(ws, y.idc),
@@ -936,9 +982,7 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
   a.str = Y;
   a.parts = lp_parts<E, D>(fused ? LP_LSEO : LP_LSE, s, C, at<int32_t>(ws, y.nv), nullptr);
   a.c2 = c2;
-  a.m = at<float>(ws, y.m);
-  a.z = at<float>(ws, y.z);
-  a.t = at<float>(ws, y.t);
+  a.stat = at<float4>(ws, y.stat);
   a.out = at<float>(ws, y.o);
   a.terms = lp_terms<E>(flags);
   if (fused)
@@ -947,11 +991,11 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
     LP_TRY((lp_launch<E, D, LP_LSE, true>(a, st)));
   else
     LP_TRY((lp_launch<E, D, LP_LSE, false>(a, st)));
-  // few positions have many parts each: a wave for each; many have few
-  const int lanes = s <= 8192 ? WAVE : 1;
-  auto finish = lanes == WAVE ? k_lp_finish<WAVE> : k_lp_finish<1>;
-  hipLaunchKernelGGL(finish, dim3((unsigned)ceil_div(s * lanes, 256)), dim3(256), 0, st, at<int32_t>(ws, y.inv), s,
-                     a.parts, a.m, a.z, a.t, at<float>(ws, y.own), c2, at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
+  // few positions have many parts each: a workgroup for each while the card holds them at once, or a wave; many have few
+  const int lanes = s <= LP_CUS ? FINISH_WIDE : s <= 8192 ? WAVE : 1, threads = std::max(256, lanes);
+  auto finish = lanes == FINISH_WIDE ? k_lp_finish<FINISH_WIDE> : lanes == WAVE ? k_lp_finish<WAVE> : k_lp_finish<1>;
+  hipLaunchKernelGGL(finish, dim3((unsigned)ceil_div(s * lanes, threads)), dim3(threads), 0, st, at<int32_t>(ws, y.inv), s,
+                     a.parts, a.stat, at<float>(ws, y.own), c2, at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
                      entropy);
   return hipGetLastError();
 }
@@ -974,7 +1018,8 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
   a.terms = terms;
   a.idc = at<int32_t>(ws, y.idc);
   auto join = [&](const int32_t* inv, int64_t n, void* out) {
-    hipLaunchKernelGGL((k_lp_join<E>), dim3((unsigned)ceil_div(n * (D / 4), 256)), dim3(256), 0, st, a.parts, D, inv,
+    const int groups = join_groups(a.parts, D);
+    hipLaunchKernelGGL((k_lp_join<E>), dim3(join_grid(n, D, groups)), dim3(256), 0, st, a.parts, D, groups, inv,
                        a.rows, a.idc, static_cast<const E*>(Y), n, out, b16);
     return hipGetLastError();
   };
@@ -989,8 +1034,10 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
       LP_TRY((lp_launch<E, D, LP_DX, false>(a, st)));
     LP_TRY(join(at<int32_t>(ws, y.inv), s, dX));
   } else {
-    hipLaunchKernelGGL((k_lp_dx<E>), dim3((unsigned)ceil_div(s * (D / 4), 256)), dim3(256), 0, st,
-                       lp_parts<E, D>(LP_LSEO, s, C, nv, at<float>(ws, y.o)), at<float>(ws, y.m), D,
+    const SweepParts sums = lp_parts<E, D>(LP_LSEO, s, C, nv, at<float>(ws, y.o));
+    const int groups = join_groups(sums, D);
+    hipLaunchKernelGGL((k_lp_dx<E>), dim3(join_grid(s, D, groups)), dim3(256), 0, st, sums,
+                       at<float4>(ws, y.stat), D, groups,
                        at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y), a.idc, at<float>(ws, y.own), c2,
                        at<float>(ws, y.lse2), dlogp, inv_t, terms, dX, b16);
     LP_TRY(hipGetLastError());

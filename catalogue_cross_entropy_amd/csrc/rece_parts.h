@@ -49,13 +49,15 @@ struct SweepParts {
     w.whole = whole != 0;
     return w;
   }
-  // f(index of a partial result) for every part of row r, in order; results are indexed [slots][nws][block].
+  // f(index of a partial result) for every step-th part of row r from the begin-th on, in order; results are
+  // indexed [slots][nws][block].
   template <class F>
-  __device__ __forceinline__ void each(const SweepWork& w, int64_t r, F f) const {
+  __device__ __forceinline__ void each(const SweepWork& w, int64_t r, F f, int begin = 0, int step = 1) const {
     const uint32_t b = (uint32_t)r / block, at = (uint32_t)r % block;
     const int64_t g0 = w.first(b), g1 = w.last(b);
+    const int q0 = (int)w.slot(b, g0) * nws, q1 = g0 <= g1 ? (int)(w.slot(b, g1) + 1) * nws : q0;
 #pragma unroll 4
-    for (int64_t q = w.slot(b, g0) * nws; q < (w.slot(b, g1) + 1) * nws && g0 <= g1; ++q) f(q * block + at);
+    for (int q = q0 + begin; q < q1; q += step) f((int64_t)q * block + at);
   }
 };
 
