@@ -38,7 +38,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LP_REF_LIMIT = 1.1529215e18f;   // 2^60: a sum beyond it is taken again with a better reference
 constexpr float LP_FLOOR = -1e28f;              // a reference where no logit is: those beyond the end lie at -1e30
@@ -55,11 +54,18 @@ struct LpRow {
   float lse2, a, b, g;   // G = [hit] g - p (a + b (x2 - lse2)),  p = exp2(x2 - lse2)
 };
 
+// log2(e) / temperature: rounded, and what the rounding left.  Its error would scale every logit alike, 6e-8 of a
+// logit's distance from the others, which is the relative error of 1 - p where p is near 1.  The second term is
+// taken for float32 inputs (their sweeps wait for the products, not for it); with bf16 inputs it is 0.
+struct LpScale {
+  float hi, lo;
+};
+
 struct LpArgs {
   const void* own;        // owner vectors [n_own][D]
   const void* str;        // streamed vectors [n_str][D]
   SweepParts parts;       // sizes, workgroups, and where parts lie
-  float c2;               // log2(e) / temperature
+  LpScale c2;             // log2(e) / temperature
   float4* stat;           // LP_LSE(O): parts (reference m, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m), 0)
   const LpRow* rows;      // LP_DX, LP_DY: of the packed positions
   const int32_t* idc;     // ids of the packed positions
@@ -113,6 +119,13 @@ __device__ __forceinline__ s16x4 lds_tr4(uint32_t off) {
 template <class T>
 __device__ __forceinline__ void lds_put(uint32_t off, T v) {
   *reinterpret_cast<__attribute__((address_space(3))) T*>((uintptr_t)off) = v;
+}
+
+// x log2(e) / temperature - r (the small term last, onto the difference)
+template <bool LO>
+__device__ __forceinline__ float lp_less(float x, LpScale c, float r) {
+  const float d = fmaf(x, c.hi, -r);
+  return LO ? fmaf(x, c.lo, d) : d;
 }
 
 // Gradient by a logit (less [own] g): -p (a + b d) with d = x2 - lse2, p = 2^d.
@@ -260,9 +273,10 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   };
   float m[OB], z[OB], tt[OB];   // LP_LSE(O): reference and sums
   f32x16 acc[ACC ? OB : 1][D / 32];
-  const float c2 = a.c2;
+  constexpr bool LO = sizeof(E) == 4;
+  const LpScale c2 = a.c2;
   // a logit that weighs nothing, finite after the factor c2
-  const float far = fmaxf(-1e30f / c2, -3e38f);
+  const float far = fmaxf(-1e30f / c2.hi, -3e38f);
 
   // behind the two tile buffers (LP_DY): the rows' constants, [2][5][TI] words: lse2, a, b, g, id
   constexpr int PB = 5 * TI * 4;
@@ -337,7 +351,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     for (int ob = 0; ob < OB; ++ob) {
       float bm = m[ob];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) bm = fmaxf(bm, x[ob][v] * c2);
+      for (int v = 0; v < 16; ++v) bm = fmaxf(bm, x[ob][v] * c2.hi);
       m[ob] = fmaxf(bm, __shfl_xor(bm, 32));
     }
   };
@@ -349,7 +363,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
         float s = 0.0f, st = 0.0f;
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const float d = fmaf(x[ob][v], c2, -m[ob]);
+          const float d = lp_less<LO>(x[ob][v], c2, m[ob]);
           x[ob][v] = exp2_fast(d);
           s += x[ob][v];
           if constexpr (ENT) st = fmaf(x[ob][v], d, st);
@@ -372,7 +386,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int v = 4 * q + e;
-            const float d = fmaf(x[ob][v], c2, DY ? -pl[e] : -olse[ob]);
+            const float d = lp_less<LO>(x[ob][v], c2, DY ? pl[e] : olse[ob]);
             x[ob][v] = lp_weight<ENT>(d, DY ? pa[e] : oa[ob], DY ? pb[e] : obt[ob]);
           }
       }
@@ -608,11 +622,22 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
 }
 
 // ------------------------------------------------------------------ joins
+// The part that position r's own item went into: the workgroup of its tile, the wave of its block of 32 rows.
+__device__ __forceinline__ int64_t lp_home(const SweepParts& parts, const SweepWork& w, uint32_t r, uint32_t id) {
+  const uint32_t b = r / parts.block;
+  const int64_t g = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
+  return (w.slot(b, g) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + r % parts.block;
+}
+
 // L lanes per position (1, a wave, a workgroup): the parts of its sum -> log-sum-exp, log-probability, entropy.
+// Where the own item is most of the sum, its term is taken out (the same bits that went in) and the others set
+// against it: the terms carry the rounding of their distance to a reference that may lie far below, 1e-6, and
+// 1 - p and log p would be as wrong.
 constexpr int FINISH_WIDE = 1024;
-template <int L>
+template <int L, bool LO>
 __global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
-    const int32_t* __restrict__ inv, int64_t s, SweepParts parts, const float4* __restrict__ stat, const float* __restrict__ own, float c2, float* __restrict__ lse2, float* __restrict__ ent_c,
+    const int32_t* __restrict__ inv, int64_t s, SweepParts parts, const float4* __restrict__ stat,
+    const float* __restrict__ own, const int32_t* __restrict__ idc, LpScale c2, float2* __restrict__ lse2, float* __restrict__ ent_c,
     float* __restrict__ logp, float* __restrict__ entropy) {
   constexpr int NT = L > WAVE ? L : 256, UNR = 4;
   const int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) / L;
@@ -673,9 +698,19 @@ __global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
     }
     if (l != 0) return;
   }
-  const float lz = log2f(zz), l2 = mm + lz;
-  lse2[r] = l2;
-  logp[i] = fmaf(own[r], c2, -l2) * LN2;
+  const float o = own[r], mh = stat[lp_home(parts, w, (uint32_t)r, (uint32_t)idc[r])].x;
+  const float x2 = o * c2.hi, x2lo = fmaf(o, c2.lo, fmaf(o, c2.hi, -x2));
+  const float lz = log2f(zz);
+  // the others' sum over the own term
+  const float others = fmaf(-exp2_fast(lp_less<LO>(o, c2, mh)), exp2_fast(mh - mm), zz);
+  const float t1 = (others < 0.0f ? 0.0f : others) * exp2_fast(fminf(mm - x2, 64.0f));   // NaN stays
+  const bool mostly = t1 < 1.0f;
+  // log-sum-exp as two floats: a step of one alone, 2^-20 for sums beyond 2^16, is as large as the rest
+  const float base = mostly ? x2 : mm, more = mostly ? log1pf(t1) * (1.0f / LN2) : lz;
+  const float l2 = base + more, back = l2 - base;
+  const float rest = (base - (l2 - back)) + (more - back) + (mostly ? x2lo : 0.0f);
+  lse2[r] = float2{l2, rest};
+  logp[i] = mostly ? -log1pf(t1) : (lp_less<true>(o, c2, l2) - rest) * LN2;
   if (entropy) {
     const float H = (lz - tt / zz) * LN2;
     entropy[i] = H;
@@ -687,8 +722,8 @@ __global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
 // logit; rows' g: what the sweep over the items leaves of the own item's g - p (..) (float32: all of g).
 template <bool ENT>
 __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_p, const int32_t* __restrict__ list,
-                                                 int64_t pad, const float* __restrict__ lse2,
-                                                 const float* __restrict__ ent_c, const float* __restrict__ own, float c2,
+                                                 int64_t pad, const float2* __restrict__ lse2,
+                                                 const float* __restrict__ ent_c, const float* __restrict__ own, LpScale c2,
                                                  const float* __restrict__ dlogp, const float* __restrict__ dent,
                                                  float inv_t, int terms, int b16, LpRow* __restrict__ rows) {
   const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -697,11 +732,16 @@ __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_
   if (r < *nv_p) {
     const int64_t i = list[r];
     const float g = dlogp[i] * inv_t, h = ENT ? dent[i] * inv_t : 0.0f;
-    c.lse2 = lse2[r];
+    const float2 l2 = lse2[r];
+    c.lse2 = l2.x;
     c.a = ENT ? fmaf(h, ent_c[r], g) : g;
     c.b = h * LN2;
-    const float w = lp_weight<ENT>(fmaf(own[r], c2, -c.lse2), c.a, c.b);
-    c.g = b16 ? g + (w - lp_taken(w, terms, true)) : g;
+    // the own item's weight g (1 - p) - p (..), less what the sweeps add for it
+    const float ds = lp_less<true>(own[r], c2, c.lse2), d = ds - l2.y;
+    const float w = lp_weight<ENT>(ds, c.a, c.b);
+    float total = g * -expm1f(d * LN2);
+    if constexpr (ENT) total -= exp2_fast(d) * fmaf(c.b, d, h * ent_c[r]);
+    c.g = total - lp_taken(w, terms, b16 != 0);
   }
   rows[r] = c;
 }
@@ -725,7 +765,7 @@ struct JoinLane {
   int col, group, groups;
   __device__ __forceinline__ JoinLane(int d, int n) : groups(n) {
     const int per = d / 4, rest = (int)threadIdx.x % per;
-    const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / per;
+    const int64_t unit = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) / per;
     row = unit / groups;
     group = (int)(unit % groups);
     col = rest * 4;
@@ -740,7 +780,10 @@ int join_groups(const SweepParts& p, int d) {
   const int64_t nb = (p.n_own + p.block - 1) / p.block;
   return !p.whole && (int64_t)p.grid * p.nws >= 16 * nb ? std::max(1, 256 / d) : 1;
 }
-unsigned join_grid(int64_t n, int d, int groups) { return (unsigned)((n * (d / 4) * groups + 255) / 256); }
+dim3 join_grid(int64_t n, int d, int groups) {   // at most 2^31 threads along x
+  const int64_t blocks = (n * (d / 4) * groups + 255) / 256, x = std::min<int64_t>(blocks, 1 << 23);
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
 
 // out row = sum of the parts' rows.  inv (dX): the row of the parts for each output row (or -1: zeros),
 // whose own item's row of Y is added g times.
@@ -776,8 +819,8 @@ __global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, int gr
 template <class E>
 __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float4* __restrict__ stat, int d, int groups,
                                                const int32_t* __restrict__ inv, int64_t s, const E* __restrict__ Y,
-                                               const int32_t* __restrict__ idc, const float* __restrict__ own, float c2,
-                                               const float* __restrict__ lse2, const float* __restrict__ dlogp,
+                                               const int32_t* __restrict__ idc, const float* __restrict__ own, LpScale c2,
+                                               const float2* __restrict__ lse2, const float* __restrict__ dlogp,
                                                float inv_t, int terms, void* __restrict__ out, int b16) {
   const JoinLane q(d, groups);
   if (q.row >= s) return;   // a row's lanes together
@@ -786,26 +829,24 @@ __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float4* _
   const int64_t r = inv[i];
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
-    const float l2 = lse2[r], g = dlogp[i] * inv_t, o = own[r];
+    const float2 l2 = lse2[r];
+    const float g = dlogp[i] * inv_t, o = own[r];
     const uint32_t id = (uint32_t)idc[r];
     const E* yp = Y + (int64_t)id * d + c;
     const float4 y = float4{to_f32(yp[0]), to_f32(yp[1]), to_f32(yp[2]), to_f32(yp[3])};
-    // the part that holds the own item: workgroup of its tile, wave of its block of 32 rows
     const SweepWork w = parts.work();
-    const uint32_t b = (uint32_t)r / parts.block;
-    const int64_t g_own = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
-    const int64_t home = (w.slot(b, g_own) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + (uint32_t)r % parts.block;
+    const int64_t home = lp_home(parts, w, (uint32_t)r, id);
     parts.each(w, r, [&](int64_t at) {
-      const float mp = stat[at].x, f = exp2_fast(mp - l2);
+      const float mp = stat[at].x, f = exp2_fast((mp - l2.x) - l2.y);
       float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       if (at == home) {
-        const float e = lp_taken(exp2_fast(fmaf(o, c2, -mp)), terms, sizeof(E) == 2);
+        const float e = lp_taken(exp2_fast(lp_less<sizeof(E) == 4>(o, c2, mp)), terms, sizeof(E) == 2);
         x = float4{fmaf(-e, y.x, x.x), fmaf(-e, y.y, x.y), fmaf(-e, y.z, x.z), fmaf(-e, y.w, x.w)};
       }
       v = float4{fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w)};
     }, q.group, q.groups);
     q.sum(v, d);
-    const float rest = -expm1f(fmaf(o, c2, -l2) * LN2);
+    const float rest = -expm1f((lp_less<true>(o, c2, l2.x) - l2.y) * LN2);
     v = float4{g * fmaf(rest, y.x, -v.x), g * fmaf(rest, y.y, -v.y), g * fmaf(rest, y.z, -v.z), g * fmaf(rest, y.w, -v.w)};
   }
   if (q.group == 0) put4(out, i * d + c, v, b16 != 0);
@@ -882,7 +923,7 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   y.inv = take(y.pad * 4);
   y.idc = take(y.pad * 4);
   y.own = take(y.pad * 4);
-  y.lse2 = take(y.pad * 4);
+  y.lse2 = take(y.pad * 8);
   y.ent = take(ent ? y.pad * 4 : 0);
   y.xc = take((size_t)y.pad * D * sizeof(E));
   const LpSweep f = lp_shape<E, D>(fused ? LP_LSEO : LP_LSE, s, C);
@@ -946,6 +987,14 @@ template <class E> int lp_terms(uint32_t flags) { return sizeof(E) == 2 && !(fla
     if (e_ != hipSuccess) return e_;     \
   } while (0)
 
+template <class E>
+LpScale lp_scale(float temperature) {
+  const double c = 1.4426950408889634 / (double)temperature;
+  LpScale s{(float)c, 0.0f};
+  if (sizeof(E) == 4 && std::isfinite(s.hi)) s.lo = (float)(c - (double)s.hi);
+  return s;
+}
+
 template <class T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
 template <class E, int D>
@@ -969,7 +1018,7 @@ template <class E, int D>
 hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags, const void* X, const void* Y,
                         const int32_t* ids, void* ws, float* logp, float* entropy, hipStream_t st) {
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
-  const float c2 = LOG2E / temperature;
+  const LpScale c2 = lp_scale<E>(temperature);
   const int64_t per = std::max<int64_t>(PACK_LEAST, ceil_div(s, PACK_BLOCKS));
   hipLaunchKernelGGL((k_lp_pack<E, D>), dim3((unsigned)ceil_div(s, per)), dim3(PACK_THREADS), 0, st,
                      static_cast<const E*>(X), static_cast<const E*>(Y), ids, s, C, per, y.pad, at<int32_t>(ws, y.nv),
@@ -993,9 +1042,10 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
     LP_TRY((lp_launch<E, D, LP_LSE, false>(a, st)));
   // few positions have many parts each: a workgroup for each while the card holds them at once, or a wave; many have few
   const int lanes = s <= LP_CUS ? FINISH_WIDE : s <= 8192 ? WAVE : 1, threads = std::max(256, lanes);
-  auto finish = lanes == FINISH_WIDE ? k_lp_finish<FINISH_WIDE> : lanes == WAVE ? k_lp_finish<WAVE> : k_lp_finish<1>;
+  constexpr bool LO = sizeof(E) == 4;
+  auto finish = lanes == FINISH_WIDE ? k_lp_finish<FINISH_WIDE, LO> : lanes == WAVE ? k_lp_finish<WAVE, LO> : k_lp_finish<1, LO>;
   hipLaunchKernelGGL(finish, dim3((unsigned)ceil_div(s * lanes, threads)), dim3(threads), 0, st, at<int32_t>(ws, y.inv), s,
-                     a.parts, a.stat, at<float>(ws, y.own), c2, at<float>(ws, y.lse2), at<float>(ws, y.ent), logp,
+                     a.parts, a.stat, at<float>(ws, y.own), at<int32_t>(ws, y.idc), c2, at<float2>(ws, y.lse2), at<float>(ws, y.ent), logp,
                      entropy);
   return hipGetLastError();
 }
@@ -1004,12 +1054,13 @@ template <class E, int D>
 hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags, const void* Y, void* ws,
                          const float* dlogp, const float* dent, void* dX, void* dY, hipStream_t st) {
   const LpLayout y = lp_layout_t<E, D>(s, C, flags);
-  const float inv_t = 1.0f / temperature, c2 = LOG2E / temperature;
+  const float inv_t = 1.0f / temperature;
+  const LpScale c2 = lp_scale<E>(temperature);
   const int b16 = flags & RECE_FLAG_BF16_GRADS ? 1 : 0, terms = lp_terms<E>(flags);
   const int32_t* nv = at<int32_t>(ws, y.nv);
   auto coef = dent ? k_lp_coef<true> : k_lp_coef<false>;
   hipLaunchKernelGGL(coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, nv, at<int32_t>(ws, y.list), y.pad,
-                     at<float>(ws, y.lse2), at<float>(ws, y.ent), at<float>(ws, y.own), c2, dlogp, dent, inv_t, terms,
+                     at<float2>(ws, y.lse2), at<float>(ws, y.ent), at<float>(ws, y.own), c2, dlogp, dent, inv_t, terms,
                      sizeof(E) == 2 ? 1 : 0, at<LpRow>(ws, y.rows));
   LP_TRY(hipGetLastError());
   LpArgs a{};
@@ -1019,7 +1070,7 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
   a.idc = at<int32_t>(ws, y.idc);
   auto join = [&](const int32_t* inv, int64_t n, void* out) {
     const int groups = join_groups(a.parts, D);
-    hipLaunchKernelGGL((k_lp_join<E>), dim3(join_grid(n, D, groups)), dim3(256), 0, st, a.parts, D, groups, inv,
+    hipLaunchKernelGGL((k_lp_join<E>), join_grid(n, D, groups), dim3(256), 0, st, a.parts, D, groups, inv,
                        a.rows, a.idc, static_cast<const E*>(Y), n, out, b16);
     return hipGetLastError();
   };
@@ -1036,10 +1087,10 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
   } else {
     const SweepParts sums = lp_parts<E, D>(LP_LSEO, s, C, nv, at<float>(ws, y.o));
     const int groups = join_groups(sums, D);
-    hipLaunchKernelGGL((k_lp_dx<E>), dim3(join_grid(s, D, groups)), dim3(256), 0, st, sums,
+    hipLaunchKernelGGL((k_lp_dx<E>), join_grid(s, D, groups), dim3(256), 0, st, sums,
                        at<float4>(ws, y.stat), D, groups,
                        at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y), a.idc, at<float>(ws, y.own), c2,
-                       at<float>(ws, y.lse2), dlogp, inv_t, terms, dX, b16);
+                       at<float2>(ws, y.lse2), dlogp, inv_t, terms, dX, b16);
     LP_TRY(hipGetLastError());
   }
   a.own = Y;

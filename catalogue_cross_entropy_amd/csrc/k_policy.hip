@@ -717,7 +717,7 @@ constexpr int PREF_EXTRA = 1024; // workgroups for what lies in no group
 // The last n_group workgroups: one group each.  Those before: the sequences in no group, and the tokens in no
 // sequence.
 template <class E, int L, int W, int NT>
-__global__ __launch_bounds__(NT) void k_pref(PrefArgs a) {
+__global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   constexpr int NS = NT / L;   // sequences at a time
   __shared__ double sh_h[PREF_LDS];
   __shared__ float sh_share[PREF_LDS];
@@ -725,10 +725,11 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a) {
   const int64_t G = a.c.n_group, nseq = a.c.n_seq;
   const int q = threadIdx.x / L, sub = threadIdx.x % L;
   const float beta = a.c.beta;
-  const int64_t extra = (int64_t)gridDim.x - G;
-  if ((int64_t)blockIdx.x < extra) {
+  const int64_t blk = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (blk >= extra + G) return;
+  if (blk < extra) {
     const int64_t first = offset_at(a.goffs, 0, nseq), end = offset_at(a.goffs, G, nseq);
-    const int64_t b = blockIdx.x;
+    const int64_t b = blk;
     for (int64_t k = b * NS + q; k < first + (nseq - end); k += extra * NS) {
       const int64_t i = k < first ? k : end + (k - first);
       if (i >= nseq) break;
@@ -746,7 +747,7 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a) {
     }
     return;
   }
-  const int64_t g = (int64_t)blockIdx.x - extra;
+  const int64_t g = blk - extra;
   const int64_t s0 = offset_at(a.goffs, g, nseq), s1 = max(s0, offset_at(a.goffs, g + 1, nseq));
   const int64_t m = s1 - s0;
   const bool in_lds = m <= PREF_LDS;
@@ -875,7 +876,8 @@ hipError_t policy_t(PolArgs& a, void* ws, hipStream_t st) {
 template <class E, int L, int W, int NT>
 hipError_t pref_launch(const PrefArgs& a, hipStream_t st) {
   const int64_t extra = std::min<int64_t>((a.c.n_seq + NT / L - 1) / (NT / L), PREF_EXTRA);
-  hipLaunchKernelGGL((k_pref<E, L, W, NT>), dim3((unsigned)(a.c.n_group + extra)), dim3(NT), 0, st, a);
+  const int64_t blocks = a.c.n_group + extra, x = std::min<int64_t>(blocks, 1 << 22);   // at most 2^30 threads along x
+  hipLaunchKernelGGL((k_pref<E, L, W, NT>), dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(NT), 0, st, a, (int)extra);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_pref_mean, dim3(1), dim3(PREF_MEAN_THREADS), 0, st, a);

@@ -198,3 +198,16 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_embed_gradient_of_many_rows():
+    """More rows than a launch has threads for at 32 a piece of 8: gradients of ones are counts, exact in float32."""
+    n, C, d = (1 << 27) + 4099, 1000, 8
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(-1, C, (n,), generator=g, device="cuda", dtype=torch.int32)
+    op = rece.ItemEmbedding(n, C, d, dtype="bf16")
+    got = op.backward(ids, torch.ones(n, d, dtype=torch.bfloat16, device="cuda"))
+    want = torch.bincount(ids.clamp(min=-1).long() + 1, minlength=C + 1)[1:].float()
+    assert torch.equal(got, want[:, None].expand(C, d).contiguous())
