@@ -7,6 +7,11 @@
 // pieces and sums each piece's runs in float32 registers; a run inside one piece is
 // written at once, a run over several pieces leaves one partial row per piece that a
 // second kernel adds in a fixed order, so every result is reproducible bit for bit.
+// Measured (MI355X, bf16 rows, float32 gradient):
+//   256 rows of 64 floats            call 7.4 us (kernel 3.1 us: the call's own time bounds it)
+//   51,200 rows of 64, 30,000 items  forward 5.2 us (13 MB), backward 36 us: sort 24, pieces 7, joins 8; latencies
+//                                    of short launches, 27 MB in all
+//   25,600 rows of 128, 1M items     forward and backward 116 us, 525 MB (512 MB of it the cleared gradient): 4.5 TB/s
 #include <algorithm>
 
 #include "rece_device.h"
@@ -23,8 +28,7 @@ constexpr int ORD_TILE = 4096;      // records per workgroup of the sort
 constexpr int ORD_BITS = 10;        // largest digit
 constexpr int ORD_BINS = 1 << ORD_BITS;
 constexpr int64_t ORD_TILES = 64;   // beyond these the library's longer sort, with a scan of its own, takes over
-constexpr int EMB_PIECE = 8;        // sorted records per piece
-constexpr int64_t EMB_JOINS = 65536;// workgroups that join runs
+constexpr int EMB_PIECE = 8;        // sorted records per piece (51,200 records: 8 a piece 6.5 us, 32 a piece 12 us)
 
 template <class E> struct Piece16 {
   static constexpr int EPL = 16 / (int)sizeof(E);
@@ -109,7 +113,7 @@ __device__ __forceinline__ void clear_share(const ClearArgs& c, int part, int pa
 __global__ __launch_bounds__(ORD_THREADS) void k_embed_clear(ClearArgs c) { clear_share(c, 0, 1, blockIdx.x, gridDim.x); }
 
 // ------------------------------------------------------------------ rows in the order of their ids
-// Stable counting sort of the records (id, row) by digits of up to 10 bits, over tiles of 4096 records.
+// Stable counting sort of the records (id, row) by digits of up to 10 bits, over tiles of 1024 to 4096 records.
 //   k_order_hist     per tile, the count of every value of a digit;
 //   k_order_scatter  per tile: every workgroup forms the digits' starting slots from all tiles' counts by
 //                    itself (at most 64 tiles: 256 KB that lie in the L2; a scan of its own would be three
@@ -438,56 +442,54 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_pieces(EmbGrad a) {
   flush(t1);
 }
 
-// A workgroup takes every gridDim.x-th piece: if a run starts in it and goes on, the run's partial rows
+// One workgroup per piece: if a run starts in it and goes on, the run's partial rows
 // are added, lane group g taking every (256 / LPR)-th of them, then the groups in order.
 template <int LPR>
 __global__ __launch_bounds__(EMB_THREADS) void k_embed_join(EmbGrad a) {
   constexpr int EPL = 8;
   constexpr int NG = EMB_THREADS / LPR;
   __shared__ float sh[NG][LPR * EPL + 4];
-  const int64_t n = (int64_t)*a.ntot;
+  const int64_t piece = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+  const int64_t n = (int64_t)*a.ntot, t0 = piece * EMB_PIECE, t1 = t0 + EMB_PIECE;
+  if (t1 >= n) return;
+  const int j = a.K[t1 - 1];
+  if (a.K[t1] != j || (t0 > 0 && a.K[t0] == j && a.K[t0 - 1] == j)) return;
+  int64_t lo = t1, hi = n;   // first record beyond the run is in (lo, hi]; a wave probes 64 places at a time
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + WAVE) / (WAVE + 1), m = lo + step * (lane_id() + 1);
+    const int hits = popc(ballot(m < hi && a.K[m < hi ? m : lo] == j));   // sorted: the first lanes
+    hi = min(hi, lo + step * (hits + 1));
+    lo += step * hits;
+  }
+  const int64_t last = lo / EMB_PIECE;
   const int g = threadIdx.x / LPR, sub = threadIdx.x % LPR;
   const int col = ((int)blockIdx.y * LPR + sub) * EPL;
-  for (int64_t piece = blockIdx.x; (piece + 1) * EMB_PIECE < n; piece += gridDim.x) {
-    const int64_t t0 = piece * EMB_PIECE, t1 = t0 + EMB_PIECE;
-    const int j = a.K[t1 - 1];
-    if (a.K[t1] != j || (t0 > 0 && a.K[t0] == j && a.K[t0 - 1] == j)) continue;
-    int64_t lo = t1, hi = n;   // first record beyond the run is in (lo, hi]; a wave probes 64 places at a time
-    while (hi - lo > 1) {
-      const int64_t step = (hi - lo + WAVE) / (WAVE + 1), m = lo + step * (lane_id() + 1);
-      const int hits = popc(ballot(m < hi && a.K[m < hi ? m : lo] == j));   // sorted: the first lanes
-      hi = min(hi, lo + step * (hits + 1));
-      lo += step * hits;
-    }
-    const int64_t last = lo / EMB_PIECE;
-    float sum[EPL];
+  float sum[EPL];
 #pragma unroll
-    for (int t = 0; t < EPL; ++t) sum[t] = 0.0f;
-    if (col < a.d) {
+  for (int t = 0; t < EPL; ++t) sum[t] = 0.0f;
+  if (col < a.d) {
 #pragma unroll 4
-      for (int64_t p = piece + g; p <= last; p += NG) {
-        const float4* h = reinterpret_cast<const float4*>(a.partial + (p * 2 + (p == piece ? 1 : 0)) * a.d + col);
+    for (int64_t p = piece + g; p <= last; p += NG) {
+      const float4* h = reinterpret_cast<const float4*>(a.partial + (p * 2 + (p == piece ? 1 : 0)) * a.d + col);
 #pragma unroll
-        for (int t = 0; t < EPL / 4; ++t) {
-          const float4 w = h[t];
-          sum[4 * t] += w.x;
-          sum[4 * t + 1] += w.y;
-          sum[4 * t + 2] += w.z;
-          sum[4 * t + 3] += w.w;
-        }
+      for (int t = 0; t < EPL / 4; ++t) {
+        const float4 w = h[t];
+        sum[4 * t] += w.x;
+        sum[4 * t + 1] += w.y;
+        sum[4 * t + 2] += w.z;
+        sum[4 * t + 3] += w.w;
       }
     }
-    __syncthreads();   // the sums of the piece before are read
-#pragma unroll
-    for (int t = 0; t < EPL; ++t) sh[g][sub * EPL + t] = sum[t];
-    __syncthreads();
-    if (g != 0 || col >= a.d) continue;
-    const int used = (int)min((int64_t)NG, last - piece + 1);
-    for (int o = 1; o < used; ++o)
-#pragma unroll
-      for (int t = 0; t < EPL; ++t) sum[t] += sh[o][sub * EPL + t];
-    put_row<EPL>(a, a.parts.rows ? a.parts.work() : SweepWork{}, j, col, sum);
   }
+#pragma unroll
+  for (int t = 0; t < EPL; ++t) sh[g][sub * EPL + t] = sum[t];
+  __syncthreads();
+  if (g != 0 || col >= a.d) return;
+  const int used = (int)min((int64_t)NG, last - piece + 1);
+  for (int o = 1; o < used; ++o)
+#pragma unroll
+    for (int t = 0; t < EPL; ++t) sum[t] += sh[o][sub * EPL + t];
+  put_row<EPL>(a, a.parts.rows ? a.parts.work() : SweepWork{}, j, col, sum);
 }
 
 // Lanes per row: the power of two that holds a row's 16-byte pieces, at most a wave
@@ -537,7 +539,8 @@ hipError_t pieces_t(const EmbGrad& a, int64_t npieces, hipStream_t st) {
 
 hipError_t join(const EmbGrad& a, int64_t npieces, hipStream_t st) {
   const int pieces = a.d / 8, lpr = lanes_per_row(pieces);
-  const dim3 grid((unsigned)std::min<int64_t>(npieces, EMB_JOINS), ceil_div(pieces, lpr));
+  const int64_t x = std::min<int64_t>(npieces, 1 << 22);   // at most 2^30 threads along x
+  const dim3 grid((unsigned)x, ceil_div(pieces, lpr), ceil_div(npieces, x));
 #define EMB_JOIN(L) hipLaunchKernelGGL((k_embed_join<L>), grid, dim3(EMB_THREADS), 0, st, a)
   EMB_LPR(EMB_JOIN, lpr)
 #undef EMB_JOIN

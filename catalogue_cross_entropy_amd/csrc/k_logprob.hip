@@ -13,11 +13,24 @@
 // also the A-operand layout of the gradient product (k = streamed rows, in that order on
 // both sides), so the weights never leave their registers; the streamed rows enter the
 // second product transposed through the LDS transpose read.
-//   LP_LSE (owners = positions, streamed = items): running sum of exp2(x2 - m)
-//   LP_DX  (owners = positions, streamed = items): dX = G Y
-//   LP_DY  (owners = items, streamed = positions): dY = G^T X
-// The streamed side is cut into `splits` ranges, one workgroup each, when the owners
-// alone would not fill the card; small kernels join the parts in a fixed order.
+//   LP_LSE  (owners = positions, streamed = items): sum of exp2(x2 - m), and with it the entropy's
+//   LP_LSEO (the same, before gradients without entropies): and the sums of item rows, so that dX
+//           needs no sweep of its own
+//   LP_DX   (owners = positions, streamed = items): dX = G Y, with entropies
+//   LP_DY   (owners = items, streamed = positions): dY = G^T X
+// The work is dealt to a grid that fills the card once (rece_parts.h); small kernels join the parts
+// in a fixed order.
+//
+// What bounds it: the exponential of each logit (v_exp_f32, about 9 cycles of a SIMD for 64 logits, with 2
+// to 4 cheaper instructions beside it) and the products share a SIMD's issue: vector and matrix units
+// were busy 115 % together at best (68 % and 47 %).  Measured (bf16):
+//   51,200 (a quarter padding) x 30,000 x 64  with gradients 707 us: LP_LSEO 342 us and LP_DY 344 us (860
+//                          TFLOP/s each, and 3.4e12 exponentials a second), packing, joins and the own items 100 us
+//   4,099 (a tenth padding) x 50,021 x 256  with entropies and gradients 685 us: LP_LSE 122, LP_DX 225,
+//                          LP_DY 307 us (770, 840, 620 TFLOP/s; LP_DY spills about 25 words per lane)
+//   2,047 (a tenth padding) x 200,000 x 128  log-probabilities 122 us: LP_LSE 117 us (810 TFLOP/s)
+//   5 x 1,000,000 x 64     log-probabilities and entropies 40 us: LP_LSE 26 us, 128 MB at 4.9 TB/s
+//   256 x 2,000 x 64 float32 with entropies and gradients 50 us: eight launches of 2 to 12 us
 //
 // Positions whose id is padding are left out first: the others are packed (rows, ids) in
 // order into the workspace, so padding costs no products and nothing it holds (NaN or
@@ -229,7 +242,7 @@ __device__ __forceinline__ float lp_taken(float g, int terms, bool b16) { return
 // NWO waves along the owners x NWS waves along a tile's rows; OB blocks of 32 owners per wave.
 // A row's own item enters LP_LSEO, LP_DX and LP_DY (bf16) with the others, as -p (..); the joins add what is
 // missing of g - p (..) in float32 (1 - p would lose its digits in a bf16 term), knowing what went in: the
-// own logits come from the same products, so the same bits.  LP_DY (float32) adds g here.
+// own logits come from the same products, so the same bits.  LP_DY (float32) adds it here.
 template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int TERMS, int MINW>
 __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   using T = LpTile<E, D, NWS>;
@@ -522,6 +535,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
 }
 
 // ------------------------------------------------------------------ packing
+// (12 us for 51,200 ids of rows of 64 bf16, 25 MB; 6 us for 256.)
 // Workgroup b takes ids [b per, (b + 1) per): it counts the ids before them that lie in
 // [0, C) itself (an L2-resident read of 4 bytes a position, in place of a scan's further
 // launches), then writes the list of its own, the packed rows and ids, and the (unscaled)
@@ -719,7 +733,7 @@ __global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
 }
 
 // Constants of the gradient per packed row; rows of no weight up to the padding.  own: the row's own
-// logit; rows' g: what the sweep over the items leaves of the own item's g - p (..) (float32: all of g).
+// logit; rows' g: what the sweeps leave of the own item's g - p (..).
 template <bool ENT>
 __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_p, const int32_t* __restrict__ list,
                                                  int64_t pad, const float2* __restrict__ lse2,
@@ -858,10 +872,17 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int LP_CUS = 256;
 
-// Launch shapes: blocks of 32 owners per wave (more: fewer LDS reads per product; fewer: more waves
-// per SIMD to overlap the exponentials with the products), workgroups per CU that the registers
-// allow (the grid: every CU filled once), and the rows up to which the waves of a workgroup share their owners
-// and split each tile's rows instead (a block of owners that is mostly empty costs as much as a full one).
+// Launch shapes, by the bytes of a row: OB blocks of 32 owners per wave (more: fewer LDS reads per product; fewer:
+// more waves per SIMD to overlap the exponentials with the products), MW waves per SIMD (the registers allow
+// them; the grid fills the card once), NWO waves per workgroup.  us, both sides of each choice:
+//   D 64, 51,200 x 30,000, LP_LSEO / LP_DY:   OB 2 MW 2  338 / 341;  OB 1 MW 4  340 / 386;  OB 1 MW 3  364 / 424
+//   D 128, 8,192 x 30,000, LP_DX / LP_DY:     OB 1 MW 3  138 / 150;  OB 1 MW 2  142 / 157;  OB 2 MW 1  149 / 165;
+//                                             OB 2 MW 2  168 / 254 (spills)
+//   D 256, 4,099 x 50,021, LP_DX / LP_DY:     NWO 8  218 / 298;  NWO 4  254 / 318;  OB 1 MW 1  370 / 413
+//   LP_LSE, MW 3 against 2:                   D 128, 2,047 x 200,000  117 / 127;  D 256, 4,099 x 50,021  120 / 128
+//   PIPE (LP_DY, D 64):                       343 against 359; LP_LSEO has no registers for it (467 against 341)
+// Up to 32 OB positions the waves of a workgroup share their owners and split each tile's rows instead (NWS 4;
+// a block of owners that is mostly empty costs as much as a full one): 5 x 1,000,000, LP_LSE 25 against 62.
 template <class E, int D> struct LpShape {
   static constexpr bool B = sizeof(E) == 2;
   static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
