@@ -7,13 +7,14 @@
 // over millions of tokens would lose the small differences these losses are made of.
 //
 // Measured (MI355X), kernels back to back:
-//   policy, 4.2M tokens float32 in 8,192 sequences, KL, mask: mean over tokens 31 us (75 MB; the tile kernel 26 us,
+//   policy, 4.2M tokens float32 in 8,192 sequences, KL, mask: mean over tokens 32 us (75 MB; the tile kernel 27 us,
 //     2.7 TB/s: half its time vector instructions, half loads and the tile's start), over sequences 37 us
 //   policy, 16 sequences of 24 tokens: 9 us in one workgroup, of a call of 15.5 us (the call bounds it)
 //   preference, 3.3M tokens bf16 in 2,048 groups of up to 8, softmax: 27 us (23 MB; loads one after the other:
 //     offsets, tokens, the group's float64 terms, the gradient; VALU 20 % busy)
 //   preference, 256 pairs of items: 7 us, of a call of 17 us
 #include <algorithm>
+#include <cmath>
 
 #include "rece_device.h"
 #include "rece_internal.h"
@@ -104,6 +105,8 @@ struct PolArgs {
   int counters;         // 0: the offsets tell (no mask, token mean)
   int32_t* cnt;         // [n_seq] tokens that count (sequence mean)
   double* partial;      // [blocks][8]
+  // log(1 - clip_low), log(1 + clip_high): rounded, and what the rounding left
+  float log_lo, log_lo2, log_hi, log_hi2;
 };
 
 // The values of one token.
@@ -130,9 +133,12 @@ __device__ __forceinline__ float exp_near(float x) {
 __device__ __forceinline__ PolTerm pol_token(const PolArgs& a, const PolToken& k, float w, float A) {
   PolTerm o;
   const float lo = 1.0f - a.c.clip_low, hi = 1.0f + a.c.clip_high;
-  o.r = exp_near(k.lp - k.old);
+  const float diff = k.lp - k.old;
+  o.r = exp_near(diff);
   const float bound = A > 0.0f ? hi : lo;
-  o.clipped = (A > 0.0f && o.r > hi) || (A < 0.0f && o.r < lo);
+  // decided on the logarithms: the difference is exact where the ratio is near its bounds, but the ratio itself is
+  // rounded, and one token in millions would fall on the other side
+  o.clipped = (A > 0.0f && diff - a.log_hi > a.log_hi2) || (A < 0.0f && diff - a.log_lo < a.log_lo2);
   o.pg = -A * (o.clipped ? bound : o.r);
   float g = o.clipped ? 0.0f : o.pg;
   o.kl = 0.0f;
@@ -727,7 +733,33 @@ __device__ __forceinline__ double pair_loss(const rece_preference_config& c, dou
 }
 
 constexpr int PREF_LDS = 512;   // sequences of a group whose h lies in LDS
+constexpr int64_t PREF_MANY = 8192, PREF_PAIRS = 2048;   // groups (pairs) above which small ones share waves
 constexpr int PREF_EXTRA = 1024; // workgroups for what lies in no group
+
+// What lies in no group, by workgroup b of `extra`: the rewards of its sequences, gradients of zero.
+template <class E, int L, int W, int NT>
+__device__ __forceinline__ void pref_outside(const PrefArgs& a, int64_t b, int64_t extra) {
+  constexpr int NS = NT / L;   // sequences at a time
+  const int64_t G = a.c.n_group, nseq = a.c.n_seq;
+  const int q = threadIdx.x / L, sub = threadIdx.x % L;
+  const float beta = a.c.beta;
+  const int64_t first = offset_at(a.goffs, 0, nseq), end = offset_at(a.goffs, G, nseq);
+  for (int64_t k = b * NS + q; k < first + (nseq - end); k += extra * NS) {
+    const int64_t i = k < first ? k : end + (k - first);
+    if (i >= nseq) break;
+    const PrefSeq seq[1] = {pref_seq(a.offs, i, a.c.n)};
+    double h[1];
+    float share[1];
+    pref_sum<E, L, W, 1>(a, seq, sub, h, share);
+    if (sub == 0) a.rewards[i] = (float)((double)beta * h[0]);
+    if (a.dlogp) pref_grad<E, L, W>(a, seq[0], sub, 0.0f);
+  }
+  if (a.dlogp) {
+    const int64_t lo = offset_at(a.offs, 0, a.c.n), hi = max(lo, offset_at(a.offs, nseq, a.c.n));
+    for (int64_t k = b * NT + threadIdx.x; k < lo + (a.c.n - hi); k += extra * NT)
+      put(static_cast<E*>(a.dlogp), k < lo ? k : hi + (k - lo), 0.0f);
+  }
+}
 
 // The last n_group workgroups: one group each.  Those before: the sequences in no group, and the tokens in no
 // sequence.
@@ -743,23 +775,7 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   const int64_t blk = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (blk >= extra + G) return;
   if (blk < extra) {
-    const int64_t first = offset_at(a.goffs, 0, nseq), end = offset_at(a.goffs, G, nseq);
-    const int64_t b = blk;
-    for (int64_t k = b * NS + q; k < first + (nseq - end); k += extra * NS) {
-      const int64_t i = k < first ? k : end + (k - first);
-      if (i >= nseq) break;
-      const PrefSeq seq[1] = {pref_seq(a.offs, i, a.c.n)};
-      double h[1];
-      float share[1];
-      pref_sum<E, L, W, 1>(a, seq, sub, h, share);
-      if (sub == 0) a.rewards[i] = (float)((double)beta * h[0]);
-      if (a.dlogp) pref_grad<E, L, W>(a, seq[0], sub, 0.0f);
-    }
-    if (a.dlogp) {
-      const int64_t lo = offset_at(a.offs, 0, a.c.n), hi = max(lo, offset_at(a.offs, nseq, a.c.n));
-      for (int64_t k = b * NT + threadIdx.x; k < lo + (a.c.n - hi); k += extra * NT)
-        put(static_cast<E*>(a.dlogp), k < lo ? k : hi + (k - lo), 0.0f);
-    }
+    pref_outside<E, L, W, NT>(a, blk, extra);
     return;
   }
   const int64_t g = blk - extra;
@@ -837,6 +853,81 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   for (int64_t k = q; k < m; k += NS) pref_grad<E, L, W>(a, seq_at(k), sub, (float)(hs[k] * up * (double)shares[k]));
 }
 
+// Many small groups: T lanes take a group, its sequences one after the other.
+constexpr int PREF_MANY_THREADS = 256;
+template <class E, int T, int W>
+__global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int extra) {
+  const int64_t blk = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (blk < extra) {
+    pref_outside<E, T, W, PREF_MANY_THREADS>(a, blk, extra);
+    return;
+  }
+  const int64_t G = a.c.n_group, nseq = a.c.n_seq;
+  const int64_t g = (blk - extra) * (PREF_MANY_THREADS / T) + threadIdx.x / T;
+  const int sub = threadIdx.x % T;
+  if (g >= G) return;   // a group's lanes together
+  const int64_t s0 = offset_at(a.goffs, g, nseq), s1 = max(s0, offset_at(a.goffs, g + 1, nseq));
+  const int64_t m = s1 - s0;
+  const double beta = a.c.beta, margin = a.c.margin;
+  const double up = beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G, per = m > 1 ? 1.0 / (double)(m - 1) : 0.0;
+  PrefSeq seq[1];
+  double h[1];
+  float share[1];
+  auto read = [&](int64_t k) {
+    seq[0] = pref_seq(a.offs, s0 + k, a.c.n);
+    pref_sum<E, T, W, 1>(a, seq, sub, h, share);
+  };
+  auto grad = [&](double dh) {   // of the sequence read last
+    if (a.dlogp) pref_grad<E, T, W>(a, seq[0], sub, (float)(dh * up * (double)share[0]));
+  };
+  double loss = 0.0, dc = 0.0;
+  if (m > 0) {
+    read(0);
+    const double hc = h[0];
+    const float share0 = share[0];
+    const PrefSeq seq0 = seq[0];
+    if (sub == 0) a.rewards[s0] = (float)(beta * hc);
+    if (a.c.kind == RECE_PREF_SOFTMAX) {
+      double top = 0.0, others = 0.0;   // others: sum of e^(-z - top)
+      for (int64_t k = 1; k < m; ++k) {
+        read(k);
+        if (sub == 0) a.rewards[s0 + k] = (float)(beta * h[0]);
+        const double v = margin - beta * (hc - h[0]);
+        if (v > top) {
+          others *= exp(top - v);
+          top = v;
+        }
+        others += exp(v - top);
+      }
+      const double tot = others + exp(-top);
+      if (m > 1) {
+        loss = top + log(tot);
+        dc = -others / tot;
+      }
+      if (a.dlogp)
+        for (int64_t k = 1; k < m; ++k) {
+          read(k);
+          grad(exp(margin - beta * (hc - h[0]) - top) / tot);
+        }
+    } else {
+      for (int64_t k = 1; k < m; ++k) {
+        read(k);
+        if (sub == 0) a.rewards[s0 + k] = (float)(beta * h[0]);
+        double dz;
+        loss += pair_loss(a.c, beta * (hc - h[0]) - margin, dz);
+        dc += dz;
+        grad(-dz * per);
+      }
+      loss *= per;
+      dc *= per;
+    }
+    seq[0] = seq0;
+    share[0] = share0;
+    grad(dc);
+  }
+  if (sub == 0) a.loss_pg[g] = (float)loss;
+}
+
 constexpr int PREF_MEAN_THREADS = 1024;
 __global__ __launch_bounds__(PREF_MEAN_THREADS) void k_pref_mean(PrefArgs a) {
   __shared__ double sh[PREF_MEAN_THREADS / WAVE];
@@ -900,14 +991,36 @@ hipError_t pref_launch(const PrefArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <class E, int T, int W>
+hipError_t pref_many_launch(const PrefArgs& a, hipStream_t st) {
+  constexpr int NG = PREF_MANY_THREADS / T;
+  const int64_t extra = std::min<int64_t>((a.c.n_seq + NG - 1) / NG, PREF_EXTRA);
+  const int64_t blocks = (a.c.n_group + NG - 1) / NG + extra, x = std::min<int64_t>(blocks, 1 << 22);   // at most 2^30 threads along x
+  hipLaunchKernelGGL((k_pref_many<E, T, W>), dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(PREF_MANY_THREADS), 0, st, a,
+                     (int)extra);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_pref_mean, dim3(1), dim3(PREF_MEAN_THREADS), 0, st, a);
+  return hipGetLastError();
+}
+
 template <class E>
 hipError_t preference_t(const PrefArgs& a, hipStream_t st) {
   const int64_t len = a.c.n / a.c.n_seq, group = a.c.n / a.c.n_group;
   const uintptr_t tok = reinterpret_cast<uintptr_t>(a.logp) | reinterpret_cast<uintptr_t>(a.ref) | reinterpret_cast<uintptr_t>(a.dlogp);
   const bool wide = tok % (4 * sizeof(E)) == 0 && reinterpret_cast<uintptr_t>(a.mask) % 4 == 0;
-  // Lanes per sequence by the mean length, four tokens each where every array allows it.  A million tokens in pairs,
-  // us with 64 / 8 lanes: length 4 165 / 155, 8 177 / 79, 16 89 / 42, 32 48 / 25; 8 lanes / 1: length 4 155 / 165.
-  // A wave takes short groups (of less than 256 tokens) alone.
+  // Many small groups: a few lanes each, members one after the other, against a workgroup each (us, softmax):
+  //   pairs of 1 / 8 / 40 tokens: 2,048 pairs 7 / 8 / 9 against 7 / 8 / 9, 8,192 7 / 8 / 9 against 13 / 15 / 17,
+  //     131,072 20 / 39 / 51 against 128 / 144 / 163
+  //   groups of 8: 8,192 groups 16 / 23 / 32 against 13 / 15 / 28, 32,768 18 / 30 / 47 against 35 / 42 / 96
+  const int64_t G = a.c.n_group;
+  if (len < 64 && ((G >= PREF_PAIRS && a.c.n_seq <= 2 * G) || (G > PREF_MANY && a.c.n_seq <= 8 * G))) {
+    if (len < 4) return pref_many_launch<E, 1, 1>(a, st);
+    return wide ? pref_many_launch<E, 8, 4>(a, st) : pref_many_launch<E, 8, 1>(a, st);
+  }
+  // Lanes per sequence by the mean length, four tokens each where every array allows it (slices of a longer batch may
+  // not).  A million tokens in groups of 16, us with 8 lanes against 1: length 8 18 against 50, 16 16 against 30, 32 11
+  // against 20; at length 4 29 against 26.  A wave takes groups of less than 256 tokens alone.
   if (len >= 64) return wide ? pref_launch<E, 64, 4, 256>(a, st) : pref_launch<E, 64, 1, 256>(a, st);
   if (len < 4) return pref_launch<E, 1, 1, 64>(a, st);
   if (group >= 256) return wide ? pref_launch<E, 8, 4, 256>(a, st) : pref_launch<E, 8, 1, 256>(a, st);
@@ -940,6 +1053,11 @@ hipError_t policy_loss(const rece_policy_config& c, const void* logp, const void
   a.stats = stats;
   a.dlogp = dlogp;
   a.dentropy = dentropy;
+  const double lo = c.clip_low < 1.0f ? std::log1p(-(double)c.clip_low) : -HUGE_VAL, hi = std::log1p((double)c.clip_high);
+  a.log_lo = (float)lo;
+  a.log_lo2 = (float)(lo - (double)a.log_lo);
+  a.log_hi = (float)hi;
+  a.log_hi2 = (float)(hi - (double)a.log_hi);
   return c.dtype == RECE_BF16 ? policy_t<bf16>(a, ws, st) : policy_t<float>(a, ws, st);
 }
 

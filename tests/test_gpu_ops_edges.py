@@ -144,6 +144,24 @@ def test_policy_extreme_ratios():
     assert np.isnan(float(loss)) and bool(dlp[77].isnan()) and not bool(dlp[:77].isnan().any())
 
 
+@pytest.mark.parametrize("n", [4000, 40000])
+def test_policy_clips_on_the_right_side_of_its_bounds(n):
+    """Differences a few steps around log(0.8) and log(1.2): clipped exactly where the float64 ratio is beyond the
+    (float32) bounds.  old is 0, so the differences are the values themselves."""
+    low, high = float(np.float32(0.2)), float(np.float32(0.2))
+    half = n // 2
+    at = np.concatenate([np.full(half, np.log1p(-low), np.float32), np.full(n - half, np.log1p(high), np.float32)])
+    bits = at.view(np.int32) + np.random.default_rng(0).integers(-6, 7, n, dtype=np.int32)
+    lp = torch.from_numpy(bits.view(np.float32).copy())
+    A = torch.cat([torch.full((half,), -1.0), torch.ones(n - half)])
+    r = lp.double().exp()
+    clipped = torch.where(A > 0, r > 1 + high, r < 1 - low)
+    assert 0.3 * n < int(clipped.sum()) < 0.7 * n
+    op = rece.PolicyLoss(n, 1, clip_low=0.2, clip_high=0.2, token_advantage=True)
+    _, stats, dlp, _ = op.forward(lp.cuda(), torch.zeros(n).cuda(), A.cuda(), torch.tensor([0, n], dtype=torch.int32).cuda())
+    assert torch.equal(dlp.cpu() == 0, clipped)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,n_seq,G", [(40000, 150, 50), (6000, 600, 20), (2400, 600, 200), (900, 900, 300)])
 def test_preference_views_at_odd_addresses(n, n_seq, G, dtype):
@@ -211,3 +229,35 @@ def test_embed_gradient_of_many_rows():
     got = op.backward(ids, torch.ones(n, d, dtype=torch.bfloat16, device="cuda"))
     want = torch.bincount(ids.clamp(min=-1).long() + 1, minlength=C + 1)[1:].float()
     assert torch.equal(got, want[:, None].expand(C, d).contiguous())
+
+
+@pytest.mark.parametrize("G,K,n,dtype,kind,smoothing,average,masked,margin,with_ref", [
+    (8193, 1, 30000, "f32", "sigmoid", 0.1, False, True, 0.2, True), (8200, 3, 50000, "bf16", "softmax", 0.0, False, True, 0.0, True),
+    (8193, 3, 190000, "f32", "softmax", 0.0, True, True, 0.3, True), (8193, 1, 200000, "bf16", "ipo", 0.0, True, False, 0.0, True),
+    (9000, 1, 20000, "f32", "hinge", 0.0, False, False, 0.1, False), (2048, 1, 5000, "bf16", "sigmoid", 0.0, False, True, 0.0, True),
+    (2047, 1, 5000, "bf16", "sigmoid", 0.0, False, True, 0.0, True),
+])
+def test_preference_many_small_groups(G, K, n, dtype, kind, smoothing, average, masked, margin, with_ref):
+    TP.test_preference_against_plain(G, K, n, dtype, kind, smoothing, average, masked, margin, with_ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("per", [1, 9])
+def test_preference_groups_are_the_same_in_a_large_call(per, kind, dtype):
+    """The first groups of 12,000 give what a call of a few gives: rewards and losses to a step, gradients (times the
+    ratio of the numbers of groups) too."""
+    big, few, K = 12000, 30, 2
+    g = torch.Generator().manual_seed(per)
+    lp, ref, _ = (t.cuda() for t in TP._tokens(g, big * K * per, dtype))
+    offs = (torch.arange(big * K + 1) * per).to(torch.int32).cuda()
+    goffs = (torch.arange(big + 1) * K).to(torch.int32).cuda()
+    n = few * K * per
+    a = rece.PreferenceLoss(big * K * per, big * K, big, kind=kind, dtype=dtype).forward(lp, ref, offs, goffs)
+    b = rece.PreferenceLoss(n, few * K, few, kind=kind, dtype=dtype).forward(
+        lp[:n].clone(), ref[:n].clone(), offs[:few * K + 1].clone(), goffs[:few + 1].clone())
+    for x, y in ((a[1][:few], b[1]), (a[2][:few * K], b[2])):
+        assert bool(((x.double() - y.double()).abs() <= 2.01 * R.U32 * y.double().abs()).all())
+    u = R.U[DT[dtype]]
+    x, y = a[3][:n].double() * (big / few), b[3].double()
+    assert bool(((x - y).abs() <= 2.1 * u * y.abs()).all())
