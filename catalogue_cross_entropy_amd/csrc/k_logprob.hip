@@ -83,7 +83,7 @@ struct LpArgs {
   const LpRow* rows;      // LP_DX, LP_DY: of the packed positions
   const int32_t* idc;     // ids of the packed positions
   float* out;             // LP_LSEO, LP_DX, LP_DY: parts.rows
-  int terms;              // bf16 terms of a weight in the products
+  int terms;              // bf16 terms of a weight in the products (2 or 3; 1 with float32 inputs)
 };
 
 // Geometry of a streamed tile: TI rows of RB bytes; 16-byte chunk c of row n is stored at
@@ -185,7 +185,7 @@ template <class E, int D, int NWS> struct LpLds {
 
 // acc[ob][nb] += G[32 owners][32 streamed] . rows[32 streamed][D], lane l holding G[owner l % 32]
 // [streamed lp_row(v) + 4 (l / 32)] in g[ob][v].  bf16: TERMS products, each with the bf16
-// rounding of what the ones before left of G (1: rounded once, 3: all 24 bits).
+// rounding of what the ones before left of G (2: off by at most 2^-16 of a weight, 3: all 24 bits).
 template <class E, int D, int NWS, int OB, int TERMS>
 __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g)[OB], const LpLds<E, D, NWS>& o,
                                            uint32_t base) {
@@ -208,10 +208,31 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
         }
       }
     };
-    u32x4 part[OB][2];
-    if constexpr (TERMS == 1) {
-      term(part);
+    if constexpr (TERMS == 2) {   // both terms against the same fragments: each row of the tile is read once
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        u32x4 hi[OB], lo[OB];
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = g[ob][8 * kk + 2 * e], b = g[ob][8 * kk + 2 * e + 1];
+            hi[ob][e] = pack_bf16(a, b);
+            lo[ob][e] = pack_bf16(a - lo_f32(hi[ob][e]), b - hi_f32(hi[ob][e]));
+          }
+#pragma unroll
+        for (int nb = 0; nb < D / 32; ++nb) {
+          const uint32_t at = o.y[nb % o.NY] + base + (nb / o.NY) * 128 + 16 * kk * T::RB;
+          const s16x4 b[2] = {lds_tr4(at), lds_tr4(at + 8 * T::RB)};
+          const u32x4 bw = __builtin_bit_cast(u32x4, b);
+#pragma unroll
+          for (int ob = 0; ob < OB; ++ob) acc[ob][nb] = LpMma<bf16>::run(hi[ob], bw, acc[ob][nb]);
+#pragma unroll
+          for (int ob = 0; ob < OB; ++ob) acc[ob][nb] = LpMma<bf16>::run(lo[ob], bw, acc[ob][nb]);
+        }
+      }
     } else {
+      u32x4 part[OB][2];
 #pragma unroll 1
       for (int t = 0; t < TERMS; ++t) {
         term(part);
@@ -236,12 +257,16 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
   }
 }
 
-// What of a weight went into the products: all of it, or (one bf16 term) its rounding.
-__device__ __forceinline__ float lp_taken(float g, int terms, bool b16) { return b16 && terms == 1 ? lo_f32(pack_bf16(g, 0.0f)) : g; }
+// What of a weight went into the products: all of it, or (bf16, two terms) its first two bf16 terms.
+__device__ __forceinline__ float lp_taken(float g, int terms, bool b16) {
+  if (!b16 || terms != 2) return g;
+  const float hi = lo_f32(pack_bf16(g, 0.0f));
+  return hi + lo_f32(pack_bf16(g - hi, 0.0f));
+}
 
 // NWO waves along the owners x NWS waves along a tile's rows; OB blocks of 32 owners per wave.
 // A row's own item enters LP_LSEO, LP_DX and LP_DY (bf16) with the others, as -p (..); the joins add what is
-// missing of g - p (..) in float32 (1 - p would lose its digits in a bf16 term), knowing what went in: the
+// missing of g - p (..) in float32 (1 - p would lose its digits in bf16 terms), knowing what went in: the
 // own logits come from the same products, so the same bits.  LP_DY (float32) adds it here.
 template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int TERMS, int MINW>
 __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
@@ -252,7 +277,6 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile
   constexpr bool ACC = MODE != LP_LSE, LSE = MODE == LP_LSE || MODE == LP_LSEO, DY = MODE == LP_DY;
   constexpr bool OWN = DY && sizeof(E) == 4;
-  constexpr bool PIPE = DY && sizeof(E) == 2 && TERMS == 1 && D <= 64;   // needs a second block's registers
   static_assert(T::BYTES % (16 * NT) == 0 && TI <= NT, "whole chunks per thread");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -432,24 +456,12 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     __syncthreads();   // the buffers may be filled again
   };
   auto main_tile = [&](uint32_t base, uint32_t par, uint32_t q0) {
-    if constexpr (PIPE) {
-      // the next block's logits are on the matrix cores while this block's weights are computed
-      f32x16 x[2][OB];
-      logits(x[0], base, q0);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        if (i + 1 < NB) logits(x[(i + 1) & 1], base + (i + 1) * (NWS * 32 * RB), q0 + (i + 1) * NWS * 32);
-        weigh(x[i & 1], par + i * (NWS * 128));
-        if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x[i & 1], lo, base + i * (NWS * 32 * RB));
-      }
-    } else {
 #pragma unroll 1
-      for (int i = 0; i < NB; ++i) {
-        f32x16 x[OB];
-        logits(x, base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
-        weigh(x, par + i * (NWS * 128));
-        if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x, lo, base + i * (NWS * 32 * RB));
-      }
+    for (int i = 0; i < NB; ++i) {
+      f32x16 x[OB];
+      logits(x, base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
+      weigh(x, par + i * (NWS * 128));
+      if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x, lo, base + i * (NWS * 32 * RB));
     }
   };
   auto run = [&]() {
@@ -874,13 +886,13 @@ constexpr int LP_CUS = 256;
 
 // Launch shapes, by the bytes of a row: OB blocks of 32 owners per wave (more: fewer LDS reads per product; fewer:
 // more waves per SIMD to overlap the exponentials with the products), MW waves per SIMD (the registers allow
-// them; the grid fills the card once), NWO waves per workgroup.  us, both sides of each choice:
-//   D 64, 51,200 x 30,000, LP_LSEO / LP_DY:   OB 2 MW 2  338 / 341;  OB 1 MW 4  340 / 386;  OB 1 MW 3  364 / 424
-//   D 128, 8,192 x 30,000, LP_DX / LP_DY:     OB 1 MW 3  138 / 150;  OB 1 MW 2  142 / 157;  OB 2 MW 1  149 / 165;
-//                                             OB 2 MW 2  168 / 254 (spills)
-//   D 256, 4,099 x 50,021, LP_DX / LP_DY:     NWO 8  218 / 298;  NWO 4  254 / 318;  OB 1 MW 1  370 / 413
-//   LP_LSE, MW 3 against 2:                   D 128, 2,047 x 200,000  117 / 127;  D 256, 4,099 x 50,021  120 / 128
-//   PIPE (LP_DY, D 64):                       343 against 359; LP_LSEO has no registers for it (467 against 341)
+// them; the grid fills the card once), NWO waves per workgroup.  Whole calls with bf16 gradients, without / with
+// entropies, us (spills: words per lane that do not fit into registers):
+//   D 64, 51,200 x 30,000:   OB 2 MW 2  958 / 1,256;  OB 1 MW 3  1,050 / 1,333;  OB 1 MW 4  1,144 / 1,484
+//   D 128, 8,192 x 30,000:   OB 1 MW 2  413 / 496;  OB 1 MW 3  462 / 552 (spills 25 to 56);  OB 2 MW 1  418 / 503
+//   D 256, 4,099 x 50,021:   NWO 8  617 / 786;  NWO 4  688 / 848;  NWO 8 MW 1  935 / 1,182 (spills 11 to 43 with MW 2)
+//   LP_LSE, MW 3 against 2:  D 128, 2,047 x 200,000  117 / 127;  D 256, 4,099 x 50,021  120 / 128
+// A second block's logits in flight while the first is weighed gave LP_DY at D 64 less than 1 %, and is not done.
 // Up to 32 OB positions the waves of a workgroup share their owners and split each tile's rows instead (NWS 4;
 // a block of owners that is mostly empty costs as much as a full one): 5 x 1,000,000, LP_LSE 25 against 62.
 template <class E, int D> struct LpShape {
@@ -888,7 +900,7 @@ template <class E, int D> struct LpShape {
   static constexpr int OB_LSE = B && D <= 128 ? 2 : 1;
   static constexpr int MW_LSE = B ? 3 : (D <= 128 ? 3 : 2);
   static constexpr int OB_GRAD = B && D <= 64 ? 2 : 1;
-  static constexpr int MW_GRAD = !B ? (D <= 64 ? 2 : 1) : D == 128 ? 3 : 2;
+  static constexpr int MW_GRAD = !B && D > 64 ? 1 : 2;
   static constexpr int NWO_GRAD = B && D == 256 ? 8 : 4;
   static constexpr int NWS_FEW = D * (int)sizeof(E) <= 256 ? 4 : 1;
   static constexpr int MW_FEW = D * (int)sizeof(E) <= 128 ? 3 : 2;
@@ -985,22 +997,24 @@ hipError_t lp_launch(const LpArgs& a, hipStream_t st) {
   using S = LpShape<E, D>;
   constexpr int NWO = MODE == LP_LSE ? 4 : S::NWO_GRAD;
   constexpr int OB = MODE == LP_LSE ? S::OB_LSE : S::OB_GRAD, MINW = MODE == LP_LSE ? S::MW_LSE : S::MW_GRAD;
-  constexpr bool THREE = sizeof(E) == 2 && MODE != LP_LSE;
+  constexpr bool THREE = sizeof(E) == 2 && MODE != LP_LSE;   // has a variant of three terms
+  constexpr int TERMS = THREE ? 2 : 1;
   if constexpr (MODE != LP_DY && S::NWS_FEW > 1) {
     constexpr int FEW = MINW < S::MW_FEW ? MINW : S::MW_FEW;
     if (a.parts.nws > 1) {
       if constexpr (THREE)
-        if (a.terms != 1) return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 3, FEW>(a, st);
-      return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 1, FEW>(a, st);
+        if (a.terms == 3) return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, 3, FEW>(a, st);
+      return lp_launch_t<E, D, OB, 1, S::NWS_FEW, MODE, ENT, TERMS, FEW>(a, st);
     }
   }
   if constexpr (THREE)
-    if (a.terms != 1) return lp_launch_t<E, D, OB, NWO, 1, MODE, ENT, 3, MINW>(a, st);
-  return lp_launch_t<E, D, OB, NWO, 1, MODE, ENT, 1, MINW>(a, st);
+    if (a.terms == 3) return lp_launch_t<E, D, OB, NWO, 1, MODE, ENT, 3, MINW>(a, st);
+  return lp_launch_t<E, D, OB, NWO, 1, MODE, ENT, TERMS, MINW>(a, st);
 }
 
-// bf16 results take one bf16 term of a weight, float32 results all of its bits.
-template <class E> int lp_terms(uint32_t flags) { return sizeof(E) == 2 && !(flags & RECE_FLAG_BF16_GRADS) ? 3 : 1; }
+// Float32 results take all 24 bits of a weight, bf16 results two bf16 terms: 2^-16 of a weight is 1/256 of the
+// result's own rounding.  (One term, 2^-8, would show in results that are small against their weights' sum.)
+template <class E> int lp_terms(uint32_t flags) { return sizeof(E) == 4 ? 1 : flags & RECE_FLAG_BF16_GRADS ? 2 : 3; }
 
 #define LP_TRY(call)                     \
   do {                                   \

@@ -273,7 +273,9 @@ rece_status rece_embed_backward(void* stream, int64_t n, int64_t C, int32_t d, i
  * Backward (same X, Y, ids, temperature, flags as the forward call that filled the workspace):
  *   dlogp [s], dentropy [s] (or NULL: zero; needs RECE_FLAG_ENTROPY)  float32 upstream gradients
  *   G_ij = (dlogp_i ([j = ids(i)] - p_ij) - dentropy_i p_ij (log p_ij + entropy_i)) / temperature
- *   dX = G Y [s][d], dY = G^T X [C][d]   float32 (bf16 with RECE_FLAG_BF16_GRADS), overwritten */
+ *   dX = G Y [s][d], dY = G^T X [C][d]   float32 (bf16 with RECE_FLAG_BF16_GRADS), overwritten
+ *   Sums are taken in float32.  Of dtype bf16, each p_ij enters the products with all 24 bits for
+ *   float32 gradients, and to 2^-16 of its value for bf16 ones. */
 rece_status rece_logprob_workspace_bytes(int64_t s, int64_t C, int32_t d, int32_t dtype, uint32_t flags, size_t* bytes);
 rece_status rece_logprob_forward(void* stream, int64_t s, int64_t C, int32_t d, int32_t dtype, float temperature,
                                  uint32_t flags, const void* X, const void* Y, const int32_t* ids, void* workspace,
