@@ -608,8 +608,9 @@ hipError_t order_rows(const int32_t* ids, int64_t n, int64_t C, const ClearArgs&
   a.ntot = counts + tiles * ORD_BINS;
   a.clear = clear;
   a.parts = 2 * passes;
-  // workgroups that clear, per launch
-  const int64_t share = clear.n16 / (tiles == 1 ? 1 : a.parts);
+  // workgroups that clear, per launch: one at least where there is anything to clear (a table of one short row is
+  // less than a piece per launch)
+  const int64_t launches = tiles == 1 ? 1 : a.parts, share = (clear.n16 + launches - 1) / launches;
   const int64_t extra = std::min<int64_t>((share + 4 * ORD_THREADS - 1) / (4 * ORD_THREADS), 16384);
   if (tiles == 1) {
     a.kout = buf[0];
