@@ -4,7 +4,10 @@ catalogue, and the policy and preference losses on them (include/rece.h).
 Argument marshalling only, like the rest of the binding: every operator runs in
 librece's HIP kernels, on torch's current stream of the tensors' device unless a
 stream is given.  An operator object holds sizes and options, no device memory;
-workspaces are allocated per call unless the caller passes one.
+workspaces are allocated per call unless the caller passes one.  On a given stream
+a call is that stream's work: what it allocates is that stream's memory, and memory
+of its arguments and results that is freed waits for both streams.  Ordering the
+streams (wait_stream, events) stays with the caller.
 """
 from __future__ import annotations
 
@@ -57,12 +60,38 @@ def _workspace(workspace, nbytes, device):
     return workspace
 
 
-def _call(fn, device, stream, before, after=()):
-    """fn(*before, stream, *after) with `device` current, on `stream` or the device's current one."""
+def _elsewhere(stream, device) -> bool:
+    """Whether a stream is given that is not the device's current one."""
+    import torch
+    if stream is None:
+        return False
+    if stream.device != device:
+        raise ValueError(f"stream must be a stream of {device}")
+    return stream.cuda_stream != torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on_stream(stream, device, method, *args, **kw):
+    """method(*args, **kw) with `stream` current: a workspace that is dropped on return is handed out again to that
+    stream alone, and results lie in no memory that the caller's stream still uses."""
+    import torch
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = method(*args, **kw)
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
+
+def _call(fn, device, before, after):
+    """fn(*before, stream, *after) with `device` current, on its current stream."""
     import torch
     index = device.index
     # the handle itself: torch.cuda.current_stream() makes an object around it, a third of a small call's time
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    s = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
         _check(fn(*before, s, *after))
         return
@@ -86,13 +115,15 @@ class ItemEmbedding:
         """Returns out [n, d] in the table's dtype."""
         import torch
         dev = table.device
+        if _elsewhere(stream, dev):
+            return _on_stream(stream, dev, self.forward, table, ids, out)
         _want("table", table, self._dt, (self.C, self.d))
         _want("ids", ids, torch.int32, (self.n,), dev)
         if out is None:
             out = torch.empty((self.n, self.d), dtype=self._dt, device=dev)
         else:
             _want("out", out, self._dt, (self.n, self.d), dev)
-        _call(lib().rece_embed_forward, dev, stream, (),
+        _call(lib().rece_embed_forward, dev, (),
               (self.n, self.C, self.d, self._code, self.scale, _ptr(table), _ptr(ids), _ptr(out)))
         return out
 
@@ -101,6 +132,8 @@ class ItemEmbedding:
         accumulate=True the gradient is added to the float32 dtable given."""
         import torch
         dev = dout.device
+        if _elsewhere(stream, dev):
+            return _on_stream(stream, dev, self.backward, ids, dout, workspace, dtable, accumulate)
         _want("dout", dout, self._dt, (self.n, self.d))
         _want("ids", ids, torch.int32, (self.n,), dev)
         gdt = torch.bfloat16 if self.bf16_grads else torch.float32
@@ -112,7 +145,7 @@ class ItemEmbedding:
             _want("dtable", dtable, gdt, (self.C, self.d), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev)
         flags = (FLAG_BF16_GRADS if self.bf16_grads else 0) | (FLAG_ACCUMULATE if accumulate else 0)
-        _call(lib().rece_embed_backward, dev, stream, (),
+        _call(lib().rece_embed_backward, dev, (),
               (self.n, self.C, self.d, self._code, self.scale, flags, _ptr(ids), _ptr(dout), _ptr(ws),
                ws.numel() * ws.element_size(), _ptr(dtable)))
         return dtable
@@ -149,13 +182,15 @@ class LogProb:
         """Returns (logp [s], entropy [s] or None, workspace); the workspace feeds backward
         (need_grad=False: it does not, and is smaller)."""
         import torch
-        self._check_inputs(X, Y, ids)
         dev = X.device
+        if _elsewhere(stream, dev):
+            return _on_stream(stream, dev, self.forward, X, Y, ids, workspace, need_grad)
+        self._check_inputs(X, Y, ids)
         flags = self._flags | (0 if need_grad else FLAG_NO_GRAD)
         ws = _workspace(workspace, self.workspace_bytes if need_grad else self.workspace_bytes_no_grad, dev)
         logp = torch.empty(self.s, dtype=torch.float32, device=dev)
         ent = torch.empty(self.s, dtype=torch.float32, device=dev) if self.entropy else None
-        _call(lib().rece_logprob_forward, dev, stream, (),
+        _call(lib().rece_logprob_forward, dev, (),
               (self.s, self.C, self.d, self._code, self.temperature, flags, _ptr(X), _ptr(Y), _ptr(ids), _ptr(ws),
                ws.numel() * ws.element_size(), _ptr(logp), _ptr(ent)))
         return logp, ent, ws
@@ -163,8 +198,10 @@ class LogProb:
     def backward(self, X, Y, ids, workspace, dlogp, dentropy=None, dX=None, dY=None, stream=None):
         """Returns (dX [s, d], dY [C, d]): float32, or bf16 with bf16_grads."""
         import torch
-        self._check_inputs(X, Y, ids)
         dev = X.device
+        if _elsewhere(stream, dev):
+            return _on_stream(stream, dev, self.backward, X, Y, ids, workspace, dlogp, dentropy, dX, dY)
+        self._check_inputs(X, Y, ids)
         gdt = torch.bfloat16 if self.bf16_grads else torch.float32
         _want("dlogp", dlogp, torch.float32, (self.s,), dev)
         if dentropy is not None:
@@ -178,7 +215,7 @@ class LogProb:
         _want("dX", dX, gdt, (self.s, self.d), dev)
         _want("dY", dY, gdt, (self.C, self.d), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev)
-        _call(lib().rece_logprob_backward, dev, stream, (),
+        _call(lib().rece_logprob_backward, dev, (),
               (self.s, self.C, self.d, self._code, self.temperature, self._flags, _ptr(X), _ptr(Y), _ptr(ids), _ptr(ws),
                ws.numel() * ws.element_size(), _ptr(dlogp), _ptr(dentropy), _ptr(dX), _ptr(dY)))
         return dX, dY
@@ -207,6 +244,9 @@ class PolicyLoss:
         None), dentropy where an entropy is given.  grads=False computes none."""
         import torch
         c, dev = self.cfg, logp.device
+        if _elsewhere(stream, dev):
+            return _on_stream(stream, dev, self.forward, logp, old_logp, advantages, offsets, ref_logp, entropy, mask, dloss,
+                              workspace, grads)
         n = (c.n,)
         for name, t in (("logp", logp), ("old_logp", old_logp), ("ref_logp", ref_logp), ("entropy", entropy)):
             if t is not None:
@@ -224,7 +264,7 @@ class PolicyLoss:
         stats = torch.empty(6, dtype=torch.float32, device=dev)
         dlogp = torch.empty(n, dtype=self._dt, device=dev) if grads else None
         dent = torch.empty(n, dtype=self._dt, device=dev) if grads and entropy is not None else None
-        _call(lib().rece_policy_loss, dev, stream, (ctypes.byref(c),),
+        _call(lib().rece_policy_loss, dev, (ctypes.byref(c),),
               (_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(entropy), _ptr(advantages), _ptr(offsets), _ptr(mask),
                _ptr(dloss), _ptr(ws), ws.numel() * ws.element_size(), _ptr(loss), _ptr(stats), _ptr(dlogp),
                _ptr(dent)))
@@ -254,6 +294,8 @@ class PreferenceLoss:
         None: a loss without a reference.  dlogp is the gradient of dloss * loss."""
         import torch
         c, dev = self.cfg, logp.device
+        if _elsewhere(stream, dev):
+            return _on_stream(stream, dev, self.forward, logp, ref_logp, offsets, group_offsets, mask, dloss, workspace, grads)
         n = (c.n,)
         _want("logp", logp, self._dt, n)
         if ref_logp is not None:
@@ -270,7 +312,7 @@ class PreferenceLoss:
         out = torch.empty(1 + c.n_group + c.n_seq, dtype=torch.float32, device=dev)
         loss, loss_pg, rewards = out[:1], out[1:1 + c.n_group], out[1 + c.n_group:]
         dlogp = torch.empty(n, dtype=self._dt, device=dev) if grads else None
-        _call(lib().rece_preference_loss, dev, stream, (ctypes.byref(c),),
+        _call(lib().rece_preference_loss, dev, (ctypes.byref(c),),
               (_ptr(logp), _ptr(ref_logp), _ptr(offsets), _ptr(group_offsets), _ptr(mask), _ptr(dloss), _ptr(ws),
                ws.numel() * ws.element_size(), _ptr(loss), _ptr(loss_pg), _ptr(rewards), _ptr(dlogp)))
         return loss, loss_pg, rewards, dlogp

@@ -24,3 +24,95 @@ def test_embed_gradient_of_a_small_table_is_cleared(n, C, d, bf16_grads):
     ids[n // 2] = C - 1
     got = op.backward(ids, dout, dtable=torch.full((C, d), float("nan"), dtype=gdt, device="cuda"))
     assert bool((got[C - 1] == 1).all()) and not bool(got[:C - 1].any())
+
+
+def _stream_calls():
+    """(name, call(stream) -> results, workspace dropped or not) of every operator, with inputs that stay alive."""
+    g = torch.Generator().manual_seed(31)
+    s, C, d, n, n_seq = 700, 3000, 64, 40000, 1500
+    f = lambda *shape: torch.randn(*shape, generator=g)  # noqa: E731
+    X, Y = f(s, d).bfloat16().cuda(), f(C, d).bfloat16().cuda()
+    ids = torch.randint(-1, C, (s,), generator=g).to(torch.int32).cuda()
+    dlogp = f(s).cuda()
+    eids = torch.randint(0, C, (9000,), generator=g).to(torch.int32).cuda()
+    dout = f(9000, d).bfloat16().cuda()
+    lp, old = (-6.0 * torch.rand(n, generator=g)).cuda(), (-6.0 * torch.rand(n, generator=g)).cuda()
+    offs = torch.sort(torch.randint(0, n + 1, (n_seq + 1,), generator=g)).values.to(torch.int32).cuda()
+    goffs = torch.tensor([0, 800, n_seq], dtype=torch.int32).cuda()   # groups whose sums lie in the workspace
+    adv = f(n_seq).cuda()
+    emb = rece.ItemEmbedding(9000, C, d)
+    lpo = rece.LogProb(s, C, d)
+    pol = rece.PolicyLoss(n, n_seq, reduction="sequence")
+    prf = rece.PreferenceLoss(n, n_seq, 2, kind="softmax")
+
+    def logprob(stream):
+        logp, _, ws = lpo.forward(X, Y, ids, stream=stream)
+        return (logp,) + tuple(lpo.backward(X, Y, ids, ws, dlogp, stream=stream))
+
+    return [("embed rows", lambda st: (emb.forward(Y, eids, stream=st),)),
+            ("embed gradient", lambda st: (emb.backward(eids, dout, stream=st),)),
+            ("log-probabilities", logprob),
+            ("log-probabilities alone", lambda st: lpo.forward(X, Y, ids, need_grad=False, stream=st)[:1]),
+            ("policy", lambda st: pol.forward(lp, old, adv, offs, stream=st)[:3]),
+            ("preference", lambda st: prf.forward(lp, old, offs, goffs, stream=st))]
+
+
+def _busy(stream):
+    """Some milliseconds of work on a stream."""
+    with torch.cuda.stream(stream):
+        a = torch.zeros(4096, 4096, dtype=torch.bfloat16, device="cuda")
+        for _ in range(40):
+            a = a @ a
+        return a
+
+
+def test_a_given_streams_workspace_is_not_handed_out_while_in_use():
+    """A call enqueued on a busy stream, then tensors of every size filled on the current one before it runs."""
+    side = torch.cuda.Stream()
+    for name, call in _stream_calls():
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        print(f"[gpu] {name} on another stream", flush=True)
+        hold = _busy(side)
+        got = call(side)
+        junk = [torch.full((1 << k,), 0xFF, dtype=torch.uint8, device="cuda") for k in range(8, 25) for _ in range(4)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+        del junk, hold
+
+
+def test_a_given_streams_results_lie_in_memory_of_its_own():
+    """Memory freed on the current stream while that still writes it (a queue of work, then fills) is not taken for
+    what the given stream writes at once."""
+    side = torch.cuda.Stream()
+    for name, call in _stream_calls():
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        print(f"[gpu] {name} into memory freed on another stream", flush=True)
+        hold = _busy(torch.cuda.current_stream())
+        junk = [torch.full((t.numel() * t.element_size(),), 0xFF, dtype=torch.uint8, device="cuda") for t in want for _ in range(8)]
+        del junk
+        got = call(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+        del hold
+
+
+def test_a_given_stream_may_be_the_current_one_and_must_be_the_devices():
+    for name, call in _stream_calls():
+        want = call(None)
+        assert all(torch.equal(a, b) for a, b in zip(call(torch.cuda.current_stream()), want)), name
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+    class Elsewhere:
+        device = torch.device("cuda", 99)
+        cuda_stream = 0
+
+    for name, call in _stream_calls():
+        with pytest.raises(ValueError):
+            call(Elsewhere())
