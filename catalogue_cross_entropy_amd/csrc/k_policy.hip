@@ -129,6 +129,29 @@ __device__ __forceinline__ float exp_near(float x) {
   return fabsf(y) < 200.0f ? fmaf(e, rest, e) : e;   // beyond: 0, infinity or NaN as it is
 }
 
+// em = e^u - 1 and kl = e^u - 1 - u.  Differences of e^u keep nothing of a small u, and a policy starts as its
+// reference, so up to |u| = 1 the series u^2 (1/2 + u/6 + ... + u^9/11!) is summed: what it leaves out is below 2^-27
+// of kl, and kl is off by at most 7 roundings (beyond |u| = 1 by 18, of which e^u has most).
+__device__ __forceinline__ void kl_terms(float u, float& em, float& kl) {
+  if (fabsf(u) < 1.0f) {
+    float p = 1.0f / 39916800.0f;
+    p = fmaf(p, u, 1.0f / 3628800.0f);
+    p = fmaf(p, u, 1.0f / 362880.0f);
+    p = fmaf(p, u, 1.0f / 40320.0f);
+    p = fmaf(p, u, 1.0f / 5040.0f);
+    p = fmaf(p, u, 1.0f / 720.0f);
+    p = fmaf(p, u, 1.0f / 120.0f);
+    p = fmaf(p, u, 1.0f / 24.0f);
+    p = fmaf(p, u, 1.0f / 6.0f);
+    p = fmaf(p, u, 0.5f);
+    kl = u * u * p;
+    em = u + kl;
+  } else {
+    em = exp_near(u) - 1.0f;
+    kl = em - u;
+  }
+}
+
 // One token of weight w and advantage A.
 __device__ __forceinline__ PolTerm pol_token(const PolArgs& a, const PolToken& k, float w, float A) {
   PolTerm o;
@@ -146,11 +169,10 @@ __device__ __forceinline__ PolTerm pol_token(const PolArgs& a, const PolToken& k
   // without a coefficient a term is no part of the loss, whatever its value
   o.loss = o.pg;
   if (a.ref) {
-    const float u = k.ref - k.lp;
-    const float eu = exp_near(u);
-    o.kl = eu - u - 1.0f;
+    float em;
+    kl_terms(k.ref - k.lp, em, o.kl);
     if (a.c.kl_coef != 0.0f) {
-      g = fmaf(a.c.kl_coef, 1.0f - eu, g);
+      g = fmaf(-a.c.kl_coef, em, g);
       o.loss = fmaf(a.c.kl_coef, o.kl, o.loss);
     }
   }
