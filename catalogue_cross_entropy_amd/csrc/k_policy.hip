@@ -159,9 +159,13 @@ __device__ __forceinline__ PolTerm pol_token(const PolArgs& a, const PolToken& k
   const float diff = k.lp - k.old;
   o.r = exp_near(diff);
   const float bound = A > 0.0f ? hi : lo;
-  // decided on the logarithms: the difference is exact where the ratio is near its bounds, but the ratio itself is
-  // rounded, and one token in millions would fall on the other side
-  o.clipped = (A > 0.0f && diff - a.log_hi > a.log_hi2) || (A < 0.0f && diff - a.log_lo < a.log_lo2);
+  // Decided on the logarithms, with what the difference's rounding left (it is exact where the two are within a factor
+  // of two, not for log-probabilities near 0) and what the bounds' left: the ratio itself is rounded, and tokens near
+  // a bound would fall on the other side.  An infinite difference has no remainder.
+  const float back = diff - k.lp;
+  float rest = (k.lp - (diff - back)) - (k.old + back);
+  rest = rest == rest ? rest : 0.0f;
+  o.clipped = (A > 0.0f && diff - a.log_hi > a.log_hi2 - rest) || (A < 0.0f && diff - a.log_lo < a.log_lo2 - rest);
   o.pg = -A * (o.clipped ? bound : o.r);
   float g = o.clipped ? 0.0f : o.pg;
   o.kl = 0.0f;
@@ -1075,9 +1079,10 @@ hipError_t policy_loss(const rece_policy_config& c, const void* logp, const void
   a.stats = stats;
   a.dlogp = dlogp;
   a.dentropy = dentropy;
+  // clip_low = 1: a bound of 0 that no ratio is below, so its logarithm is minus infinity, with nothing left
   const double lo = c.clip_low < 1.0f ? std::log1p(-(double)c.clip_low) : -HUGE_VAL, hi = std::log1p((double)c.clip_high);
   a.log_lo = (float)lo;
-  a.log_lo2 = (float)(lo - (double)a.log_lo);
+  a.log_lo2 = c.clip_low < 1.0f ? (float)(lo - (double)a.log_lo) : 0.0f;
   a.log_hi = (float)hi;
   a.log_hi2 = (float)(hi - (double)a.log_hi);
   return c.dtype == RECE_BF16 ? policy_t<bf16>(a, ws, st) : policy_t<float>(a, ws, st);

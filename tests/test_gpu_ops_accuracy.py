@@ -1,4 +1,5 @@
 """How near the operators come to their 64-bit forms where float32 or bf16 intermediates would show."""
+import numpy as np
 import pytest
 import torch
 
@@ -65,3 +66,45 @@ def test_policy_kl_of_a_policy_that_is_its_reference(n, dtype):
     loss, stats, dlp, _ = op.forward(lp, lp, torch.zeros(1, device="cuda"),
                                      torch.tensor([0, n], dtype=torch.int32, device="cuda"), ref_logp=lp)
     assert float(loss) == 0.0 and float(stats[1]) == 0.0 and not bool(dlp.any())
+
+
+@pytest.mark.parametrize("n", [4000, 40000])
+def test_policy_clips_on_the_right_side_with_old_log_probabilities(n):
+    """Log-probabilities near 0 and old ones a few steps around the bounds: their float32 difference is rounded, the
+    side of the bound is that of the difference of the values themselves (64 bits hold it)."""
+    g = np.random.default_rng(n)
+    low = high = float(np.float32(0.2))
+    half = n // 2
+    lp = -g.uniform(1e-4, 0.05, n).astype(np.float32)
+    lp[:half] -= np.float32(0.25)   # a ratio below 1 - low: the old one is the one near 0
+    bound = np.where(np.arange(n) < half, np.log1p(-low), np.log1p(high))
+    old = (lp.astype(np.float64) - bound).astype(np.float32)
+    old = (old.view(np.int32) + g.integers(-2, 3, n, dtype=np.int32)).view(np.float32)
+    diff = lp.astype(np.float64) - old.astype(np.float64)
+    clipped = torch.from_numpy(np.where(np.arange(n) < half, diff < bound, diff > bound))
+    assert 0.2 * n < int(clipped.sum()) < 0.8 * n and float(np.abs(diff - bound).min()) > 1e-14
+    rounded = (lp - old).astype(np.float64)
+    assert (np.where(np.arange(n) < half, rounded < bound, rounded > bound) != clipped.numpy()).sum() > n // 100
+    A = torch.cat([torch.full((half,), -1.0), torch.ones(n - half)]).cuda()
+    op = rece.PolicyLoss(n, 1, clip_low=0.2, clip_high=0.2, token_advantage=True)
+    _, stats, dlp, _ = op.forward(torch.from_numpy(lp).cuda(), torch.from_numpy(old).cuda(), A,
+                                  torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    assert torch.equal(dlp.cpu() == 0, clipped)
+    assert abs(float(stats[3]) - float(clipped.double().mean())) <= R.U32
+
+
+def test_policy_without_a_lower_bound():
+    """clip_low = 1 bounds nothing: ratios down to 0 pass with a negative advantage."""
+    lp = torch.tensor([-1.0, -50.0, -300.0, float("-inf")]).repeat(2500)
+    for n in (4, 10000):
+        op = rece.PolicyLoss(n, 1, clip_low=1.0, clip_high=0.2)
+        _, stats, dlp, _ = op.forward(lp[:n].cuda(), torch.zeros(n, device="cuda"), torch.tensor([-1.0], device="cuda"),
+                                      torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+        assert float(stats[3]) == 0.0
+        want = lp[:n].double().exp() / n
+        assert bool(((dlp.cpu().double() - want).abs() <= 9 * R.U32 * want + 1e-35).all())
+    # and a ratio of 0 is below any other
+    op = rece.PolicyLoss(4, 1, clip_low=0.9, clip_high=0.2)
+    _, stats, dlp, _ = op.forward(lp[:4].cuda(), torch.zeros(4, device="cuda"), torch.tensor([-1.0], device="cuda"),
+                                  torch.tensor([0, 4], dtype=torch.int32, device="cuda"))
+    assert float(stats[3]) == 0.75 and (dlp == 0).tolist() == [False, True, True, True]
