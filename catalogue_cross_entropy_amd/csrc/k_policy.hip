@@ -754,8 +754,10 @@ __device__ __forceinline__ double pair_loss(const rece_preference_config& c, dou
     dz = 2.0 * v / b;
     return v * v;
   }
-  dz = z < 1.0 ? -1.0 : 0.0;
-  return fmax(0.0, 1.0 - z);
+  // comparisons that leave a NaN a NaN
+  const double v = 1.0 - z;
+  dz = v > 0.0 ? -1.0 : v <= 0.0 ? 0.0 : v;
+  return v < 0.0 ? 0.0 : v;
 }
 
 constexpr int PREF_LDS = 512;   // sequences of a group whose h lies in LDS
