@@ -612,8 +612,9 @@ __global__ __launch_bounds__(POL_SMALL_THREADS) void k_pol_small(PolArgs a) {
       dlp = o.dlp;
       dent = o.dent;
     }
-    if (a.dlogp) put(static_cast<E*>(a.dlogp), t, up * dlp);
-    if (a.dentropy) put(static_cast<E*>(a.dentropy), t, up * dent);
+    const bool live = sq[q] >= 0;   // others get 0 whatever dloss is
+    if (a.dlogp) put(static_cast<E*>(a.dlogp), t, live ? up * dlp : 0.0f);
+    if (a.dentropy) put(static_cast<E*>(a.dentropy), t, live ? up * dent : 0.0f);
   }
   double v[POL_SUMS];
   s.get(v);

@@ -31,3 +31,20 @@ def test_preference_nan_is_not_swallowed(kind, G, per, which):
     assert math.isnan(float(loss)) and torch.equal(pg.isnan().cpu(), group)
     assert torch.equal(dlp.isnan().cpu().view(G, -1), group[:, None].expand(G, 2 * per))
     assert torch.equal(rewards.isnan().cpu(), torch.arange(2 * G) == 6 + which)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [300, 20000])
+@pytest.mark.parametrize("up", [float("inf"), float("nan")])
+def test_policy_tokens_that_do_not_count_get_zero_whatever_dloss_is(n, up, dtype):
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    lp = (-torch.rand(n, generator=torch.Generator().manual_seed(n))).to(dt).cuda()
+    mask = torch.arange(n, device="cuda") % 3 > 0
+    offs = torch.tensor([5, n // 2, n - 4], dtype=torch.int32, device="cuda")
+    op = rece.PolicyLoss(n, 2, entropy_coef=0.1, dtype=dtype)
+    _, _, dlp, dH = op.forward(lp, lp, torch.ones(2, device="cuda"), offs, entropy=-lp, mask=mask,
+                               dloss=torch.tensor([up], device="cuda"))
+    at = torch.arange(n, device="cuda")
+    on = mask & (at >= 5) & (at < n - 4)
+    for v in (dlp, dH):
+        assert not bool(v[~on].any()) and not bool(v[on].isfinite().any())
