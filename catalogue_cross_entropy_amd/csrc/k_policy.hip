@@ -741,6 +741,9 @@ __device__ __forceinline__ void pref_grad(const PrefArgs& a, PrefSeq seq, int su
   }
 }
 
+// e^(v - top) with top the largest: 1 for v = top, also where both are infinite.
+__device__ __forceinline__ double exp_below(double v, double top) { return exp(v == top ? 0.0 : v - top); }
+
 __device__ __forceinline__ double softplus_d(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
 
 // Loss of one pair and its derivative by z.
@@ -748,7 +751,8 @@ __device__ __forceinline__ double pair_loss(const rece_preference_config& c, dou
   if (c.kind == RECE_PREF_SIGMOID) {
     const double e = c.smoothing;
     dz = 1.0 / (1.0 + exp(-z)) - (1.0 - e);
-    return (1.0 - e) * softplus_d(-z) + e * softplus_d(z);
+    // without smoothing its term is no part of the loss, also where z is infinite (an item of no probability)
+    return (1.0 - e) * softplus_d(-z) + (e > 0.0 ? e * softplus_d(z) : 0.0);
   }
   if (c.kind == RECE_PREF_IPO) {
     const double b = c.beta, v = z / b - 0.5 / b;
@@ -851,7 +855,7 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
         for (int64_t k = 1 + l; k < m; k += WAVE) top = fmax(top, -z_of(k));
         top = wave_max_d(top);
         for (int64_t k = 1 + l; k < m; k += WAVE) {
-          const double e = exp(-z_of(k) - top);
+          const double e = exp_below(-z_of(k), top);
           others += e;
           hs[k] = e;
         }
@@ -926,7 +930,7 @@ __global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int
           others *= exp(top - v);
           top = v;
         }
-        others += exp(v - top);
+        others += exp_below(v, top);
       }
       const double tot = others + exp(-top);
       if (m > 1) {
@@ -936,7 +940,7 @@ __global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int
       if (a.dlogp)
         for (int64_t k = 1; k < m; ++k) {
           read(k);
-          grad(exp(margin - beta * (hc - h[0]) - top) / tot);
+          grad(exp_below(margin - beta * (hc - h[0]), top) / tot);
         }
     } else {
       for (int64_t k = 1; k < m; ++k) {

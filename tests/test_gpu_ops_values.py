@@ -48,3 +48,35 @@ def test_policy_tokens_that_do_not_count_get_zero_whatever_dloss_is(n, up, dtype
     on = mask & (at >= 5) & (at < n - 4)
     for v in (dlp, dH):
         assert not bool(v[~on].any()) and not bool(v[on].isfinite().any())
+
+
+@pytest.mark.parametrize("G,per", [(4, 1), (4, 80), (9000, 1), (9000, 5)])
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_preference_of_an_impossible_rejected_sequence(kind, G, per):
+    """A rejected sequence of log-probability minus infinity: that group's loss is 0 and moves nothing."""
+    offs, goffs = _pairs(G, per)
+    n = G * 2 * per
+    lp = -torch.rand(n, generator=torch.Generator().manual_seed(3))
+    lp[(2 * 2 + 1) * per] = float("-inf")
+    loss, pg, _, dlp = rece.PreferenceLoss(n, 2 * G, G, kind=kind).forward(lp.cuda(), None, offs, goffs)
+    assert float(pg[2]) == 0.0 and bool(pg.isfinite().all()) and math.isfinite(float(loss))
+    grads = dlp.view(G, -1)
+    assert not bool(grads[2].any()) and bool(grads[:2].all()) and bool(grads.isfinite().all())
+
+
+@pytest.mark.parametrize("G,per", [(4, 1), (4, 80), (9000, 1), (9000, 5)])
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax", "hinge"])
+@pytest.mark.parametrize("members", [2, 3])
+def test_preference_of_an_impossible_preferred_sequence(kind, G, per, members):
+    """A preferred sequence of log-probability minus infinity: an infinite loss, with the slope it has there."""
+    offs, goffs = _pairs(G, per, members)
+    n = G * members * per
+    lp = -torch.rand(n, generator=torch.Generator().manual_seed(4))
+    lp[2 * members * per] = float("-inf")
+    op = rece.PreferenceLoss(n, members * G, G, beta=0.5, kind=kind)
+    loss, pg, _, dlp = op.forward(lp.cuda(), None, offs, goffs)
+    assert float(pg[2]) == math.inf and float(loss) == math.inf and bool(pg.isfinite().cpu()[torch.arange(G) != 2].all())
+    got = dlp.view(G, members, per)[2].cpu().double()
+    want = torch.full((members, per), 0.5 / G / (members - 1), dtype=torch.float64)
+    want[0] = -0.5 / G
+    assert bool(((got - want).abs() <= 2.0 ** -23 * want.abs()).all())
