@@ -3,8 +3,8 @@
 // groups of sequences.  Formulas in include/rece.h.  Both are bound by memory: a token is
 // a few floats read and one written, and every token is touched once (the policy loss
 // reads the mask a second time, for the number of tokens its mean divides by).
-// Sums are taken in float64 (four tokens of the policy loss in float32 first): a float32 sum
-// over millions of tokens would lose the small differences these losses are made of.
+// Sums and the weights of a mean are float64, token by token: a float32 sum over millions of tokens would lose the
+// small differences these losses are made of, and one weight rounded to float32 would be off for all tokens alike.
 //
 // Measured (MI355X), kernels back to back:
 //   policy, 4.2M tokens float32 in 8,192 sequences, KL, mask: mean over tokens 32 us (75 MB; the tile kernel 27 us,
@@ -115,7 +115,7 @@ struct PolToken {
 };
 // What it adds to the sums, and its gradients by logp and entropy (without dloss).
 struct PolTerm {
-  float loss, pg, kl, H, r;
+  float loss, pg, kl, H, r;   // loss: without the weight
   bool clipped;
   float dlp, dent;
 };
@@ -184,33 +184,23 @@ __device__ __forceinline__ PolTerm pol_token(const PolArgs& a, const PolToken& k
     o.H = k.H;
     if (a.c.entropy_coef != 0.0f) o.loss = fmaf(-a.c.entropy_coef, o.H, o.loss);
   }
-  o.loss *= w;
   o.dlp = w * g;
   o.dent = -a.c.entropy_coef * w;
   return o;
 }
 
-// Sums of a thread's tokens.  Up to four are added in float32 first (their terms carry a float32 rounding each
-// as it is; a float64 addition of each costs as much as the rest of the token), then in float64.
+// Sums of a thread's tokens.
 struct PolSums {
   double v[5] = {};   // loss, pg, kl, entropy, ratio
-  float f[5] = {};
   int clipped = 0, tokens = 0;
-  __device__ __forceinline__ void add(const PolTerm& o, bool on) {
-    f[0] += on ? o.loss : 0.0f;
-    f[1] += on ? o.pg : 0.0f;
-    f[2] += on ? o.kl : 0.0f;
-    f[3] += on ? o.H : 0.0f;
-    f[4] += on ? o.r : 0.0f;
+  __device__ __forceinline__ void add(const PolTerm& o, bool on, double w) {
+    v[0] = fma((double)(on ? o.loss : 0.0f), w, v[0]);
+    v[1] += on ? o.pg : 0.0f;
+    v[2] += on ? o.kl : 0.0f;
+    v[3] += on ? o.H : 0.0f;
+    v[4] += on ? o.r : 0.0f;
     clipped += on && o.clipped ? 1 : 0;
     tokens += on ? 1 : 0;
-  }
-  __device__ __forceinline__ void flush() {
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      v[k] += f[k];
-      f[k] = 0.0f;
-    }
   }
   __device__ __forceinline__ void get(double (&o)[POL_SUMS]) const {
     o[0] = v[0], o[1] = v[1], o[2] = v[2], o[3] = v[3], o[4] = clipped, o[5] = v[4], o[6] = tokens;
@@ -367,7 +357,8 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
   static_assert(STEPS % GROUP == 0, "tile");
   __shared__ double sh[POL_THREADS / WAVE][POL_SUMS];
   __shared__ int32_t soff[POL_LDS_SEQ + 1];
-  __shared__ float sadv[POL_LDS_SEQ], sw[POL_LDS_SEQ];
+  __shared__ float sadv[POL_LDS_SEQ];
+  __shared__ double sw[POL_LDS_SEQ];
   __shared__ int64_t srange[2];
   __shared__ int scount[2][POL_THREADS / WAVE];
   const uint32_t n = (uint32_t)a.c.n, ns = (uint32_t)a.c.n_seq;   // below 2^31: a tile beyond fits in 32 bits
@@ -438,10 +429,10 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
       with += scount[1][w];
     }
   }
-  const float wt = 1.0f / (float)max(tokens, 1), nonempty = (float)max(with, 1);
+  const double wt = 1.0 / (double)max(tokens, 1), nonempty = (double)max(with, 1);
   const uint32_t s0 = need_seq ? (uint32_t)srange[0] : 0, s1 = need_seq ? max(s0, (uint32_t)srange[1]) : 0;
   const bool in_lds = s1 - s0 < POL_LDS_SEQ;
-  auto weight_of = [&](uint32_t sq) { return per_seq ? 1.0f / ((float)max(a.cnt[sq], 1) * nonempty) : wt; };
+  auto weight_of = [&](uint32_t sq) { return per_seq ? 1.0 / ((double)max(a.cnt[sq], 1) * nonempty) : wt; };
   if (need_seq && in_lds)
     for (uint32_t q = tid; q <= s1 - s0 + 1; q += POL_THREADS) {
       soff[q] = a.offs[s0 + q];
@@ -459,7 +450,8 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
     for (int u = 0; u < GROUP; ++u) {
       const uint32_t t = base + ((g + u) * POL_THREADS + tid) * W;
       if (t >= n) continue;
-      float dlp[W], dent[W], A[W], w[W];
+      float dlp[W], dent[W], A[W];
+      double w[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         A[e] = 0.0f;
@@ -496,12 +488,11 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
       for (int e = 0; e < W; ++e) {
         const bool live = (on[u] >> (8 * e)) & 0x80u;
         if (!seq_adv) A[e] = live ? a.adv[t + e] : 0.0f;
-        const PolTerm o = pol_token(a, PolToken{lp[u][e], old[u][e], ref[u][e], ent[u][e]}, w[e], A[e]);
-        s.add(o, live);   // what lies at a token that does not count is selected away, NaN included
+        const PolTerm o = pol_token(a, PolToken{lp[u][e], old[u][e], ref[u][e], ent[u][e]}, (float)w[e], A[e]);
+        s.add(o, live, w[e]);   // what lies at a token that does not count is selected away, NaN included
         dlp[e] = live ? up * o.dlp : 0.0f;
         dent[e] = live ? up * o.dent : 0.0f;
       }
-      if (W > 1) s.flush();
       if (t + W <= n) {
         if (a.dlogp) store_tokens<W>(static_cast<E*>(a.dlogp), t, dlp);
         if (a.dentropy) store_tokens<W>(static_cast<E*>(a.dentropy), t, dent);
@@ -514,7 +505,6 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_main(PolArgs a) {
           }
       }
     }
-    s.flush();
   }
   double v[POL_SUMS];
   s.get(v);
@@ -596,7 +586,7 @@ __global__ __launch_bounds__(POL_SMALL_THREADS) void k_pol_small(PolArgs a) {
     for (int i = threadIdx.x; i < ns; i += POL_SMALL_THREADS) with += cnt[i] > 0 ? 1.0 : 0.0;
     with = block_sum_d<POL_SMALL_THREADS>(with, sh);
   }
-  const float wt = 1.0f / (float)fmax(tokens, 1.0), nonempty = (float)fmax(with, 1.0);
+  const double wt = 1.0 / fmax(tokens, 1.0), nonempty = fmax(with, 1.0);
   const float up = a.dloss ? a.dloss[0] : 1.0f;
   PolSums s;
 #pragma unroll
@@ -605,10 +595,9 @@ __global__ __launch_bounds__(POL_SMALL_THREADS) void k_pol_small(PolArgs a) {
     if (t >= n) break;
     float dlp = 0.0f, dent = 0.0f;
     if (sq[q] >= 0) {
-      const float w = per_seq ? 1.0f / ((float)cnt[sq[q]] * nonempty) : wt;
-      const PolTerm o = pol_token(a, k[q], w, A[q]);
-      s.add(o, true);
-      s.flush();
+      const double w = per_seq ? 1.0 / ((double)cnt[sq[q]] * nonempty) : wt;
+      const PolTerm o = pol_token(a, k[q], (float)w, A[q]);
+      s.add(o, true, w);
       dlp = o.dlp;
       dent = o.dent;
     }

@@ -108,3 +108,41 @@ def test_policy_without_a_lower_bound():
     _, stats, dlp, _ = op.forward(lp[:4].cuda(), torch.zeros(4, device="cuda"), torch.tensor([-1.0], device="cuda"),
                                   torch.tensor([0, 4], dtype=torch.int32, device="cuda"))
     assert float(stats[3]) == 0.75 and (dlp == 0).tolist() == [False, True, True, True]
+
+
+@pytest.mark.parametrize("n", [16, 8000, 40000, 300000])
+@pytest.mark.parametrize("reduction", ["token", "sequence"])
+@pytest.mark.parametrize("lead", [0, 1])
+def test_policy_sums_lose_nothing(n, reduction, lead):
+    """Terms that cancel across neighbouring tokens (advantages 1e8, 1, -1e8, 1, ratios of 1): the sums are exact in
+    64 bits, so loss and mean are off by their own rounding and that of a 64-bit weight."""
+    A = torch.tensor([1e8, 1.0, -1e8, 1.0]).repeat(n // 4)
+    lp = torch.full((n + lead,), -1.0, device="cuda")[lead:]
+    op = rece.PolicyLoss(n, 2, reduction=reduction, token_advantage=True)
+    offs = torch.tensor([0, n // 4, n], dtype=torch.int32, device="cuda")
+    loss, stats, _, _ = op.forward(lp, lp, A.cuda(), offs)
+    # the plain sum is one of whole numbers below 2^53.  Weighted: a thread's 16 additions and some ten levels of joins,
+    # each off by 2^-53 of at most 1e8 times the number of tokens so far, weights of at most 2 / n: below 60 of them
+    most = 64 * 2.0 ** -53 * 1e8 + R.U32
+    assert abs(float(loss) + 0.5) <= most and abs(float(stats[0]) + 0.5) <= most
+
+
+@pytest.mark.parametrize("n,n_seq", [(7000, 3), (50001, 3), (400003, 7), (50001, 5000)])
+@pytest.mark.parametrize("reduction", ["token", "sequence"])
+def test_policy_loss_is_off_by_its_own_rounding(n, n_seq, reduction):
+    """Ratios of 1 leave no rounding in the terms: the loss is the float64 mean of the advantages, rounded once."""
+    g = torch.Generator().manual_seed(n)
+    cut = torch.sort(torch.randint(0, n + 1, (n_seq + 1,), generator=g)).values
+    cut[0], cut[-1] = 0, n
+    mask = torch.rand(n, generator=g) < 0.7
+    A = 1.0 + torch.rand(n, generator=g)
+    lp = torch.full((n,), -2.0, device="cuda")
+    op = rece.PolicyLoss(n, n_seq, reduction=reduction, token_advantage=True)
+    loss, stats, _, _ = op.forward(lp, lp, A.cuda(), cut.to(torch.int32).cuda(), mask=mask.cuda())
+    seq = R.seq_of_tokens(cut, n)
+    on = mask & (seq >= 0)
+    count = torch.zeros(n_seq, dtype=torch.float64).index_add_(0, seq[on], torch.ones(int(on.sum()), dtype=torch.float64))
+    w = 1.0 / on.sum().double() if reduction == "token" else 1.0 / (count[seq[on]] * (count > 0).sum())
+    want = -float((A[on].double() * w).sum())
+    assert abs(float(loss) - want) <= (R.U32 + 1e-12) * abs(want)
+    assert abs(float(stats[0]) + float(A[on].double().mean())) <= (R.U32 + 1e-12) * abs(want) * 1.5
