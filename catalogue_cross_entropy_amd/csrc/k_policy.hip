@@ -618,8 +618,9 @@ struct PrefArgs {
   const int32_t *offs, *goffs;
   const uint8_t* mask;
   const float* dloss;
+  double* group_loss;   // [n_group]
   double* h;            // [n_seq]
-  float* share;         // [n_seq] 1, or 1 / tokens that count (average)
+  double* share;        // [n_seq] 1, or 1 / tokens that count (average)
   float *loss, *loss_pg, *rewards;
   void* dlogp;
 };
@@ -645,7 +646,7 @@ __device__ __forceinline__ uint32_t pref_in(PrefSeq q, uint32_t t) {
 
 // h of K sequences by L lanes (all of them get them); the K sequences' tokens are requested together.
 template <class E, int L, int W, int K>
-__device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)[K], int sub, double (&s)[K], float (&share)[K]) {
+__device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)[K], int sub, double (&s)[K], double (&share)[K]) {
   const E* lp = static_cast<const E*>(a.logp);
   const E* rf = static_cast<const E*>(a.ref);
   const uint32_t n = (uint32_t)a.c.n;
@@ -700,11 +701,11 @@ __device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)
     for (int q = 0; q < K; ++q) s[q] += __shfl_xor(s[q], o);
 #pragma unroll
   for (int q = 0; q < K; ++q) {
-    share[q] = 1.0f;
+    share[q] = 1.0;
     if (a.c.average) {
 #pragma unroll
       for (int o = L / 2; o >= 1; o >>= 1) c[q] += __shfl_xor(c[q], o);
-      share[q] = 1.0f / (float)max(c[q], 1);
+      share[q] = 1.0 / (double)max(c[q], 1);
       s[q] /= (double)max(c[q], 1);
     }
   }
@@ -770,8 +771,7 @@ __device__ __forceinline__ void pref_outside(const PrefArgs& a, int64_t b, int64
     const int64_t i = k < first ? k : end + (k - first);
     if (i >= nseq) break;
     const PrefSeq seq[1] = {pref_seq(a.offs, i, a.c.n)};
-    double h[1];
-    float share[1];
+    double h[1], share[1];
     pref_sum<E, L, W, 1>(a, seq, sub, h, share);
     if (sub == 0) a.rewards[i] = (float)((double)beta * h[0]);
     if (a.dlogp) pref_grad<E, L, W>(a, seq[0], sub, 0.0f);
@@ -789,7 +789,7 @@ template <class E, int L, int W, int NT>
 __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   constexpr int NS = NT / L;   // sequences at a time
   __shared__ double sh_h[PREF_LDS];
-  __shared__ float sh_share[PREF_LDS];
+  __shared__ double sh_share[PREF_LDS];
   __shared__ int32_t sh_offs[PREF_LDS + 1];
   const int64_t G = a.c.n_group, nseq = a.c.n_seq;
   const int q = threadIdx.x / L, sub = threadIdx.x % L;
@@ -811,8 +811,7 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   auto seq_at = [&](int64_t k) { return in_lds ? pref_seq(sh_offs, k, a.c.n) : pref_seq(a.offs, s0 + k, a.c.n); };
   for (int64_t k = q; k < m; k += 2 * NS) {
     const PrefSeq seq[2] = {seq_at(k), k + NS < m ? seq_at(k + NS) : PrefSeq{0, 0}};
-    double h[2];
-    float share[2];
+    double h[2], share[2];
     pref_sum<E, L, W, 2>(a, seq, sub, h, share);
     if (sub != 0) continue;
 #pragma unroll
@@ -832,7 +831,7 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   __syncthreads();
   // The first wave takes the group's loss, a member per lane, and leaves the derivatives by h where the h were.
   double* hs = in_lds ? sh_h : a.h + s0;
-  const float* shares = in_lds ? sh_share : a.share + s0;
+  const double* shares = in_lds ? sh_share : a.share + s0;
   if (threadIdx.x < WAVE) {
     const int l = lane_id();
     double loss = 0.0, dc = 0.0;
@@ -866,13 +865,14 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
     }
     if (l == 0) {
       a.loss_pg[g] = (float)loss;
+      a.group_loss[g] = loss;
       if (m > 0) hs[0] = dc;
     }
   }
   if (!a.dlogp) return;
   __syncthreads();
   const double up = (double)beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G;
-  for (int64_t k = q; k < m; k += NS) pref_grad<E, L, W>(a, seq_at(k), sub, (float)(hs[k] * up * (double)shares[k]));
+  for (int64_t k = q; k < m; k += NS) pref_grad<E, L, W>(a, seq_at(k), sub, (float)(hs[k] * up * shares[k]));
 }
 
 // Many small groups: T lanes take a group, its sequences one after the other.
@@ -893,20 +893,19 @@ __global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int
   const double beta = a.c.beta, margin = a.c.margin;
   const double up = beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G, per = m > 1 ? 1.0 / (double)(m - 1) : 0.0;
   PrefSeq seq[1];
-  double h[1];
-  float share[1];
+  double h[1], share[1];
   auto read = [&](int64_t k) {
     seq[0] = pref_seq(a.offs, s0 + k, a.c.n);
     pref_sum<E, T, W, 1>(a, seq, sub, h, share);
   };
   auto grad = [&](double dh) {   // of the sequence read last
-    if (a.dlogp) pref_grad<E, T, W>(a, seq[0], sub, (float)(dh * up * (double)share[0]));
+    if (a.dlogp) pref_grad<E, T, W>(a, seq[0], sub, (float)(dh * up * share[0]));
   };
   double loss = 0.0, dc = 0.0;
   if (m > 0) {
     read(0);
     const double hc = h[0];
-    const float share0 = share[0];
+    const double share0 = share[0];
     const PrefSeq seq0 = seq[0];
     if (sub == 0) a.rewards[s0] = (float)(beta * hc);
     if (a.c.kind == RECE_PREF_SOFTMAX) {
@@ -947,7 +946,10 @@ __global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int
     share[0] = share0;
     grad(dc);
   }
-  if (sub == 0) a.loss_pg[g] = (float)loss;
+  if (sub == 0) {
+    a.loss_pg[g] = (float)loss;
+    a.group_loss[g] = loss;
+  }
 }
 
 constexpr int PREF_MEAN_THREADS = 1024;
@@ -955,7 +957,7 @@ __global__ __launch_bounds__(PREF_MEAN_THREADS) void k_pref_mean(PrefArgs a) {
   __shared__ double sh[PREF_MEAN_THREADS / WAVE];
   double v = 0.0;
 #pragma unroll 4
-  for (int64_t g = threadIdx.x; g < a.c.n_group; g += PREF_MEAN_THREADS) v += a.loss_pg[g];
+  for (int64_t g = threadIdx.x; g < a.c.n_group; g += PREF_MEAN_THREADS) v += a.group_loss[g];
   v = block_sum_d<PREF_MEAN_THREADS>(v, sh);
   if (threadIdx.x == 0) a.loss[0] = (float)(v / (double)a.c.n_group);
 }
@@ -1085,8 +1087,9 @@ hipError_t policy_loss(const rece_policy_config& c, const void* logp, const void
 }
 
 size_t preference_workspace_bytes(const rece_preference_config& c) {
-  if (c.n_seq <= PREF_LDS) return 16;   // every group's values fit into LDS
-  return align256((size_t)c.n_seq * 8) + align256((size_t)c.n_seq * 4);
+  const size_t groups = align256((size_t)c.n_group * 8);
+  if (c.n_seq <= PREF_LDS) return groups;   // every group's members fit into LDS
+  return groups + 2 * align256((size_t)c.n_seq * 8);
 }
 
 hipError_t preference_loss(const rece_preference_config& c, const void* logp, const void* ref, const int32_t* offsets,
@@ -1100,8 +1103,9 @@ hipError_t preference_loss(const rece_preference_config& c, const void* logp, co
   a.goffs = group_offsets;
   a.mask = mask;
   a.dloss = dloss;
-  a.h = static_cast<double*>(ws);
-  a.share = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)c.n_seq * 8));
+  a.group_loss = static_cast<double*>(ws);
+  a.h = reinterpret_cast<double*>(static_cast<char*>(ws) + align256((size_t)c.n_group * 8));
+  a.share = reinterpret_cast<double*>(static_cast<char*>(ws) + align256((size_t)c.n_group * 8) + align256((size_t)c.n_seq * 8));
   a.loss = loss;
   a.loss_pg = loss_pg;
   a.rewards = rewards;

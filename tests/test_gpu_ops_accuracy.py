@@ -146,3 +146,52 @@ def test_policy_loss_is_off_by_its_own_rounding(n, n_seq, reduction):
     want = -float((A[on].double() * w).sum())
     assert abs(float(loss) - want) <= (R.U32 + 1e-12) * abs(want)
     assert abs(float(stats[0]) + float(A[on].double().mean())) <= (R.U32 + 1e-12) * abs(want) * 1.5
+
+
+def _token_pairs(G, lens, seed):
+    """Sequences of the given lengths in turn, two a group; values in 1/64 steps, so that float32 holds their
+    differences and float64 their sums exactly."""
+    g = torch.Generator().manual_seed(seed)
+    count = torch.tensor([lens[i % len(lens)] for i in range(2 * G)])
+    offs = torch.cat([torch.zeros(1, dtype=torch.long), count.cumsum(0)])
+    lp = -torch.randint(1, 512, (int(offs[-1]),), generator=g) / 64.0
+    return lp, offs.to(torch.int32), (torch.arange(G + 1) * 2).to(torch.int32)
+
+
+def test_preference_loss_is_off_by_its_own_rounding():
+    """The mean is taken of the groups' float64 losses, not of their roundings: off by half a step however they lie
+    (among 300 draws of three groups, roundings of the three that add up to more are common)."""
+    for seed in range(300):
+        lp, offs, goffs = _token_pairs(3, (1, 2), seed)
+        cfg = dict(beta=0.25, kind="sigmoid", smoothing=0.0, average=False, margin=0.0)
+        op = rece.PreferenceLoss(lp.numel(), 6, 3, beta=0.25)
+        loss, pg, _, _ = op.forward(lp.cuda(), None, offs.cuda(), goffs.cuda())
+        want, want_pg, _, _ = R.preference(lp, None, offs, goffs, cfg)
+        assert abs(float(loss) - want) <= (R.U32 + 1e-12) * want, seed
+        assert bool(((pg.cpu().double() - want_pg).abs() <= (R.U32 + 1e-12) * want_pg).all()), seed
+
+
+@pytest.mark.parametrize("G,lens", [(40, (3, 7, 5)), (40, (90, 70, 110)), (3000, (3, 2, 3)), (3000, (11, 7, 13)), (30, (1, 3))])
+def test_preference_average_gradient_is_off_by_its_own_rounding(G, lens):
+    """The share 1 / tokens of an averaged sequence is not rounded before the product."""
+    lp, offs, goffs = _token_pairs(G, lens, 5)
+    cfg = dict(beta=0.5, kind="sigmoid", smoothing=0.25, average=True, margin=0.0)
+    op = rece.PreferenceLoss(lp.numel(), 2 * G, G, beta=0.5, label_smoothing=0.25, average=True)
+    _, _, _, dlp = op.forward(lp.cuda(), None, offs.cuda(), goffs.cuda())
+    want = R.preference(lp, None, offs, goffs, cfg)[3]
+    assert bool(((dlp.cpu().double() - want).abs() <= (R.U32 + 1e-12) * want.abs() + 1e-17).all())
+
+
+def test_preference_average_gradient_of_a_large_group():
+    """More members than the workgroup's own memory holds: their shares lie in the workspace."""
+    m, lens = 700, (3, 7, 1, 5)
+    count = torch.tensor([lens[i % 4] for i in range(m)])
+    offs = torch.cat([torch.zeros(1, dtype=torch.long), count.cumsum(0)]).to(torch.int32)
+    lp = -torch.randint(1, 512, (int(offs[-1]),), generator=torch.Generator().manual_seed(2)) / 64.0
+    goffs = torch.tensor([0, m], dtype=torch.int32)
+    cfg = dict(beta=0.5, kind="softmax", smoothing=0.0, average=True, margin=0.0)
+    op = rece.PreferenceLoss(lp.numel(), m, 1, beta=0.5, kind="softmax", average=True)
+    loss, _, _, dlp = op.forward(lp.cuda(), None, offs.cuda(), goffs.cuda())
+    want, _, _, grad = R.preference(lp, None, offs, goffs, cfg)
+    assert abs(float(loss) - want) <= (R.U32 + 1e-12) * want
+    assert bool(((dlp.cpu().double() - grad).abs() <= (R.U32 + 1e-12) * grad.abs() + 1e-17).all())
