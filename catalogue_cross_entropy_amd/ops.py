@@ -309,8 +309,9 @@ class PreferenceLoss:
         if dloss is not None:
             _want("dloss", dloss, torch.float32, (1,), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev)
-        out = torch.empty(1 + c.n_group + c.n_seq, dtype=torch.float32, device=dev)
-        loss, loss_pg, rewards = out[:1], out[1:1 + c.n_group], out[1 + c.n_group:]
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        out = torch.empty(c.n_group + c.n_seq, dtype=torch.float32, device=dev)
+        loss_pg, rewards = out[:c.n_group], out[c.n_group:]
         dlogp = torch.empty(n, dtype=self._dt, device=dev) if grads else None
         _call(lib().rece_preference_loss, dev, (ctypes.byref(c),),
               (_ptr(logp), _ptr(ref_logp), _ptr(offsets), _ptr(group_offsets), _ptr(mask), _ptr(dloss), _ptr(ws),
@@ -370,7 +371,7 @@ def _function(name):
             loss, stats, dlogp, dent = op.forward(logp, old, adv, offsets, ref_logp=ref, entropy=entropy, mask=mask)
             ctx.save_for_backward(dlogp, dent)
             ctx.mark_non_differentiable(stats)
-            return loss.reshape(()), stats
+            return loss.squeeze_(), stats   # no view: a view made here could not be changed in place
 
         @staticmethod
         @torch.autograd.function.once_differentiable
@@ -384,7 +385,7 @@ def _function(name):
             loss, loss_pg, rewards, dlogp = op.forward(logp, ref, offsets, group_offsets, mask=mask)
             ctx.save_for_backward(dlogp)
             ctx.mark_non_differentiable(loss_pg, rewards)
-            return loss.reshape(()), loss_pg, rewards
+            return loss.squeeze_(), loss_pg, rewards
 
         @staticmethod
         @torch.autograd.function.once_differentiable

@@ -116,3 +116,36 @@ def test_a_given_stream_may_be_the_current_one_and_must_be_the_devices():
     for name, call in _stream_calls():
         with pytest.raises(ValueError):
             call(Elsewhere())
+
+
+def _losses():
+    """The two losses through autograd: (name, call(logp) -> results, number of tokens)."""
+    n, n_seq = 600, 12
+    g = torch.Generator().manual_seed(41)
+    ref = (-6.0 * torch.rand(n, generator=g)).cuda()
+    offs = (torch.arange(n_seq + 1) * (n // n_seq)).to(torch.int32).cuda()
+    goffs = (torch.arange(5) * 3).to(torch.int32).cuda()
+    adv = torch.randn(n_seq, generator=g).cuda()
+    pol, prf = rece.PolicyLoss(n, n_seq), rece.PreferenceLoss(n, n_seq, 4)
+    lp = ref + 0.1 * torch.randn(n, generator=g).cuda()
+    return lp, [("policy", lambda t: rece.policy_loss(t, ref, adv, offs, pol)),
+                ("preference", lambda t: rece.preference_loss(t, ref, offs, goffs, prf))]
+
+
+def test_losses_may_be_changed_in_place():
+    """loss /= steps, loss += other, and the other results too; the gradient follows."""
+    lp, calls = _losses()
+    for name, call in calls:
+        a = lp.clone().requires_grad_(True)
+        call(a)[0].backward()
+        b = lp.clone().requires_grad_(True)
+        loss, *rest = call(b)
+        assert loss.shape == ()
+        value = float(loss.detach())
+        loss /= 4
+        loss += b.detach().sum() * 0
+        for t in rest:
+            t *= 2
+        assert float(loss.detach()) == value / 4
+        loss.backward()
+        assert torch.equal(b.grad, a.grad / 4), name
