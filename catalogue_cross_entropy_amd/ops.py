@@ -348,7 +348,7 @@ def _function(name):
     class LogProbs(torch.autograd.Function):
         @staticmethod
         def forward(ctx, X, Y, ids, op):
-            logp, ent, ws = op.forward(X, Y, ids, need_grad=any(ctx.needs_input_grad[:2]))
+            logp, ent, ws = op.forward(X, Y, ids)
             ctx.op = op
             ctx.save_for_backward(X, Y, ids, ws)
             ctx.set_materialize_grads(False)
@@ -397,21 +397,39 @@ def _function(name):
     return _functions[name]
 
 
+def _wanted(*tensors) -> bool:
+    """Whether a gradient of some of these will be asked for (inside a Function the answer is lost: gradients are
+    switched off there, and needs_input_grad stays set under no_grad)."""
+    import torch
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 def embed(table, ids, op: ItemEmbedding):
     """op.forward with autograd: the table's gradient is op.backward's."""
     return _function("embed").apply(table, ids, op)
 
 
 def log_probs(X, Y, ids, op: LogProb):
-    """logp [s] (and entropy [s] where op has it) with autograd for X and Y."""
+    """logp [s] (and entropy [s] where op has it) with autograd for X and Y.  Where no gradient is wanted (no_grad, or
+    neither requires one) the call computes and keeps nothing for it."""
+    if not _wanted(X, Y):
+        logp, ent, _ = op.forward(X, Y, ids, need_grad=False)
+        return (logp, ent) if op.entropy else logp
     return _function("log_probs").apply(X, Y, ids, op)
 
 
 def policy_loss(logp, old_logp, advantages, offsets, op: PolicyLoss, ref_logp=None, entropy=None, mask=None):
     """(mean loss, stats [6]) with autograd for logp and entropy."""
+    if not _wanted(logp, entropy):
+        loss, stats, _, _ = op.forward(logp, old_logp, advantages, offsets, ref_logp=ref_logp, entropy=entropy, mask=mask,
+                                       grads=False)
+        return loss.squeeze_(), stats
     return _function("policy").apply(logp, entropy, old_logp, advantages, offsets, ref_logp, mask, op)
 
 
 def preference_loss(logp, ref_logp, offsets, group_offsets, op: PreferenceLoss, mask=None):
     """(mean loss, loss per group, rewards per sequence) with autograd for logp."""
+    if not _wanted(logp):
+        loss, loss_pg, rewards, _ = op.forward(logp, ref_logp, offsets, group_offsets, mask=mask, grads=False)
+        return loss.squeeze_(), loss_pg, rewards
     return _function("preference").apply(logp, ref_logp, offsets, group_offsets, mask, op)

@@ -149,3 +149,54 @@ def test_losses_may_be_changed_in_place():
         assert float(loss.detach()) == value / 4
         loss.backward()
         assert torch.equal(b.grad, a.grad / 4), name
+
+
+def test_scoring_without_gradients_makes_no_gradients(monkeypatch):
+    """Under no_grad (and with inputs that need none) the functions ask for no gradient, with a parameter as the table
+    too, take the smaller workspace, and give the same values."""
+    s, C, d = 3000, 2000, 64
+    g = torch.Generator().manual_seed(42)
+    X = torch.randn(s, d, generator=g).bfloat16().cuda()
+    table = torch.nn.Parameter(torch.randn(C, d, generator=g).bfloat16().cuda())
+    ids = torch.randint(-1, C, (s,), generator=g).to(torch.int32).cuda()
+    asked = []
+
+    def watch(cls, key):
+        real = cls.forward
+
+        def forward(self, *args, **kw):
+            asked.append(kw.get(key, True))
+            return real(self, *args, **kw)
+        monkeypatch.setattr(cls, "forward", forward)
+
+    watch(rece.LogProb, "need_grad")
+    watch(rece.PolicyLoss, "grads")
+    watch(rece.PreferenceLoss, "grads")
+    for entropy in (False, True):
+        op = rece.LogProb(s, C, d, entropy=entropy)
+        both = lambda y: rece.log_probs(X, y, ids, op) if entropy else (rece.log_probs(X, y, ids, op),)  # noqa: E731
+        want = both(table)
+        assert asked.pop() is True and all(t.requires_grad for t in want)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        with torch.no_grad():
+            got = both(table)
+        assert torch.cuda.max_memory_allocated() - before <= op.workspace_bytes_no_grad + 8 * s + 4096
+        assert asked.pop() is False and not any(t.requires_grad for t in got)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(both(table.detach()), want)) and asked.pop() is False
+        with torch.inference_mode():
+            both(table)
+        assert asked.pop() is False
+    lp, calls = _losses()
+    for name, call in calls:
+        want = call(lp.clone().requires_grad_(True))
+        assert asked.pop() is True and want[0].requires_grad
+        with torch.no_grad():
+            got = call(lp.clone().requires_grad_(True))
+        plain = call(lp)
+        assert asked == [False, False]
+        asked.clear()
+        for r in (got, plain):
+            assert r[0].shape == () and not r[0].requires_grad and all(torch.equal(a, b) for a, b in zip(r, want)), name
