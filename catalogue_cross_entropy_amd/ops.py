@@ -343,7 +343,10 @@ def _function(name):
         @torch.autograd.function.once_differentiable
         def backward(ctx, dout):
             (ids,) = ctx.saved_tensors
-            return ctx.op.backward(ids, dout.contiguous()), None, None
+            dout = dout.contiguous()
+            if dout.data_ptr() % 16:   # a part of a longer gradient (of a concatenation) may begin anywhere
+                dout = dout.clone()
+            return ctx.op.backward(ids, dout), None, None
 
     class LogProbs(torch.autograd.Function):
         @staticmethod

@@ -200,3 +200,19 @@ def test_scoring_without_gradients_makes_no_gradients(monkeypatch):
         asked.clear()
         for r in (got, plain):
             assert r[0].shape == () and not r[0].requires_grad and all(torch.equal(a, b) for a, b in zip(r, want)), name
+
+
+@pytest.mark.parametrize("lead", [1, 3, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_embed_gradient_that_begins_anywhere(lead, dtype):
+    """The rows as a part of a longer vector: their gradient is a part of its gradient, at any address."""
+    n, C, d = 300, 40, 32
+    g = torch.Generator().manual_seed(lead)
+    ids = torch.randint(-1, C, (n,), generator=g).to(torch.int32).cuda()
+    w = torch.randn(lead + n * d, generator=g).to(dtype).cuda()
+    op = rece.ItemEmbedding(n, C, d, dtype="f32" if dtype is torch.float32 else "bf16", bf16_grads=dtype is torch.bfloat16)
+    table = torch.randn(C, d, generator=g).to(dtype).cuda().requires_grad_(True)
+    head = torch.zeros(lead, dtype=dtype, device="cuda", requires_grad=True)
+    (torch.cat([head, rece.embed(table, ids, op).flatten()]) * w).sum().backward()
+    assert torch.equal(table.grad, op.backward(ids, w[lead:].clone().view(n, d)))
+    assert torch.equal(head.grad, w[:lead])
