@@ -44,7 +44,9 @@ rece_status check_logprob_call(int64_t s, int64_t C, int32_t d, int32_t dtype, f
                                const void* X, const void* Y, const int32_t* ids, const void* ws, size_t ws_bytes) {
   const rece_status v = check_logprob(s, C, d, dtype, flags);
   if (v != RECE_OK) return v;
-  if (!(temperature > 0.0f) || !std::isfinite(temperature)) return invalid("temperature must be positive and finite");
+  // Below, a logit in base 2 may pass 2^31, where its float32 steps are beyond the range of the exponential that a
+  // reference is taken out of; above, the values that stand for rows beyond the end come near 0.
+  if (!(temperature >= 0x1p-20f && temperature <= 0x1p64f)) return invalid("temperature must be positive, from 2^-20 to 2^64");
   if (!X || !Y || !ids || !ws) return invalid("NULL input or workspace pointer");
   if (misaligned(X, 16) || misaligned(Y, 16) || misaligned(ws, 16)) return invalid("X, Y and workspace must be 16-byte aligned");
   if (misaligned(ids, 4)) return invalid("ids must be 4-byte aligned");

@@ -162,8 +162,8 @@ class LogProb:
         self.temperature, self.entropy, self.bf16_grads = float(temperature), bool(entropy), bool(bf16_grads)
         self._code, self._dt = _dtype(dtype)
         self._flags = (FLAG_ENTROPY if entropy else 0) | (FLAG_BF16_GRADS if bf16_grads else 0)
-        if not self.temperature > 0.0:
-            raise ValueError("temperature must be positive")
+        if not 2.0 ** -20 <= self.temperature <= 2.0 ** 64:
+            raise ValueError("temperature must be positive, from 2^-20 to 2^64")
         self.workspace_bytes = self._bytes(self._flags)
         self.workspace_bytes_no_grad = self._bytes(self._flags | FLAG_NO_GRAD)
 

@@ -264,7 +264,8 @@ rece_status rece_embed_backward(void* stream, int64_t n, int64_t C, int32_t d, i
  * catalogue, and the entropy of that softmax; no array of size s x C exists:
  *   x_ij = X_i . Y_j / temperature,  lse_i = log sum_j exp(x_ij),  p_ij = exp(x_ij - lse_i)
  *   logp_i = x_i,ids(i) - lse_i          entropy_i = lse_i - sum_j p_ij x_ij
- *   X [s][d], Y [C][d] dtype, d in {32, 64, 128, 256}; ids [s] int32; temperature > 0
+ *   X [s][d], Y [C][d] dtype, d in {32, 64, 128, 256}; ids [s] int32; 2^-20 <= temperature <= 2^64
+ *   and |X_i . Y_j| / temperature below 2^30
  *   logp [s] float32; entropy [s] float32 (RECE_FLAG_ENTROPY, else NULL)
  * An id outside [0, C) is padding: logp and entropy are 0, the row of X is not
  * read into any result (it may hold anything) and gets a zero gradient.

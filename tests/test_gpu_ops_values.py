@@ -80,3 +80,31 @@ def test_preference_of_an_impossible_preferred_sequence(kind, G, per, members):
     want = torch.full((members, per), 0.5 / G / (members - 1), dtype=torch.float64)
     want[0] = -0.5 / G
     assert bool(((got - want).abs() <= 2.0 ** -23 * want.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("s,C", [(3, 20), (5, 700), (300, 45)])
+def test_logprob_at_the_ends_of_its_temperatures(s, C, dtype):
+    """2^64: all items alike, whatever the logits (below 2^-50 here).  2^-20: the best item alone (others are 2^10 below)."""
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    g = torch.Generator().manual_seed(C)
+    X = torch.ones(s, 32)
+    Y = torch.zeros(C, 32)
+    Y[:, 0] = torch.randperm(C, generator=g) / 1024.0 - 0.3   # all different, exact in bf16 up to 256 of them
+    Y = Y.to(dt)
+    best = int(Y[:, 0].float().argmax())
+    ids = torch.randint(0, C, (s,), generator=g).to(torch.int32)
+    ids[0] = best
+    args = (X.to(dt).cuda(), Y.cuda(), ids.cuda())
+    for T in (2.0 ** 64, 2.0 ** -20):
+        op = rece.LogProb(s, C, 32, dtype=dtype, temperature=T, entropy=True)
+        logp, ent, ws = op.forward(*args)
+        dX, dY = op.backward(*args, ws, torch.full((s,), T, device="cuda"))
+        assert bool(dX.isfinite().all()) and bool(dY.isfinite().all())
+        if T > 1:
+            want = -float(torch.tensor(float(C), dtype=torch.float64).log())
+            assert bool(((logp.cpu().double() - want).abs() <= 16 * 2.0 ** -24 * abs(want)).all())
+            assert bool(((ent.cpu().double() + want).abs() <= 16 * 2.0 ** -24 * abs(want)).all())
+        elif int((Y[:, 0] == Y[best, 0]).sum()) == 1:
+            hit = ids == best
+            assert bool((logp.cpu()[hit] == 0).all()) and bool((logp.cpu()[~hit] < -2.0 ** 9).all())
