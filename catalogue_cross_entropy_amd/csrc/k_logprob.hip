@@ -118,6 +118,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Two floats as two bf16 terms each.  The differences are those of the rounded floats everywhere: fused with the product
+// that made a weight in one place and not in another, a second term would differ between them.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+#pragma clang fp contract(off)
+  hi = pack_bf16(a, b);
+  const float ra = a - lo_f32(hi), rb = b - hi_f32(hi);
+  lo = pack_bf16(ra, rb);
+}
 
 // LDS by byte offset: a per-lane offset and a constant that becomes the instruction's.
 template <class T>
@@ -216,9 +224,10 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
         for (int ob = 0; ob < OB; ++ob)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float a = g[ob][8 * kk + 2 * e], b = g[ob][8 * kk + 2 * e + 1];
-            hi[ob][e] = pack_bf16(a, b);
-            lo[ob][e] = pack_bf16(a - lo_f32(hi[ob][e]), b - hi_f32(hi[ob][e]));
+            uint32_t first, second;
+            split_bf16(g[ob][8 * kk + 2 * e], g[ob][8 * kk + 2 * e + 1], first, second);
+            hi[ob][e] = first;
+            lo[ob][e] = second;
           }
 #pragma unroll
         for (int nb = 0; nb < D / 32; ++nb) {
@@ -260,8 +269,9 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
 // What of a weight went into the products: all of it, or (bf16, two terms) its first two bf16 terms.
 __device__ __forceinline__ float lp_taken(float g, int terms, bool b16) {
   if (!b16 || terms != 2) return g;
-  const float hi = lo_f32(pack_bf16(g, 0.0f));
-  return hi + lo_f32(pack_bf16(g - hi, 0.0f));
+  uint32_t hi, lo;
+  split_bf16(g, 0.0f, hi, lo);
+  return lo_f32(hi) + lo_f32(lo);   // exact
 }
 
 // NWO waves along the owners x NWS waves along a tile's rows; OB blocks of 32 owners per wave.

@@ -195,3 +195,65 @@ def test_preference_average_gradient_of_a_large_group():
     want, _, _, grad = R.preference(lp, None, offs, goffs, cfg)
     assert abs(float(loss) - want) <= (R.U32 + 1e-12) * want
     assert bool(((dlp.cpu().double() - grad).abs() <= (R.U32 + 1e-12) * grad.abs() + 1e-17).all())
+
+
+def _near_one(s, C, d, dtype, seed):
+    """Positions whose own item has a probability from 0.99 to 1 - 1e-6, each an item of its own."""
+    g = torch.Generator().manual_seed(seed)
+    Y = torch.randn(C, d, generator=g) * d ** -0.25
+    ids = torch.randperm(C, generator=g)[:s].to(torch.int32)
+    a = Y[ids.long()]
+    rest = torch.randn(s, d, generator=g) * 0.3 * d ** -0.25
+    X = a / (a * a).sum(1, keepdim=True) * torch.linspace(9.0, 25.0, s)[:, None] + rest
+    X, Y = X.to(TL.DT[dtype]), Y.to(TL.DT[dtype])
+    left = 1.0 - torch.softmax(X.double() @ Y.double().T, 1)[torch.arange(s), ids.long()]
+    keep = (left < 0.01) & (left > 1e-6)
+    assert int(keep.sum()) > s // 3 and float(left[keep].min()) < 1e-5
+    ids[~keep] = -1
+    return X, Y, ids, torch.randn(s, generator=g) / s, torch.randn(s, generator=g) / s * 0.1
+
+
+@pytest.mark.parametrize("s,C,d", [(60, 90, 64), (150, 160, 128), (150, 160, 32), (100, 130, 256)])
+@pytest.mark.parametrize("dtype,bf16_grads", [("f32", False), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_logprob_near_certainty(s, C, d, dtype, bf16_grads, entropy):
+    """Where p is near 1: log p is off relative to 1 - p, and so is the own item's weight g (1 - p), but for the
+    roundings of float32 sums that its term and its row pass through (one per 16 rows of the products and per join)."""
+    X, Y, ids, dlogp, dent = _near_one(s, C, d, dtype, seed=s + d)
+    if not entropy:
+        dent = None
+    print(f"[gpu] logprob near 1 s={s} C={C} d={d} {dtype} bf16_grads={bf16_grads} entropy={entropy}", flush=True)
+    logp, _, dX, dY = TL._run(X, Y, ids, dlogp, dent, 1.0, entropy, bf16_grads)
+    w = R.logprob(X, Y, ids, 1.0, dlogp, dent)
+    on = ids >= 0
+    k = torch.arange(int(on.sum()))
+    a, Xk, Yd = ids[on].long(), X.double()[on], Y.double()
+    L = Xk @ Yd.T
+    logq = torch.log_softmax(L, 1)
+    q = logq.exp()
+    left = -torch.expm1(logq[k, a])
+    # the bounds of R.logprob for logits, exponentials and their sum, relative to what they scale
+    ex = (d + 4) * R.U32 * (Xk.abs() @ Yd.abs().T).amax(1)
+    elog = 2 * ex + (16 + C / 32 + 112 + 8 * L.abs().amax(1)) * R.U32
+    rel = 2 * ex + elog + 8 * R.U32
+    # log p = -log1p((1 - p) / p), (1 - p) / p the others' sum over the own term.  The others' sum is the float32 sum of
+    # all less the own term, and nearly all of that sum is the own term: each addition after it (at most 16 of its
+    # block, one per block, 4 of lane halves and parts) rounds by U32 of it, and so does each product and difference
+    # that takes it out (3), whatever is left.
+    most = (rel + 4 * R.U32) * left + (16 + C / 32 + 4 + 3) * R.U32
+    assert bool(((logp.double()[on] - logq[k, a]).abs() <= 1.02 * most).all())
+    gk = dlogp.double()[on].abs()
+    hk = dent.double()[on].abs() if entropy else torch.zeros_like(gk)
+    H = -(q * logq).sum(1)
+    size = q * (gk[:, None] + hk[:, None] * (logq.abs() + H[:, None]))
+    size[k, a] = gk * left + hk * q[k, a] * (logq[k, a].abs() + H)
+    off = size * (rel[:, None] + (2.0 ** -16 if bf16_grads else 0.0)) + q * (hk * w["e_entropy"][on])[:, None]
+    hot = torch.zeros_like(q)
+    hot[k, a] = gk
+    steps = (C + s) / 16 + 24
+    u = R.U[torch.bfloat16] if bf16_grads else R.U32
+    for got, want, bound in ((dX[on], w["dX"][on], off @ Yd.abs() + steps * R.U32 * ((hot + size) @ Yd.abs())),
+                             (dY, w["dY"], off.T @ Xk.abs() + steps * R.U32 * ((hot + size).T @ Xk.abs()))):
+        bound = bound + u * (want.abs() + bound) + 1e-30
+        err = (got.double() - want).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
