@@ -644,17 +644,41 @@ __device__ __forceinline__ uint32_t pref_in(PrefSeq q, uint32_t t) {
   return in;
 }
 
-// h of K sequences by L lanes (all of them get them); the K sequences' tokens are requested together.
+// A few lanes take PREF_STEPS steps of their sequence by themselves; what is left of a longer one the whole wave takes
+// (lengths are known on the device alone, and a mean of two says nothing of the longest: one sequence of 10,000 tokens
+// among 100,000 of two 1,680 us by its own lane, 53 by the wave).
+constexpr int PREF_STEPS = 32;
+
+// First token of the part that the wave takes; hi where there is none.
+template <int L, int W>
+__device__ __forceinline__ uint32_t pref_rest(PrefSeq q) {
+  if constexpr (L == WAVE) return q.hi;
+  return min((uint64_t)q.hi, (uint64_t)(q.lo / W * W) + (uint64_t)PREF_STEPS * L * W);
+}
+
+// f(lane, first token, end) for the lane that speaks for each sequence with such a part, by the whole wave.
+template <int L, class F>
+__device__ __forceinline__ void pref_rests(uint32_t from, uint32_t hi, int sub, F f) {
+  for (uint64_t left = ballot(sub == 0 && from < hi); left; left &= left - 1) {
+    const int lane = __ffsll((unsigned long long)left) - 1;
+    f(lane, __builtin_amdgcn_readlane(from, lane), __builtin_amdgcn_readlane(hi, lane));
+  }
+}
+
+// h of K sequences by L lanes (all of them get them); the K sequences' tokens are requested together.  All lanes of a
+// wave come here together, those without a sequence with an empty one.
 template <class E, int L, int W, int K>
-__device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)[K], int sub, double (&s)[K], double (&share)[K]) {
+__device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&whole)[K], int sub, double (&s)[K], double (&share)[K]) {
   const E* lp = static_cast<const E*>(a.logp);
   const E* rf = static_cast<const E*>(a.ref);
   const uint32_t n = (uint32_t)a.c.n;
   int c[K];
   uint32_t t[K];
+  PrefSeq seq[K];   // the part that the lanes take by themselves
   bool more = false;
 #pragma unroll
   for (int q = 0; q < K; ++q) {
+    seq[q] = PrefSeq{whole[q].lo, pref_rest<L, W>(whole[q])};
     s[q] = 0.0;
     c[q] = 0;
     t[q] = seq[q].lo / W * W + sub * W;
@@ -695,6 +719,37 @@ __device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)
       more |= t[q] < seq[q].hi;
     }
   }
+  if constexpr (L < WAVE) {
+#pragma unroll
+    for (int q = 0; q < K; ++q)
+      pref_rests<L>(seq[q].hi, whole[q].hi, sub, [&](int lane, uint32_t from, uint32_t hi) {
+        constexpr int UNR = 8;   // tokens of a lane in flight
+        double v = 0.0;
+        int on = 0;
+        for (uint32_t t0 = from; t0 < hi; t0 += UNR * WAVE) {
+          float x[UNR], y[UNR];
+          bool in[UNR];
+#pragma unroll
+          for (int u = 0; u < UNR; ++u) {
+            const uint32_t at = t0 + u * WAVE + lane_id();
+            in[u] = at < hi && (!a.mask || a.mask[at]);
+            x[u] = at < hi ? to_f32(lp[at]) : 0.0f;
+            y[u] = at < hi && rf ? to_f32(rf[at]) : 0.0f;
+          }
+#pragma unroll
+          for (int u = 0; u < UNR; ++u) {
+            v += (double)(in[u] ? x[u] - y[u] : 0.0f);
+            on += in[u] ? 1 : 0;
+          }
+        }
+        v = wave_sum_d(v);
+        on = wave_sum(on);
+        if (lane_id() == lane) {
+          s[q] += v;
+          c[q] += on;
+        }
+      });
+  }
 #pragma unroll
   for (int o = L / 2; o >= 1; o >>= 1)
 #pragma unroll
@@ -711,10 +766,16 @@ __device__ __forceinline__ void pref_sum(const PrefArgs& a, const PrefSeq (&seq)
   }
 }
 
-// Gradient of a sequence's tokens: v where they count, else 0.
+// Gradient of a sequence's tokens: v where they count, else 0.  All lanes of a wave come here together.
 template <class E, int L, int W>
-__device__ __forceinline__ void pref_grad(const PrefArgs& a, PrefSeq seq, int sub, float v) {
+__device__ __forceinline__ void pref_grad(const PrefArgs& a, PrefSeq whole, int sub, float v) {
   E* out = static_cast<E*>(a.dlogp);
+  const PrefSeq seq{whole.lo, pref_rest<L, W>(whole)};
+  if constexpr (L < WAVE)
+    pref_rests<L>(seq.hi, whole.hi, sub, [&](int lane, uint32_t from, uint32_t hi) {
+      const float x = __shfl(v, lane);
+      for (uint32_t t = from + lane_id(); t < hi; t += WAVE) put(out, t, load_mask<1>(a.mask, t) ? x : 0.0f);
+    });
   for (uint32_t t = seq.lo / W * W + sub * W; t < seq.hi; t += L * W) {
     const uint32_t in = pref_in<W>(seq, t);
     if (W == 1 || in == 0x80808080u) {   // inside the sequence, so inside the array
@@ -767,13 +828,13 @@ __device__ __forceinline__ void pref_outside(const PrefArgs& a, int64_t b, int64
   const int q = threadIdx.x / L, sub = threadIdx.x % L;
   const float beta = a.c.beta;
   const int64_t first = offset_at(a.goffs, 0, nseq), end = offset_at(a.goffs, G, nseq);
-  for (int64_t k = b * NS + q; k < first + (nseq - end); k += extra * NS) {
-    const int64_t i = k < first ? k : end + (k - first);
-    if (i >= nseq) break;
-    const PrefSeq seq[1] = {pref_seq(a.offs, i, a.c.n)};
+  for (int64_t k0 = b * NS; k0 < first + (nseq - end); k0 += extra * NS) {   // lanes together
+    const int64_t k = k0 + q, i = k < first ? k : end + (k - first);
+    const bool on = k < first + (nseq - end) && i < nseq;
+    const PrefSeq seq[1] = {on ? pref_seq(a.offs, i, a.c.n) : PrefSeq{0, 0}};
     double h[1], share[1];
     pref_sum<E, L, W, 1>(a, seq, sub, h, share);
-    if (sub == 0) a.rewards[i] = (float)((double)beta * h[0]);
+    if (on && sub == 0) a.rewards[i] = (float)((double)beta * h[0]);
     if (a.dlogp) pref_grad<E, L, W>(a, seq[0], sub, 0.0f);
   }
   if (a.dlogp) {
@@ -809,8 +870,9 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
     __syncthreads();
   }
   auto seq_at = [&](int64_t k) { return in_lds ? pref_seq(sh_offs, k, a.c.n) : pref_seq(a.offs, s0 + k, a.c.n); };
-  for (int64_t k = q; k < m; k += 2 * NS) {
-    const PrefSeq seq[2] = {seq_at(k), k + NS < m ? seq_at(k + NS) : PrefSeq{0, 0}};
+  for (int64_t k0 = 0; k0 < m; k0 += 2 * NS) {   // lanes together
+    const int64_t k = k0 + q;
+    const PrefSeq seq[2] = {k < m ? seq_at(k) : PrefSeq{0, 0}, k + NS < m ? seq_at(k + NS) : PrefSeq{0, 0}};
     double h[2], share[2];
     pref_sum<E, L, W, 2>(a, seq, sub, h, share);
     if (sub != 0) continue;
@@ -872,7 +934,11 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
   if (!a.dlogp) return;
   __syncthreads();
   const double up = (double)beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G;
-  for (int64_t k = q; k < m; k += NS) pref_grad<E, L, W>(a, seq_at(k), sub, (float)(hs[k] * up * shares[k]));
+  for (int64_t k0 = 0; k0 < m; k0 += NS) {
+    const int64_t k = k0 + q;
+    const bool on = k < m;
+    pref_grad<E, L, W>(a, on ? seq_at(k) : PrefSeq{0, 0}, sub, on ? (float)(hs[k] * up * shares[k]) : 0.0f);
+  }
 }
 
 // Many small groups: T lanes take a group, its sequences one after the other.
@@ -887,66 +953,65 @@ __global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int
   const int64_t G = a.c.n_group, nseq = a.c.n_seq;
   const int64_t g = (blk - extra) * (PREF_MANY_THREADS / T) + threadIdx.x / T;
   const int sub = threadIdx.x % T;
-  if (g >= G) return;   // a group's lanes together
-  const int64_t s0 = offset_at(a.goffs, g, nseq), s1 = max(s0, offset_at(a.goffs, g + 1, nseq));
+  const bool there = g < G;
+  const int64_t s0 = there ? offset_at(a.goffs, g, nseq) : 0, s1 = there ? max(s0, offset_at(a.goffs, g + 1, nseq)) : 0;
   const int64_t m = s1 - s0;
   const double beta = a.c.beta, margin = a.c.margin;
   const double up = beta * (a.dloss ? (double)a.dloss[0] : 1.0) / (double)G, per = m > 1 ? 1.0 / (double)(m - 1) : 0.0;
   PrefSeq seq[1];
   double h[1], share[1];
-  auto read = [&](int64_t k) {
-    seq[0] = pref_seq(a.offs, s0 + k, a.c.n);
+  auto read = [&](int64_t k) {   // lanes together, also those whose group has fewer members
+    seq[0] = k < m ? pref_seq(a.offs, s0 + k, a.c.n) : PrefSeq{0, 0};
     pref_sum<E, T, W, 1>(a, seq, sub, h, share);
+    if (k < m && sub == 0) a.rewards[s0 + k] = (float)(beta * h[0]);
   };
+  const int64_t most = wave_max_i((int)m);   // the wave's largest group
   auto grad = [&](double dh) {   // of the sequence read last
     if (a.dlogp) pref_grad<E, T, W>(a, seq[0], sub, (float)(dh * up * share[0]));
   };
   double loss = 0.0, dc = 0.0;
-  if (m > 0) {
-    read(0);
-    const double hc = h[0];
-    const double share0 = share[0];
-    const PrefSeq seq0 = seq[0];
-    if (sub == 0) a.rewards[s0] = (float)(beta * hc);
-    if (a.c.kind == RECE_PREF_SOFTMAX) {
-      double top = 0.0, others = 0.0;   // others: sum of e^(-z - top)
-      for (int64_t k = 1; k < m; ++k) {
-        read(k);
-        if (sub == 0) a.rewards[s0 + k] = (float)(beta * h[0]);
-        const double v = margin - beta * (hc - h[0]);
-        if (v > top) {
-          others *= exp(top - v);
-          top = v;
-        }
-        others += exp_below(v, top);
+  read(0);
+  const double hc = h[0], share0 = share[0];
+  const PrefSeq seq0 = seq[0];
+  if (a.c.kind == RECE_PREF_SOFTMAX) {
+    double top = 0.0, others = 0.0;   // others: sum of e^(-z - top)
+    for (int64_t k = 1; k < most; ++k) {
+      read(k);
+      if (k >= m) continue;
+      const double v = margin - beta * (hc - h[0]);
+      if (v > top) {
+        others *= exp(top - v);
+        top = v;
       }
-      const double tot = others + exp(-top);
-      if (m > 1) {
-        loss = top + log(tot);
-        dc = -others / tot;
-      }
-      if (a.dlogp)
-        for (int64_t k = 1; k < m; ++k) {
-          read(k);
-          grad(exp_below(margin - beta * (hc - h[0]), top) / tot);
-        }
-    } else {
-      for (int64_t k = 1; k < m; ++k) {
+      others += exp_below(v, top);
+    }
+    const double tot = others + exp(-top);
+    if (m > 1) {
+      loss = top + log(tot);
+      dc = -others / tot;
+    }
+    if (a.dlogp)
+      for (int64_t k = 1; k < most; ++k) {
         read(k);
-        if (sub == 0) a.rewards[s0 + k] = (float)(beta * h[0]);
-        double dz;
+        grad(exp_below(margin - beta * (hc - h[0]), top) / tot);
+      }
+  } else {
+    for (int64_t k = 1; k < most; ++k) {
+      read(k);
+      double dz = 0.0;
+      if (k < m) {
         loss += pair_loss(a.c, beta * (hc - h[0]) - margin, dz);
         dc += dz;
-        grad(-dz * per);
       }
-      loss *= per;
-      dc *= per;
+      grad(-dz * per);
     }
-    seq[0] = seq0;
-    share[0] = share0;
-    grad(dc);
+    loss *= per;
+    dc *= per;
   }
-  if (sub == 0) {
+  seq[0] = seq0;
+  share[0] = share0;
+  grad(dc);
+  if (there && sub == 0) {
     a.loss_pg[g] = (float)loss;
     a.group_loss[g] = loss;
   }

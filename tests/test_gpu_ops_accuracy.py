@@ -257,3 +257,71 @@ def test_logprob_near_certainty(s, C, d, dtype, bf16_grads, entropy):
         bound = bound + u * (want.abs() + bound) + 1e-30
         err = (got.double() - want).abs()
         assert bool((err <= bound).all()), float((err / bound).max())
+
+
+def _long_among_short(G, members, short, long, seed):
+    """Groups of sequences of `short` tokens, a few of `long` tokens, and one each before and behind the groups."""
+    g = torch.Generator().manual_seed(seed)
+    n_seq = G * members + 2
+    lens = torch.full((n_seq,), short)
+    at = torch.randperm(n_seq - 2, generator=g)[:5] + 1
+    lens[at] = torch.tensor([long, long - 1, long // 2 + 3, 33, 1025])
+    lens[0], lens[-1] = long // 3, long + 5
+    offs = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)]) + 3
+    n = int(offs[-1]) + 2
+    lp, ref = (-4.0 * torch.rand(n, generator=g) for _ in range(2))
+    return lp, ref, offs.to(torch.int32), (1 + torch.arange(G + 1) * members).to(torch.int32), torch.rand(n, generator=g) < 0.8
+
+
+@pytest.mark.parametrize("G,members,short", [(3000, 2, 1), (3000, 2, 9), (9000, 4, 1), (9000, 3, 6), (60, 5, 1), (60, 3, 7), (60, 90, 5)])
+@pytest.mark.parametrize("kind,average", [("sigmoid", True), ("softmax", False)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lead", [0, 1])
+def test_preference_long_sequences_among_short_ones(G, members, short, kind, average, dtype, lead):
+    """Lanes per sequence go by the mean length; what is left of a longer sequence the whole wave takes.  Every ratio of
+    float32 or bf16 tokens is off by U32 of at most 4 in its difference, its sum is float64; the gradient is beta times a
+    slope of at most 1 / G whose own slope by h is at most beta."""
+    dt = TL.DT[dtype]
+    long = 3000 if short < 4 else 6000
+    lp, ref, offs, goffs, mask = _long_among_short(G, members, short, long, G + short)
+    lp, ref = lp.to(dt), ref.to(dt)
+    n, n_seq = lp.numel(), offs.numel() - 1
+    beta = 0.125
+    op = rece.PreferenceLoss(n, n_seq, G, beta=beta, kind=kind, average=average, dtype=dtype)
+    put = lambda t: torch.cat([t[:1].expand(lead), t]).cuda()[lead:]  # noqa: E731
+    print(f"[gpu] preference long G={G} members={members} short={short} {kind} {dtype} lead={lead}", flush=True)
+    poison = torch.full((), float("nan"), dtype=dt)
+    loss, pg, rewards, dlp = op.forward(put(torch.where(mask, lp, poison)), put(ref), offs.cuda(), goffs.cuda(), mask=put(mask))
+    # the float64 form over sums per sequence (thousands of groups: without the loop of the plain one)
+    seq = torch.repeat_interleave(torch.arange(n_seq), offs.long().diff())
+    inside = slice(int(offs[0]), int(offs[-1]))
+    ratio = torch.where(mask, lp.double() - ref.double(), 0.0)[inside]
+    zero = torch.zeros(n_seq, dtype=torch.float64)
+    count = zero.index_add(0, seq, mask[inside].double())
+    h = zero.index_add(0, seq, ratio)
+    eh = 4 * R.U32 * count + 1e-12
+    if average:
+        h, eh = h / count.clamp(min=1), eh / count.clamp(min=1)
+    assert bool(((rewards.cpu().double() - beta * h).abs() <= beta * eh + 1.01 * R.U32 * beta * h.abs()).all())
+    hg, eg = h[1:-1].view(G, members), eh[1:-1].view(G, members)
+    z, ez = beta * (hg[:, :1] - hg[:, 1:]), beta * (eg[:, :1] + eg[:, 1:])
+    if kind == "softmax":
+        tot = 1.0 + (-z).exp().sum(1)
+        want_pg, dz = tot.log(), -(-z).exp() / tot[:, None]
+    else:
+        want_pg = torch.nn.functional.softplus(-z, threshold=1e9).mean(1)
+        dz = (torch.sigmoid(z) - 1.0) / (members - 1)
+    assert bool(((pg.cpu().double() - want_pg).abs() <= ez.sum(1) + 1.01 * R.U32 * want_pg).all())
+    assert abs(float(loss) - float(want_pg.mean())) <= float(ez.sum(1).mean()) + 1.01 * R.U32 * float(want_pg.mean())
+    dh, edh = zero.clone(), zero.clone()
+    dh[1:-1] = torch.cat([dz.sum(1, keepdim=True), -dz], 1).flatten() * beta / G
+    slope = ez.sum(1, keepdim=True) * beta / G   # each derivative moves by at most the sum of the z's errors
+    edh[1:-1] = slope.expand(G, members).flatten()
+    if average:
+        dh, edh = dh / count.clamp(min=1), edh / count.clamp(min=1)
+    want, err = torch.zeros(n, dtype=torch.float64), torch.zeros(n, dtype=torch.float64)
+    want[inside], err[inside] = dh[seq], edh[seq]
+    want = torch.where(mask, want, 0.0)
+    got = dlp.cpu().double()
+    assert bool(((got - want).abs() <= err + 1.01 * R.U[dt] * (want.abs() + err)).all())
+    assert not bool(got[~mask].any()) and not bool(got[:int(offs[1])].any()) and not bool(got[int(offs[-2]):].any())
