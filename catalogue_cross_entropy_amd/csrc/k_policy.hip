@@ -792,6 +792,11 @@ __device__ __forceinline__ void pref_grad(const PrefArgs& a, PrefSeq whole, int 
   }
 }
 
+// log(1 + sum of e^v) from top, the largest v or 0, and the sum of e^(v - top): small where every v is far below 0.
+__device__ __forceinline__ double softmax_loss(double top, double others) {
+  return top > 0.0 ? top + log(others + exp(-top)) : log1p(others);
+}
+
 // e^(v - top) with top the largest: 1 for v = top, also where both are infinite.
 __device__ __forceinline__ double exp_below(double v, double top) { return exp(v == top ? 0.0 : v - top); }
 
@@ -801,7 +806,7 @@ __device__ __forceinline__ double softplus_d(double x) { return fmax(x, 0.0) + l
 __device__ __forceinline__ double pair_loss(const rece_preference_config& c, double z, double& dz) {
   if (c.kind == RECE_PREF_SIGMOID) {
     const double e = c.smoothing;
-    dz = 1.0 / (1.0 + exp(-z)) - (1.0 - e);
+    dz = e - 1.0 / (1.0 + exp(z));   // as sigmoid(z) - (1 - e) nothing would be left of it where z is large
     // without smoothing its term is no part of the loss, also where z is infinite (an item of no probability)
     return (1.0 - e) * softplus_d(-z) + (e > 0.0 ? e * softplus_d(z) : 0.0);
   }
@@ -912,7 +917,7 @@ __global__ __launch_bounds__(NT) void k_pref(PrefArgs a, int extra) {
         others = wave_sum_d(others);
         const double tot = others + exp(-top);
         for (int64_t k = 1 + l; k < m; k += WAVE) hs[k] = hs[k] / tot;
-        loss = top + log(tot);
+        loss = softmax_loss(top, others);
         dc = -others / tot;
       } else {
         for (int64_t k = 1 + l; k < m; k += WAVE) {
@@ -987,7 +992,7 @@ __global__ __launch_bounds__(PREF_MANY_THREADS) void k_pref_many(PrefArgs a, int
     }
     const double tot = others + exp(-top);
     if (m > 1) {
-      loss = top + log(tot);
+      loss = softmax_loss(top, others);
       dc = -others / tot;
     }
     if (a.dlogp)

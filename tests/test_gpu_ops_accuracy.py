@@ -325,3 +325,30 @@ def test_preference_long_sequences_among_short_ones(G, members, short, kind, ave
     got = dlp.cpu().double()
     assert bool(((got - want).abs() <= err + 1.01 * R.U[dt] * (want.abs() + err)).all())
     assert not bool(got[~mask].any()) and not bool(got[:int(offs[1])].any()) and not bool(got[int(offs[-2]):].any())
+
+
+@pytest.mark.parametrize("G", [200, 9000])
+@pytest.mark.parametrize("kind,members", [("sigmoid", 2), ("sigmoid", 4), ("softmax", 2), ("softmax", 4)])
+def test_preference_pairs_that_are_well_apart(G, kind, members):
+    """z from 1 to 80: loss and gradient fall to e^-80 and stay exact to their own rounding (values in steps of 1/64, so
+    z is exact, and e^-z is off by 80 steps of 2^-53)."""
+    g = torch.Generator().manual_seed(G)
+    h = -40.0 * torch.rand(G, members, generator=g)
+    h[:, 0] = 1.0 + 39.0 * torch.rand(G, generator=g)
+    h = (h * 64).round() / 64
+    n = G * members
+    op = rece.PreferenceLoss(n, n, G, beta=1.0, kind=kind)
+    loss, pg, _, dlp = op.forward(h.flatten().cuda(), None, torch.arange(n + 1, dtype=torch.int32, device="cuda"),
+                                  (torch.arange(G + 1) * members).to(torch.int32).cuda())
+    z = h[:, :1].double() - h[:, 1:].double()
+    if kind == "softmax":
+        e = (-z).exp()
+        want, dz = torch.log1p(e.sum(1)), -e / (1.0 + e.sum(1, keepdim=True))
+    else:
+        want, dz = torch.log1p((-z).exp()).mean(1), -1.0 / (1.0 + z.exp()) / (members - 1)
+    grad = torch.cat([dz.sum(1, keepdim=True), -dz], 1) / G
+    u = R.U32 + 1e-13
+    assert bool(((pg.cpu().double() - want).abs() <= u * want).all())
+    assert abs(float(loss) - float(want.mean())) <= u * float(want.mean())
+    # (e^-80 / 9,000 lies below the normal float32 numbers)
+    assert bool(((dlp.cpu().double().view(G, members) - grad).abs() <= u * grad.abs() + 2.0 ** -126).all())
