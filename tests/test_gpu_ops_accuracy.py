@@ -352,3 +352,52 @@ def test_preference_pairs_that_are_well_apart(G, kind, members):
     assert abs(float(loss) - float(want.mean())) <= u * float(want.mean())
     # (e^-80 / 9,000 lies below the normal float32 numbers)
     assert bool(((dlp.cpu().double().view(G, members) - grad).abs() <= u * grad.abs() + 2.0 ** -126).all())
+
+
+@pytest.mark.parametrize("per", [1, 2, 9])
+@pytest.mark.parametrize("kind", ["sigmoid", "ipo", "hinge", "softmax"])
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_large_groups_among_many_small_ones(per, kind, average):
+    """Groups of 64, 65, 200 and 3,000 members among 9,000 pairs.  Tokens in steps of 1/64 and no reference, so that every
+    h is exact in 64 bits: results are off by their own rounding, but for 64-bit sums of up to 3,000 terms (and what
+    lies below the normal float32 numbers: z reaches 300)."""
+    G = 9000
+    size = torch.full((G,), 2)
+    size[[5, 6, 7000, G - 1, 100]] = torch.tensor([64, 65, 3000, 200, 0])
+    goffs = torch.cat([torch.zeros(1, dtype=torch.long), size.cumsum(0)])
+    n_seq = int(goffs[-1])
+    lens = torch.full((n_seq,), per)
+    lens[::5] += 1
+    lens[20:3000:700] = 600
+    offs = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)])
+    n = int(offs[-1])
+    lp = -torch.randint(1, 512, (n,), generator=torch.Generator().manual_seed(per)) / 64.0
+    beta = 0.125
+    op = rece.PreferenceLoss(n, n_seq, G, beta=beta, kind=kind, average=average, margin=0.25)
+    print(f"[gpu] preference large groups {kind} per={per} average={average}", flush=True)
+    loss, pg, rewards, dlp = op.forward(lp.cuda(), None, offs.to(torch.int32).cuda(), goffs.to(torch.int32).cuda())
+    seq, grp = torch.repeat_interleave(torch.arange(n_seq), lens), torch.repeat_interleave(torch.arange(G), size)
+    x = lp.double().requires_grad_(True)
+    h = torch.zeros(n_seq, dtype=torch.float64).index_add(0, seq, x)
+    if average:
+        h = h / lens
+    first = goffs[:-1][grp]
+    other = torch.arange(n_seq) > first
+    z = (beta * (h[first] - h) - 0.25)[other]
+    per_group = lambda v: torch.zeros(G, dtype=torch.float64).index_add(0, grp[other], v)  # noqa: E731
+    if kind == "softmax":
+        want = torch.log1p(per_group((-z).exp()))
+    else:
+        each = {"sigmoid": lambda: -torch.nn.functional.logsigmoid(z), "hinge": lambda: torch.relu(1 - z),
+                "ipo": lambda: (z / beta - 0.5 / beta) ** 2}[kind]()
+        want = per_group(each) / (size - 1).clamp(min=1)
+    want.mean().backward()
+    tiny = 3000 * 2.0 ** -52
+    want = want.detach()
+    assert bool(((pg.cpu().double() - want).abs() <= (R.U32 + tiny) * want + 2.0 ** -126).all())
+    assert abs(float(loss) - float(want.mean())) <= (R.U32 + tiny) * float(want.mean())
+    assert bool(((rewards.cpu().double() - beta * h.detach()).abs() <= (R.U32 + tiny) * beta * h.detach().abs()).all())
+    # the preferred one's gradient is a sum of its group's, which may cancel for ipo
+    scale = torch.zeros(G, dtype=torch.float64).index_add(0, grp, torch.zeros(n_seq, dtype=torch.float64).index_add(
+        0, seq, x.grad.abs()))[grp][seq]
+    assert bool(((dlp.cpu().double() - x.grad).abs() <= (R.U32 + 1e-12) * x.grad.abs() + tiny * scale + 2.0 ** -126).all())
