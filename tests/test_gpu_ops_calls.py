@@ -216,3 +216,27 @@ def test_embed_gradient_that_begins_anywhere(lead, dtype):
     (torch.cat([head, rece.embed(table, ids, op).flatten()]) * w).sum().backward()
     assert torch.equal(table.grad, op.backward(ids, w[lead:].clone().view(n, d)))
     assert torch.equal(head.grad, w[:lead])
+
+
+def test_a_given_stream_inside_a_captured_graph():
+    """A capture that forks to another stream, calls the operators on it and joins again: replays between eager work give
+    the eager results."""
+    for name, call in _stream_calls():
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        print(f"[gpu] {name} captured on a forked stream", flush=True)
+        main, fork = torch.cuda.Stream(), torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        main.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(main):
+            with torch.cuda.graph(graph, stream=main):
+                fork.wait_stream(main)
+                got = call(fork)
+                main.wait_stream(fork)
+        for r in range(3):
+            for t in got:
+                t.fill_(3.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (name, r)
+            assert all(torch.equal(a, b) for a, b in zip(call(None), want)), (name, r)
