@@ -22,15 +22,24 @@
 // in a fixed order.
 //
 // What bounds it: the exponential of each logit (v_exp_f32, about 9 cycles of a SIMD for 64 logits, with 2
-// to 4 cheaper instructions beside it) and the products share a SIMD's issue: vector and matrix units
-// were busy 115 % together at best (68 % and 47 %).  Measured (bf16):
-//   51,200 (a quarter padding) x 30,000 x 64  with gradients 707 us: LP_LSEO 342 us and LP_DY 344 us (860
-//                          TFLOP/s each, and 3.4e12 exponentials a second), packing, joins and the own items 100 us
-//   4,099 (a tenth padding) x 50,021 x 256  with entropies and gradients 685 us: LP_LSE 122, LP_DX 225,
-//                          LP_DY 307 us (770, 840, 620 TFLOP/s; LP_DY spills about 25 words per lane)
-//   2,047 (a tenth padding) x 200,000 x 128  log-probabilities 122 us: LP_LSE 117 us (810 TFLOP/s)
+// to 4 cheaper instructions beside it), the split of each weight into bf16 terms (6 more), and the products share a
+// SIMD's issue: at d 64 vector and matrix units are busy 67 % and 48 % of LP_LSEO, 65 % and 47 % of LP_DY; at d 256
+// waves wait half of their cycles (two per SIMD, registers spilled).  Measured (bf16 vectors; products counted with
+// both terms of a weight):
+//   51,200 (a quarter padding) x 30,000 x 64  with bf16 gradients 931 us: LP_LSEO 470 us and LP_DY 481 us (940 and
+//                          920 TFLOP/s, 2.4e12 exponentials a second each), packing, joins and the own items 100 us;
+//                          with float32 gradients (three terms) 1,307 us: 734 and 655 us
+//   4,099 (a tenth padding) x 50,021 x 256  with entropies and bf16 gradients 763 us: LP_LSE 120, LP_DX 273,
+//                          LP_DY 333 us (790, 1,040, 850 TFLOP/s; LP_DX spills 12, LP_DY 30 words per lane); with
+//                          float32 gradients 1,009 us
+//   8,192 (a tenth padding) x 30,000 x 128  with bf16 gradients 406 us: LP_LSEO 175, LP_DY 183 us
+//   40 (a tenth padding) x 1,000,000 x 64  with bf16 gradients 356 us: LP_LSEO 43, LP_DY 88, the joins of its float32
+//                          parts 113, of the 3,000 parts of 36 positions 73 us
+//   2,047 (a tenth padding) x 200,000 x 128  log-probabilities 120 us: LP_LSE 117 us (810 TFLOP/s)
 //   5 x 1,000,000 x 64     log-probabilities and entropies 40 us: LP_LSE 26 us, 128 MB at 4.9 TB/s
 //   256 x 2,000 x 64 float32 with entropies and gradients 50 us: eight launches of 2 to 12 us
+//   636 (a tenth padding) x 30,018 x 256 float32 with gradients 565 us: LP_LSEO 276, LP_DY 271 us (64 TFLOP/s of
+//                          154: one wave per SIMD); 2,047 x 30,018 x 64 log-probabilities 88 us (84: 84 TFLOP/s)
 //
 // Positions whose id is padding are left out first: the others are packed (rows, ids) in
 // order into the workspace, so padding costs no products and nothing it holds (NaN or
@@ -898,10 +907,13 @@ constexpr int LP_CUS = 256;
 // more waves per SIMD to overlap the exponentials with the products), MW waves per SIMD (the registers allow
 // them; the grid fills the card once), NWO waves per workgroup.  Whole calls with bf16 gradients, without / with
 // entropies, us (spills: words per lane that do not fit into registers):
-//   D 64, 51,200 x 30,000:   OB 2 MW 2  958 / 1,256;  OB 1 MW 3  1,050 / 1,333;  OB 1 MW 4  1,144 / 1,484
-//   D 128, 8,192 x 30,000:   OB 1 MW 2  413 / 496;  OB 1 MW 3  462 / 552 (spills 25 to 56);  OB 2 MW 1  418 / 503
-//   D 256, 4,099 x 50,021:   NWO 8  617 / 786;  NWO 4  688 / 848;  NWO 8 MW 1  935 / 1,182 (spills 11 to 43 with MW 2)
-//   LP_LSE, MW 3 against 2:  D 128, 2,047 x 200,000  117 / 127;  D 256, 4,099 x 50,021  120 / 128
+//   D 64, 51,200 x 30,000:   OB 2 MW 2  928 / 1,208;  OB 1 MW 3  1,032 / 1,317;  OB 1 MW 4  1,043 / 1,301
+//   D 128, 8,192 x 30,000:   OB 1 MW 2  406 / 488;  OB 1 MW 3  415 / 493;  OB 2 MW 1  412 / 496 (with float32 gradients
+//                            545 / 624, 574 / 621 and 526 / 600)
+//   D 256, 4,099 x 50,021:   NWO 8  597 / 737;  NWO 4  660 / 788;  NWO 8 MW 1  919 / 1,081
+//   LP_LSE, MW 3 against 2:  D 128, 2,047 x 200,000  132 / 137;  D 256, 4,099 x 50,021  120 / 128
+// Spills remain at D 256 (LP_LSEO 11 to 24, LP_DX 10 to 14, LP_DY 26 to 30; float32 23, 0 and 51 to 74), in the few-
+// positions LP_LSEO at D 128 (3 to 14) and in LP_LSE at D 128 (4 to 6).
 // A second block's logits in flight while the first is weighed gave LP_DY at D 64 less than 1 %, and is not done.
 // Up to 32 OB positions the waves of a workgroup share their owners and split each tile's rows instead (NWS 4;
 // a block of owners that is mostly empty costs as much as a full one): 5 x 1,000,000, LP_LSE 25 against 62.

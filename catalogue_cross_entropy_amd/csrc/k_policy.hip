@@ -6,13 +6,15 @@
 // Sums and the weights of a mean are float64, token by token: a float32 sum over millions of tokens would lose the
 // small differences these losses are made of, and one weight rounded to float32 would be off for all tokens alike.
 //
-// Measured (MI355X), kernels back to back:
-//   policy, 4.2M tokens float32 in 8,192 sequences, KL, mask: mean over tokens 32 us (75 MB; the tile kernel 27 us,
-//     2.7 TB/s: half its time vector instructions, half loads and the tile's start), over sequences 37 us
-//   policy, 16 sequences of 24 tokens: 9 us in one workgroup, of a call of 15.5 us (the call bounds it)
+// Measured (MI355X), calls back to back:
+//   policy, 4.2M tokens float32 in 8,192 sequences, KL, mask: mean over tokens 36 us (75 MB; the tile kernel 29.5 us,
+//     2.5 TB/s: one generation of workgroups, vector unit 40 % busy, waves waiting 56 % of their cycles), over
+//     sequences 41 us of kernels in a graph, 49 a call (four launches)
+//   policy, 16 sequences of 24 tokens: 9 us in one workgroup, of a call of 16 us (the call bounds it)
 //   preference, 3.3M tokens bf16 in 2,048 groups of up to 8, softmax: 27 us (23 MB; loads one after the other:
-//     offsets, tokens, the group's float64 terms, the gradient; VALU 20 % busy)
-//   preference, 256 pairs of items: 7 us, of a call of 17 us
+//     offsets, tokens, the group's float64 terms, the gradient; vector unit 30 % busy, waves waiting 70 %)
+//   preference, 131,072 pairs of items: 24 us, 16 of them the mean of the groups' losses by one workgroup
+//   preference, 256 pairs of items: 7 us, of a call of 17.5 us
 #include <algorithm>
 #include <cmath>
 
@@ -83,8 +85,8 @@ __device__ __forceinline__ int64_t seq_of_wave(const int32_t* __restrict__ offs,
 constexpr int POL_THREADS = 256;
 constexpr int POL_TILE = 4096;      // tokens per workgroup
 // One workgroup takes the whole call up to 8,192 tokens (us against the three or four launches of the general path,
-// mean over tokens / sequences: 2,048 tokens 9 / 12 against 9 to 12 / 20; 4,096: 11 / 15 against 12 to 15 / 28;
-// 8,192: 14 / 21 against 13 to 16 / 24) ...
+// with a mask, mean over tokens / sequences: 400 tokens 8.2 / 9.1 against 12.2 / 25.9; 2,048: 9.7 / 11.9 against
+// 13.3 / 17.1; 4,096: 12.1 / 15.5 against 17.6 / 22.2; 8,192: 17.0 / 22.9 against 18.5 / 22.7) ...
 constexpr int POL_SMALL_N = 8192;
 constexpr int POL_SMALL_SEQ = 2048; // ... and sequences (their offsets and counts lie in LDS)
 constexpr int POL_SUMS = 7;         // loss, pg, kl, entropy, clipped, ratio, tokens
@@ -1060,8 +1062,8 @@ hipError_t policy_t(PolArgs& a, void* ws, hipStream_t st) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  // four tokens at a time where every array allows it (slices of a longer batch may not): 65,536 tokens 12 us
-  // against 17, 4.2M 26 against 27
+  // four tokens at a time where every array allows it (slices of a longer batch may not): mean over tokens, 65,536 of
+  // them 17.8 us against 22.6, a million 19.4 against 24.0, 4.2M 34.9 against 36.0
   uintptr_t tok = 0;
   for (const void* p : {a.logp, a.old, a.ref, a.entropy, static_cast<const void*>(a.dlogp), static_cast<const void*>(a.dentropy)})
     tok |= reinterpret_cast<uintptr_t>(p);
@@ -1104,17 +1106,17 @@ hipError_t preference_t(const PrefArgs& a, hipStream_t st) {
   const uintptr_t tok = reinterpret_cast<uintptr_t>(a.logp) | reinterpret_cast<uintptr_t>(a.ref) | reinterpret_cast<uintptr_t>(a.dlogp);
   const bool wide = tok % (4 * sizeof(E)) == 0 && reinterpret_cast<uintptr_t>(a.mask) % 4 == 0;
   // Many small groups: a few lanes each, members one after the other, against a workgroup each (us, softmax):
-  //   pairs of 1 / 8 / 40 tokens: 2,048 pairs 7 / 8 / 9 against 7 / 8 / 9, 8,192 7 / 8 / 9 against 13 / 15 / 17,
-  //     131,072 20 / 39 / 51 against 128 / 144 / 163
-  //   groups of 8: 8,192 groups 16 / 23 / 32 against 13 / 15 / 28, 32,768 18 / 30 / 47 against 35 / 42 / 96
+  //   pairs of 1 / 8 / 40 tokens: 1,024 pairs 7.4 / 9.0 / 9.9 against 7.2 / 7.9 / 8.2, 2,048 7.6 / 8.8 / 9.9 against
+  //     8.2 / 8.7 / 9.4, 8,192 8.2 / 9.6 / 10.8 against 15.7 / 17.7 / 19.3, 131,072 25 / 48 / 60 against 165 / 189 / 210
+  //   groups of 8: 8,192 groups 18 / 27 / 36 against 16 / 18 / 32, 32,768 26 / 35 / 50 against 43 / 52 / 110
   const int64_t G = a.c.n_group;
   if (len < 64 && ((G >= PREF_PAIRS && a.c.n_seq <= 2 * G) || (G > PREF_MANY && a.c.n_seq <= 8 * G))) {
     if (len < 4) return pref_many_launch<E, 1, 1>(a, st);
     return wide ? pref_many_launch<E, 8, 4>(a, st) : pref_many_launch<E, 8, 1>(a, st);
   }
   // Lanes per sequence by the mean length, four tokens each where every array allows it (slices of a longer batch may
-  // not).  A million tokens in groups of 16, us with 8 lanes against 1: length 8 18 against 50, 16 16 against 30, 32 11
-  // against 20; at length 4 29 against 26.  A wave takes groups of less than 256 tokens alone.
+  // not).  A million tokens in groups of 16, us with 8 lanes against 1: length 2 60 against 46, 3 43 against 35, 4 33
+  // against 29, 8 20 against 21, 16 18 against 21, 32 13 against 18.  A wave takes groups of less than 256 tokens alone.
   if (len >= 64) return wide ? pref_launch<E, 64, 4, 256>(a, st) : pref_launch<E, 64, 1, 256>(a, st);
   if (len < 4) return pref_launch<E, 1, 1, 64>(a, st);
   if (group >= 256) return wide ? pref_launch<E, 8, 4, 256>(a, st) : pref_launch<E, 8, 1, 256>(a, st);

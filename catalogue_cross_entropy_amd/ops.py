@@ -101,7 +101,9 @@ def _call(fn, device, before, after):
 
 class ItemEmbedding:
     """Rows of an item table as a model's inputs (times `scale`) for n ids, and the
-    table's gradient.  Ids outside [0, C) are padding: zero rows, no gradient."""
+    table's gradient.  Ids outside [0, C) are padding: zero rows, no gradient.  For a bf16
+    table trained through `embed` give bf16_grads=True: a float32 gradient (the default, for
+    sums over several calls) is written whole and then converted by autograd."""
 
     def __init__(self, n: int, C: int, d: int, dtype: str = "bf16", scale: float = 1.0, bf16_grads: bool = False):
         self.n, self.C, self.d, self.dtype, self.scale = n, C, d, dtype, float(scale)
@@ -154,7 +156,9 @@ class ItemEmbedding:
 class LogProb:
     """Log-probability of one item per position under the softmax over the whole
     catalogue (logits X Y^T / temperature), optionally the entropy of that softmax, and
-    the gradients of both.  Ids outside [0, C) are padding: 0, no gradient."""
+    the gradients of both.  Ids outside [0, C) are padding: 0, no gradient.  For bf16 X and
+    Y trained through `log_probs` give bf16_grads=True: float32 gradients (the default)
+    take three products per weight instead of two, and autograd converts them."""
 
     def __init__(self, s: int, C: int, d: int, dtype: str = "bf16", temperature: float = 1.0, entropy: bool = False,
                  bf16_grads: bool = False):
@@ -329,7 +333,7 @@ def _function(name):
         return _functions[name]
     import torch
 
-    def scaled(grad, g):
+    def scaled(grad, g):   # in bf16 a second rounding, unless g is a power of two
         return None if grad is None else (grad.float() * g).to(grad.dtype)
 
     class Embed(torch.autograd.Function):
