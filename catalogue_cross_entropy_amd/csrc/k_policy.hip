@@ -245,7 +245,7 @@ __global__ __launch_bounds__(POL_THREADS) void k_pol_count(PolArgs a) {
     if (wave0 >= n) continue;   // whole waves
     const int64_t s0 = seq_of_wave(a.offs, 0, ns - 1, wave0);
     const int64_t s1 = seq_of_wave(a.offs, s0, ns - 1, min(n, wave0 + WAVE * PER) - 1);
-    if (s1 - s0 < 16) {   // few sequences: one atomic each per wave (64 lanes on one word: 66 us for 4.2M tokens, not 35)
+    if (s1 - s0 < 16) {   // few sequences: one atomic each per wave (64 lanes on one word cost 30 us more for 4.2M tokens)
       for (int64_t s = s0; s <= s1; ++s) {
         const int64_t b = s == s0 ? t0 : max(t0, offset_at(a.offs, s, n)), e = s == s1 ? t0 + PER : offset_at(a.offs, s + 1, n);
         const int64_t from = min(b - t0, (int64_t)PER), to = min(max(e - t0, (int64_t)0), (int64_t)PER);
