@@ -17,7 +17,6 @@
 
 #include "rece_device.h"
 #include "rece_internal.h"
-#include "rece_parts.h"
 
 namespace rece {
 
@@ -325,9 +324,6 @@ struct EmbGrad {
   const int32_t* V;        // their rows (bit 31 may be set)
   const uint32_t* ntot;    // records
   const void* dout;
-  const float* weight;     // per row, every wstride-th, or NULL
-  int wstride;
-  SweepParts parts;        // partial rows added first (rows NULL: none)
   float* partial;          // [pieces][2][d]: the piece's part of a run that began earlier, and of one that goes on
   void* dtable;
   int d;
@@ -337,28 +333,10 @@ struct EmbGrad {
 
 // EPL values of row j: written, or added (accumulate: the only writer of the row in this call).
 template <int EPL>
-__device__ __forceinline__ void put_row(const EmbGrad& a, const SweepWork& w, int64_t j, int col, float (&v)[EPL]) {
+__device__ __forceinline__ void put_row(const EmbGrad& a, int64_t j, int col, float (&v)[EPL]) {
 #pragma unroll
   for (int t = 0; t < EPL; ++t) v[t] *= a.scale;
   const int64_t off = j * a.d + col;
-  if (a.parts.rows) {
-    float base[EPL];
-#pragma unroll
-    for (int t = 0; t < EPL; ++t) base[t] = 0.0f;
-    a.parts.each(w, j, [&](int64_t at) {
-      const float4* h = reinterpret_cast<const float4*>(a.parts.rows + at * a.d + col);
-#pragma unroll
-      for (int t = 0; t < EPL / 4; ++t) {
-        const float4 x = h[t];
-        base[4 * t] += x.x;
-        base[4 * t + 1] += x.y;
-        base[4 * t + 2] += x.z;
-        base[4 * t + 3] += x.w;
-      }
-    });
-#pragma unroll
-    for (int t = 0; t < EPL; ++t) v[t] += base[t];
-  }
   if (a.b16) {
     uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.dtable) + off);
 #pragma unroll
@@ -397,37 +375,31 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_pieces(EmbGrad a) {
   const int64_t t1 = min(n, t0 + EMB_PIECE);
   const int prev = t0 > 0 ? a.K[t0 - 1] : -1, next = t1 < n ? a.K[t1] : -1;
   const E* __restrict__ dout = static_cast<const E*>(a.dout);
-  const SweepWork work = a.parts.rows ? a.parts.work() : SweepWork{};
   int cur = -1;
   int64_t start = t0;
   float sum[EPL];
   auto flush = [&](int64_t end) {
     const bool head = start == t0 && cur == prev, tail = end == t1 && cur == next;
     if (!head && !tail)
-      put_row<EPL>(a, work, cur, col, sum);
+      put_row<EPL>(a, cur, col, sum);
     else
       put_partial<EPL>(a.partial + (piece * 2 + (head ? 0 : 1)) * a.d + col, sum);
   };
   for (int64_t tb = t0; tb < t1; tb += UNR) {
     int key[UNR];
     u32x4 raw[UNR];
-    float wgt[UNR];
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
       const int64_t t = min(tb + u, t1 - 1);
       const int64_t i = a.V[t] & 0x7FFFFFFF;
       key[u] = a.K[t];
       raw[u] = *reinterpret_cast<const u32x4*>(dout + i * a.d + col);
-      wgt[u] = a.weight ? a.weight[i * a.wstride] : 1.0f;
     }
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
       if (tb + u >= t1) break;
       float v[EPL];
       unpack16(raw[u], v);
-      if (a.weight)
-#pragma unroll
-        for (int t = 0; t < EPL; ++t) v[t] *= wgt[u];
       if (key[u] != cur) {
         if (cur >= 0) flush(tb + u);
         cur = key[u];
@@ -490,7 +462,7 @@ __global__ __launch_bounds__(EMB_THREADS) void k_embed_join(EmbGrad a) {
   for (int o = 1; o < used; ++o)
 #pragma unroll
     for (int t = 0; t < EPL; ++t) sum[t] += sh[o][sub * EPL + t];
-  put_row<EPL>(a, a.parts.rows ? a.parts.work() : SweepWork{}, j, col, sum);
+  put_row<EPL>(a, j, col, sum);
 }
 
 // Lanes per row: the power of two that holds a row's 16-byte pieces, at most a wave
@@ -651,45 +623,12 @@ hipError_t order_rows(const int32_t* ids, int64_t n, int64_t C, const ClearArgs&
   return hipSuccess;
 }
 
-hipError_t row_sums_clear(const RowSums& r, const ClearArgs& clear, void* ws, void* out, hipStream_t st) {
-  const int64_t n = r.n;
-  if (n == 0) return clear.n16 > 0 ? clear_only(clear, st) : hipSuccess;
-  char* p = static_cast<char*>(ws);
-  void* scratch = p;
-  p += order_bytes(n, r.C);
-  int32_t* buf[4];
-  for (int q = 0; q < 4; ++q, p += align256((size_t)n * 4)) buf[q] = reinterpret_cast<int32_t*>(p);
-  EmbGrad a{};
-  hipError_t e = order_rows(r.ids, n, r.C, clear, scratch, buf, a, st);
-  if (e != hipSuccess) return e;
-  a.dout = r.rows;
-  a.weight = r.weight;
-  a.wstride = r.wstride;
-  if (r.parts) a.parts = *r.parts;
-  a.partial = reinterpret_cast<float*>(p);
-  a.dtable = out;
-  a.d = r.d;
-  a.scale = r.scale;
-  a.b16 = r.grad_bf16;
-  a.acc = r.accumulate;
-  const int64_t np = piece_count(n);
-  e = r.bf16v ? pieces_t<bf16>(a, np, st) : pieces_t<float>(a, np, st);
-  if (e != hipSuccess) return e;
-  return join(a, np, st);
-}
-
 }  // namespace
 
-size_t row_sums_bytes(int64_t n, int64_t C, int d) {
+size_t embed_workspace_bytes(int64_t n, int64_t C, int d) {
   if (n == 0) return 16;
   return order_bytes(n, C) + 4 * align256((size_t)n * 4) + align256((size_t)piece_count(n) * 2 * d * 4);
 }
-
-hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st) {
-  return row_sums_clear(r, ClearArgs{}, ws, out, st);
-}
-
-size_t embed_workspace_bytes(int64_t n, int64_t C, int d) { return row_sums_bytes(n, C, d); }
 
 hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, const void* table, const int32_t* ids,
                          void* out, hipStream_t st) {
@@ -701,17 +640,26 @@ hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, 
                           const int32_t* ids, const void* dout, void* ws, void* dtable, hipStream_t st) {
   ClearArgs clear{};
   if (!accumulate) clear = ClearArgs{static_cast<u32x4*>(dtable), C * d * (grad_bf16 ? 2 : 4) / 16};
-  RowSums r{};
-  r.bf16v = bf16v;
-  r.n = n;
-  r.C = C;
-  r.d = d;
-  r.scale = scale;
-  r.grad_bf16 = grad_bf16;
-  r.accumulate = accumulate;
-  r.ids = ids;
-  r.rows = dout;
-  return row_sums_clear(r, clear, ws, dtable, st);
+  if (n == 0) return clear.n16 > 0 ? clear_only(clear, st) : hipSuccess;
+  char* p = static_cast<char*>(ws);
+  void* scratch = p;
+  p += order_bytes(n, C);
+  int32_t* buf[4];
+  for (int q = 0; q < 4; ++q, p += align256((size_t)n * 4)) buf[q] = reinterpret_cast<int32_t*>(p);
+  EmbGrad a{};
+  hipError_t e = order_rows(ids, n, C, clear, scratch, buf, a, st);
+  if (e != hipSuccess) return e;
+  a.dout = dout;
+  a.partial = reinterpret_cast<float*>(p);
+  a.dtable = dtable;
+  a.d = d;
+  a.scale = scale;
+  a.b16 = grad_bf16;
+  a.acc = accumulate;
+  const int64_t np = piece_count(n);
+  e = bf16v ? pieces_t<bf16>(a, np, st) : pieces_t<float>(a, np, st);
+  if (e != hipSuccess) return e;
+  return join(a, np, st);
 }
 
 }  // namespace rece

@@ -73,7 +73,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // Per packed row of the backward pass.
 struct LpRow {
-  float lse2, a, b, g;   // G = [hit] g - p (a + b (x2 - lse2)),  p = exp2(x2 - lse2)
+  float lse2, a, b, g;   // G = g for the row's own item, -p (a + b (x2 - lse2)) for others, p = exp2(x2 - lse2)
 };
 
 // log2(e) / temperature: rounded, and what the rounding left.  Its error would scale every logit alike, 6e-8 of a
@@ -89,7 +89,7 @@ struct LpArgs {
   SweepParts parts;       // sizes, workgroups, and where parts lie
   LpScale c2;             // log2(e) / temperature
   float4* stat;           // LP_LSE(O): parts (reference m, sum of 2^(x2 - m), sum of 2^(x2 - m) (x2 - m), 0)
-  const LpRow* rows;      // LP_DX, LP_DY: of the packed positions
+  const LpRow* rows;      // LP_DX, LP_DY: of the packed positions (LP_DY: padded with rows of no weight)
   const int32_t* idc;     // ids of the packed positions
   float* out;             // LP_LSEO, LP_DX, LP_DY: parts.rows
   int terms;              // bf16 terms of a weight in the products (2 or 3; 1 with float32 inputs)
@@ -127,10 +127,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// Two floats as two bf16 terms each.  The differences are those of the rounded floats everywhere: fused with the product
-// that made a weight in one place and not in another, a second term would differ between them.
+// Two floats as two bf16 terms each.
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-#pragma clang fp contract(off)
   hi = pack_bf16(a, b);
   const float ra = a - lo_f32(hi), rb = b - hi_f32(hi);
   lo = pack_bf16(ra, rb);
@@ -158,7 +156,7 @@ __device__ __forceinline__ float lp_less(float x, LpScale c, float r) {
   return LO ? fmaf(x, c.lo, d) : d;
 }
 
-// Gradient by a logit (less [own] g): -p (a + b d) with d = x2 - lse2, p = 2^d.
+// Gradient by a logit of another item: -p (a + b d) with d = x2 - lse2, p = 2^d.
 template <bool ENT>
 __device__ __forceinline__ float lp_weight(float d, float a, float b) {
   return -exp2_fast(d) * (ENT ? fmaf(b, d, a) : a);
@@ -275,18 +273,11 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
   }
 }
 
-// What of a weight went into the products: all of it, or (bf16, two terms) its first two bf16 terms.
-__device__ __forceinline__ float lp_taken(float g, int terms, bool b16) {
-  if (!b16 || terms != 2) return g;
-  uint32_t hi, lo;
-  split_bf16(g, 0.0f, hi, lo);
-  return lo_f32(hi) + lo_f32(lo);   // exact
-}
-
 // NWO waves along the owners x NWS waves along a tile's rows; OB blocks of 32 owners per wave.
-// A row's own item enters LP_LSEO, LP_DX and LP_DY (bf16) with the others, as -p (..); the joins add what is
-// missing of g - p (..) in float32 (1 - p would lose its digits in bf16 terms), knowing what went in: the
-// own logits come from the same products, so the same bits.  LP_DY (float32) adds it here.
+// A position's own item is left out of the sums (its logit becomes one that weighs nothing), and its weight g in LP_DX
+// and LP_DY is the whole of it, g (1 - p) and the entropy's, formed before: as one of the sum's terms, p would round
+// what the others add by 2^-24 each time, and where it is near 1 nothing else is left of 1 - p.  Few blocks hold an own
+// item, so what costs is the question (a comparison of ids per block).
 template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int TERMS, int MINW>
 __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   using T = LpTile<E, D, NWS>;
@@ -295,7 +286,6 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   constexpr int KC = L::KC;
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile
   constexpr bool ACC = MODE != LP_LSE, LSE = MODE == LP_LSE || MODE == LP_LSEO, DY = MODE == LP_DY;
-  constexpr bool OWN = DY && sizeof(E) == 4;
   static_assert(T::BYTES % (16 * NT) == 0 && TI <= NT, "whole chunks per thread");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -310,7 +300,8 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   lo.init();
   uint32_t o0 = 0, tb = 0, te = 0;   // the wave's first owner, the run's tiles of its block
   u32x4 bown[OB][KC];
-  float olse[OB], oa[OB], obt[OB];   // LP_DX: the owner's constants
+  uint32_t oid[OB];                            // the owners' own items (not LP_DY)
+  float olse[OB], oa[OB], obt[OB], og[OB];     // LP_DX: the owners' constants
   auto load_owners = [&]() {
     const uint32_t rr = settled(r), hh = settled(h);
 #pragma unroll
@@ -319,12 +310,28 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
       const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.own) + (int64_t)o * RB) + hh;
 #pragma unroll
       for (int t = 0; t < KC; ++t) bown[ob][t] = p[2 * t];
+      if constexpr (!DY) oid[ob] = (uint32_t)a.idc[o];
       if constexpr (MODE == LP_DX) {
         const LpRow c = a.rows[o];
         olse[ob] = c.lse2;
         oa[ob] = c.a;
         obt[ob] = c.b;
+        og[ob] = c.g;
       }
+    }
+  };
+  // the values of own items in the block of rows that begins at q0 become f(ob) (not LP_DY)
+  auto own_items = [&](f32x16 (&x)[OB], uint32_t q0, auto f) {
+    bool near = false;
+#pragma unroll
+    for (int ob = 0; ob < OB; ++ob) near = near || oid[ob] - q0 < 32u;
+    if (!ballot(near)) return;
+#pragma unroll
+    for (int ob = 0; ob < OB; ++ob) {
+      const uint32_t at = oid[ob] - q0 - 4 * h;
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        x[ob][v] = at == (uint32_t)lp_row(v) ? f(ob) : x[ob][v];
     }
   };
   float m[OB], z[OB], tt[OB];   // LP_LSE(O): reference and sums
@@ -359,7 +366,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     if constexpr (DY) {
       if (tid < TI) {   // packed rows are padded with rows of no weight to whole tiles
         nrow = *reinterpret_cast<const u32x4*>(a.rows + ((int64_t)t * TI + tid));
-        if constexpr (OWN) nid = (uint32_t)a.idc[(int64_t)t * TI + tid];
+        nid = (uint32_t)a.idc[(int64_t)t * TI + tid];
       }
     }
   };
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
       if (tid < TI) {
         const uint32_t par = par0 + (t & 1) * PB + 4 * tid;
 #pragma unroll
-        for (int q = 0; q < (OWN ? 5 : 3); ++q) lds_put(par + q * TI * 4, q < 4 ? nrow[q < 4 ? q : 0] : nid);
+        for (int q = 0; q < 5; ++q) lds_put(par + q * TI * 4, q < 4 ? nrow[q < 4 ? q : 0] : nid);
       }
     }
   };
@@ -400,6 +407,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
             if (lp_row(v) >= lim) x[ob][v] = far;
       }
     }
+    if constexpr (LSE) own_items(x, q0, [&](int) { return far; });
   };
   // m = max(m, the block's logits), the same in both lane halves of an owner
   auto raise = [&](f32x16 (&x)[OB]) {
@@ -412,7 +420,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     }
   };
   // the block's logits become weights, and join the sums
-  auto weigh = [&](f32x16 (&x)[OB], uint32_t par) {
+  auto weigh = [&](f32x16 (&x)[OB], uint32_t par, uint32_t q0) {
     if constexpr (LSE) {
 #pragma unroll
       for (int ob = 0; ob < OB; ++ob) {
@@ -446,7 +454,8 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
             x[ob][v] = lp_weight<ENT>(d, DY ? pa[e] : oa[ob], DY ? pb[e] : obt[ob]);
           }
       }
-      if constexpr (OWN) {
+      if constexpr (MODE == LP_DX) own_items(x, q0, [&](int ob) { return og[ob]; });
+      if constexpr (DY) {
         if (ballot(lds_at<uint32_t>(par + 4 * TI * 4 + 4 * r) - o0 < 32 * OB)) {
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
@@ -454,7 +463,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
             const uint32_t id = lds_at<uint32_t>(at + 4 * TI * 4);
             const float g = lds_at<float>(at + 3 * TI * 4);
 #pragma unroll
-            for (int ob = 0; ob < OB; ++ob) x[ob][v] += id == o0 + 32 * ob + r ? g : 0.0f;
+            for (int ob = 0; ob < OB; ++ob) x[ob][v] = id == o0 + 32 * ob + r ? g : x[ob][v];
           }
         }
       }
@@ -479,7 +488,7 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
     for (int i = 0; i < NB; ++i) {
       f32x16 x[OB];
       logits(x, base + i * (NWS * 32 * RB), q0 + i * NWS * 32);
-      weigh(x, par + i * (NWS * 128));
+      weigh(x, par + i * (NWS * 128), q0 + i * NWS * 32);
       if constexpr (ACC) lp_product<E, D, NWS, OB, TERMS>(acc, x, lo, base + i * (NWS * 32 * RB));
     }
   };
@@ -570,8 +579,8 @@ __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
 // Workgroup b takes ids [b per, (b + 1) per): it counts the ids before them that lie in
 // [0, C) itself (an L2-resident read of 4 bytes a position, in place of a scan's further
 // launches), then writes the list of its own, the packed rows and ids, and the (unscaled)
-// logit of each row's own item, the diagonal of a 32 x 32 product, so that it has the
-// same bits as in the sweeps.  The last workgroup fills the padding with zero rows.
+// logit of each row's own item, the diagonal of a 32 x 32 product.  The last workgroup fills the
+// padding with zero rows.
 constexpr int PACK_THREADS = 256;
 constexpr int64_t PACK_BLOCKS = 256, PACK_LEAST = 64;   // workgroups at most, ids of each at least
 
@@ -667,22 +676,13 @@ __global__ __launch_bounds__(PACK_THREADS) void k_lp_pack(const E* __restrict__ 
 }
 
 // ------------------------------------------------------------------ joins
-// The part that position r's own item went into: the workgroup of its tile, the wave of its block of 32 rows.
-__device__ __forceinline__ int64_t lp_home(const SweepParts& parts, const SweepWork& w, uint32_t r, uint32_t id) {
-  const uint32_t b = r / parts.block;
-  const int64_t g = (int64_t)div_u64((uint64_t)b * w.nt + id / parts.tile, w.per);
-  return (w.slot(b, g) * parts.nws + (id % parts.tile) / 32 % parts.nws) * parts.block + r % parts.block;
-}
-
-// L lanes per position (1, a wave, a workgroup): the parts of its sum -> log-sum-exp, log-probability, entropy.
-// Where the own item is most of the sum, its term is taken out (the same bits that went in) and the others set
-// against it: the terms carry the rounding of their distance to a reference that may lie far below, 1e-6, and
-// 1 - p and log p would be as wrong.
+// L lanes per position (1, a wave, a workgroup): the parts of the others' sum -> log-sum-exp, log-probability, entropy.
+// Where the own item is most of it, log p = -log1p(the others' sum over the own term), which keeps every digit of 1 - p.
 constexpr int FINISH_WIDE = 1024;
-template <int L, bool LO>
+template <int L>
 __global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
     const int32_t* __restrict__ inv, int64_t s, SweepParts parts, const float4* __restrict__ stat,
-    const float* __restrict__ own, const int32_t* __restrict__ idc, LpScale c2, float2* __restrict__ lse2, float* __restrict__ ent_c,
+    const float* __restrict__ own, LpScale c2, float2* __restrict__ lse2, float* __restrict__ logp_c, float* __restrict__ ent_c,
     float* __restrict__ logp, float* __restrict__ entropy) {
   constexpr int NT = L > WAVE ? L : 256, UNR = 4;
   const int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) / L;
@@ -743,34 +743,42 @@ __global__ __launch_bounds__(L > WAVE ? L : 256) void k_lp_finish(
     }
     if (l != 0) return;
   }
-  const float o = own[r], mh = stat[lp_home(parts, w, (uint32_t)r, (uint32_t)idc[r])].x;
-  const float x2 = o * c2.hi, x2lo = fmaf(o, c2.lo, fmaf(o, c2.hi, -x2));
-  const float lz = log2f(zz);
-  // the others' sum over the own term
-  const float others = fmaf(-exp2_fast(lp_less<LO>(o, c2, mh)), exp2_fast(mh - mm), zz);
-  const float t1 = (others < 0.0f ? 0.0f : others) * exp2_fast(fminf(mm - x2, 64.0f));   // NaN stays
+  // the own logit in two floats; the others' sum zz stands for zz 2^mm
+  const float o = own[r], x2 = o * c2.hi, x2lo = fmaf(o, c2.lo, fmaf(o, c2.hi, -x2));
+  // over the own term (NaN stays); x2lo is below a step of x2, so it goes in as a factor
+  const float t1 = zz * exp2_fast(fminf(mm - x2, 64.0f)) * fmaf(-LN2, x2lo, 1.0f);
   const bool mostly = t1 < 1.0f;
+  const float e = mostly ? 0.0f : exp2_fast(x2 - mm), all = zz + e;   // at most zz, where it is taken
   // log-sum-exp as two floats: a step of one alone, 2^-20 for sums beyond 2^16, is as large as the rest
-  const float base = mostly ? x2 : mm, more = mostly ? log1pf(t1) * (1.0f / LN2) : lz;
+  const float base = mostly ? x2 : mm, more = mostly ? log1pf(t1) * (1.0f / LN2) : log2f(all);
   const float l2 = base + more, back = l2 - base;
   const float rest = (base - (l2 - back)) + (more - back) + (mostly ? x2lo : 0.0f);
+  const float lp = mostly ? -log1pf(t1) : (lp_less<true>(o, c2, l2) - rest) * LN2;
   lse2[r] = float2{l2, rest};
-  logp[i] = mostly ? -log1pf(t1) : (lp_less<true>(o, c2, l2) - rest) * LN2;
+  logp_c[r] = lp;
+  logp[i] = lp;
   if (entropy) {
-    const float H = (lz - tt / zz) * LN2;
+    // sum of p (lse - x), the own item's part apart where it is most: (1 - p) times the others' mean distance, and p log p
+    float H;
+    if (mostly) {
+      const float p = 1.0f / (1.0f + t1);
+      H = zz > 0.0f ? t1 * p * ((l2 - mm) - tt / zz) * LN2 - p * lp : 0.0f;
+    } else {
+      H = (more - (tt + e * (x2 - mm)) / all) * LN2;
+    }
     entropy[i] = H;
     ent_c[r] = H;
   }
 }
 
-// Constants of the gradient per packed row; rows of no weight up to the padding.  own: the row's own
-// logit; rows' g: what the sweeps leave of the own item's g - p (..).
+// Constants of the gradient per packed row; rows of no weight up to the padding.  What lse2's second float leaves goes
+// into the factors.
 template <bool ENT>
 __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_p, const int32_t* __restrict__ list,
                                                  int64_t pad, const float2* __restrict__ lse2,
-                                                 const float* __restrict__ ent_c, const float* __restrict__ own, LpScale c2,
+                                                 const float* __restrict__ logp_c, const float* __restrict__ ent_c,
                                                  const float* __restrict__ dlogp, const float* __restrict__ dent,
-                                                 float inv_t, int terms, int b16, LpRow* __restrict__ rows) {
+                                                 float inv_t, LpRow* __restrict__ rows) {
   const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (r >= pad) return;
   LpRow c{LP_NEVER, 0.0f, 0.0f, 0.0f};
@@ -778,15 +786,12 @@ __global__ __launch_bounds__(256) void k_lp_coef(const int32_t* __restrict__ nv_
     const int64_t i = list[r];
     const float g = dlogp[i] * inv_t, h = ENT ? dent[i] * inv_t : 0.0f;
     const float2 l2 = lse2[r];
+    const float lp = logp_c[r], H = ENT ? ent_c[r] : 0.0f, f = fmaf(-LN2, l2.y, 1.0f);
     c.lse2 = l2.x;
-    c.a = ENT ? fmaf(h, ent_c[r], g) : g;
-    c.b = h * LN2;
-    // the own item's weight g (1 - p) - p (..), less what the sweeps add for it
-    const float ds = lp_less<true>(own[r], c2, c.lse2), d = ds - l2.y;
-    const float w = lp_weight<ENT>(ds, c.a, c.b);
-    float total = g * -expm1f(d * LN2);
-    if constexpr (ENT) total -= exp2_fast(d) * fmaf(c.b, d, h * ent_c[r]);
-    c.g = total - lp_taken(w, terms, b16 != 0);
+    c.a = (ENT ? fmaf(h, H, g) : g) * f;
+    c.b = h * LN2 * f;
+    c.g = g * -expm1f(lp);
+    if constexpr (ENT) c.g -= expf(lp) * h * (lp + H);
   }
   rows[r] = c;
 }
@@ -830,12 +835,9 @@ dim3 join_grid(int64_t n, int d, int groups) {   // at most 2^31 threads along x
   return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
 }
 
-// out row = sum of the parts' rows.  inv (dX): the row of the parts for each output row (or -1: zeros),
-// whose own item's row of Y is added g times.
-template <class E>
-__global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, int groups, const int32_t* __restrict__ inv,
-                                                 const LpRow* __restrict__ rows, const int32_t* __restrict__ idc,
-                                                 const E* __restrict__ Y, int64_t n, void* __restrict__ out, int b16) {
+// out row = sum of the parts' rows.  inv (dX): the row of the parts for each output row (or -1: zeros).
+__global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, int groups, const int32_t* __restrict__ inv, int64_t n,
+                                                 void* __restrict__ out, int b16) {
   const JoinLane q(d, groups);
   if (q.row >= n) return;   // a row's lanes together
   const int64_t i = q.row;
@@ -848,25 +850,18 @@ __global__ __launch_bounds__(256) void k_lp_join(SweepParts parts, int d, int gr
       v = float4{v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w};
     }, q.group, q.groups);
     q.sum(v, d);
-    if (inv) {
-      const float g = rows[r].g;
-      const E* y = Y + (int64_t)idc[r] * d + c;
-      v = float4{fmaf(g, to_f32(y[0]), v.x), fmaf(g, to_f32(y[1]), v.y), fmaf(g, to_f32(y[2]), v.z), fmaf(g, to_f32(y[3]), v.w)};
-    }
   }
   if (q.group == 0) put4(out, i * d + c, v, b16 != 0);
 }
 
-// dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j:
-//   dX_i = g_i (y_own - sum over the parts of O 2^(m - lse2))
-// with the own item's share of the sum taken out and 1 - p_own in its place, so that nothing is lost where
-// p_own is near 1.
+// dX without an entropy gradient, from the forward pass's sums O of 2^(x2 - m) y_j over the other items:
+//   dX_i = g_i ((1 - p_own) y_own - sum over the parts of O 2^(m - lse2))
 template <class E>
 __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float4* __restrict__ stat, int d, int groups,
                                                const int32_t* __restrict__ inv, int64_t s, const E* __restrict__ Y,
-                                               const int32_t* __restrict__ idc, const float* __restrict__ own, LpScale c2,
-                                               const float2* __restrict__ lse2, const float* __restrict__ dlogp,
-                                               float inv_t, int terms, void* __restrict__ out, int b16) {
+                                               const int32_t* __restrict__ idc, const float2* __restrict__ lse2,
+                                               const float* __restrict__ logp_c, const float* __restrict__ dlogp,
+                                               float inv_t, void* __restrict__ out, int b16) {
   const JoinLane q(d, groups);
   if (q.row >= s) return;   // a row's lanes together
   const int64_t i = q.row;
@@ -875,23 +870,15 @@ __global__ __launch_bounds__(256) void k_lp_dx(SweepParts parts, const float4* _
   float4 v = float4{0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
     const float2 l2 = lse2[r];
-    const float g = dlogp[i] * inv_t, o = own[r];
-    const uint32_t id = (uint32_t)idc[r];
-    const E* yp = Y + (int64_t)id * d + c;
+    const float g = dlogp[i] * inv_t, rest = -expm1f(logp_c[r]);
+    const E* yp = Y + (int64_t)idc[r] * d + c;
     const float4 y = float4{to_f32(yp[0]), to_f32(yp[1]), to_f32(yp[2]), to_f32(yp[3])};
-    const SweepWork w = parts.work();
-    const int64_t home = lp_home(parts, w, (uint32_t)r, id);
-    parts.each(w, r, [&](int64_t at) {
-      const float mp = stat[at].x, f = exp2_fast((mp - l2.x) - l2.y);
-      float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
-      if (at == home) {
-        const float e = lp_taken(exp2_fast(lp_less<sizeof(E) == 4>(o, c2, mp)), terms, sizeof(E) == 2);
-        x = float4{fmaf(-e, y.x, x.x), fmaf(-e, y.y, x.y), fmaf(-e, y.z, x.z), fmaf(-e, y.w, x.w)};
-      }
+    parts.each(parts.work(), r, [&](int64_t at) {
+      const float f = exp2_fast((stat[at].x - l2.x) - l2.y);
+      const float4 x = *reinterpret_cast<const float4*>(parts.rows + at * d + c);
       v = float4{fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w)};
     }, q.group, q.groups);
     q.sum(v, d);
-    const float rest = -expm1f((lp_less<true>(o, c2, l2.x) - l2.y) * LN2);
     v = float4{g * fmaf(rest, y.x, -v.x), g * fmaf(rest, y.y, -v.y), g * fmaf(rest, y.z, -v.z), g * fmaf(rest, y.w, -v.w)};
   }
   if (q.group == 0) put4(out, i * d + c, v, b16 != 0);
@@ -957,7 +944,7 @@ LpSweep lp_shape(int mode, int64_t n_own, int64_t n_str) {
 
 struct LpLayout {
   int64_t pad;
-  size_t nv, list, inv, idc, own, lse2, ent, rows, xc, stat, o, dx, sums, bytes;
+  size_t nv, list, inv, idc, own, lse2, logp, ent, rows, xc, stat, o, dx, bytes;
 };
 
 template <class E, int D>
@@ -979,6 +966,7 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
   y.idc = take(y.pad * 4);
   y.own = take(y.pad * 4);
   y.lse2 = take(y.pad * 8);
+  y.logp = take(y.pad * 4);
   y.ent = take(ent ? y.pad * 4 : 0);
   y.xc = take((size_t)y.pad * D * sizeof(E));
   const LpSweep f = lp_shape<E, D>(fused ? LP_LSEO : LP_LSE, s, C);
@@ -996,7 +984,6 @@ LpLayout lp_layout_t(int64_t s, int64_t C, uint32_t flags) {
     y.rows = take(y.pad * sizeof(LpRow));
     // dX is finished before the dY sweep starts
     y.dx = take(std::max(ent ? (size_t)x.slots(s) * x.block() : 0, (size_t)v.slots(C) * v.block()) * D * 4);
-    if (sizeof(E) == 2) y.sums = take(row_sums_bytes(y.pad, C, D));
   }
   y.bytes = std::max(fwd, off);
   return y;
@@ -1089,6 +1076,7 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
   a.parts = lp_parts<E, D>(fused ? LP_LSEO : LP_LSE, s, C, at<int32_t>(ws, y.nv), nullptr);
   a.c2 = c2;
   a.stat = at<float4>(ws, y.stat);
+  a.idc = at<int32_t>(ws, y.idc);
   a.out = at<float>(ws, y.o);
   a.terms = lp_terms<E>(flags);
   if (fused)
@@ -1099,10 +1087,9 @@ hipError_t lp_forward_t(int64_t s, int64_t C, float temperature, uint32_t flags,
     LP_TRY((lp_launch<E, D, LP_LSE, false>(a, st)));
   // few positions have many parts each: a workgroup for each while the card holds them at once, or a wave; many have few
   const int lanes = s <= LP_CUS ? FINISH_WIDE : s <= 8192 ? WAVE : 1, threads = std::max(256, lanes);
-  constexpr bool LO = sizeof(E) == 4;
-  auto finish = lanes == FINISH_WIDE ? k_lp_finish<FINISH_WIDE, LO> : lanes == WAVE ? k_lp_finish<WAVE, LO> : k_lp_finish<1, LO>;
+  auto finish = lanes == FINISH_WIDE ? k_lp_finish<FINISH_WIDE> : lanes == WAVE ? k_lp_finish<WAVE> : k_lp_finish<1>;
   hipLaunchKernelGGL(finish, dim3((unsigned)ceil_div(s * lanes, threads)), dim3(threads), 0, st, at<int32_t>(ws, y.inv), s,
-                     a.parts, a.stat, at<float>(ws, y.own), at<int32_t>(ws, y.idc), c2, at<float2>(ws, y.lse2), at<float>(ws, y.ent), logp,
+                     a.parts, a.stat, at<float>(ws, y.own), c2, at<float2>(ws, y.lse2), at<float>(ws, y.logp), at<float>(ws, y.ent), logp,
                      entropy);
   return hipGetLastError();
 }
@@ -1117,8 +1104,8 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
   const int32_t* nv = at<int32_t>(ws, y.nv);
   auto coef = dent ? k_lp_coef<true> : k_lp_coef<false>;
   hipLaunchKernelGGL(coef, dim3((unsigned)ceil_div(y.pad, 256)), dim3(256), 0, st, nv, at<int32_t>(ws, y.list), y.pad,
-                     at<float2>(ws, y.lse2), at<float>(ws, y.ent), at<float>(ws, y.own), c2, dlogp, dent, inv_t, terms,
-                     sizeof(E) == 2 ? 1 : 0, at<LpRow>(ws, y.rows));
+                     at<float2>(ws, y.lse2), at<float>(ws, y.logp), at<float>(ws, y.ent), dlogp, dent, inv_t,
+                     at<LpRow>(ws, y.rows));
   LP_TRY(hipGetLastError());
   LpArgs a{};
   a.c2 = c2;
@@ -1127,8 +1114,7 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
   a.idc = at<int32_t>(ws, y.idc);
   auto join = [&](const int32_t* inv, int64_t n, void* out) {
     const int groups = join_groups(a.parts, D);
-    hipLaunchKernelGGL((k_lp_join<E>), join_grid(n, D, groups), dim3(256), 0, st, a.parts, D, groups, inv,
-                       a.rows, a.idc, static_cast<const E*>(Y), n, out, b16);
+    hipLaunchKernelGGL(k_lp_join, join_grid(n, D, groups), dim3(256), 0, st, a.parts, D, groups, inv, n, out, b16);
     return hipGetLastError();
   };
   if (flags & RECE_FLAG_ENTROPY) {
@@ -1146,8 +1132,8 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
     const int groups = join_groups(sums, D);
     hipLaunchKernelGGL((k_lp_dx<E>), join_grid(s, D, groups), dim3(256), 0, st, sums,
                        at<float4>(ws, y.stat), D, groups,
-                       at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y), a.idc, at<float>(ws, y.own), c2,
-                       at<float2>(ws, y.lse2), dlogp, inv_t, terms, dX, b16);
+                       at<int32_t>(ws, y.inv), s, static_cast<const E*>(Y), a.idc, at<float2>(ws, y.lse2),
+                       at<float>(ws, y.logp), dlogp, inv_t, dX, b16);
     LP_TRY(hipGetLastError());
   }
   a.own = Y;
@@ -1158,22 +1144,7 @@ hipError_t lp_backward_t(int64_t s, int64_t C, float temperature, uint32_t flags
     LP_TRY((lp_launch<E, D, LP_DY, true>(a, st)));
   else
     LP_TRY((lp_launch<E, D, LP_DY, false>(a, st)));
-  LP_TRY(join(nullptr, C, dY));
-  if (sizeof(E) == 4) return hipSuccess;
-  // the items that are some position's own: their rows once more, with what the sweep left of g
-  RowSums r{};
-  r.bf16v = true;
-  r.n = y.pad;
-  r.C = C;
-  r.d = D;
-  r.scale = 1.0f;
-  r.grad_bf16 = b16 != 0;
-  r.ids = a.idc;
-  r.rows = a.str;
-  r.weight = &a.rows[0].g;
-  r.wstride = sizeof(LpRow) / 4;
-  r.parts = &a.parts;
-  return row_sums(r, at<void>(ws, y.sums), dY, st);
+  return join(nullptr, C, dY);
 }
 
 }  // namespace

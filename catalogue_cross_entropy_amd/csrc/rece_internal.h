@@ -192,25 +192,6 @@ hipError_t embed_forward(bool bf16v, int64_t n, int64_t C, int d, float scale, c
                          void* out, hipStream_t st);
 hipError_t embed_backward(bool bf16v, int64_t n, int64_t C, int d, float scale, bool grad_bf16, bool accumulate,
                           const int32_t* ids, const void* dout, void* ws, void* dtable, hipStream_t st);
-struct SweepParts;
-// Sums of rows by id, out_j = scale * sum over i with ids[i] = j of weight_i rows_i (+ parts), in a fixed
-// order: the embedding's gradient, and the own items' share of the log-probabilities' dY.
-struct RowSums {
-  bool bf16v;             // type of rows
-  int64_t n, C;
-  int d;
-  float scale;
-  bool grad_bf16;         // type of out
-  bool accumulate;        // add to out
-  const int32_t* ids;     // [n]; outside [0, C): left out
-  const void* rows;       // [n][d]
-  const float* weight;    // weight of row i at weight[i * wstride], or NULL: 1
-  int wstride;
-  const SweepParts* parts;   // a sweep's partial rows of out that are summed first, or NULL
-};
-size_t row_sums_bytes(int64_t n, int64_t C, int d);
-// Writes the rows of out that some id names; the others stay.
-hipError_t row_sums(const RowSums& r, void* ws, void* out, hipStream_t st);
 // Log-probabilities over the catalogue (k_logprob.hip).
 size_t logprob_workspace_bytes(bool bf16v, int64_t s, int64_t C, int d, uint32_t flags);
 hipError_t logprob_forward(bool bf16v, int64_t s, int64_t C, int d, float temperature, uint32_t flags, const void* X,

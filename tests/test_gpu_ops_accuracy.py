@@ -401,3 +401,55 @@ def test_preference_large_groups_among_many_small_ones(per, kind, average):
     scale = torch.zeros(G, dtype=torch.float64).index_add(0, grp, torch.zeros(n_seq, dtype=torch.float64).index_add(
         0, seq, x.grad.abs()))[grp][seq]
     assert bool(((dlp.cpu().double() - x.grad).abs() <= (R.U32 + 1e-12) * x.grad.abs() + tiny * scale + 2.0 ** -126).all())
+
+
+@pytest.mark.parametrize("s,C,d", [(1, 1006, 128), (2, 300, 64), (24, 1006, 32), (60, 90, 64), (150, 160, 128), (100, 130, 256)])
+@pytest.mark.parametrize("dtype,bf16_grads", [("f32", False), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_logprob_keeps_the_digits_of_what_is_left(s, C, d, dtype, bf16_grads, entropy):
+    """1 - p from 1e-2 to 1e-9: log p, entropy and the gradients are off relative to 1 - p alone.  No sum holds the own
+    item's term, so nothing rounds by it: the others' sums are off by their logits, exponentials and additions (rel, as in
+    R.logprob), and the own item's weight g (1 - p) - h p (log p + H) by what those leave in log p and H."""
+    g = torch.Generator().manual_seed(s + C + d)
+    Y = torch.randn(C, d, generator=g) * d ** -0.25
+    ids = torch.randperm(C, generator=g)[:s].to(torch.int32)
+    a = Y[ids.long()]
+    X = a / (a * a).sum(1, keepdim=True) * torch.linspace(12.0, 24.0, s)[:, None] + \
+        torch.randn(s, d, generator=g) * 0.1 * d ** -0.25
+    X, Y = X.to(TL.DT[dtype]), Y.to(TL.DT[dtype])
+    dlogp, dent = torch.randn(s, generator=g) / s, torch.randn(s, generator=g) / s * 0.1
+    if not entropy:
+        dent = None
+    print(f"[gpu] logprob what is left s={s} C={C} d={d} {dtype} bf16_grads={bf16_grads} entropy={entropy}", flush=True)
+    logp, ent, dX, dY = TL._run(X, Y, ids, dlogp, dent, 1.0, entropy, bf16_grads)
+    Xd, Yd, k, at = X.double(), Y.double(), torch.arange(s), ids.long()
+    L = Xd @ Yd.T
+    far = L - L[k, at][:, None]
+    e = far.exp()
+    e[k, at] = 0.0
+    t1 = e.sum(1)
+    want = -torch.log1p(t1)
+    left = t1 / (1.0 + t1)
+    assert float(left.min()) < 1e-2 and float(left.max()) < 0.2
+    q = (far + want[:, None]).exp()
+    logq = far + want[:, None]
+    H = -(q * logq).sum(1)
+    mag = (Xd.abs() @ Yd.abs().T).amax(1)
+    ex = (d + 4) * R.U32 * mag
+    rel = 4 * ex + (16 + C / 32 + 112 + 8 * L.abs().amax(1) + 8) * R.U32
+    assert bool(((logp.double() - want).abs() <= 1.02 * (rel + 4 * R.U32) * left).all())
+    if entropy:
+        # terms of one sign, p (-log p): p off by rel, log p by the logits' error, of a size of 1 and more but the own one's
+        assert bool(((ent.double() - H).abs() <= 2.0 * (rel + 16 * R.U32) * (H + left)).all())
+    gk, hk = dlogp.double(), dent.double() if entropy else torch.zeros(s, dtype=torch.float64)
+    G = -q * (gk[:, None] + hk[:, None] * (logq + H[:, None]))
+    G[k, at] = gk * left - hk * q[k, at] * (want + H)
+    size = q * (gk.abs()[:, None] + hk.abs()[:, None] * (logq.abs() + H[:, None] + 1.0))
+    size[k, at] = gk.abs() * left + 2.0 * hk.abs() * (want.abs() + H + left)
+    off = size * (1.02 * rel[:, None] + 16 * R.U32 + (2.0 ** -16 if bf16_grads else 0.0))
+    steps = (C + s) / 16 + 24   # additions that a result passes through, each off by U32 of at most the sum of sizes
+    u = R.U[torch.bfloat16] if bf16_grads else R.U32
+    for got, w, bound in ((dX, G @ Yd, (off + steps * R.U32 * size) @ Yd.abs()), (dY, G.T @ Xd, (off + steps * R.U32 * size).T @ Xd.abs())):
+        bound = bound + u * (w.abs() + bound) + 1e-30
+        err = (got.double() - w).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
