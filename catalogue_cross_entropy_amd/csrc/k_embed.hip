@@ -9,10 +9,10 @@
 // second kernel adds in a fixed order, so every result is reproducible bit for bit.
 // Measured (MI355X, bf16 rows, float32 gradient):
 //   256 rows of 64 floats            call 7.4 us (kernel 3.1 us: the call's own time bounds it)
-//   51,200 rows of 64, 30,000 items  forward 5.2 us (13 MB), backward 36 us: sort 24, pieces 7, joins 8; latencies
+//   51,200 rows of 64, 30,000 items  forward 5.2 us (13 MB), backward 34 us: sort 24, pieces 5, joins 7; latencies
 //                                    of short launches, 27 MB in all
-//   25,600 rows of 128, 1M items     forward and backward 115 us, 525 MB (512 MB of it the cleared gradient): 4.6 TB/s;
-//                                    with a bf16 gradient 66 us, adding to a float32 one 41 us
+//   25,600 rows of 128, 1M items     forward and backward 113 us, 525 MB (512 MB of it the cleared gradient): 4.6 TB/s;
+//                                    with a bf16 gradient 64 us, adding to a float32 one 38 us
 #include <algorithm>
 
 #include "rece_device.h"

@@ -23,23 +23,22 @@
 //
 // What bounds it: the exponential of each logit (v_exp_f32, about 9 cycles of a SIMD for 64 logits, with 2
 // to 4 cheaper instructions beside it), the split of each weight into bf16 terms (6 more), and the products share a
-// SIMD's issue: at d 64 vector and matrix units are busy 67 % and 48 % of LP_LSEO, 65 % and 47 % of LP_DY; at d 256
-// waves wait half of their cycles (two per SIMD, registers spilled).  Measured (bf16 vectors; products counted with
-// both terms of a weight):
-//   51,200 (a quarter padding) x 30,000 x 64  with bf16 gradients 931 us: LP_LSEO 470 us and LP_DY 481 us (940 and
-//                          920 TFLOP/s, 2.4e12 exponentials a second each), packing, joins and the own items 100 us;
-//                          with float32 gradients (three terms) 1,307 us: 734 and 655 us
-//   4,099 (a tenth padding) x 50,021 x 256  with entropies and bf16 gradients 763 us: LP_LSE 120, LP_DX 273,
-//                          LP_DY 333 us (790, 1,040, 850 TFLOP/s; LP_DX spills 12, LP_DY 30 words per lane); with
-//                          float32 gradients 1,009 us
-//   8,192 (a tenth padding) x 30,000 x 128  with bf16 gradients 406 us: LP_LSEO 175, LP_DY 183 us
-//   40 (a tenth padding) x 1,000,000 x 64  with bf16 gradients 356 us: LP_LSEO 43, LP_DY 88, the joins of its float32
-//                          parts 113, of the 3,000 parts of 36 positions 73 us
-//   2,047 (a tenth padding) x 200,000 x 128  log-probabilities 120 us: LP_LSE 117 us (810 TFLOP/s)
+// SIMD's issue: at d 64 vector and matrix units are busy 67 % and 46 % of LP_LSEO, 57 % and 39 % of LP_DY (popular
+// items meet their own positions in most tiles); at d 256 waves wait more than half of their cycles (two per SIMD,
+// registers spilled).  Measured (bf16 vectors; products counted with both terms of a weight):
+//   51,200 (a quarter padding) x 30,000 x 64  with bf16 gradients 935 us: LP_LSEO 507 and LP_DY 571 us alone (870 and
+//                          775 TFLOP/s, 2.0e12 exponentials a second and more), packing and joins 45 us; with float32
+//                          gradients (three terms) 1,293 us
+//   4,099 (a tenth padding) x 50,021 x 256  with entropies and bf16 gradients 771 us: LP_LSE 124, LP_DX 292,
+//                          LP_DY 407 us alone (760, 970, 700 TFLOP/s); with float32 gradients 985 us
+//   8,192 (a tenth padding) x 30,000 x 128  with bf16 gradients 374 us: LP_LSEO 187, LP_DY 209 us alone
+//   40 (a tenth padding) x 1,000,000 x 64  with bf16 gradients 301 us: LP_LSEO 43, LP_DY 86, the join of its float32
+//                          parts 111, of the 3,000 parts of 36 positions 60 us
+//   2,047 (a tenth padding) x 200,000 x 128  log-probabilities 121 us: LP_LSE 118 us (800 TFLOP/s)
 //   5 x 1,000,000 x 64     log-probabilities and entropies 40 us: LP_LSE 26 us, 128 MB at 4.9 TB/s
 //   256 x 2,000 x 64 float32 with entropies and gradients 50 us: eight launches of 2 to 12 us
-//   636 (a tenth padding) x 30,018 x 256 float32 with gradients 565 us: LP_LSEO 276, LP_DY 271 us (64 TFLOP/s of
-//                          154: one wave per SIMD); 2,047 x 30,018 x 64 log-probabilities 88 us (84: 84 TFLOP/s)
+//   636 (a tenth padding) x 30,018 x 256 float32 with gradients 564 us: LP_LSEO 275, LP_DY 272 us (64 TFLOP/s of
+//                          154: one wave per SIMD); 2,047 x 30,018 x 64 log-probabilities 89 us (85: 83 TFLOP/s)
 //
 // Positions whose id is padding are left out first: the others are packed (rows, ids) in
 // order into the workspace, so padding costs no products and nothing it holds (NaN or
@@ -894,13 +893,13 @@ constexpr int LP_CUS = 256;
 // more waves per SIMD to overlap the exponentials with the products), MW waves per SIMD (the registers allow
 // them; the grid fills the card once), NWO waves per workgroup.  Whole calls with bf16 gradients, without / with
 // entropies, us (spills: words per lane that do not fit into registers):
-//   D 64, 51,200 x 30,000:   OB 2 MW 2  928 / 1,208;  OB 1 MW 3  1,032 / 1,317;  OB 1 MW 4  1,043 / 1,301
-//   D 128, 8,192 x 30,000:   OB 1 MW 2  406 / 488;  OB 1 MW 3  415 / 493;  OB 2 MW 1  412 / 496 (with float32 gradients
-//                            545 / 624, 574 / 621 and 526 / 600)
-//   D 256, 4,099 x 50,021:   NWO 8  597 / 737;  NWO 4  660 / 788;  NWO 8 MW 1  919 / 1,081
+//   D 64, 51,200 x 30,000:   OB 2 MW 2  933 / 1,222;  OB 1 MW 3  997 / 1,281;  OB 1 MW 4  1,031 / 1,286
+//   D 128, 8,192 x 30,000:   OB 1 MW 2  369 / 454;  OB 1 MW 3  388 / 470;  OB 2 MW 1  394 / 485 (with float32 gradients
+//                            501 / 579, 545 / 596 and 511 / 573)
+//   D 256, 4,099 x 50,021:   NWO 8  588 / 748;  NWO 4  672 / 1,028;  NWO 8 MW 1  975 / 1,165
 //   LP_LSE, MW 3 against 2:  D 128, 2,047 x 200,000  132 / 137;  D 256, 4,099 x 50,021  120 / 128
-// Spills remain at D 256 (LP_LSEO 11 to 24, LP_DX 10 to 14, LP_DY 26 to 30; float32 23, 0 and 51 to 74), in the few-
-// positions LP_LSEO at D 128 (3 to 14) and in LP_LSE at D 128 (4 to 6).
+// Spills remain at D 256 (LP_LSEO 10 to 27, LP_DX 14 to 22, LP_DY 35 to 60; float32 24, 0 and 51 to 74), in the few-
+// positions LP_LSEO at D 128 (3 to 21) and in LP_LSE at D 128 (6 to 8).
 // A second block's logits in flight while the first is weighed gave LP_DY at D 64 less than 1 %, and is not done.
 // Up to 32 OB positions the waves of a workgroup share their owners and split each tile's rows instead (NWS 4;
 // a block of owners that is mostly empty costs as much as a full one): 5 x 1,000,000, LP_LSE 25 against 62.
