@@ -90,7 +90,7 @@ def test_logprob_of_a_catalogue_beyond_32_bits(entropy):
 
 @pytest.mark.parametrize("bf16_grads", [False, True])
 def test_logprob_of_many_positions(bf16_grads):
-    """More positions than the short sort of the own items takes."""
+    """Many positions on few items: own items in most blocks, several parts per item block."""
     s, C, d = 270_011, 37, 32
     X, Y, ids, dlogp, dent, bad = TL._case(s, C, d, "bf16", seed=4, pad=0.02, peak=1.0)
     print(f"[gpu] logprob s={s} bf16_grads={bf16_grads}", flush=True)
