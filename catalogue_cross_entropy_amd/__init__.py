@@ -33,6 +33,10 @@ EXPORTED = ["rece_plan", "rece_plan_destroy", "rece_workspace_bytes", "rece_forw
             "rece_logprob_workspace_bytes", "rece_logprob_forward", "rece_logprob_backward",
             "rece_policy_workspace_bytes", "rece_policy_loss",
             "rece_preference_workspace_bytes", "rece_preference_loss",
+            "rece_attention_workspace_bytes", "rece_attention_forward", "rece_attention_backward",
+            "rece_last_attention_workspace_bytes", "rece_last_attention",
+            "rece_norm_workspace_bytes", "rece_norm_forward", "rece_norm_forward_int8", "rece_norm_backward",
+            "rece_quantize_rows", "rece_int8_scores",
             "rece_status_string", "rece_last_error", "rece_version"]
 PHASES = ["project", "sort", "select", "loss", "bwd_dx", "bwd_dy", "bwd_sort", "other"]
 
@@ -95,6 +99,18 @@ def lib() -> ctypes.CDLL:
         L.rece_policy_loss.argtypes = [vp] * 11 + [ctypes.c_size_t] + [vp] * 4
         L.rece_preference_workspace_bytes.argtypes = [vp, sz]
         L.rece_preference_loss.argtypes = [vp] * 9 + [ctypes.c_size_t] + [vp] * 4
+        szt = ctypes.c_size_t
+        L.rece_attention_workspace_bytes.argtypes = [vp, sz]
+        L.rece_attention_forward.argtypes = [vp] * 8 + [szt, vp]
+        L.rece_attention_backward.argtypes = [vp] * 9 + [szt, vp, i64, i64, i64] + [vp] * 4
+        L.rece_last_attention_workspace_bytes.argtypes = [vp, i64, sz]
+        L.rece_last_attention.argtypes = [vp, vp, i64] + [vp] * 7 + [szt, vp]
+        L.rece_norm_workspace_bytes.argtypes = [i64, i32t, sz]
+        L.rece_norm_forward.argtypes = [vp, i64, i32t, i32t, f32t] + [vp] * 6
+        L.rece_norm_forward_int8.argtypes = [vp, i64, i32t, i32t, f32t] + [vp] * 6
+        L.rece_norm_backward.argtypes = [vp, i64, i32t, i32t] + [vp] * 6 + [szt, vp, vp]
+        L.rece_quantize_rows.argtypes = [vp, i64, i32t, i32t, vp, vp, vp]
+        L.rece_int8_scores.argtypes = [vp, i64, i64, i32t, i32t] + [vp] * 5
         L.rece_status_string.argtypes = [i32]
         L.rece_status_string.restype = ctypes.c_char_p
         L.rece_last_error.restype = ctypes.c_char_p
@@ -106,7 +122,11 @@ def lib() -> ctypes.CDLL:
                      "rece_embed_forward", "rece_embed_workspace_bytes", "rece_embed_backward",
                      "rece_logprob_workspace_bytes", "rece_logprob_forward", "rece_logprob_backward",
                      "rece_policy_workspace_bytes", "rece_policy_loss",
-                     "rece_preference_workspace_bytes", "rece_preference_loss"):
+                     "rece_preference_workspace_bytes", "rece_preference_loss",
+                     "rece_attention_workspace_bytes", "rece_attention_forward", "rece_attention_backward",
+                     "rece_last_attention_workspace_bytes", "rece_last_attention",
+                     "rece_norm_workspace_bytes", "rece_norm_forward", "rece_norm_forward_int8", "rece_norm_backward",
+                     "rece_quantize_rows", "rece_int8_scores"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -418,4 +438,8 @@ def version() -> str:
 from .ops import (  # noqa: E402,F401  (the operators around the losses use the names above)
     FLAG_ACCUMULATE, FLAG_ENTROPY, FLAG_NO_GRAD, ItemEmbedding, LogProb, PolicyConfig, PolicyLoss, PreferenceConfig,
     PreferenceLoss, embed, log_probs, policy_loss, preference_loss,
+)
+from .encoder import (  # noqa: E402,F401
+    AttentionConfig, Int8Scores, LastAttention, ResidualNorm, SequenceAttention, attention, attention_qkv, log_buckets,
+    quantize_rows, residual_norm,
 )

@@ -1,0 +1,976 @@
+// Causal attention over packed sequences of different lengths, grouped heads, with a learned bias by
+// buckets of the distance, and its gradients (formulas in include/rece.h).  No array of scores exists: the
+// softmax runs over the keys with a running maximum and sum.
+//
+// Products are formed transposed: a block S^T of 32 keys x 32 queries leaves lane l with query l % 32
+// and 16 keys, so a query's maximum and sum need one exchange between two lanes, its factors are one
+// register, and the block is the operand of the second product as it stands (rece_tile.h).
+//   k_attn      owners = queries (32 per wave, their rows in registers), keys and values through LDS
+//   k_attn_dq   the same sweep again: dq, and the exact row sums D_i = sum_j p_ij dp_ij
+//   k_attn_dkv  owners = keys (32 per wave), the queries of all heads of a group through LDS: dk, dv and
+//               the bias's gradient
+// Tiles pass through two LDS buffers, the next tile's loads in flight during the current tile's work.
+//
+// Sequences are found by the workgroups themselves: with tiles of T rows, sequence u owns the slots
+// from floor(o_u / T) + u on.  That number grows by at least ceil(length / T) from one sequence to the next, so
+// the slots are distinct, floor(n / T) + n_seq of them are enough, and no list of tiles is made.
+//
+// Scores and sums are float32.  bf16: scores carry the factor log2(e), p and ds are rounded to bf16 for the second
+// products alone.  float32: scores stay in natural units and their difference to the maximum is scaled.
+// D from the rounded outputs is a first value only: its error would be the bias gradient's.  k_attn_dq adds the sum of
+// p (dp - D) over the row to it, which is 0 for the exact D.
+#include <algorithm>
+#include <cmath>
+
+#include "rece_device.h"
+#include "rece_internal.h"
+#include "rece_tile.h"
+
+namespace rece {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float NO_WEIGHT = 1e30f;     // log-sum-exp of a row without weight: exp(t - 1e30) = 0
+constexpr int CLEAN = 64;              // workgroups that clear rows of no sequence
+
+struct AttnArgs {
+  const char* q;              // rows of heads of d elements; strides between rows in bytes
+  const char* k;
+  const char* v;
+  const char* dout;           // [n][hq][d]
+  char* out;                  // [n][hq][d]
+  char* dq;
+  char* dk;
+  char* dv;
+  int64_t qs, ks, vs, dqs, dks, dvs;
+  const int32_t* offs;        // [n_seq + 1]
+  const float* bias;          // [n_bounds + 1][hq] or nullptr
+  float2* lse;                // [hq][n] log-sum-exp (value, what its rounding left), or nullptr
+  float* delta;               // [hq][n] D
+  float* part;                // [slots][n_bounds + 1][hq] partial bias gradients
+  int64_t n;
+  int n_seq, d, hq, hk, slots;
+  float scale, c;             // c: the factor of a product, with log2(e) for bf16
+  int nbounds, dlast;         // dlast: from this distance on there is one bucket
+  int32_t bounds[RECE_MAX_BOUNDS];
+};
+
+struct SeqTile {
+  int64_t begin;   // first row of the sequence
+  int len;         // its rows; 0: the slot has no tile
+  int first;       // first row of the tile within the sequence
+};
+
+// The tile of a slot (see above).  Every wave finds it by itself, 64 probes at a time.  What is found lies inside the
+// rows whatever the offsets hold.
+__device__ __forceinline__ SeqTile find_tile(const int32_t* offs, int n_seq, int64_t n, int slot, int T) {
+  int lo = 0, size = n_seq;
+  const int l = lane_id();
+  auto clamped = [&](int u) { return max(0, min(offs[u], (int32_t)n)); };
+  SeqTile t{0, 0, 0};
+  while (true) {
+    const int step = (size + 63) / 64, at = lo + l * step;
+    const bool below = l * step < size && clamped(at) / T + at <= slot;
+    const int cnt = popc(ballot(below));
+    if (cnt == 0) return t;
+    lo += (cnt - 1) * step;
+    if (step == 1) break;
+    size = min(step, size - (cnt - 1) * step);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int b = clamped(lo), e = max(b, clamped(lo + 1));
+  t.begin = __builtin_amdgcn_readfirstlane(b);
+  t.first = __builtin_amdgcn_readfirstlane((slot - (b / T + lo)) * T);
+  t.len = __builtin_amdgcn_readfirstlane(t.first < e - b && t.first >= 0 ? e - b : 0);
+  return t;
+}
+
+// Rows before the first and behind the last sequence become zero.
+__device__ __forceinline__ void clean_rows(const AttnArgs& a, int which, int nt, char* p, int64_t stride, int row_bytes) {
+  const int64_t first = max(0, min(a.offs[0], (int32_t)a.n)), last = max(first, (int64_t)min(a.offs[a.n_seq], (int32_t)a.n));
+  const int cpr = row_bytes / 16;
+  const int64_t rows = first + (a.n - last);
+  for (int64_t t = (int64_t)which * nt + threadIdx.x; t < rows * cpr; t += (int64_t)CLEAN * nt) {
+    const int64_t r = t / cpr, row = r < first ? r : last + (r - first);
+    *reinterpret_cast<u32x4*>(p + row * stride + t % cpr * 16) = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+// TI rows of D elements from memory to LDS: NT threads, PT chunks each.  Rows at or beyond `len` and elements
+// beyond the head's are zero.
+template <class E, int D, int NT, int TI> struct Copy {
+  using T = TileRows<E, D>;
+  static constexpr int PT = TI * T::CPR / NT, BYTES = TI * T::RB;
+  static_assert(TI * T::CPR % NT == 0, "whole chunks per thread");
+  u32x4 r[PT];
+  __device__ __forceinline__ void fetch(const char* head, int64_t stride, int row0, int len, int cpr) {
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      const int i = q * NT + (int)threadIdx.x, row = row0 + i / T::CPR, c = i % T::CPR;
+      r[q] = u32x4{0u, 0u, 0u, 0u};
+      if (row < len && c < cpr) r[q] = *reinterpret_cast<const u32x4*>(head + row * stride + c * 16);
+    }
+  }
+  __device__ __forceinline__ void stash(uint32_t buf) const {
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      const int i = q * NT + (int)threadIdx.x, row = i / T::CPR, c = i % T::CPR;
+      lds_put(buf + row * T::RB + ((c ^ (row & T::SWM)) << 4), r[q]);
+    }
+  }
+};
+
+// A wave's 32 rows as an operand: chunks 2 k + h of row l % 32.
+template <class E, int D> struct Owners {
+  static constexpr int KC = TileRows<E, D>::RB / 32;
+  u32x4 v[KC];
+  __device__ __forceinline__ void load(const char* head, int64_t stride, int row0, int len, int cpr) {
+    const int l = lane_id(), h = l >> 5, row = row0 + (l & 31);
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+      if (row < len && 2 * k + h < cpr) v[k] = *reinterpret_cast<const u32x4*>(head + row * stride + (2 * k + h) * 16);
+    }
+  }
+};
+
+// block[32 rows of the tile at base][32 owners]
+template <class E, int D>
+__device__ __forceinline__ f32x16 block_of(const TileReads<E, D>& o, uint32_t base, const Owners<E, D>& own) {
+  f32x16 s = {};
+#pragma unroll
+  for (int k = 0; k < Owners<E, D>::KC; ++k) s = TileMma<E>::run(TileReads<E, D>::frag(o, base, k), own.v[k], s);
+  return s;
+}
+
+// acc[nb][32 coordinates][32 owners] += rows^T[coordinates][32 rows] g[32 rows][32 owners]
+template <class E, int D>
+__device__ __forceinline__ void add_product(f32x16 (&acc)[D / 32], const f32x16& g, const TileReads<E, D>& o, uint32_t base) {
+  if constexpr (sizeof(E) == 2) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4 b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = pack_bf16(g[8 * kk + 2 * e], g[8 * kk + 2 * e + 1]);
+#pragma unroll
+      for (int nb = 0; nb < D / 32; ++nb) acc[nb] = TileMma<E>::run(TileReads<E, D>::across(o, base, nb, kk), b, acc[nb]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+#pragma unroll
+      for (int nb = 0; nb < D / 32; ++nb)
+        acc[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(TileReads<E, D>::across1(o, base, nb, v), g[v], acc[nb], 0, 0, 0);
+  }
+}
+
+// Rows of results: coordinates 32 nb + tile_row(v) + 4 h of owner l % 32.
+template <class E, int D>
+__device__ __forceinline__ void store_rows(char* head, int64_t stride, int row0, int len, int d, const f32x16 (&acc)[D / 32],
+                                           float f) {
+  const int l = lane_id(), h = l >> 5, row = row0 + (l & 31);
+  if (row >= len) return;
+  char* p = head + row * stride;
+#pragma unroll
+  for (int nb = 0; nb < D / 32; ++nb)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = 32 * nb + 8 * g + 4 * h;
+      if (at < d) {
+        if constexpr (sizeof(E) == 2)
+          *reinterpret_cast<uint2*>(p + at * 2) = make_uint2(pack_bf16(acc[nb][4 * g] * f, acc[nb][4 * g + 1] * f),
+                                                             pack_bf16(acc[nb][4 * g + 2] * f, acc[nb][4 * g + 3] * f));
+        else
+          *reinterpret_cast<f32x4*>(p + at * 4) =
+              f32x4{acc[nb][4 * g] * f, acc[nb][4 * g + 1] * f, acc[nb][4 * g + 2] * f, acc[nb][4 * g + 3] * f};
+      }
+    }
+}
+
+// exp of a difference of scores, in the scores' unit (bf16: base 2)
+template <class E>
+__device__ __forceinline__ float exp_of(float t) {
+  return __builtin_amdgcn_exp2f(sizeof(E) == 2 ? t : t * LOG2E);
+}
+
+// The bias by distance in LDS, in the scores' unit: words 0 .. dlast + 95.  Ascending: distance word - 32;
+// else distance dlast + 63 - word.  Distances below 0 (masked) hold 0, those of at least dlast the last bucket's.
+// A bias of at most -1e30 leaves no weight.
+template <class E, bool ASC>
+__device__ __forceinline__ void fill_bias(const AttnArgs& a, uint32_t lut, uint32_t tmp, int head, int nt) {
+  for (int t = threadIdx.x; t < a.nbounds; t += nt) lds_put<int>(tmp + 4 * t, a.bounds[t]);
+  __syncthreads();
+  for (int t = threadIdx.x; t < a.dlast + 96; t += nt) {
+    const int dist = ASC ? t - 32 : a.dlast + 63 - t;
+    int lo = 0, hi = a.nbounds;   // bounds before the first one that is larger than the distance
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (lds_at<int>(tmp + 4 * mid) <= dist) lo = mid + 1;
+      else hi = mid;
+    }
+    float b = dist < 0 ? 0.0f : a.bias[(int64_t)lo * a.hq + head];
+    b = b <= -NO_WEIGHT ? -__builtin_huge_valf() : sizeof(E) == 2 ? b * LOG2E : b;
+    lds_put<float>(lut + 4 * t, b);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ f32x4 lds_f4(uint32_t off) {   // four words at any word
+  typedef f32x4 any __attribute__((aligned(4)));
+  return *reinterpret_cast<const __attribute__((address_space(3))) any*>((uintptr_t)off);
+}
+
+// Scores of a block of 32 keys (rows, from j0) x 32 queries (from i0 >= j0), from their products x, in place.
+template <class E, bool BIAS>
+__device__ __forceinline__ void scores_keys(f32x16& x, float c, int i0, int j0, uint32_t lut, int dlast, float far) {
+  const int l = lane_id(), h = l >> 5, r = l & 31;
+  if (BIAS && i0 - j0 - 31 < dlast) {
+    const uint32_t at = lut + 4 * (dlast + 63 - (i0 - j0 + r - 4 * h));
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 b = lds_f4(at + 32 * g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * g + e] = fmaf(x[4 * g + e], c, b[e]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) x[v] = BIAS ? fmaf(x[v], c, far) : x[v] * c;
+  }
+  if (j0 == i0) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) x[v] = tile_row(v) + 4 * h > r ? -__builtin_huge_valf() : x[v];
+  }
+}
+
+template <class E, int DH, int NW> struct Shape {
+  static constexpr int NT = 64 * NW;
+  static constexpr int T = 32 * NW;                                              // owners of a workgroup
+  static constexpr int TJ = NW == 1 || TileRows<E, DH>::RB > 256 ? 32 : 64;      // streamed rows of a tile (k_attn, k_attn_dq)
+  static constexpr int TQ = NW > 1 && TileRows<E, DH>::RB <= 128 ? 64 : 32;      // (k_attn_dkv)
+  static constexpr int BYTES = TJ * TileRows<E, DH>::RB, QBYTES = TQ * TileRows<E, DH>::RB;
+};
+
+template <class E, int DH, int NW, bool BIAS>
+__global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
+  using S = Shape<E, DH, NW>;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const uint32_t lut = lds0 + 4 * S::BYTES, tmp = lut + 4 * (a.dlast + 96);
+  const int es = sizeof(E), cpr = a.d * es / 16;
+  const int64_t os = (int64_t)a.hq * a.d * es;
+  const int b = blockIdx.x;
+  if (b >= a.slots * a.hq) {
+    clean_rows(a, b - a.slots * a.hq, S::NT, a.out, os, (int)os);
+    return;
+  }
+  // last slots first: within a sequence they have the most keys
+  const int head = b % a.hq, kvh = head / (a.hq / a.hk);
+  const SeqTile st = find_tile(a.offs, a.n_seq, a.n, a.slots - 1 - b / a.hq, S::T);
+  if (st.len == 0) return;
+  if constexpr (BIAS) fill_bias<E, false>(a, lut, tmp, head, S::NT);
+  const float far = BIAS ? lds_at<float>(lut) : 0.0f;
+  const char* kh = a.k + st.begin * a.ks + (int64_t)kvh * a.d * es;
+  const char* vh = a.v + st.begin * a.vs + (int64_t)kvh * a.d * es;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i0 = st.first + 32 * w;
+  Owners<E, DH> q;
+  q.load(a.q + st.begin * a.qs + (int64_t)head * a.d * es, a.qs, i0, st.len, cpr);
+  TileReads<E, DH> o;
+  o.init();
+  f32x16 acc[DH / 32] = {};
+  float m = NEG_INF, sum = 0.0f;
+  const int nt = (min(st.first + S::T, st.len) + S::TJ - 1) / S::TJ;
+  Copy<E, DH, S::NT, S::TJ> ck, cv;
+  ck.fetch(kh, a.ks, 0, st.len, cpr);
+  cv.fetch(vh, a.vs, 0, st.len, cpr);
+  ck.stash(lds0);
+  cv.stash(lds0 + S::BYTES);
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    if (t + 1 < nt) {
+      ck.fetch(kh, a.ks, (t + 1) * S::TJ, st.len, cpr);
+      cv.fetch(vh, a.vs, (t + 1) * S::TJ, st.len, cpr);
+    }
+    const uint32_t kb = lds0 + (t & 1) * 2 * S::BYTES, vb = kb + S::BYTES;
+#pragma unroll
+    for (int jb = 0; jb < S::TJ / 32; ++jb) {
+      const int j0 = t * S::TJ + 32 * jb;
+      if (j0 > i0 || i0 >= st.len) continue;
+      f32x16 x = block_of<E, DH>(o, kb + jb * 32 * TileRows<E, DH>::RB, q);
+      scores_keys<E, BIAS>(x, a.c, i0, j0, lut, a.dlast, far);
+      float bm = x[0];
+#pragma unroll
+      for (int v = 1; v < 16; ++v) bm = fmaxf(bm, x[v]);
+      bm = fmaxf(bm, __shfl_xor(bm, 32));
+      // the reference follows the maximum in steps: terms stay below 2^8
+      if (ballot(bm > m + (sizeof(E) == 2 ? 8.0f : 5.5f))) {
+        const float up = fmaxf(m, bm);
+        const float f = m == NEG_INF ? 0.0f : exp_of<E>(m - up);
+        sum *= f;
+#pragma unroll
+        for (int nb = 0; nb < DH / 32; ++nb)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[nb][v] *= f;
+        m = up;
+      }
+      const float ref = fmaxf(m, -NO_WEIGHT);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        x[v] = exp_of<E>(x[v] - ref);
+        sum += x[v];
+      }
+      add_product<E, DH>(acc, x, o, vb + jb * 32 * TileRows<E, DH>::RB);
+    }
+    if (t + 1 < nt) {
+      const uint32_t nb = lds0 + ((t + 1) & 1) * 2 * S::BYTES;
+      ck.stash(nb);
+      cv.stash(nb + S::BYTES);
+      __syncthreads();
+    }
+  }
+  sum += __shfl_xor(sum, 32);
+  store_rows<E, DH>(a.out + st.begin * os + (int64_t)head * a.d * es, os, i0, st.len, a.d, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
+  const int l = lane_id();
+  if (a.lse && l < 32 && i0 + l < st.len) {
+    float2 v = make_float2(NO_WEIGHT, 0.0f);
+    if (sum != 0.0f) {
+      const float lg = sizeof(E) == 2 ? log2f(sum) : logf(sum);
+      v.x = m + lg;
+      const float bb = v.x - m;
+      v.y = (m - (v.x - bb)) + (lg - bb);
+    }
+    a.lse[(int64_t)head * a.n + st.begin + i0 + l] = v;
+  }
+}
+
+template <class E, int DH, int NW, bool BIAS>
+__global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
+  using S = Shape<E, DH, NW>;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const uint32_t lut = lds0 + 4 * S::BYTES, tmp = lut + 4 * (a.dlast + 96);
+  const int es = sizeof(E), cpr = a.d * es / 16;
+  const int64_t os = (int64_t)a.hq * a.d * es;
+  const int b = blockIdx.x;
+  if (b >= a.slots * a.hq) {
+    clean_rows(a, b - a.slots * a.hq, S::NT, a.dq, a.dqs, (int)os);
+    return;
+  }
+  const int head = b % a.hq, kvh = head / (a.hq / a.hk);
+  const SeqTile st = find_tile(a.offs, a.n_seq, a.n, a.slots - 1 - b / a.hq, S::T);
+  if (st.len == 0) return;
+  if constexpr (BIAS) fill_bias<E, false>(a, lut, tmp, head, S::NT);
+  const float far = BIAS ? lds_at<float>(lut) : 0.0f;
+  const int64_t hb = (int64_t)head * a.d * es;
+  const char* kh = a.k + st.begin * a.ks + (int64_t)kvh * a.d * es;
+  const char* vh = a.v + st.begin * a.vs + (int64_t)kvh * a.d * es;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l = lane_id();
+  const int i0 = st.first + 32 * w;
+  Owners<E, DH> q, go;
+  q.load(a.q + st.begin * a.qs + hb, a.qs, i0, st.len, cpr);
+  go.load(a.dout + st.begin * os + hb, os, i0, st.len, cpr);
+  const bool live = i0 + (l & 31) < st.len;
+  const int64_t row = (int64_t)head * a.n + st.begin + i0 + (l & 31);
+  const float2 lse = live ? a.lse[row] : make_float2(NO_WEIGHT, 0.0f);
+  float d0 = 0.0f;   // D by the rounded outputs
+  {
+    Owners<E, DH> ov;
+    ov.load(a.out + st.begin * os + hb, os, i0, st.len, cpr);
+#pragma unroll
+    for (int k = 0; k < Owners<E, DH>::KC; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(E) == 2) {
+          d0 = fmaf(lo_f32(ov.v[k][e]), lo_f32(go.v[k][e]), d0);
+          d0 = fmaf(hi_f32(ov.v[k][e]), hi_f32(go.v[k][e]), d0);
+        } else {
+          d0 = fmaf(__uint_as_float(ov.v[k][e]), __uint_as_float(go.v[k][e]), d0);
+        }
+      }
+    d0 += __shfl_xor(d0, 32);
+  }
+  TileReads<E, DH> o;
+  o.init();
+  f32x16 acc[DH / 32] = {};
+  float rest = 0.0f;
+  const int nt = (min(st.first + S::T, st.len) + S::TJ - 1) / S::TJ;
+  Copy<E, DH, S::NT, S::TJ> ck, cv;
+  ck.fetch(kh, a.ks, 0, st.len, cpr);
+  cv.fetch(vh, a.vs, 0, st.len, cpr);
+  ck.stash(lds0);
+  cv.stash(lds0 + S::BYTES);
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    if (t + 1 < nt) {
+      ck.fetch(kh, a.ks, (t + 1) * S::TJ, st.len, cpr);
+      cv.fetch(vh, a.vs, (t + 1) * S::TJ, st.len, cpr);
+    }
+    const uint32_t kb = lds0 + (t & 1) * 2 * S::BYTES, vb = kb + S::BYTES;
+#pragma unroll
+    for (int jb = 0; jb < S::TJ / 32; ++jb) {
+      const int j0 = t * S::TJ + 32 * jb;
+      if (j0 > i0 || i0 >= st.len) continue;
+      const uint32_t at = jb * 32 * TileRows<E, DH>::RB;
+      f32x16 x = block_of<E, DH>(o, kb + at, q);
+      const f32x16 dp = block_of<E, DH>(o, vb + at, go);
+      scores_keys<E, BIAS>(x, a.c, i0, j0, lut, a.dlast, far);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        x[v] = exp_of<E>((x[v] - lse.x) - lse.y) * (dp[v] - d0);
+        rest += x[v];
+      }
+      add_product<E, DH>(acc, x, o, kb + at);
+    }
+    if (t + 1 < nt) {
+      const uint32_t nb = lds0 + ((t + 1) & 1) * 2 * S::BYTES;
+      ck.stash(nb);
+      cv.stash(nb + S::BYTES);
+      __syncthreads();
+    }
+  }
+  rest += __shfl_xor(rest, 32);
+  store_rows<E, DH>(a.dq + st.begin * a.dqs + hb, a.dqs, i0, st.len, a.d, acc, a.scale);
+  if (l < 32 && live) a.delta[row] = d0 + rest;
+}
+
+template <class E, int DH, int NW, bool BIAS>
+__global__ __launch_bounds__(64 * NW) void k_attn_dkv(AttnArgs a) {
+  using S = Shape<E, DH, NW>;
+  constexpr int TQ = S::TQ, RB = TileRows<E, DH>::RB;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const uint32_t par0 = lds0 + 4 * S::QBYTES;          // [2][3][TQ] log-sum-exp, its rest, D
+  const uint32_t lut = par0 + 2 * 3 * TQ * 4, tmp = lut + 4 * (a.dlast + 96);
+  const int words = a.dlast + 96;
+  const uint32_t hist0 = tmp + 4 * a.nbounds;          // [NW][words] sums of ds by distance
+  const int es = sizeof(E), cpr = a.d * es / 16, group = a.hq / a.hk;
+  const int64_t os = (int64_t)a.hq * a.d * es;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  if (b >= a.slots * a.hk) {
+    const int which = b - a.slots * a.hk;
+    clean_rows(a, which, S::NT, a.dk, a.dks, a.hk * a.d * es);
+    clean_rows(a, which, S::NT, a.dv, a.dvs, a.hk * a.d * es);
+    return;
+  }
+  const int kvh = b % a.hk, slot = b / a.hk, nbk = a.nbounds + 1;
+  const SeqTile st = find_tile(a.offs, a.n_seq, a.n, slot, S::T);
+  if (st.len == 0) {
+    if constexpr (BIAS)
+      for (int t = tid; t < nbk * group; t += S::NT)
+        a.part[((int64_t)slot * nbk + t / group) * a.hq + kvh * group + t % group] = 0.0f;
+    return;
+  }
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
+  const int j0 = st.first + 32 * w;
+  Owners<E, DH> kk, vv;
+  kk.load(a.k + st.begin * a.ks + (int64_t)kvh * a.d * es, a.ks, j0, st.len, cpr);
+  vv.load(a.v + st.begin * a.vs + (int64_t)kvh * a.d * es, a.vs, j0, st.len, cpr);
+  TileReads<E, DH> o;
+  o.init();
+  f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
+  const int t0 = st.first / TQ, t1 = (st.len + TQ - 1) / TQ;   // tiles of queries
+  Copy<E, DH, S::NT, TQ> cq, cg;
+  float2 nl = make_float2(0.0f, 0.0f);
+  float nd = 0.0f;
+  auto fetch = [&](int head, int t) {
+    const int64_t hb = (int64_t)head * a.d * es;
+    cq.fetch(a.q + st.begin * a.qs + hb, a.qs, t * TQ, st.len, cpr);
+    cg.fetch(a.dout + st.begin * os + hb, os, t * TQ, st.len, cpr);
+    if (tid < TQ) {
+      const int i = t * TQ + tid;
+      const int64_t row = (int64_t)head * a.n + st.begin + i;
+      nl = i < st.len ? a.lse[row] : make_float2(NO_WEIGHT, 0.0f);
+      nd = i < st.len ? a.delta[row] : 0.0f;
+    }
+  };
+  auto stash = [&](int buf) {
+    cq.stash(lds0 + buf * 2 * S::QBYTES);
+    cg.stash(lds0 + buf * 2 * S::QBYTES + S::QBYTES);
+    if (tid < TQ) {
+      const uint32_t p = par0 + buf * 3 * TQ * 4 + 4 * tid;
+      lds_put<float>(p, nl.x);
+      lds_put<float>(p + TQ * 4, nl.y);
+      lds_put<float>(p + 2 * TQ * 4, nd);
+    }
+  };
+  int buf = 0;
+  for (int hh = 0; hh < group; ++hh) {
+    const int head = kvh * group + hh;
+    float far = 0.0f, farsum = 0.0f;
+    if constexpr (BIAS) {
+      __syncthreads();
+      fill_bias<E, true>(a, lut, tmp, head, S::NT);
+      far = lds_at<float>(lut + 4 * (words - 1));
+      for (int t = tid; t < NW * words; t += S::NT) lds_put<float>(hist0 + 4 * t, 0.0f);
+    }
+    const uint32_t hist = hist0 + 4 * words * w;
+    if (hh == 0) {
+      fetch(head, t0);
+      stash(0);
+    }
+    __syncthreads();
+    for (int t = t0; t < t1; ++t) {
+      const bool more = t + 1 < t1 || hh + 1 < group;
+      if (more) fetch(t + 1 < t1 ? head : head + 1, t + 1 < t1 ? t + 1 : t0);
+      const uint32_t qb = lds0 + buf * 2 * S::QBYTES, gb = qb + S::QBYTES, par = par0 + buf * 3 * TQ * 4;
+#pragma unroll
+      for (int ib = 0; ib < TQ / 32; ++ib) {
+        const int i0 = t * TQ + 32 * ib;
+        if (i0 < j0 || j0 >= st.len) continue;
+        f32x16 x = block_of<E, DH>(o, qb + ib * 32 * RB, kk);
+        f32x16 dp = block_of<E, DH>(o, gb + ib * 32 * RB, vv);
+        const bool near = BIAS && i0 - j0 - 31 < a.dlast;
+        const uint32_t la = lut + 4 * (i0 - j0 - r + 4 * h + 32), pa = par + 4 * (32 * ib + 4 * h);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 lh = lds_at<f32x4>(pa + 32 * g), ll = lds_at<f32x4>(pa + TQ * 4 + 32 * g),
+                      dd = lds_at<f32x4>(pa + 2 * TQ * 4 + 32 * g);
+          f32x4 bias = {far, far, far, far};
+          if (near) bias = lds_f4(la + 32 * g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int v = 4 * g + e;
+            float s = BIAS ? fmaf(x[v], a.c, bias[e]) : x[v] * a.c;
+            if (i0 == j0) s = tile_row(v) + 4 * h < r ? NEG_INF : s;
+            x[v] = exp_of<E>((s - lh[e]) - ll[e]);
+            dp[v] = x[v] * (dp[v] - dd[e]);
+          }
+        }
+        add_product<E, DH>(dv, x, o, gb + ib * 32 * RB);
+        add_product<E, DH>(dk, dp, o, qb + ib * 32 * RB);
+        if constexpr (BIAS) {
+          if (near) {
+            const uint32_t ha = hist + 4 * (i0 - j0 - r + 4 * h + 32);
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              __builtin_amdgcn_ds_faddf((__attribute__((address_space(3))) float*)(uintptr_t)(ha + 4 * tile_row(v)), dp[v], 0, 0,
+                                        false);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) farsum += dp[v];
+          }
+        }
+      }
+      if (more) {
+        stash(buf ^ 1);
+        __syncthreads();
+      }
+      buf ^= 1;
+    }
+    if constexpr (BIAS) {
+      farsum = wave_sumf(farsum);
+      if (l == 0) {   // distances of at least dlast that no block listed
+        const uint32_t p = hist + 4 * (words - 1);
+        lds_put<float>(p, lds_at<float>(p) + farsum);
+      }
+      __syncthreads();
+      for (int t = tid; t < words; t += S::NT) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) s += lds_at<float>(hist0 + 4 * (q * words + t));
+        lds_put<float>(hist0 + 4 * t, s);
+      }
+      __syncthreads();
+      // eight lanes to a bucket
+      for (int t = tid; t < ((nbk * 8 + S::NT - 1) & ~(S::NT - 1)); t += S::NT) {
+        const int bk = t >> 3;
+        float s = 0.0f;
+        if (bk < nbk) {
+          const int from = bk == 0 ? 0 : a.bounds[bk - 1], to = bk == a.nbounds ? words - 32 : a.bounds[bk];
+          for (int x = from + (t & 7); x < to; x += 8) s += lds_at<float>(hist0 + 4 * (x + 32));
+        }
+#pragma unroll
+        for (int q = 4; q >= 1; q >>= 1) s += __shfl_xor(s, q);
+        if (bk < nbk && (t & 7) == 0) a.part[((int64_t)slot * nbk + bk) * a.hq + head] = s;
+      }
+    }
+  }
+  store_rows<E, DH>(a.dk + st.begin * a.dks + (int64_t)kvh * a.d * es, a.dks, j0, st.len, a.d, dk, a.scale);
+  store_rows<E, DH>(a.dv + st.begin * a.dvs + (int64_t)kvh * a.d * es, a.dvs, j0, st.len, a.d, dv, 1.0f);
+}
+
+// ------------------------------------------------------------------ the last token of every sequence
+struct LastArgs {
+  const char* q;              // [n_seq] rows of hq heads
+  const char* k;              // [rows] rows of hk heads
+  const char* v;
+  char* out;                  // [n_seq][hq][d]
+  int64_t qs, ks, vs;
+  const int32_t* begin;       // [n_seq]
+  const int32_t* length;      // [n_seq]
+  const float* bias;
+  float* part;                // [n_seq][hq][splits][d + 2]: sums of p v, then the reference and the sum of p
+  int64_t rows;
+  int n_seq, d, hq, hk, splits;
+  float c;
+  int nbounds, dlast;
+  int32_t bounds[RECE_MAX_BOUNDS];
+};
+
+// One workgroup for a sequence, a key head and a part of the keys.  The query heads of the group are the columns
+// of a block (up to 32), so keys and values are read once.  Every wave goes over blocks of 32 keys by itself, with LDS of
+// its own; the four are joined at the end, and the parts of a sequence by k_last_join.
+template <class E, int DH, bool BIAS>
+__global__ __launch_bounds__(256) void k_last(LastArgs a) {
+  constexpr int RB = TileRows<E, DH>::RB, BYTES = 32 * RB, P = DH + 4;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const int group = a.hq / a.hk;
+  const uint32_t map = lds0 + max(8 * BYTES, 16 * group * P);   // bucket of every distance up to dlast, a byte each
+  const int es = sizeof(E), cpr = a.d * es / 16;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
+  const int kvh = blockIdx.x % a.hk, u = blockIdx.x / a.hk % a.n_seq, split = blockIdx.x / a.hk / a.n_seq;
+  const int64_t begin = min(max((int64_t)a.begin[u], (int64_t)0), a.rows);
+  const int len = (int)min(max((int64_t)a.length[u], (int64_t)0), a.rows - begin);
+  const int head = kvh * group + min(r, group - 1);
+  Owners<E, DH> q;
+  q.load(a.q + u * a.qs + (int64_t)kvh * group * a.d * es, (int64_t)a.d * es, 0, group, cpr);
+  const char* kh = a.k + begin * a.ks + (int64_t)kvh * a.d * es;
+  const char* vh = a.v + begin * a.vs + (int64_t)kvh * a.d * es;
+  float far = 0.0f;
+  auto unit = [](float b) { return b <= -NO_WEIGHT ? NEG_INF : sizeof(E) == 2 ? b * LOG2E : b; };
+  if constexpr (BIAS) {
+    for (int t = tid; t <= a.dlast; t += 256) {
+      int lo = 0, hi = a.nbounds;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.bounds[mid] <= t) lo = mid + 1;
+        else hi = mid;
+      }
+      lds_put<uint8_t>(map + t, (uint8_t)lo);
+    }
+    far = unit(a.bias[(int64_t)a.nbounds * a.hq + head]);
+    __syncthreads();
+  }
+  TileReads<E, DH> o;
+  o.init();
+  const uint32_t kb = lds0 + w * 2 * BYTES, vb = kb + BYTES;
+  f32x16 acc[DH / 32] = {};
+  float m = NEG_INF, sum = 0.0f;
+  const int nb32 = (len + 31) / 32, step = 4 * a.splits;
+  // copies of 64 lanes
+  constexpr int PT = 32 * TileRows<E, DH>::CPR / 64;
+  u32x4 rk[PT], rv[PT];
+  auto fetch = [&](int blk) {
+#pragma unroll
+    for (int x = 0; x < PT; ++x) {
+      const int i = x * 64 + l, row = blk * 32 + i / TileRows<E, DH>::CPR, c = i % TileRows<E, DH>::CPR;
+      rk[x] = rv[x] = u32x4{0u, 0u, 0u, 0u};
+      if (row < len && c < cpr) {
+        rk[x] = *reinterpret_cast<const u32x4*>(kh + row * a.ks + c * 16);
+        rv[x] = *reinterpret_cast<const u32x4*>(vh + row * a.vs + c * 16);
+      }
+    }
+  };
+  int blk = split * 4 + w;
+  if (blk < nb32) fetch(blk);
+  for (; blk < nb32; blk += step) {
+    wave_sync();
+#pragma unroll
+    for (int x = 0; x < PT; ++x) {
+      const int i = x * 64 + l, row = i / TileRows<E, DH>::CPR, c = i % TileRows<E, DH>::CPR;
+      const uint32_t at = row * RB + ((c ^ (row & TileRows<E, DH>::SWM)) << 4);
+      lds_put(kb + at, rk[x]);
+      lds_put(vb + at, rv[x]);
+    }
+    wave_sync();
+    if (blk + step < nb32) fetch(blk + step);
+    f32x16 x = block_of<E, DH>(o, kb, q);
+    const int j0 = blk * 32, back = len - 1 - j0 - 4 * h;   // distance of the lane's key of row tile_row(v): back - tile_row(v)
+    if (BIAS && len - 1 - j0 - 31 < a.dlast) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int bk = lds_at<uint8_t>(map + max(0, min(back - tile_row(v), a.dlast)));
+        x[v] = fmaf(x[v], a.c, unit(a.bias[(int64_t)bk * a.hq + head]));
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) x[v] = BIAS ? fmaf(x[v], a.c, far) : x[v] * a.c;
+    }
+    if (j0 + 32 > len) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) x[v] = back - tile_row(v) < 0 ? NEG_INF : x[v];
+    }
+    float bm = x[0];
+#pragma unroll
+    for (int v = 1; v < 16; ++v) bm = fmaxf(bm, x[v]);
+    bm = fmaxf(bm, __shfl_xor(bm, 32));
+    if (ballot(bm > m + (sizeof(E) == 2 ? 8.0f : 5.5f))) {
+      const float up = fmaxf(m, bm);
+      const float f = m == NEG_INF ? 0.0f : exp_of<E>(m - up);
+      sum *= f;
+#pragma unroll
+      for (int nb = 0; nb < DH / 32; ++nb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[nb][v] *= f;
+      m = up;
+    }
+    const float ref = fmaxf(m, -NO_WEIGHT);
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      x[v] = exp_of<E>(x[v] - ref);
+      sum += x[v];
+    }
+    add_product<E, DH>(acc, x, o, vb);
+  }
+  sum += __shfl_xor(sum, 32);
+  // the four waves: [4][group][P] of LDS, elements, then reference and sum
+  __syncthreads();
+  if (r < group) {
+    const uint32_t at = lds0 + 4 * P * (w * group + r);
+#pragma unroll
+    for (int nb = 0; nb < DH / 32; ++nb)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        lds_put(at + 4 * (32 * nb + 8 * g + 4 * h),
+                f32x4{acc[nb][4 * g], acc[nb][4 * g + 1], acc[nb][4 * g + 2], acc[nb][4 * g + 3]});
+    if (h == 0) {
+      lds_put<float>(at + 4 * DH, m);
+      lds_put<float>(at + 4 * DH + 4, sum);
+    }
+  }
+  __syncthreads();
+  for (int t = tid; t < group * a.d; t += 256) {
+    const int g = t / a.d, e = t % a.d;
+    float top = -NO_WEIGHT, mm[4], all = 0.0f, val = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      mm[x] = lds_at<float>(lds0 + 4 * (P * (x * group + g) + DH));
+      top = fmaxf(top, mm[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t at = lds0 + 4 * P * (x * group + g);
+      const float f = exp_of<E>(mm[x] - top);
+      all = fmaf(f, lds_at<float>(at + 4 * DH + 4), all);
+      val = fmaf(f, lds_at<float>(at + 4 * e), val);
+    }
+    const int64_t row = (int64_t)u * a.hq + kvh * group + g;
+    if (a.splits == 1) {
+      const float y = all == 0.0f ? 0.0f : val / all;
+      if constexpr (sizeof(E) == 2)
+        reinterpret_cast<uint16_t*>(a.out)[row * a.d + e] = (uint16_t)pack_bf16(y, 0.0f);
+      else
+        reinterpret_cast<float*>(a.out)[row * a.d + e] = y;
+    } else {
+      float* p = a.part + (row * a.splits + split) * (a.d + 2);
+      p[e] = val;
+      if (e == 0) {
+        p[a.d] = top;
+        p[a.d + 1] = all;
+      }
+    }
+  }
+}
+
+// A workgroup joins the parts of one head of one sequence: d columns x 256 / d (or fewer) slices of the parts.
+template <class E>
+__global__ __launch_bounds__(256) void k_last_join(LastArgs a) {
+  __shared__ float sv[256], sw[256], sm[4];
+  const int tid = threadIdx.x, slices = 256 / a.d, e = tid % a.d, sl = tid / a.d, W = a.d + 2;
+  const float* p = a.part + (int64_t)blockIdx.x * a.splits * W;
+  float top = -NO_WEIGHT;
+  for (int s = tid; s < a.splits; s += 256) top = fmaxf(top, p[(int64_t)s * W + a.d]);
+  top = wave_max(top);
+  if (lane_id() == 0) sm[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  float val = 0.0f, all = 0.0f;
+  if (sl < slices) {
+#pragma unroll 4
+    for (int s = sl; s < a.splits; s += slices) {
+      const float f = exp_of<E>(p[(int64_t)s * W + a.d] - top);
+      val = fmaf(f, p[(int64_t)s * W + e], val);
+      all = fmaf(f, p[(int64_t)s * W + a.d + 1], all);
+    }
+  }
+  sv[tid] = val;
+  sw[tid] = all;
+  __syncthreads();
+  if (tid < a.d) {
+    for (int s = 1; s < slices; ++s) {
+      val += sv[s * a.d + e];
+      all += sw[s * a.d + e];
+    }
+    const float y = all == 0.0f ? 0.0f : val / all;
+    const int64_t at = (int64_t)blockIdx.x * a.d + e;
+    if constexpr (sizeof(E) == 2)
+      reinterpret_cast<uint16_t*>(a.out)[at] = (uint16_t)pack_bf16(y, 0.0f);
+    else
+      reinterpret_cast<float*>(a.out)[at] = y;
+  }
+}
+
+constexpr int ATTN_WAVES = 4;
+
+int slots_of(int64_t n, int64_t n_seq, int T) { return (int)(n / T + n_seq); }
+
+// A launch with dynamic LDS (beyond 64 KB it has to be allowed first).
+template <class A>
+hipError_t launch(void (*kernel)(A), int64_t grid, int threads, size_t lds, hipStream_t st, const A& a) {
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<(unsigned)grid, threads, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+// f(type tag, padded head width, bias or not)
+template <class F>
+hipError_t attn_shape(bool bf16v, int d, bool bias, F f) {
+  auto by_bias = [&](auto e, auto dh) { return bias ? f(e, dh, std::true_type()) : f(e, dh, std::false_type()); };
+  auto by_width = [&](auto e) {
+    if (d <= 32) return by_bias(e, std::integral_constant<int, 32>());
+    if (d <= 64) return by_bias(e, std::integral_constant<int, 64>());
+    return by_bias(e, std::integral_constant<int, 128>());
+  };
+  return bf16v ? by_width(bf16{}) : by_width(0.0f);
+}
+
+AttnArgs common_args(const rece_attention_config& c, const void* q, const void* k, const void* v, const int32_t* offs,
+                     const float* bias) {
+  AttnArgs a{};
+  const int es = c.dtype == RECE_BF16 ? 2 : 4;
+  a.q = static_cast<const char*>(q);
+  a.k = static_cast<const char*>(k);
+  a.v = static_cast<const char*>(v);
+  a.qs = c.q_stride * es;
+  a.ks = c.k_stride * es;
+  a.vs = c.v_stride * es;
+  a.offs = offs;
+  a.bias = bias;
+  a.n = c.n;
+  a.n_seq = (int)c.n_seq;
+  a.d = c.d;
+  a.hq = c.heads;
+  a.hk = c.kv_heads;
+  a.scale = c.scale;
+  a.c = c.dtype == RECE_BF16 ? (float)((double)c.scale * 1.4426950408889634074) : c.scale;
+  a.nbounds = bias ? c.n_bounds : 0;
+  a.dlast = a.nbounds ? c.bounds[a.nbounds - 1] : 0;
+  for (int t = 0; t < a.nbounds; ++t) a.bounds[t] = c.bounds[t];
+  return a;
+}
+
+// Workspace: log-sum-exp [hq][n] float2, D [hq][n], partial bias gradients.
+struct AttnSpace {
+  size_t lse, delta, part, total;
+};
+AttnSpace attn_space(const rece_attention_config& c) {
+  AttnSpace s{};
+  const size_t rows = (size_t)c.heads * c.n;
+  const size_t slots = (size_t)(c.n / 32 + c.n_seq);   // of the smallest workgroups
+  s.lse = 0;
+  s.delta = (rows * 8 + 15) & ~(size_t)15;
+  s.part = (s.delta + rows * 4 + 15) & ~(size_t)15;
+  s.total = s.part + slots * (c.n_bounds + 1) * c.heads * 4;
+  return s;
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes(const rece_attention_config& c) { return attn_space(c).total; }
+
+hipError_t attention_forward(const rece_attention_config& c, const void* q, const void* k, const void* v,
+                             const int32_t* offs, const float* bias, void* ws, void* out, hipStream_t st) {
+  AttnArgs a = common_args(c, q, k, v, offs, bias);
+  a.out = static_cast<char*>(out);
+  a.lse = static_cast<float2*>(ws);
+  return attn_shape(c.dtype == RECE_BF16, c.d, bias != nullptr, [&](auto e, auto dh, auto bb) {
+    using E = decltype(e);
+    constexpr int DH = decltype(dh)::value, NW = ATTN_WAVES;
+    constexpr bool B = decltype(bb)::value;
+    using S = Shape<E, DH, NW>;
+    a.slots = slots_of(c.n, c.n_seq, S::T);
+    const size_t lds = 4 * S::BYTES + (B ? 4 * (a.dlast + 96 + a.nbounds) : 0);
+    return launch(k_attn<E, DH, NW, B>, (int64_t)a.slots * a.hq + CLEAN, S::NT, lds, st, a);
+  });
+}
+
+hipError_t attention_backward(const rece_attention_config& c, const void* q, const void* k, const void* v,
+                              const int32_t* offs, const float* bias, const void* out, void* ws, const void* dout,
+                              void* dq, void* dk, void* dv, float* dbias, const int64_t (&strides)[3], hipStream_t st) {
+  AttnArgs a = common_args(c, q, k, v, offs, bias);
+  if (c.n == 0) return bias ? launch_join_rows(nullptr, 0, (a.nbounds + 1) * a.hq, dbias, st) : hipSuccess;
+  const int es = c.dtype == RECE_BF16 ? 2 : 4;
+  const AttnSpace sp = attn_space(c);
+  a.out = const_cast<char*>(static_cast<const char*>(out));
+  a.dout = static_cast<const char*>(dout);
+  a.lse = static_cast<float2*>(ws);
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + sp.delta);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + sp.part);
+  a.dq = static_cast<char*>(dq);
+  a.dk = static_cast<char*>(dk);
+  a.dv = static_cast<char*>(dv);
+  a.dqs = strides[0] * es;
+  a.dks = strides[1] * es;
+  a.dvs = strides[2] * es;
+  hipError_t r = attn_shape(c.dtype == RECE_BF16, c.d, bias != nullptr, [&](auto e, auto dh, auto bb) {
+    using E = decltype(e);
+    constexpr int DH = decltype(dh)::value, NW = ATTN_WAVES;
+    constexpr bool B = decltype(bb)::value;
+    using S = Shape<E, DH, NW>;
+    a.slots = slots_of(c.n, c.n_seq, S::T);
+    const int words = a.dlast + 96;
+    const size_t lds = 4 * S::BYTES + (B ? 4 * (words + a.nbounds) : 0);
+    const hipError_t e1 = launch(k_attn_dq<E, DH, NW, B>, (int64_t)a.slots * a.hq + CLEAN, S::NT, lds, st, a);
+    if (e1 != hipSuccess) return e1;
+    const size_t lds2 = 4 * S::QBYTES + 24 * S::TQ + (B ? 4 * (words + a.nbounds + NW * words) : 0);
+    return launch(k_attn_dkv<E, DH, NW, B>, (int64_t)a.slots * a.hk + CLEAN, S::NT, lds2, st, a);
+  });
+  if (r != hipSuccess || !bias) return r;
+  return launch_join_rows(a.part, a.slots, (a.nbounds + 1) * a.hq, dbias, st);
+}
+
+// Parts of a sequence's keys: enough workgroups for two per CU, each wave with two blocks of 32 keys at least.
+int64_t last_splits(const rece_attention_config& c, int64_t max_len) {
+  const int64_t wgs = c.n_seq * c.kv_heads, want = (512 + wgs - 1) / wgs, most = (max_len + 255) / 256;
+  return std::max<int64_t>(1, std::min<int64_t>({want, most, 512}));
+}
+
+size_t last_attention_workspace_bytes(const rece_attention_config& c, int64_t max_len) {
+  const int64_t s = last_splits(c, max_len);
+  return s == 1 ? 0 : (size_t)c.n_seq * c.heads * s * (c.d + 2) * 4;
+}
+
+hipError_t last_attention(const rece_attention_config& c, int64_t max_len, const void* q, const void* k, const void* v,
+                          const int32_t* begin, const int32_t* length, const float* bias, void* ws, void* out,
+                          hipStream_t st) {
+  const int es = c.dtype == RECE_BF16 ? 2 : 4;
+  LastArgs a{};
+  a.q = static_cast<const char*>(q);
+  a.k = static_cast<const char*>(k);
+  a.v = static_cast<const char*>(v);
+  a.out = static_cast<char*>(out);
+  a.qs = c.q_stride * es;
+  a.ks = c.k_stride * es;
+  a.vs = c.v_stride * es;
+  a.begin = begin;
+  a.length = length;
+  a.bias = bias;
+  a.part = static_cast<float*>(ws);
+  a.rows = c.n;
+  a.n_seq = (int)c.n_seq;
+  a.d = c.d;
+  a.hq = c.heads;
+  a.hk = c.kv_heads;
+  a.splits = (int)last_splits(c, max_len);
+  a.c = c.dtype == RECE_BF16 ? (float)((double)c.scale * 1.4426950408889634074) : c.scale;
+  a.nbounds = bias ? c.n_bounds : 0;
+  a.dlast = a.nbounds ? c.bounds[a.nbounds - 1] : 0;
+  for (int t = 0; t < a.nbounds; ++t) a.bounds[t] = c.bounds[t];
+  return attn_shape(c.dtype == RECE_BF16, c.d, bias != nullptr, [&](auto e, auto dh, auto bb) {
+    using E = decltype(e);
+    constexpr int DH = decltype(dh)::value;
+    constexpr bool B = decltype(bb)::value;
+    const size_t lds = std::max<size_t>(8 * 32 * TileRows<E, DH>::RB, 16 * (a.hq / a.hk) * (DH + 4)) + (B ? a.dlast + 1 : 0);
+    const hipError_t r = launch(k_last<E, DH, B>, c.n_seq * a.hk * a.splits, 256, lds, st, a);
+    if (r != hipSuccess || a.splits == 1) return r;
+    k_last_join<E><<<(unsigned)(c.n_seq * a.hq), 256, 0, st>>>(a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace rece

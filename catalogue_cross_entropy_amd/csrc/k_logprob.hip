@@ -49,15 +49,11 @@
 #include "rece_device.h"
 #include "rece_internal.h"
 #include "rece_parts.h"
+#include "rece_tile.h"
 
 namespace rece {
 
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LP_REF_LIMIT = 1.1529215e18f;   // 2^60: a sum beyond it is taken again with a better reference
@@ -104,48 +100,13 @@ template <class E, int D, int NWS> struct LpTile {
   static constexpr int BYTES = TI * RB;
 };
 
-template <class E> struct LpMma;
-template <> struct LpMma<bf16> {
-  static __device__ __forceinline__ f32x16 run(u32x4 a, u32x4 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  }
-};
-template <> struct LpMma<float> {   // four coordinates per chunk and lane half: four products of depth 2
-  static __device__ __forceinline__ f32x16 run(u32x4 a, u32x4 b, f32x16 c) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
-    return c;
-  }
-};
+template <class E> using LpMma = TileMma<E>;
 
-// bf16 pair of two floats, rounded to nearest even.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const f32x2 v = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
-__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // Two floats as two bf16 terms each.
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16(a, b);
   const float ra = a - lo_f32(hi), rb = b - hi_f32(hi);
   lo = pack_bf16(ra, rb);
-}
-
-// LDS by byte offset: a per-lane offset and a constant that becomes the instruction's.
-template <class T>
-__device__ __forceinline__ T lds_at(uint32_t off) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) T*>((uintptr_t)off);
-}
-__device__ __forceinline__ s16x4 lds_tr4(uint32_t off) {
-  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)off);
-}
-
-template <class T>
-__device__ __forceinline__ void lds_put(uint32_t off, T v) {
-  *reinterpret_cast<__attribute__((address_space(3))) T*>((uintptr_t)off) = v;
 }
 
 // x log2(e) / temperature - r (the small term last, onto the difference)
@@ -162,40 +123,9 @@ __device__ __forceinline__ float lp_weight(float d, float a, float b) {
 }
 
 // Row of value v of a 32 x 32 block (less 4 h for the lane half h).
-__device__ __forceinline__ constexpr int lp_row(int v) { return 8 * (v >> 2) + (v & 3); }
+__device__ __forceinline__ constexpr int lp_row(int v) { return tile_row(v); }
 
-// Per-lane LDS offsets of a wave's fragment reads inside a tile.  The swizzle only mixes the low bits of
-// a chunk's number, so a few offsets serve all reads, with constants added.
-template <class E, int D, int NWS> struct LpLds {
-  using T = LpTile<E, D, NWS>;
-  static constexpr int KC = T::RB / 32;
-  static constexpr int NX = KC < (T::SWM + 1) / 2 ? KC : (T::SWM + 1) / 2;
-  static constexpr int NY = sizeof(E) == 2 ? (D / 32 < 2 ? 1 : 2) : 4;
-  uint32_t x[NX], y[NY];
-  __device__ __forceinline__ void init() {
-    const int l = lane_id(), h = l >> 5, r = l & 31;
-#pragma unroll
-    for (int k = 0; k < NX; ++k) x[k] = r * T::RB + (((2 * k + h) ^ (r & T::SWM)) << 4);
-    if constexpr (sizeof(E) == 2) {
-      // rows 4 h + j / 4, coordinates 16 ((l / 16) % 2) + 4 (j % 4) .. + 3 of each 32: within a 16-lane
-      // group the transpose read hands lane i coordinate i of the group's four rows
-      const int j = l & 15, half = (l >> 4) & 1, row = 4 * h + (j >> 2);
-#pragma unroll
-      for (int q = 0; q < NY; ++q)
-        y[q] = row * T::RB + (((4 * q + 2 * half + ((j & 3) >> 1)) ^ (row & T::SWM)) << 4) + (j & 1) * 8;
-    } else {
-#pragma unroll
-      for (int q = 0; q < NY; ++q) {
-        const int row = 4 * h + q;
-        y[q] = row * T::RB + (((r >> 2) ^ (row & T::SWM)) << 4) + 4 * (r & 3);
-      }
-    }
-  }
-  // 16-byte chunk 2 k + h of row l % 32
-  static __device__ __forceinline__ u32x4 frag(const LpLds& o, uint32_t base, int k) {
-    return lds_at<u32x4>(o.x[k % NX] + base + (k / NX) * (NX * 32));
-  }
-};
+template <class E, int D, int NWS> using LpLds = TileReads<E, D>;
 
 // acc[ob][nb] += G[32 owners][32 streamed] . rows[32 streamed][D], lane l holding G[owner l % 32]
 // [streamed lp_row(v) + 4 (l / 32)] in g[ob][v].  bf16: TERMS products, each with the bf16

@@ -362,6 +362,101 @@ rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream
                                  const float* dloss, void* workspace, size_t workspace_bytes, float* loss,
                                  float* loss_pg, float* rewards, void* dlogp);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the sequence encoder between the item embedding and the loss, and of
+ * scoring the catalogue in 8 bits.  The conventions of the operators above hold.
+ * ------------------------------------------------------------------------- */
+
+/* Causal attention over packed sequences with grouped heads and a learned bias by
+ * buckets of the distance.  Sequence u holds the tokens offsets[u] .. offsets[u + 1] - 1;
+ * for its tokens i and j <= i, and head h with key head g = h / (heads / kv_heads):
+ *   t_ij = scale q_ih . k_jg + bias[bucket(i - j)][h],   p_ij = softmax over j,   out_ih = sum_j p_ij v_jg
+ *   bucket(t) = how many of the bounds are <= t
+ *   q [n] rows of heads x d elements, k and v [n] rows of kv_heads x d, dtype; a row's elements are
+ *   contiguous, rows begin q_stride, k_stride, v_stride elements apart (multiples of 8: slices of one
+ *   projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads.
+ *   offsets [n_seq + 1] int32 non-decreasing (values outside [0, n] are clamped; a sequence may be empty)
+ *   bias [n_bounds + 1][heads] float32, or NULL: none.  bounds: distances >= 1, increasing, at most
+ *   RECE_MAX_DISTANCE.  An entry of at most -1e30 leaves its pairs no weight; a row that
+ *   has nothing left gives 0, and no gradient.
+ *   out [n][heads][d] dtype.  Rows of no sequence (before the first, behind the last) become 0, in
+ *   out and in the gradients, and what the inputs hold there (NaN or infinity) reaches nothing; what a row of
+ *   a sequence holds reaches rows of that sequence alone.
+ *   workspace  rece_attention_workspace_bytes bytes for a call that a backward call follows; NULL: none will.
+ * Backward (same inputs; out and workspace as the forward call left them):
+ *   ds_ij = p_ij (dout_i . v_j - D_i), D_i = sum_j p_ij dout_i . v_j
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i (over the heads of a group)
+ *   dbias[b][h] = sum of ds_ij over the pairs of bucket b (NULL with bias NULL)
+ *   dout [n][heads][d]; dq, dk, dv dtype, rows dq_stride, dk_stride, dv_stride elements apart; dbias float32
+ * Sums are float32 (dbias: float32 within a workgroup, float64 over them).  Of dtype bf16, p and ds enter their
+ * products with the gradients and values rounded to bf16. */
+#define RECE_MAX_BOUNDS 127
+#define RECE_MAX_DISTANCE 4096
+typedef struct {
+  int64_t n;            /* tokens (rece_last_attention: rows of the cache); 0 <= n <= 2^31 - 1 */
+  int64_t n_seq;        /* >= 1 */
+  int64_t q_stride;     /* elements between rows */
+  int64_t k_stride;
+  int64_t v_stride;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t d;
+  int32_t dtype;        /* rece_dtype of q, k, v, out and the gradients */
+  float scale;          /* > 0, finite */
+  int32_t n_bounds;     /* 0 .. RECE_MAX_BOUNDS */
+  int32_t bounds[RECE_MAX_BOUNDS];
+} rece_attention_config;
+rece_status rece_attention_workspace_bytes(const rece_attention_config* cfg, size_t* bytes);
+rece_status rece_attention_forward(const rece_attention_config* cfg, void* stream, const void* q, const void* k,
+                                   const void* v, const int32_t* offsets, const float* bias, void* workspace,
+                                   size_t workspace_bytes, void* out);
+rece_status rece_attention_backward(const rece_attention_config* cfg, void* stream, const void* q, const void* k,
+                                    const void* v, const int32_t* offsets, const float* bias, const void* out,
+                                    void* workspace, size_t workspace_bytes, const void* dout, int64_t dq_stride,
+                                    int64_t dk_stride, int64_t dv_stride, void* dq, void* dk, void* dv, float* dbias);
+
+/* The same attention for one token per sequence, the last one, over a cache: sequence u's keys and values
+ * are rows begin[u] .. begin[u] + length[u] - 1 of k and v (n rows in all; begin and length [n_seq] int32,
+ * clamped to them; sequences may share rows), its query, row u of q, stands at the last of them:
+ *   out_uh = softmax_j(scale q_uh . k_jg + bias[bucket(length[u] - 1 - j)][h]) v_jg      out [n_seq][heads][d]
+ * A sequence of length 0 gives 0.  heads / kv_heads at most 32.  max_len >= 1: the lengths to plan for (longer
+ * sequences are right too, but slower).  workspace: rece_last_attention_workspace_bytes bytes, temporary (may be 0). */
+rece_status rece_last_attention_workspace_bytes(const rece_attention_config* cfg, int64_t max_len, size_t* bytes);
+rece_status rece_last_attention(const rece_attention_config* cfg, void* stream, int64_t max_len, const void* q,
+                                const void* k, const void* v, const int32_t* begin, const int32_t* length,
+                                const float* bias, void* workspace, size_t workspace_bytes, void* out);
+
+/* Root-mean-square norm of a residual stream after the addition of a branch:
+ *   h = x + residual (rounded to dtype; residual NULL: h = x),  rstd = 1 / sqrt(mean h^2 + eps),  y = h rstd weight
+ *   x, residual, h, y [n][d] dtype; d a multiple of 8, at most 8192; weight [d] float32; eps >= 0
+ *   h may be NULL (not stored), or x or residual itself; rstd [n] float32 or NULL
+ * In 8 bits: with m = max_t |h_t weight_t| of a row,
+ *   y8_t = rint(127 h_t weight_t / m) (ties to even),  scale = m rstd / 127     (y = scale y8)
+ *   y8 [n][d] int8, scale [n] float32; a row of zeros has scale 0, a row that holds a NaN or an infinity has
+ *   values 0 and scale NaN.
+ * Backward: dy, dh (or NULL: the gradient that reaches h past the norm) [n][d], h and rstd of the forward call:
+ *   dx = dh + rstd (dy weight - h rstd^2 mean(dy weight h)): the gradient of x and of the residual alike
+ *   dweight [d] float32 = sum over rows of dy h rstd
+ *   workspace  rece_norm_workspace_bytes bytes, temporary */
+rece_status rece_norm_workspace_bytes(int64_t n, int32_t d, size_t* bytes);
+rece_status rece_norm_forward(void* stream, int64_t n, int32_t d, int32_t dtype, float eps, const void* x,
+                              const void* residual, const float* weight, void* h, void* y, float* rstd);
+rece_status rece_norm_forward_int8(void* stream, int64_t n, int32_t d, int32_t dtype, float eps, const void* x,
+                                   const void* residual, const float* weight, void* h, int8_t* y8, float* scale);
+rece_status rece_norm_backward(void* stream, int64_t n, int32_t d, int32_t dtype, const void* dy, const void* h,
+                               const void* dh, const float* weight, const float* rstd, void* workspace,
+                               size_t workspace_bytes, void* dx, float* dweight);
+
+/* Rows in 8 bits: x8 = rint(127 x / m), scale = m / 127 with m = max |x| of a row (as above).  An item table is laid
+ * out once like this for rece_int8_scores. */
+rece_status rece_quantize_rows(void* stream, int64_t n, int32_t d, int32_t dtype, const void* x, int8_t* x8, float* scale);
+
+/* Scores of positions against items, both in 8 bits with a scale per row:
+ *   out_ij = sx_i sy_j sum_t x8_it y8_jt      (integer sum, then float32, rounded once to dtype)
+ *   x8 [s][d], y8 [C][d] int8, sx [s], sy [C] float32, out [s][C] dtype; d a multiple of 16, at most 8192 */
+rece_status rece_int8_scores(void* stream, int64_t s, int64_t C, int32_t d, int32_t dtype, const int8_t* x8,
+                             const float* sx, const int8_t* y8, const float* sy, void* out);
+
 /* Intermediate results kept in `saved` (the steps of Algorithm 1, RECE page,
  * Section 3), copied asynchronously into the caller's `dst`. */
 typedef enum {
