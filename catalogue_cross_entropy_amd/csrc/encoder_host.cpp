@@ -32,7 +32,8 @@ bool missing(P... p) {
 
 bool bad_dtype(int32_t t) { return t != RECE_F32 && t != RECE_BF16; }
 
-bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8 != 0 || stride > I32_MAX; }
+// offsets within a tile of up to 64 rows stay below 2^31 bytes
+bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8 != 0 || stride > (1 << 23); }
 
 rece_status check_attention(const rece_attention_config* c) {
   if (!c) return invalid("config is NULL");
@@ -46,7 +47,7 @@ rece_status check_attention(const rece_attention_config* c) {
   if (!(c->scale > 0.0f) || !std::isfinite(c->scale)) return invalid("scale must be positive and finite");
   if (bad_stride(c->q_stride, (int64_t)c->heads * c->d) || bad_stride(c->k_stride, (int64_t)c->kv_heads * c->d) ||
       bad_stride(c->v_stride, (int64_t)c->kv_heads * c->d))
-    return invalid("strides must be multiples of 8, at least a row's elements and fit in int32");
+    return invalid("strides must be multiples of 8, at least a row's elements, at most 2^23");
   if (c->n_bounds < 0 || c->n_bounds > RECE_MAX_BOUNDS) return invalid("n_bounds must be in [0, RECE_MAX_BOUNDS]");
   for (int t = 0; t < c->n_bounds; ++t)
     if (c->bounds[t] < 1 || c->bounds[t] > RECE_MAX_DISTANCE || (t > 0 && c->bounds[t] <= c->bounds[t - 1]))
@@ -112,7 +113,7 @@ rece_status rece_attention_backward(const rece_attention_config* cfg, void* stre
   if (r != RECE_OK) return r;
   if (bad_stride(dq_stride, (int64_t)cfg->heads * cfg->d) || bad_stride(dk_stride, (int64_t)cfg->kv_heads * cfg->d) ||
       bad_stride(dv_stride, (int64_t)cfg->kv_heads * cfg->d))
-    return invalid("strides must be multiples of 8, at least a row's elements and fit in int32");
+    return invalid("strides must be multiples of 8, at least a row's elements, at most 2^23");
   if (!bias != !dbias) return invalid("dbias goes with bias");
   if (misaligned(4, offsets, bias, dbias)) return invalid("offsets, bias and dbias must be 4-byte aligned");
   if (cfg->n > 0) {

@@ -17,8 +17,9 @@
 //
 // Scores and sums are float32.  bf16: scores carry the factor log2(e), p and ds are rounded to bf16 for the second
 // products alone.  float32: scores stay in natural units and their difference to the maximum is scaled.
-// D from the rounded outputs is a first value only: its error would be the bias gradient's.  k_attn_dq adds the sum of
-// p (dp - D) over the row to it, which is 0 for the exact D.
+// D comes from the outputs with what their rounding left (k_attn keeps it; from the rounded outputs alone dq would be off
+// by 1.4 times as much).  The rounding of p in the outputs is still in it and would be the bias gradient's error:
+// k_attn_dq adds the sum of p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
 #include <algorithm>
 #include <cmath>
 
@@ -32,6 +33,7 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NO_WEIGHT = 1e30f;     // log-sum-exp of a row without weight: exp(t - 1e30) = 0
+constexpr size_t MAX_LDS = 160 * 1024; // of a workgroup
 constexpr int CLEAN = 64;              // workgroups that clear rows of no sequence
 
 struct AttnArgs {
@@ -46,6 +48,7 @@ struct AttnArgs {
   int64_t qs, ks, vs, dqs, dks, dvs;
   const int32_t* offs;        // [n_seq + 1]
   const float* bias;          // [n_bounds + 1][hq] or nullptr
+  char* low;                  // bf16: [n][hq][d] what the rounding of out left, or nullptr
   float2* lse;                // [hq][n] log-sum-exp (value, what its rounding left), or nullptr
   float* delta;               // [hq][n] D
   float* part;                // [slots][n_bounds + 1][hq] partial bias gradients
@@ -53,7 +56,7 @@ struct AttnArgs {
   int n_seq, d, hq, hk, slots;
   float scale, c;             // c: the factor of a product, with log2(e) for bf16
   int nbounds, dlast;         // dlast: from this distance on there is one bucket
-  int32_t bounds[RECE_MAX_BOUNDS];
+  int32_t bounds[RECE_MAX_BOUNDS + 1];
 };
 
 struct SeqTile {
@@ -62,7 +65,7 @@ struct SeqTile {
   int first;       // first row of the tile within the sequence
 };
 
-// The tile of a slot (see above).  Every wave finds it by itself, 64 probes at a time.  What is found lies inside the
+// The tile of a slot (see above).  Every wave finds it by itself, 256 probes at a time.  What is found lies inside the
 // rows whatever the offsets hold.
 __device__ __forceinline__ SeqTile find_tile(const int32_t* offs, int n_seq, int64_t n, int slot, int T) {
   int lo = 0, size = n_seq;
@@ -70,9 +73,14 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* offs, int n_seq, int
   auto clamped = [&](int u) { return max(0, min(offs[u], (int32_t)n)); };
   SeqTile t{0, 0, 0};
   while (true) {
-    const int step = (size + 63) / 64, at = lo + l * step;
-    const bool below = l * step < size && clamped(at) / T + at <= slot;
-    const int cnt = popc(ballot(below));
+    const int step = (int)(((int64_t)size + 255) / 256);
+    int cnt = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int64_t d = (int64_t)(4 * l + x) * step;
+      const int at = lo + (int)(d < size ? d : 0);
+      cnt += popc(ballot(d < size && clamped(at) / T + at <= slot));
+    }
     if (cnt == 0) return t;
     lo += (cnt - 1) * step;
     if (step == 1) break;
@@ -97,27 +105,38 @@ __device__ __forceinline__ void clean_rows(const AttnArgs& a, int which, int nt,
   }
 }
 
-// TI rows of D elements from memory to LDS: NT threads, PT chunks each.  Rows at or beyond `len` and elements
-// beyond the head's are zero.
+// TI rows of D elements from memory to LDS by NT threads (a workgroup or a wave), PT chunks each.  Rows beyond the end
+// repeat the sequence's last one and chunks beyond the head its last one: their weights and the owners' elements
+// there are 0.  Whole tiles take one lane offset beside scalar ones.
 template <class E, int D, int NT, int TI> struct Copy {
   using T = TileRows<E, D>;
   static constexpr int PT = TI * T::CPR / NT, BYTES = TI * T::RB;
-  static_assert(TI * T::CPR % NT == 0, "whole chunks per thread");
+  static constexpr int RPQ = NT / T::CPR;                   // rows of a step
+  static constexpr int NV = RPQ >= 8 ? 1 : 8 / RPQ;         // the swizzle repeats every 8 rows
+  static_assert(TI * T::CPR % NT == 0 && NT % T::CPR == 0, "whole chunks per thread, whole rows per step");
   u32x4 r[PT];
-  __device__ __forceinline__ void fetch(const char* head, int64_t stride, int row0, int len, int cpr) {
+  uint32_t off, to[NV];
+  __device__ __forceinline__ void init(int64_t stride, int cpr) {
+    const int i = (int)threadIdx.x % NT, row = i / T::CPR, c = i % T::CPR;
+    off = (uint32_t)row * (uint32_t)stride + min(c, cpr - 1) * 16;
 #pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      const int i = q * NT + (int)threadIdx.x, row = row0 + i / T::CPR, c = i % T::CPR;
-      r[q] = u32x4{0u, 0u, 0u, 0u};
-      if (row < len && c < cpr) r[q] = *reinterpret_cast<const u32x4*>(head + row * stride + c * 16);
+    for (int v = 0; v < NV; ++v) to[v] = row * T::RB + ((c ^ ((row + v * RPQ) & T::SWM)) << 4);
+  }
+  __device__ __forceinline__ void fetch(const char* head, int64_t stride, int row0, int len) {
+    const char* p = head + row0 * stride;
+    if (row0 + TI <= len) {
+#pragma unroll
+      for (int q = 0; q < PT; ++q) r[q] = *reinterpret_cast<const u32x4*>(p + q * RPQ * stride + off);
+    } else {
+      const int row = (int)threadIdx.x % NT / T::CPR;
+#pragma unroll
+      for (int q = 0; q < PT; ++q)   // rows back to the last one
+        r[q] = *reinterpret_cast<const u32x4*>(p + (q * RPQ - max(0, row0 + q * RPQ + row - (len - 1))) * stride + off);
     }
   }
   __device__ __forceinline__ void stash(uint32_t buf) const {
 #pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      const int i = q * NT + (int)threadIdx.x, row = i / T::CPR, c = i % T::CPR;
-      lds_put(buf + row * T::RB + ((c ^ (row & T::SWM)) << 4), r[q]);
-    }
+    for (int q = 0; q < PT; ++q) lds_put(buf + to[q % NV] + q * RPQ * T::RB, r[q]);
   }
 };
 
@@ -135,12 +154,28 @@ template <class E, int D> struct Owners {
   }
 };
 
-// block[32 rows of the tile at base][32 owners]
+// The values are taken as loaded here: reads issued together are waited for once (left to itself the compiler waits for
+// each read before its product and issues the next one after it).
+template <int N>
+__device__ __forceinline__ void together(u32x4 (&f)[N]) {
+#pragma unroll
+  for (int q = 0; q < N; ++q) asm volatile("" : "+v"(f[q]));
+}
+
+// block[32 rows of the tile at base][32 owners], reads in batches of up to 8 fragments
 template <class E, int D>
 __device__ __forceinline__ f32x16 block_of(const TileReads<E, D>& o, uint32_t base, const Owners<E, D>& own) {
+  constexpr int KC = Owners<E, D>::KC, B = KC < 8 ? KC : 8;
   f32x16 s = {};
 #pragma unroll
-  for (int k = 0; k < Owners<E, D>::KC; ++k) s = TileMma<E>::run(TileReads<E, D>::frag(o, base, k), own.v[k], s);
+  for (int k0 = 0; k0 < KC; k0 += B) {
+    u32x4 f[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) f[k] = TileReads<E, D>::frag(o, base, k0 + k);
+    together(f);
+#pragma unroll
+    for (int k = 0; k < B; ++k) s = TileMma<E>::run(f[k], own.v[k0 + k], s);
+  }
   return s;
 }
 
@@ -148,13 +183,20 @@ __device__ __forceinline__ f32x16 block_of(const TileReads<E, D>& o, uint32_t ba
 template <class E, int D>
 __device__ __forceinline__ void add_product(f32x16 (&acc)[D / 32], const f32x16& g, const TileReads<E, D>& o, uint32_t base) {
   if constexpr (sizeof(E) == 2) {
+    constexpr int N = D / 32;
+    u32x4 b[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[kk][e] = pack_bf16(g[8 * kk + 2 * e], g[8 * kk + 2 * e + 1]);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      u32x4 b;
+      u32x4 f[N];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = pack_bf16(g[8 * kk + 2 * e], g[8 * kk + 2 * e + 1]);
+      for (int nb = 0; nb < N; ++nb) f[nb] = TileReads<E, D>::across(o, base, nb, kk);
+      together(f);
 #pragma unroll
-      for (int nb = 0; nb < D / 32; ++nb) acc[nb] = TileMma<E>::run(TileReads<E, D>::across(o, base, nb, kk), b, acc[nb]);
+      for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], b[kk], acc[nb]);
     }
   } else {
 #pragma unroll
@@ -198,32 +240,34 @@ __device__ __forceinline__ float exp_of(float t) {
 // else distance dlast + 63 - word.  Distances below 0 (masked) hold 0, those of at least dlast the last bucket's.
 // A bias of at most -1e30 leaves no weight.
 template <class E, bool ASC>
-__device__ __forceinline__ void fill_bias(const AttnArgs& a, uint32_t lut, uint32_t tmp, int head, int nt) {
-  for (int t = threadIdx.x; t < a.nbounds; t += nt) lds_put<int>(tmp + 4 * t, a.bounds[t]);
-  __syncthreads();
-  for (int t = threadIdx.x; t < a.dlast + 96; t += nt) {
-    const int dist = ASC ? t - 32 : a.dlast + 63 - t;
-    int lo = 0, hi = a.nbounds;   // bounds before the first one that is larger than the distance
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (lds_at<int>(tmp + 4 * mid) <= dist) lo = mid + 1;
-      else hi = mid;
-    }
-    float b = dist < 0 ? 0.0f : a.bias[(int64_t)lo * a.hq + head];
+__device__ __forceinline__ void fill_bias(const AttnArgs& a, uint32_t lut, int head, int nt, int len) {
+  // only distances that a sequence of this length has, up to a block's end, and the one that stands for all far ones
+  const int reach = min(len + 31, a.dlast + 63);
+  for (int u = threadIdx.x; u < reach + 34; u += nt) {
+    const int dist = u == reach + 33 ? a.dlast + 63 : u - 32, t = ASC ? dist + 32 : a.dlast + 63 - dist;
+    int bucket = 0;   // the bounds are the same for all lanes: a comparison each, and no search in memory
+    for (int x = 0; x < a.nbounds; x += 8)
+#pragma unroll
+      for (int y = 0; y < 8; ++y) bucket += a.bounds[x + y] <= dist;   // behind the last one: no distance
+    float b = dist < 0 ? 0.0f : a.bias[(int64_t)bucket * a.hq + head];
     b = b <= -NO_WEIGHT ? -__builtin_huge_valf() : sizeof(E) == 2 ? b * LOG2E : b;
     lds_put<float>(lut + 4 * t, b);
   }
-  __syncthreads();
 }
 __device__ __forceinline__ f32x4 lds_f4(uint32_t off) {   // four words at any word
   typedef f32x4 any __attribute__((aligned(4)));
   return *reinterpret_cast<const __attribute__((address_space(3))) any*>((uintptr_t)off);
 }
 
-// Scores of a block of 32 keys (rows, from j0) x 32 queries (from i0 >= j0), from their products x, in place.
+// The products x of a block of 32 keys (rows, from j0) x 32 queries (from i0 >= j0), made ready: the scores are
+// x mul + add, where `near` blocks have the bias in x already.
+struct Affine {
+  float mul, add;
+};
 template <class E, bool BIAS>
-__device__ __forceinline__ void scores_keys(f32x16& x, float c, int i0, int j0, uint32_t lut, int dlast, float far) {
+__device__ __forceinline__ Affine scores_keys(f32x16& x, float c, int i0, int j0, uint32_t lut, int dlast, float far) {
   const int l = lane_id(), h = l >> 5, r = l & 31;
+  Affine f{c, far};
   if (BIAS && i0 - j0 - 31 < dlast) {
     const uint32_t at = lut + 4 * (dlast + 63 - (i0 - j0 + r - 4 * h));
 #pragma unroll
@@ -232,30 +276,30 @@ __device__ __forceinline__ void scores_keys(f32x16& x, float c, int i0, int j0, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[4 * g + e] = fmaf(x[4 * g + e], c, b[e]);
     }
-  } else {
-#pragma unroll
-    for (int v = 0; v < 16; ++v) x[v] = BIAS ? fmaf(x[v], c, far) : x[v] * c;
+    f.mul = 1.0f;
+    f.add = 0.0f;
   }
   if (j0 == i0) {
 #pragma unroll
     for (int v = 0; v < 16; ++v) x[v] = tile_row(v) + 4 * h > r ? -__builtin_huge_valf() : x[v];
   }
+  return f;
 }
 
+// Of k_attn and k_attn_dq: waves, their queries, and the keys of a tile.
 template <class E, int DH, int NW> struct Shape {
   static constexpr int NT = 64 * NW;
-  static constexpr int T = 32 * NW;                                              // owners of a workgroup
-  static constexpr int TJ = NW == 1 || TileRows<E, DH>::RB > 256 ? 32 : 64;      // streamed rows of a tile (k_attn, k_attn_dq)
-  static constexpr int TQ = NW > 1 && TileRows<E, DH>::RB <= 128 ? 64 : 32;      // (k_attn_dkv)
-  static constexpr int BYTES = TJ * TileRows<E, DH>::RB, QBYTES = TQ * TileRows<E, DH>::RB;
+  static constexpr int T = 32 * NW;
+  static constexpr int TJ = NW == 1 || TileRows<E, DH>::RB > 256 ? 32 : 64;
+  static constexpr int BYTES = TJ * TileRows<E, DH>::RB;
 };
 
 template <class E, int DH, int NW, bool BIAS>
-__global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, 2) void k_attn(AttnArgs a) {
   using S = Shape<E, DH, NW>;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-  const uint32_t lut = lds0 + 4 * S::BYTES, tmp = lut + 4 * (a.dlast + 96);
+  const uint32_t lut = lds0 + 4 * S::BYTES;
   const int es = sizeof(E), cpr = a.d * es / 16;
   const int64_t os = (int64_t)a.hq * a.d * es;
   const int b = blockIdx.x;
@@ -267,8 +311,6 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   const int head = b % a.hq, kvh = head / (a.hq / a.hk);
   const SeqTile st = find_tile(a.offs, a.n_seq, a.n, a.slots - 1 - b / a.hq, S::T);
   if (st.len == 0) return;
-  if constexpr (BIAS) fill_bias<E, false>(a, lut, tmp, head, S::NT);
-  const float far = BIAS ? lds_at<float>(lut) : 0.0f;
   const char* kh = a.k + st.begin * a.ks + (int64_t)kvh * a.d * es;
   const char* vh = a.v + st.begin * a.vs + (int64_t)kvh * a.d * es;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -281,15 +323,19 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   float m = NEG_INF, sum = 0.0f;
   const int nt = (min(st.first + S::T, st.len) + S::TJ - 1) / S::TJ;
   Copy<E, DH, S::NT, S::TJ> ck, cv;
-  ck.fetch(kh, a.ks, 0, st.len, cpr);
-  cv.fetch(vh, a.vs, 0, st.len, cpr);
+  ck.init(a.ks, cpr);
+  cv.init(a.vs, cpr);
+  ck.fetch(kh, a.ks, 0, st.len);
+  cv.fetch(vh, a.vs, 0, st.len);
+  if constexpr (BIAS) fill_bias<E, false>(a, lut, head, S::NT, st.len);
   ck.stash(lds0);
   cv.stash(lds0 + S::BYTES);
   __syncthreads();
+  const float far = BIAS ? lds_at<float>(lut) : 0.0f;
   for (int t = 0; t < nt; ++t) {
     if (t + 1 < nt) {
-      ck.fetch(kh, a.ks, (t + 1) * S::TJ, st.len, cpr);
-      cv.fetch(vh, a.vs, (t + 1) * S::TJ, st.len, cpr);
+      ck.fetch(kh, a.ks, (t + 1) * S::TJ, st.len);
+      cv.fetch(vh, a.vs, (t + 1) * S::TJ, st.len);
     }
     const uint32_t kb = lds0 + (t & 1) * 2 * S::BYTES, vb = kb + S::BYTES;
 #pragma unroll
@@ -297,11 +343,11 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
       const int j0 = t * S::TJ + 32 * jb;
       if (j0 > i0 || i0 >= st.len) continue;
       f32x16 x = block_of<E, DH>(o, kb + jb * 32 * TileRows<E, DH>::RB, q);
-      scores_keys<E, BIAS>(x, a.c, i0, j0, lut, a.dlast, far);
+      const Affine af = scores_keys<E, BIAS>(x, a.c, i0, j0, lut, a.dlast, far);
       float bm = x[0];
 #pragma unroll
       for (int v = 1; v < 16; ++v) bm = fmaxf(bm, x[v]);
-      bm = fmaxf(bm, __shfl_xor(bm, 32));
+      bm = fmaf(fmaxf(bm, __shfl_xor(bm, 32)), af.mul, af.add);
       // the reference follows the maximum in steps: terms stay below 2^8
       if (ballot(bm > m + (sizeof(E) == 2 ? 8.0f : 5.5f))) {
         const float up = fmaxf(m, bm);
@@ -313,12 +359,14 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
           for (int v = 0; v < 16; ++v) acc[nb][v] *= f;
         m = up;
       }
-      const float ref = fmaxf(m, -NO_WEIGHT);
+      const float off = af.add - fmaxf(m, -NO_WEIGHT);
+      float part[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        x[v] = exp_of<E>(x[v] - ref);
-        sum += x[v];
+        x[v] = exp_of<E>(fmaf(x[v], af.mul, off));
+        part[v & 1] += x[v];
       }
+      sum += part[0] + part[1];
       add_product<E, DH>(acc, x, o, vb + jb * 32 * TileRows<E, DH>::RB);
     }
     if (t + 1 < nt) {
@@ -331,6 +379,19 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   sum += __shfl_xor(sum, 32);
   store_rows<E, DH>(a.out + st.begin * os + (int64_t)head * a.d * es, os, i0, st.len, a.d, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
   const int l = lane_id();
+  if (sizeof(E) == 2 && a.low) {
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int nb = 0; nb < DH / 32; ++nb)
+#pragma unroll
+      for (int v = 0; v < 16; v += 2) {
+        const float x = acc[nb][v] * f, y = acc[nb][v + 1] * f;
+        const uint32_t p = pack_bf16(x, y);
+        acc[nb][v] = x - lo_f32(p);
+        acc[nb][v + 1] = y - hi_f32(p);
+      }
+    store_rows<E, DH>(a.low + st.begin * os + (int64_t)head * a.d * es, os, i0, st.len, a.d, acc, 1.0f);
+  }
   if (a.lse && l < 32 && i0 + l < st.len) {
     float2 v = make_float2(NO_WEIGHT, 0.0f);
     if (sum != 0.0f) {
@@ -344,11 +405,11 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
 }
 
 template <class E, int DH, int NW, bool BIAS>
-__global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= 256 ? 2 : 1) void k_attn_dq(AttnArgs a) {
   using S = Shape<E, DH, NW>;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-  const uint32_t lut = lds0 + 4 * S::BYTES, tmp = lut + 4 * (a.dlast + 96);
+  const uint32_t lut = lds0 + 4 * S::BYTES;
   const int es = sizeof(E), cpr = a.d * es / 16;
   const int64_t os = (int64_t)a.hq * a.d * es;
   const int b = blockIdx.x;
@@ -359,8 +420,6 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
   const int head = b % a.hq, kvh = head / (a.hq / a.hk);
   const SeqTile st = find_tile(a.offs, a.n_seq, a.n, a.slots - 1 - b / a.hq, S::T);
   if (st.len == 0) return;
-  if constexpr (BIAS) fill_bias<E, false>(a, lut, tmp, head, S::NT);
-  const float far = BIAS ? lds_at<float>(lut) : 0.0f;
   const int64_t hb = (int64_t)head * a.d * es;
   const char* kh = a.k + st.begin * a.ks + (int64_t)kvh * a.d * es;
   const char* vh = a.v + st.begin * a.vs + (int64_t)kvh * a.d * es;
@@ -372,10 +431,11 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
   const bool live = i0 + (l & 31) < st.len;
   const int64_t row = (int64_t)head * a.n + st.begin + i0 + (l & 31);
   const float2 lse = live ? a.lse[row] : make_float2(NO_WEIGHT, 0.0f);
-  float d0 = 0.0f;   // D by the rounded outputs
-  {
+  float d0 = 0.0f;   // D by the outputs
+#pragma unroll 1
+  for (int part = 0; part < (int)(4 / sizeof(E)); ++part) {
     Owners<E, DH> ov;
-    ov.load(a.out + st.begin * os + hb, os, i0, st.len, cpr);
+    ov.load((part ? a.low : a.out) + st.begin * os + hb, os, i0, st.len, cpr);
 #pragma unroll
     for (int k = 0; k < Owners<E, DH>::KC; ++k)
 #pragma unroll
@@ -387,23 +447,27 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
           d0 = fmaf(__uint_as_float(ov.v[k][e]), __uint_as_float(go.v[k][e]), d0);
         }
       }
-    d0 += __shfl_xor(d0, 32);
   }
+  d0 += __shfl_xor(d0, 32);
   TileReads<E, DH> o;
   o.init();
   f32x16 acc[DH / 32] = {};
   float rest = 0.0f;
   const int nt = (min(st.first + S::T, st.len) + S::TJ - 1) / S::TJ;
   Copy<E, DH, S::NT, S::TJ> ck, cv;
-  ck.fetch(kh, a.ks, 0, st.len, cpr);
-  cv.fetch(vh, a.vs, 0, st.len, cpr);
+  ck.init(a.ks, cpr);
+  cv.init(a.vs, cpr);
+  ck.fetch(kh, a.ks, 0, st.len);
+  cv.fetch(vh, a.vs, 0, st.len);
+  if constexpr (BIAS) fill_bias<E, false>(a, lut, head, S::NT, st.len);
   ck.stash(lds0);
   cv.stash(lds0 + S::BYTES);
   __syncthreads();
+  const float far = BIAS ? lds_at<float>(lut) : 0.0f;
   for (int t = 0; t < nt; ++t) {
     if (t + 1 < nt) {
-      ck.fetch(kh, a.ks, (t + 1) * S::TJ, st.len, cpr);
-      cv.fetch(vh, a.vs, (t + 1) * S::TJ, st.len, cpr);
+      ck.fetch(kh, a.ks, (t + 1) * S::TJ, st.len);
+      cv.fetch(vh, a.vs, (t + 1) * S::TJ, st.len);
     }
     const uint32_t kb = lds0 + (t & 1) * 2 * S::BYTES, vb = kb + S::BYTES;
 #pragma unroll
@@ -413,12 +477,17 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
       const uint32_t at = jb * 32 * TileRows<E, DH>::RB;
       f32x16 x = block_of<E, DH>(o, kb + at, q);
       const f32x16 dp = block_of<E, DH>(o, vb + at, go);
-      scores_keys<E, BIAS>(x, a.c, i0, j0, lut, a.dlast, far);
+      const Affine af = scores_keys<E, BIAS>(x, a.c, i0, j0, lut, a.dlast, far);
+      const float off = sizeof(E) == 2 ? (af.add - lse.x) - lse.y : af.add - lse.x;   // (bf16: off by 2^-24 of it)
+      float part[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        x[v] = exp_of<E>((x[v] - lse.x) - lse.y) * (dp[v] - d0);
-        rest += x[v];
+        float s = fmaf(x[v], af.mul, off);
+        if (sizeof(E) == 4) s -= lse.y;
+        x[v] = exp_of<E>(s) * (dp[v] - d0);
+        part[v & 1] += x[v];
       }
+      rest += part[0] + part[1];
       add_product<E, DH>(acc, x, o, kb + at);
     }
     if (t + 1 < nt) {
@@ -433,129 +502,150 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(AttnArgs a) {
   if (l < 32 && live) a.delta[row] = d0 + rest;
 }
 
-template <class E, int DH, int NW, bool BIAS>
-__global__ __launch_bounds__(64 * NW) void k_attn_dkv(AttnArgs a) {
-  using S = Shape<E, DH, NW>;
-  constexpr int TQ = S::TQ, RB = TileRows<E, DH>::RB;
+constexpr int SKEW = 64 * 33 * 4;   // bytes of a block by distance
+
+// One workgroup for 32 keys and a key head.  Its IW waves deal the group's (head, 32 queries) pairs among themselves, each
+// with LDS of its own and no barrier on the way, and add up what they have at the end.
+template <class E, int DH, int IW, bool BIAS>
+__global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn_dkv(AttnArgs a) {
+  constexpr int NT = 64 * IW, RB = TileRows<E, DH>::RB, BYTES = 32 * RB;
+  constexpr bool REST = BIAS || sizeof(E) == 4;   // what the log-sum-exp's rounding left counts (dbias, float32)
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-  const uint32_t par0 = lds0 + 4 * S::QBYTES;          // [2][3][TQ] log-sum-exp, its rest, D
-  const uint32_t lut = par0 + 2 * 3 * TQ * 4, tmp = lut + 4 * (a.dlast + 96);
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
+  const uint32_t qb = lds0 + w * 2 * BYTES, gb = qb + BYTES;
+  const uint32_t par = lds0 + IW * 2 * BYTES + w * 3 * 128;      // [3][32] log-sum-exp, its rest, D
   const int words = a.dlast + 96;
-  const uint32_t hist0 = tmp + 4 * a.nbounds;          // [NW][words] sums of ds by distance
+  const uint32_t lut = lds0 + IW * (2 * BYTES + 3 * 128), hist0 = lut + 4 * words;
+  const uint32_t hist = hist0 + 4 * words * w;   // [IW][words] sums of ds by distance
+  const uint32_t skew = hist0 + 4 * words * IW + w * SKEW;                    // [IW] blocks by distance
   const int es = sizeof(E), cpr = a.d * es / 16, group = a.hq / a.hk;
   const int64_t os = (int64_t)a.hq * a.d * es;
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x;
   if (b >= a.slots * a.hk) {
     const int which = b - a.slots * a.hk;
-    clean_rows(a, which, S::NT, a.dk, a.dks, a.hk * a.d * es);
-    clean_rows(a, which, S::NT, a.dv, a.dvs, a.hk * a.d * es);
+    clean_rows(a, which, NT, a.dk, a.dks, a.hk * a.d * es);
+    clean_rows(a, which, NT, a.dv, a.dvs, a.hk * a.d * es);
     return;
   }
   const int kvh = b % a.hk, slot = b / a.hk, nbk = a.nbounds + 1;
-  const SeqTile st = find_tile(a.offs, a.n_seq, a.n, slot, S::T);
+  const SeqTile st = find_tile(a.offs, a.n_seq, a.n, slot, 32);
   if (st.len == 0) {
     if constexpr (BIAS)
-      for (int t = tid; t < nbk * group; t += S::NT)
+      for (int t = tid; t < nbk * group; t += NT)
         a.part[((int64_t)slot * nbk + t / group) * a.hq + kvh * group + t % group] = 0.0f;
     return;
   }
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
-  const int j0 = st.first + 32 * w;
+  const int j0 = st.first, t0 = j0 / 32, t1 = (st.len + 31) / 32;   // tiles of queries
   Owners<E, DH> kk, vv;
   kk.load(a.k + st.begin * a.ks + (int64_t)kvh * a.d * es, a.ks, j0, st.len, cpr);
   vv.load(a.v + st.begin * a.vs + (int64_t)kvh * a.d * es, a.vs, j0, st.len, cpr);
   TileReads<E, DH> o;
   o.init();
   f32x16 dk[DH / 32] = {}, dv[DH / 32] = {};
-  const int t0 = st.first / TQ, t1 = (st.len + TQ - 1) / TQ;   // tiles of queries
-  Copy<E, DH, S::NT, TQ> cq, cg;
+  Copy<E, DH, 64, 32> cq, cg;
+  cq.init(a.qs, cpr);
+  cg.init(os, cpr);
   float2 nl = make_float2(0.0f, 0.0f);
   float nd = 0.0f;
   auto fetch = [&](int head, int t) {
     const int64_t hb = (int64_t)head * a.d * es;
-    cq.fetch(a.q + st.begin * a.qs + hb, a.qs, t * TQ, st.len, cpr);
-    cg.fetch(a.dout + st.begin * os + hb, os, t * TQ, st.len, cpr);
-    if (tid < TQ) {
-      const int i = t * TQ + tid;
-      const int64_t row = (int64_t)head * a.n + st.begin + i;
-      nl = i < st.len ? a.lse[row] : make_float2(NO_WEIGHT, 0.0f);
-      nd = i < st.len ? a.delta[row] : 0.0f;
+    cq.fetch(a.q + st.begin * a.qs + hb, a.qs, t * 32, st.len);
+    cg.fetch(a.dout + st.begin * os + hb, os, t * 32, st.len);
+    const int i = t * 32 + r;
+    const int64_t row = (int64_t)head * a.n + st.begin + i;
+    nl = make_float2(NO_WEIGHT, 0.0f);
+    nd = 0.0f;
+    if (i < st.len) {
+      nl = a.lse[row];
+      nd = a.delta[row];
     }
   };
-  auto stash = [&](int buf) {
-    cq.stash(lds0 + buf * 2 * S::QBYTES);
-    cg.stash(lds0 + buf * 2 * S::QBYTES + S::QBYTES);
-    if (tid < TQ) {
-      const uint32_t p = par0 + buf * 3 * TQ * 4 + 4 * tid;
-      lds_put<float>(p, nl.x);
-      lds_put<float>(p + TQ * 4, nl.y);
-      lds_put<float>(p + 2 * TQ * 4, nd);
-    }
-  };
-  int buf = 0;
+  fetch(kvh * group, min(t0 + w, t1 - 1));
+  if constexpr (BIAS)
+    for (int t = l; t < SKEW / 4; t += 64) lds_put<float>(skew + 4 * t, 0.0f);
   for (int hh = 0; hh < group; ++hh) {
     const int head = kvh * group + hh;
     float far = 0.0f, farsum = 0.0f;
     if constexpr (BIAS) {
+      if (hh > 0) __syncthreads();
+      fill_bias<E, true>(a, lut, head, NT, st.len);
+      for (int t = l; t < words; t += 64) lds_put<float>(hist + 4 * t, 0.0f);
       __syncthreads();
-      fill_bias<E, true>(a, lut, tmp, head, S::NT);
       far = lds_at<float>(lut + 4 * (words - 1));
-      for (int t = tid; t < NW * words; t += S::NT) lds_put<float>(hist0 + 4 * t, 0.0f);
     }
-    const uint32_t hist = hist0 + 4 * words * w;
-    if (hh == 0) {
-      fetch(head, t0);
-      stash(0);
-    }
-    __syncthreads();
-    for (int t = t0; t < t1; ++t) {
-      const bool more = t + 1 < t1 || hh + 1 < group;
-      if (more) fetch(t + 1 < t1 ? head : head + 1, t + 1 < t1 ? t + 1 : t0);
-      const uint32_t qb = lds0 + buf * 2 * S::QBYTES, gb = qb + S::QBYTES, par = par0 + buf * 3 * TQ * 4;
+    for (int t = t0 + w; t < t1; t += IW) {
+      wave_sync();
+      cq.stash(qb);
+      cg.stash(gb);
+      const int i0 = t * 32;
+      const bool near = BIAS && i0 - j0 - 31 < a.dlast;
+      if (h == 0) {
+        lds_put<float>(par + 4 * r, nl.x);
+        if (REST) lds_put<float>(par + 128 + 4 * r, near ? nl.y : nl.y - far);
+        lds_put<float>(par + 256 + 4 * r, nd);
+      }
+      wave_sync();
+      if (t + IW < t1) fetch(head, t + IW);
+      else if (hh + 1 < group) fetch(head + 1, min(t0 + w, t1 - 1));
+      f32x16 x = block_of<E, DH>(o, qb, kk);
+      f32x16 dp = block_of<E, DH>(o, gb, vv);
+      const uint32_t la = lut + 4 * (i0 - j0 - r + 4 * h + 32), pa = par + 16 * h;
+      __builtin_amdgcn_sched_barrier(0);
+      if (i0 == j0) {
 #pragma unroll
-      for (int ib = 0; ib < TQ / 32; ++ib) {
-        const int i0 = t * TQ + 32 * ib;
-        if (i0 < j0 || j0 >= st.len) continue;
-        f32x16 x = block_of<E, DH>(o, qb + ib * 32 * RB, kk);
-        f32x16 dp = block_of<E, DH>(o, gb + ib * 32 * RB, vv);
-        const bool near = BIAS && i0 - j0 - 31 < a.dlast;
-        const uint32_t la = lut + 4 * (i0 - j0 - r + 4 * h + 32), pa = par + 4 * (32 * ib + 4 * h);
+        for (int v = 0; v < 16; ++v) x[v] = tile_row(v) + 4 * h < r ? NEG_INF : x[v];
+      }
+      if (near) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 lh = lds_at<f32x4>(pa + 32 * g), ll = lds_at<f32x4>(pa + TQ * 4 + 32 * g),
-                      dd = lds_at<f32x4>(pa + 2 * TQ * 4 + 32 * g);
-          f32x4 bias = {far, far, far, far};
-          if (near) bias = lds_f4(la + 32 * g);
+          const f32x4 bias = lds_f4(la + 32 * g), lh = lds_at<f32x4>(pa + 32 * g);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int v = 4 * g + e;
-            float s = BIAS ? fmaf(x[v], a.c, bias[e]) : x[v] * a.c;
-            if (i0 == j0) s = tile_row(v) + 4 * h < r ? NEG_INF : s;
-            x[v] = exp_of<E>((s - lh[e]) - ll[e]);
-            dp[v] = x[v] * (dp[v] - dd[e]);
-          }
+          for (int e = 0; e < 4; ++e) x[4 * g + e] = fmaf(x[4 * g + e], a.c, bias[e]) - lh[e];
         }
-        add_product<E, DH>(dv, x, o, gb + ib * 32 * RB);
-        add_product<E, DH>(dk, dp, o, qb + ib * 32 * RB);
-        if constexpr (BIAS) {
-          if (near) {
-            const uint32_t ha = hist + 4 * (i0 - j0 - r + 4 * h + 32);
+      } else {
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-              __builtin_amdgcn_ds_faddf((__attribute__((address_space(3))) float*)(uintptr_t)(ha + 4 * tile_row(v)), dp[v], 0, 0,
-                                        false);
-          } else {
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 lh = lds_at<f32x4>(pa + 32 * g);
 #pragma unroll
-            for (int v = 0; v < 16; ++v) farsum += dp[v];
-          }
+          for (int e = 0; e < 4; ++e) x[4 * g + e] = fmaf(x[4 * g + e], a.c, -lh[e]);
         }
       }
-      if (more) {
-        stash(buf ^ 1);
-        __syncthreads();
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 ll = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (REST) ll = lds_at<f32x4>(pa + 128 + 32 * g);
+        const f32x4 dd = lds_at<f32x4>(pa + 256 + 32 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 4 * g + e;
+          x[v] = exp_of<E>(REST ? x[v] - ll[e] : x[v]);
+          dp[v] = x[v] * (dp[v] - dd[e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      buf ^= 1;
+      add_product<E, DH>(dv, x, o, gb);
+      __builtin_amdgcn_sched_barrier(0);
+      add_product<E, DH>(dk, dp, o, qb);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (BIAS) {
+        if (near) {
+          // ds of query i and key j to word i of row i - j + 31 (33 words a row: lanes meet in no bank), what no pair has
+          // stays 0; then lane x adds up row x
+          const uint32_t at = skew + 4 * (33 * (4 * h - r + 31) + 4 * h);
+#pragma unroll
+          for (int v = 0; v < 16; ++v) lds_put<float>(at + 4 * 34 * tile_row(v), dp[v]);
+          wave_sync();
+          const uint32_t ha = hist + 4 * (i0 - j0 + 1 + l), ra = skew + 4 * 33 * l;
+          float s[4] = {lds_at<float>(ha), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int x = 0; x < 32; ++x) s[x & 3] += lds_at<float>(ra + 4 * x);
+          lds_put<float>(ha, (s[0] + s[1]) + (s[2] + s[3]));
+        } else {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) farsum += dp[v];
+        }
+      }
     }
     if constexpr (BIAS) {
       farsum = wave_sumf(farsum);
@@ -564,20 +654,15 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(AttnArgs a) {
         lds_put<float>(p, lds_at<float>(p) + farsum);
       }
       __syncthreads();
-      for (int t = tid; t < words; t += S::NT) {
-        float s = 0.0f;
-#pragma unroll
-        for (int q = 0; q < NW; ++q) s += lds_at<float>(hist0 + 4 * (q * words + t));
-        lds_put<float>(hist0 + 4 * t, s);
-      }
-      __syncthreads();
       // eight lanes to a bucket
-      for (int t = tid; t < ((nbk * 8 + S::NT - 1) & ~(S::NT - 1)); t += S::NT) {
+      for (int t = tid; t < ((nbk * 8 + NT - 1) & ~(NT - 1)); t += NT) {
         const int bk = t >> 3;
         float s = 0.0f;
         if (bk < nbk) {
           const int from = bk == 0 ? 0 : a.bounds[bk - 1], to = bk == a.nbounds ? words - 32 : a.bounds[bk];
-          for (int x = from + (t & 7); x < to; x += 8) s += lds_at<float>(hist0 + 4 * (x + 32));
+          for (int x = from + (t & 7); x < to; x += 8)
+#pragma unroll
+            for (int q = 0; q < IW; ++q) s += lds_at<float>(hist0 + 4 * (q * words + x + 32));
         }
 #pragma unroll
         for (int q = 4; q >= 1; q >>= 1) s += __shfl_xor(s, q);
@@ -585,8 +670,43 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(AttnArgs a) {
       }
     }
   }
-  store_rows<E, DH>(a.dk + st.begin * a.dks + (int64_t)kvh * a.d * es, a.dks, j0, st.len, a.d, dk, a.scale);
-  store_rows<E, DH>(a.dv + st.begin * a.dvs + (int64_t)kvh * a.d * es, a.dvs, j0, st.len, a.d, dv, 1.0f);
+  if constexpr (IW == 1) {
+    store_rows<E, DH>(a.dk + st.begin * a.dks + (int64_t)kvh * a.d * es, a.dks, j0, st.len, a.d, dk, a.scale);
+    store_rows<E, DH>(a.dv + st.begin * a.dvs + (int64_t)kvh * a.d * es, a.dvs, j0, st.len, a.d, dv, 1.0f);
+  } else {
+    // [IW][32][DH] float32 through the tiles' LDS, 16-byte piece c of row q at c ^ (q & 7)
+    auto join = [&](const f32x16 (&acc)[DH / 32], char* out, int64_t stride, float f) {
+      __syncthreads();
+#pragma unroll
+      for (int nb = 0; nb < DH / 32; ++nb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          lds_put(lds0 + (w * 32 + r) * DH * 4 + (((8 * nb + 2 * g + h) ^ (r & 7)) << 4),
+                  f32x4{acc[nb][4 * g], acc[nb][4 * g + 1], acc[nb][4 * g + 2], acc[nb][4 * g + 3]});
+      __syncthreads();
+      constexpr int EPC = 16 / sizeof(E);          // elements of a 16-byte piece of the result
+      for (int t = tid; t < 32 * (DH / EPC); t += NT) {
+        const int row = t / (DH / EPC), c = t % (DH / EPC);
+        if (j0 + row >= st.len || c >= cpr) continue;
+        float y[EPC];
+#pragma unroll
+        for (int p = 0; p < EPC / 4; ++p) {
+          f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int q = 0; q < IW; ++q)
+            s += lds_at<f32x4>(lds0 + (q * 32 + row) * DH * 4 + (((c * (EPC / 4) + p) ^ (row & 7)) << 4));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[4 * p + e] = s[e] * f;
+        }
+        u32x4 o4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o4[e] = sizeof(E) == 2 ? pack_bf16(y[(2 * e) % EPC], y[(2 * e + 1) % EPC]) : __float_as_uint(y[e]);
+        *reinterpret_cast<u32x4*>(out + (j0 + row) * stride + c * 16) = o4;
+      }
+    };
+    join(dk, a.dk + st.begin * a.dks + (int64_t)kvh * a.d * es, a.dks, a.scale);
+    join(dv, a.dv + st.begin * a.dvs + (int64_t)kvh * a.d * es, a.dvs, 1.0f);
+  }
 }
 
 // ------------------------------------------------------------------ the last token of every sequence
@@ -611,7 +731,7 @@ struct LastArgs {
 // of a block (up to 32), so keys and values are read once.  Every wave goes over blocks of 32 keys by itself, with LDS of
 // its own; the four are joined at the end, and the parts of a sequence by k_last_join.
 template <class E, int DH, bool BIAS>
-__global__ __launch_bounds__(256) void k_last(LastArgs a) {
+__global__ __launch_bounds__(256, 2) void k_last(LastArgs a) {
   constexpr int RB = TileRows<E, DH>::RB, BYTES = 32 * RB, P = DH + 4;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -801,9 +921,22 @@ __global__ __launch_bounds__(256) void k_last_join(LastArgs a) {
   }
 }
 
-constexpr int ATTN_WAVES = 4;
-
 int slots_of(int64_t n, int64_t n_seq, int T) { return (int)(n / T + n_seq); }
+
+// Waves of a workgroup of k_attn and k_attn_dq: four that share the tiles, or one by itself where a sequence has few more
+// tokens than one wave's 32.  Measured (bf16, both kernels): 2,000 x 20 tokens, 4 heads of 64: 84 us with one wave, 154 with
+// four; 200 x 200: 92 and 82; 16 x 1,021, 8 heads: 194 and 152.
+int query_waves(const rece_attention_config& c) { return c.n <= 64 * c.n_seq ? 1 : 4; }
+
+// Waves of a workgroup of k_attn_dkv: more of them deal one tile's queries among themselves where there are too few tiles
+// of keys to fill the card (two waves per SIMD, 2,048) and enough queries to deal.  Measured (bf16, with 1, 2, 4 waves):
+// 4,000 tokens, 4 heads on 1: 575, 333, 168 us; 16 x 1,021, 8 heads on 2: 333, 207, 176; 200 x 200, 4 heads: 72, 90, 130.
+int key_waves(const rece_attention_config& c) {
+  const int64_t tasks = (c.n / 32 + c.n_seq) * c.kv_heads, items = c.heads / c.kv_heads * (c.n / c.n_seq) / 64;
+  const int most = tasks <= 1536 ? 4 : tasks <= 3072 ? 2 : 1;
+  return items >= 4 ? most : items >= 2 ? std::min(most, 2) : 1;
+}
+
 
 // A launch with dynamic LDS (beyond 64 KB it has to be allowed first).
 template <class A>
@@ -850,21 +983,22 @@ AttnArgs common_args(const rece_attention_config& c, const void* q, const void* 
   a.c = c.dtype == RECE_BF16 ? (float)((double)c.scale * 1.4426950408889634074) : c.scale;
   a.nbounds = bias ? c.n_bounds : 0;
   a.dlast = a.nbounds ? c.bounds[a.nbounds - 1] : 0;
-  for (int t = 0; t < a.nbounds; ++t) a.bounds[t] = c.bounds[t];
+  for (int t = 0; t <= RECE_MAX_BOUNDS; ++t) a.bounds[t] = t < a.nbounds ? c.bounds[t] : INT32_MAX;
   return a;
 }
 
-// Workspace: log-sum-exp [hq][n] float2, D [hq][n], partial bias gradients.
+// Workspace: log-sum-exp [hq][n] float2, D [hq][n], bf16: what the outputs' rounding left, partial bias gradients.
 struct AttnSpace {
-  size_t lse, delta, part, total;
+  size_t lse, delta, low, part, total;
 };
 AttnSpace attn_space(const rece_attention_config& c) {
   AttnSpace s{};
   const size_t rows = (size_t)c.heads * c.n;
-  const size_t slots = (size_t)(c.n / 32 + c.n_seq);   // of the smallest workgroups
   s.lse = 0;
   s.delta = (rows * 8 + 15) & ~(size_t)15;
-  s.part = (s.delta + rows * 4 + 15) & ~(size_t)15;
+  s.low = (s.delta + rows * 4 + 15) & ~(size_t)15;
+  s.part = s.low + (c.dtype == RECE_BF16 ? rows * c.d * 2 : 0);
+  const size_t slots = (size_t)slots_of(c.n, c.n_seq, 32);
   s.total = s.part + slots * (c.n_bounds + 1) * c.heads * 4;
   return s;
 }
@@ -878,14 +1012,18 @@ hipError_t attention_forward(const rece_attention_config& c, const void* q, cons
   AttnArgs a = common_args(c, q, k, v, offs, bias);
   a.out = static_cast<char*>(out);
   a.lse = static_cast<float2*>(ws);
+  a.low = ws && c.dtype == RECE_BF16 ? static_cast<char*>(ws) + attn_space(c).low : nullptr;
   return attn_shape(c.dtype == RECE_BF16, c.d, bias != nullptr, [&](auto e, auto dh, auto bb) {
-    using E = decltype(e);
-    constexpr int DH = decltype(dh)::value, NW = ATTN_WAVES;
-    constexpr bool B = decltype(bb)::value;
-    using S = Shape<E, DH, NW>;
-    a.slots = slots_of(c.n, c.n_seq, S::T);
-    const size_t lds = 4 * S::BYTES + (B ? 4 * (a.dlast + 96 + a.nbounds) : 0);
-    return launch(k_attn<E, DH, NW, B>, (int64_t)a.slots * a.hq + CLEAN, S::NT, lds, st, a);
+    const auto run = [&](auto nw) {
+      using E = decltype(e);
+      constexpr int DH = decltype(dh)::value, NW = decltype(nw)::value;
+      constexpr bool B = decltype(bb)::value;
+      using S = Shape<E, DH, NW>;
+      a.slots = slots_of(c.n, c.n_seq, S::T);
+      const size_t lds = 4 * S::BYTES + (B ? 4 * (a.dlast + 96) : 0);
+      return launch(k_attn<E, DH, NW, B>, (int64_t)a.slots * a.hq + CLEAN, S::NT, lds, st, a);
+    };
+    return query_waves(c) == 1 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, 4>());
   });
 }
 
@@ -907,18 +1045,34 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
   a.dqs = strides[0] * es;
   a.dks = strides[1] * es;
   a.dvs = strides[2] * es;
+  a.low = static_cast<char*>(ws) + sp.low;
+  const int words = a.dlast + 96;
   hipError_t r = attn_shape(c.dtype == RECE_BF16, c.d, bias != nullptr, [&](auto e, auto dh, auto bb) {
     using E = decltype(e);
-    constexpr int DH = decltype(dh)::value, NW = ATTN_WAVES;
+    constexpr int DH = decltype(dh)::value;
     constexpr bool B = decltype(bb)::value;
-    using S = Shape<E, DH, NW>;
-    a.slots = slots_of(c.n, c.n_seq, S::T);
-    const int words = a.dlast + 96;
-    const size_t lds = 4 * S::BYTES + (B ? 4 * (words + a.nbounds) : 0);
-    const hipError_t e1 = launch(k_attn_dq<E, DH, NW, B>, (int64_t)a.slots * a.hq + CLEAN, S::NT, lds, st, a);
+    const auto dq_run = [&](auto nw) {
+      constexpr int NW = decltype(nw)::value;
+      using S = Shape<E, DH, NW>;
+      a.slots = slots_of(c.n, c.n_seq, S::T);
+      const size_t lds = 4 * S::BYTES + (B ? 4 * words : 0);
+      return launch(k_attn_dq<E, DH, NW, B>, (int64_t)a.slots * a.hq + CLEAN, S::NT, lds, st, a);
+    };
+    const hipError_t e1 =
+        query_waves(c) == 1 ? dq_run(std::integral_constant<int, 1>()) : dq_run(std::integral_constant<int, 4>());
     if (e1 != hipSuccess) return e1;
-    const size_t lds2 = 4 * S::QBYTES + 24 * S::TQ + (B ? 4 * (words + a.nbounds + NW * words) : 0);
-    return launch(k_attn_dkv<E, DH, NW, B>, (int64_t)a.slots * a.hk + CLEAN, S::NT, lds2, st, a);
+    const auto lds_of = [&](int iw) {
+      return (size_t)(iw * (2 * 32 * TileRows<E, DH>::RB + 3 * 128) + (B ? 4 * (words + iw * words) + iw * SKEW : 0));
+    };
+    int waves = key_waves(c);
+    while (waves > 1 && lds_of(waves) > MAX_LDS) waves /= 2;
+    a.slots = slots_of(c.n, c.n_seq, 32);
+    const auto dkv_run = [&](auto iw) {
+      constexpr int IW = decltype(iw)::value;
+      return launch(k_attn_dkv<E, DH, IW, B>, (int64_t)a.slots * a.hk + CLEAN, 64 * IW, lds_of(IW), st, a);
+    };
+    return waves == 1 ? dkv_run(std::integral_constant<int, 1>())
+                      : waves == 2 ? dkv_run(std::integral_constant<int, 2>()) : dkv_run(std::integral_constant<int, 4>());
   });
   if (r != hipSuccess || !bias) return r;
   return launch_join_rows(a.part, a.slots, (a.nbounds + 1) * a.hq, dbias, st);

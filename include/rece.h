@@ -373,8 +373,8 @@ rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream
  *   t_ij = scale q_ih . k_jg + bias[bucket(i - j)][h],   p_ij = softmax over j,   out_ih = sum_j p_ij v_jg
  *   bucket(t) = how many of the bounds are <= t
  *   q [n] rows of heads x d elements, k and v [n] rows of kv_heads x d, dtype; a row's elements are
- *   contiguous, rows begin q_stride, k_stride, v_stride elements apart (multiples of 8: slices of one
- *   projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads.
+ *   contiguous, rows begin q_stride, k_stride, v_stride elements apart (multiples of 8, at most 2^23: slices
+ *   of one projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads.
  *   offsets [n_seq + 1] int32 non-decreasing (values outside [0, n] are clamped; a sequence may be empty)
  *   bias [n_bounds + 1][heads] float32, or NULL: none.  bounds: distances >= 1, increasing, at most
  *   RECE_MAX_DISTANCE.  An entry of at most -1e30 leaves its pairs no weight; a row that

@@ -115,3 +115,16 @@ def test_last_tokens(hq, hk, d, lens, max_len, n_buckets, dtype):
     worst = close(out, last_reference(q, kv[:, 0], kv[:, 1], begin, length, op, bias))
     print(f"  out: {worst:.3f} of its bound")
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,hq,hk,d", [
+    ([20] * 40, 2, 2, 64),             # a wave for a sequence
+    ([64] * 3 + [70], 2, 2, 32),       # four waves; keys: one
+    ([160], 1, 1, 64),                 # keys: two waves
+    ([300, 200], 4, 1, 128),           # keys: four waves
+    ([300, 200], 4, 1, 64),
+])
+def test_every_split_of_the_work(lens, hq, hk, d, dtype):
+    check(lens, hq, hk, d, dtype, n_buckets=16)
+    check(lens, hq, hk, d, dtype)
