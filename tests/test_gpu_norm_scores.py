@@ -86,3 +86,22 @@ def test_scores(s, C, d, dtype):
     want = (x8.double() @ y8.double().T) * sx.double()[:, None] * sy.double()
     # the sum to float32, two products, the result
     near(out, want, (HALF[DT[dtype]] + 3 * U) * want.abs())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("s,C,d,shift", [
+    (33, 1, 32, 0), (40, 63, 64, 1), (130, 64, 64, 0), (257, 65, 96, 3), (64, 127, 128, 2), (100, 1000, 256, 5),
+    (129, 20001, 64, 7), (70, 30004, 112, 4), (2000, 997, 160, 1), (300, 4100, 272, 1),
+])
+def test_scores_at_any_address(s, C, d, shift, dtype):
+    """Rows of results that begin anywhere in a line of memory; what lies around them stays."""
+    print(f"[gpu] scores s={s} C={C} d={d} shift={shift} {dtype}", flush=True)
+    g = torch.Generator().manual_seed(s + C + d)
+    x8, y8 = (torch.randint(-128, 128, (n, d), generator=g, dtype=torch.int8) for n in (s, C))
+    sx, sy = (torch.rand(n, generator=g) * 0.02 for n in (s, C))
+    room = torch.full((s * C + shift + 256,), 7.0, dtype=DT[dtype], device="cuda")
+    out = room[shift:shift + s * C].view(s, C)
+    assert rece.Int8Scores(s, C, d, dtype=dtype).forward(x8.cuda(), sx.cuda(), y8.cuda(), sy.cuda(), out=out) is out
+    want = (x8.double() @ y8.double().T) * sx.double()[:, None] * sy.double()
+    near(out, want, (HALF[DT[dtype]] + 3 * U) * want.abs())
+    assert (room[:shift] == 7.0).all() and (room[shift + s * C:] == 7.0).all()
