@@ -34,6 +34,7 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NO_WEIGHT = 1e30f;     // log-sum-exp of a row without weight: exp(t - 1e30) = 0
 constexpr size_t MAX_LDS = 160 * 1024; // of a workgroup
+constexpr int LAST_SPLITS = 256;       // parts of a sequence at most
 constexpr int CLEAN = 64;              // workgroups that clear rows of no sequence
 
 struct AttnArgs {
@@ -54,6 +55,7 @@ struct AttnArgs {
   float* part;                // [slots][n_bounds + 1][hq] partial bias gradients
   int64_t n;
   int n_seq, d, hq, hk, slots;
+  int hp;                     // k_attn_dkv: heads whose tables of the bias are in LDS at a time
   float scale, c;             // c: the factor of a product, with log2(e) for bf16
   int nbounds, dlast;         // dlast: from this distance on there is one bucket
   int32_t bounds[RECE_MAX_BOUNDS + 1];
@@ -502,10 +504,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= 256 ? 2 : 1) void k_attn
   if (l < 32 && live) a.delta[row] = d0 + rest;
 }
 
-constexpr int SKEW = 64 * 33 * 4;   // bytes of a block by distance
+constexpr int SKEW = 63 * 33 * 4;   // bytes of a block by distance
 
 // One workgroup for 32 keys and a key head.  Its IW waves deal the group's (head, 32 queries) pairs among themselves, each
-// with LDS of its own and no barrier on the way, and add up what they have at the end.
+// with LDS of its own and no barrier on the way, and add up what they have at the end.  Where the tables of the bias of
+// all heads of a group and its gradients do not fit in LDS, they take `hp` heads at a time.
 template <class E, int DH, int IW, bool BIAS>
 __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn_dkv(AttnArgs a) {
   constexpr int NT = 64 * IW, RB = TileRows<E, DH>::RB, BYTES = 32 * RB;
@@ -515,10 +518,11 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id(), h = l >> 5, r = l & 31;
   const uint32_t qb = lds0 + w * 2 * BYTES, gb = qb + BYTES;
   const uint32_t par = lds0 + IW * 2 * BYTES + w * 3 * 128;      // [3][32] log-sum-exp, its rest, D
-  const int words = a.dlast + 96;
-  const uint32_t lut = lds0 + IW * (2 * BYTES + 3 * 128), hist0 = lut + 4 * words;
-  const uint32_t hist = hist0 + 4 * words * w;   // [IW][words] sums of ds by distance
-  const uint32_t skew = hist0 + 4 * words * IW + w * SKEW;                    // [IW] blocks by distance
+  const int words = a.dlast + 96, hw = a.dlast + 34;
+  const uint32_t lut0 = lds0 + IW * (2 * BYTES + 3 * 128);       // [hp][words] bias by distance
+  const uint32_t hist0 = lut0 + 4 * words * a.hp;                // [IW][hp][hw] sums of ds by distance (word - 32), the last
+                                                                 // word: of at least dlast
+  const uint32_t skew = hist0 + 4 * hw * a.hp * IW + w * SKEW;   // [IW] blocks by distance
   const int es = sizeof(E), cpr = a.d * es / 16, group = a.hq / a.hk;
   const int64_t os = (int64_t)a.hq * a.d * es;
   const int b = blockIdx.x;
@@ -536,7 +540,7 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
         a.part[((int64_t)slot * nbk + t / group) * a.hq + kvh * group + t % group] = 0.0f;
     return;
   }
-  const int j0 = st.first, t0 = j0 / 32, t1 = (st.len + 31) / 32;   // tiles of queries
+  const int j0 = st.first, t0 = j0 / 32, nt = (st.len + 31) / 32 - t0;   // tiles of queries from t0 on
   Owners<E, DH> kk, vv;
   kk.load(a.k + st.begin * a.ks + (int64_t)kvh * a.d * es, a.ks, j0, st.len, cpr);
   vv.load(a.v + st.begin * a.vs + (int64_t)kvh * a.d * es, a.vs, j0, st.len, cpr);
@@ -561,24 +565,40 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
       nd = a.delta[row];
     }
   };
-  fetch(kvh * group, min(t0 + w, t1 - 1));
   if constexpr (BIAS)
     for (int t = l; t < SKEW / 4; t += 64) lds_put<float>(skew + 4 * t, 0.0f);
-  for (int hh = 0; hh < group; ++hh) {
-    const int head = kvh * group + hh;
-    float far = 0.0f, farsum = 0.0f;
+  for (int h0 = 0; h0 < group; h0 += a.hp) {
+    const int nh = min(a.hp, group - h0), head0 = kvh * group + h0;
+    int hh = w / nt, t = w - hh * nt;      // the wave's pair: a head of these, a tile
+    if (hh < nh) fetch(head0 + hh, t0 + t);
     if constexpr (BIAS) {
-      if (hh > 0) __syncthreads();
-      fill_bias<E, true>(a, lut, head, NT, st.len);
-      for (int t = l; t < words; t += 64) lds_put<float>(hist + 4 * t, 0.0f);
+      if (h0 > 0) __syncthreads();
+      for (int x = 0; x < nh; ++x) fill_bias<E, true>(a, lut0 + 4 * words * x, head0 + x, NT, st.len);
+      for (int x = l; x < nh * hw; x += 64) lds_put<float>(hist0 + 4 * (w * a.hp * hw + x), 0.0f);
       __syncthreads();
-      far = lds_at<float>(lut + 4 * (words - 1));
     }
-    for (int t = t0 + w; t < t1; t += IW) {
+    float far = 0.0f, farsum = 0.0f;       // of the head at hand: its far distances' bias, and their sum of ds
+    int at_head = -1;
+    uint32_t lut = lut0, hist = hist0;
+    auto leave_head = [&]() {
+      farsum = wave_sumf(farsum);
+      if (l == 0 && at_head >= 0) lds_put<float>(hist + 4 * (hw - 1), farsum);
+      farsum = 0.0f;
+    };
+    while (hh < nh) {
+      if constexpr (BIAS) {
+        if (hh != at_head) {
+          leave_head();
+          at_head = hh;
+          lut = lut0 + 4 * words * hh;
+          hist = hist0 + 4 * (w * a.hp + hh) * hw;
+          far = lds_at<float>(lut + 4 * (words - 1));
+        }
+      }
       wave_sync();
       cq.stash(qb);
       cg.stash(gb);
-      const int i0 = t * 32;
+      const int i0 = (t0 + t) * 32;
       const bool near = BIAS && i0 - j0 - 31 < a.dlast;
       if (h == 0) {
         lds_put<float>(par + 4 * r, nl.x);
@@ -586,8 +606,12 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
         lds_put<float>(par + 256 + 4 * r, nd);
       }
       wave_sync();
-      if (t + IW < t1) fetch(head, t + IW);
-      else if (hh + 1 < group) fetch(head + 1, min(t0 + w, t1 - 1));
+      t += IW;
+      while (t >= nt && hh < nh) {
+        t -= nt;
+        ++hh;
+      }
+      if (hh < nh) fetch(head0 + hh, t0 + t);
       f32x16 x = block_of<E, DH>(o, qb, kk);
       f32x16 dp = block_of<E, DH>(o, gb, vv);
       const uint32_t la = lut + 4 * (i0 - j0 - r + 4 * h + 32), pa = par + 16 * h;
@@ -636,37 +660,44 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
 #pragma unroll
           for (int v = 0; v < 16; ++v) lds_put<float>(at + 4 * 34 * tile_row(v), dp[v]);
           wave_sync();
-          const uint32_t ha = hist + 4 * (i0 - j0 + 1 + l), ra = skew + 4 * 33 * l;
-          float s[4] = {lds_at<float>(ha), 0.0f, 0.0f, 0.0f};
+          const uint32_t ha = hist + 4 * (i0 - j0 + 1 + l), ra = skew + 4 * 33 * min(l, 62);
+          const bool in = i0 - j0 - 31 + l < a.dlast;
+          float s[4] = {in ? lds_at<float>(ha) : farsum, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int x = 0; x < 32; ++x) s[x & 3] += lds_at<float>(ra + 4 * x);
-          lds_put<float>(ha, (s[0] + s[1]) + (s[2] + s[3]));
+          for (int y = 0; y < 32; ++y) s[y & 3] += lds_at<float>(ra + 4 * y);
+          const float all = (s[0] + s[1]) + (s[2] + s[3]);
+          if (l < 63) {
+            if (in) lds_put<float>(ha, all);
+            else farsum = all;
+          }
         } else {
+          float s[2] = {0.0f, 0.0f};
 #pragma unroll
-          for (int v = 0; v < 16; ++v) farsum += dp[v];
+          for (int v = 0; v < 16; ++v) s[v & 1] += dp[v];
+          farsum += s[0] + s[1];
         }
       }
     }
     if constexpr (BIAS) {
-      farsum = wave_sumf(farsum);
-      if (l == 0) {   // distances of at least dlast that no block listed
-        const uint32_t p = hist + 4 * (words - 1);
-        lds_put<float>(p, lds_at<float>(p) + farsum);
-      }
+      leave_head();
       __syncthreads();
-      // eight lanes to a bucket
-      for (int t = tid; t < ((nbk * 8 + NT - 1) & ~(NT - 1)); t += NT) {
-        const int bk = t >> 3;
+      // eight lanes to a bucket of a head
+      for (int x = tid; x < ((nh * nbk * 8 + NT - 1) & ~(NT - 1)); x += NT) {
+        const int k = x >> 3, hd = k / nbk, bk = k - hd * nbk;
         float s = 0.0f;
-        if (bk < nbk) {
-          const int from = bk == 0 ? 0 : a.bounds[bk - 1], to = bk == a.nbounds ? words - 32 : a.bounds[bk];
-          for (int x = from + (t & 7); x < to; x += 8)
+        if (hd < nh) {
+          const uint32_t from = hist0 + 4 * hd * hw;
+          if (bk == a.nbounds) {
+            if ((x & 7) < IW) s = lds_at<float>(from + 4 * ((x & 7) * a.hp * hw + hw - 1));
+          } else {
+            for (int y = (bk == 0 ? 0 : a.bounds[bk - 1]) + (x & 7); y < a.bounds[bk]; y += 8)
 #pragma unroll
-            for (int q = 0; q < IW; ++q) s += lds_at<float>(hist0 + 4 * (q * words + x + 32));
+              for (int q = 0; q < IW; ++q) s += lds_at<float>(from + 4 * (q * a.hp * hw + y + 32));
+          }
         }
 #pragma unroll
         for (int q = 4; q >= 1; q >>= 1) s += __shfl_xor(s, q);
-        if (bk < nbk && (t & 7) == 0) a.part[((int64_t)slot * nbk + bk) * a.hq + head] = s;
+        if (hd < nh && (x & 7) == 0) a.part[((int64_t)slot * nbk + bk) * a.hq + head0 + hd] = s;
       }
     }
   }
@@ -719,7 +750,7 @@ struct LastArgs {
   const int32_t* begin;       // [n_seq]
   const int32_t* length;      // [n_seq]
   const float* bias;
-  float* part;                // [n_seq][hq][splits][d + 2]: sums of p v, then the reference and the sum of p
+  float* part;                // [n_seq][hq][splits][d] sums of p v, then [n_seq][hq][2][splits]: reference, sum of p
   int64_t rows;
   int n_seq, d, hq, hk, splits;
   float c;
@@ -873,45 +904,47 @@ __global__ __launch_bounds__(256, 2) void k_last(LastArgs a) {
       else
         reinterpret_cast<float*>(a.out)[row * a.d + e] = y;
     } else {
-      float* p = a.part + (row * a.splits + split) * (a.d + 2);
-      p[e] = val;
+      a.part[(row * a.splits + split) * a.d + e] = val;
       if (e == 0) {
-        p[a.d] = top;
-        p[a.d + 1] = all;
+        float* p = a.part + ((int64_t)a.n_seq * a.hq * a.d + row * 2) * a.splits + split;
+        p[0] = top;
+        p[a.splits] = all;
       }
     }
   }
 }
 
-// A workgroup joins the parts of one head of one sequence: d columns x 256 / d (or fewer) slices of the parts.
+// A workgroup joins the parts of one head of one sequence: d columns x 1024 / d (or fewer) slices of the parts, whose
+// factors are formed first.
 template <class E>
-__global__ __launch_bounds__(256) void k_last_join(LastArgs a) {
-  __shared__ float sv[256], sw[256], sm[4];
-  const int tid = threadIdx.x, slices = 256 / a.d, e = tid % a.d, sl = tid / a.d, W = a.d + 2;
-  const float* p = a.part + (int64_t)blockIdx.x * a.splits * W;
-  float top = -NO_WEIGHT;
-  for (int s = tid; s < a.splits; s += 256) top = fmaxf(top, p[(int64_t)s * W + a.d]);
-  top = wave_max(top);
-  if (lane_id() == 0) sm[tid >> 6] = top;
+__global__ __launch_bounds__(1024) void k_last_join(LastArgs a) {
+  __shared__ float sv[1024], f[LAST_SPLITS], red[16];
+  const int tid = threadIdx.x, slices = 1024 / a.d, e = tid % a.d, sl = tid / a.d;
+  const float* p = a.part + (int64_t)blockIdx.x * a.splits * a.d;
+  const float* stat = a.part + ((int64_t)a.n_seq * a.hq * a.d + (int64_t)blockIdx.x * 2) * a.splits;
+  const float mine = tid < a.splits ? stat[tid] : -NO_WEIGHT, part = tid < a.splits ? stat[a.splits + tid] : 0.0f;
+  float top = wave_max(mine);
+  if (lane_id() == 0) red[tid >> 6] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float val = 0.0f, all = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) top = fmaxf(top, red[q]);
+  const float w = exp_of<E>(mine - top);
+  if (tid < a.splits) f[tid] = w;
+  const float some = wave_sumf(w * part);
+  __syncthreads();
+  if (lane_id() == 0) red[tid >> 6] = some;
+  float val = 0.0f;
   if (sl < slices) {
-#pragma unroll 4
-    for (int s = sl; s < a.splits; s += slices) {
-      const float f = exp_of<E>(p[(int64_t)s * W + a.d] - top);
-      val = fmaf(f, p[(int64_t)s * W + e], val);
-      all = fmaf(f, p[(int64_t)s * W + a.d + 1], all);
-    }
+#pragma unroll 8
+    for (int s = sl; s < a.splits; s += slices) val = fmaf(f[s], p[(int64_t)s * a.d + e], val);
   }
   sv[tid] = val;
-  sw[tid] = all;
   __syncthreads();
   if (tid < a.d) {
-    for (int s = 1; s < slices; ++s) {
-      val += sv[s * a.d + e];
-      all += sw[s * a.d + e];
-    }
+    for (int s = 1; s < slices; ++s) val += sv[s * a.d + e];
+    float all = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) all += red[q];
     const float y = all == 0.0f ? 0.0f : val / all;
     const int64_t at = (int64_t)blockIdx.x * a.d + e;
     if constexpr (sizeof(E) == 2)
@@ -1061,15 +1094,20 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
     const hipError_t e1 =
         query_waves(c) == 1 ? dq_run(std::integral_constant<int, 1>()) : dq_run(std::integral_constant<int, 4>());
     if (e1 != hipSuccess) return e1;
-    const auto lds_of = [&](int iw) {
-      return (size_t)(iw * (2 * 32 * TileRows<E, DH>::RB + 3 * 128) + (B ? 4 * (words + iw * words) + iw * SKEW : 0));
+    // as few waves as the tiles leave room for, as many heads' tables as then fit
+    const int group = a.hq / a.hk;
+    const auto lds_of = [&](int iw, int hp) {
+      return (size_t)(iw * (2 * 32 * TileRows<E, DH>::RB + 3 * 128) + (B ? 4 * hp * (words + iw * (a.dlast + 34)) + iw * SKEW : 0));
     };
     int waves = key_waves(c);
-    while (waves > 1 && lds_of(waves) > MAX_LDS) waves /= 2;
+    while (waves > 1 && lds_of(waves, 1) > MAX_LDS) waves /= 2;
+    // (more heads than this would cost the second workgroup of a CU)
+    a.hp = 1;
+    while (a.hp < group && lds_of(waves, a.hp + 1) <= std::max<size_t>(MAX_LDS / 2, lds_of(waves, 1))) ++a.hp;
     a.slots = slots_of(c.n, c.n_seq, 32);
     const auto dkv_run = [&](auto iw) {
       constexpr int IW = decltype(iw)::value;
-      return launch(k_attn_dkv<E, DH, IW, B>, (int64_t)a.slots * a.hk + CLEAN, 64 * IW, lds_of(IW), st, a);
+      return launch(k_attn_dkv<E, DH, IW, B>, (int64_t)a.slots * a.hk + CLEAN, 64 * IW, lds_of(IW, a.hp), st, a);
     };
     return waves == 1 ? dkv_run(std::integral_constant<int, 1>())
                       : waves == 2 ? dkv_run(std::integral_constant<int, 2>()) : dkv_run(std::integral_constant<int, 4>());
@@ -1078,10 +1116,12 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
   return launch_join_rows(a.part, a.slots, (a.nbounds + 1) * a.hq, dbias, st);
 }
 
-// Parts of a sequence's keys: enough workgroups for two per CU, each wave with two blocks of 32 keys at least.
+// Parts of a sequence's keys: enough workgroups for two per CU, each wave with four blocks of 32 keys at least, and none
+// below 1,024 keys (the join is another launch).
 int64_t last_splits(const rece_attention_config& c, int64_t max_len) {
-  const int64_t wgs = c.n_seq * c.kv_heads, want = (512 + wgs - 1) / wgs, most = (max_len + 255) / 256;
-  return std::max<int64_t>(1, std::min<int64_t>({want, most, 512}));
+  if (max_len <= 1024) return 1;
+  const int64_t wgs = c.n_seq * c.kv_heads, want = (512 + wgs - 1) / wgs, most = (max_len + 511) / 512;
+  return std::max<int64_t>(1, std::min<int64_t>({want, most, LAST_SPLITS}));
 }
 
 size_t last_attention_workspace_bytes(const rece_attention_config& c, int64_t max_len) {
@@ -1122,7 +1162,7 @@ hipError_t last_attention(const rece_attention_config& c, int64_t max_len, const
     const size_t lds = std::max<size_t>(8 * 32 * TileRows<E, DH>::RB, 16 * (a.hq / a.hk) * (DH + 4)) + (B ? a.dlast + 1 : 0);
     const hipError_t r = launch(k_last<E, DH, B>, c.n_seq * a.hk * a.splits, 256, lds, st, a);
     if (r != hipSuccess || a.splits == 1) return r;
-    k_last_join<E><<<(unsigned)(c.n_seq * a.hq), 256, 0, st>>>(a);
+    k_last_join<E><<<(unsigned)(c.n_seq * a.hq), 1024, 0, st>>>(a);
     return hipGetLastError();
   });
 }

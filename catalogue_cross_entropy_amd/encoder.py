@@ -70,13 +70,14 @@ class _Attention:
 
     def _heads(self, name, t, rows, heads, device=None):
         """Check rows of heads (a slice of a wider projection will do); returns the stride of its rows."""
-        if (t.dtype is not self._dt or t.shape != (rows, heads, self.d) or not t.is_cuda or t.stride(2) != 1
-                or (heads > 1 and t.stride(1) != self.d)):
-            raise ValueError(f"{name} must be a CUDA {self._dt} tensor of shape {(rows, heads, self.d)} whose rows are "
+        d, at = self.d, t.stride()
+        if (t.dtype is not self._dt or t.shape != (rows, heads, d) or not t.is_cuda or at[2] != 1
+                or (heads > 1 and at[1] != d)):
+            raise ValueError(f"{name} must be a CUDA {self._dt} tensor of shape {(rows, heads, d)} whose rows are "
                              "contiguous")
         if device is not None and t.device != device:
             raise ValueError(f"{name} must be on {device}")
-        return t.stride(0) if rows > 1 else heads * self.d
+        return at[0] if rows > 1 else heads * d
 
     def _bias(self, bias, device):
         import torch
@@ -115,7 +116,7 @@ class SequenceAttention(_Attention):
             return _on_stream(stream, dev, self.forward, q, k, v, offsets, bias, out, workspace, need_grad)
         c = self._check_inputs(q, k, v, offsets, bias)
         if out is None:
-            out = torch.empty((self.n, self.heads, self.d), dtype=self._dt, device=dev)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _want("out", out, self._dt, (self.n, self.heads, self.d), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev) if need_grad else None
@@ -135,10 +136,11 @@ class SequenceAttention(_Attention):
         _want("out", out, self._dt, shape, dev)
         _want("dout", dout, self._dt, shape, dev)
         grads = []
-        for name, t, heads in (("dq", dq, self.heads), ("dk", dk, self.kv_heads), ("dv", dv, self.kv_heads)):
+        for name, t, like, heads in (("dq", dq, q, self.heads), ("dk", dk, k, self.kv_heads), ("dv", dv, v, self.kv_heads)):
             if t is None:
-                t = torch.empty((self.n, heads, self.d), dtype=self._dt, device=dev)
-            grads.append((t, self._heads(name, t, self.n, heads, dev)))
+                grads.append((torch.empty_like(like, memory_format=torch.contiguous_format), heads * self.d))
+            else:
+                grads.append((t, self._heads(name, t, self.n, heads, dev)))
         dbias = None if bias is None else torch.empty_like(bias)
         ws = _workspace(workspace, self.workspace_bytes, dev)
         (dq, sq), (dk, sk), (dv, sv) = grads
@@ -173,7 +175,7 @@ class LastAttention(_Attention):
         _want("length", length, torch.int32, (self.n_seq,), dev)
         self._bias(bias, dev)
         if out is None:
-            out = torch.empty((self.n_seq, self.heads, self.d), dtype=self._dt, device=dev)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _want("out", out, self._dt, (self.n_seq, self.heads, self.d), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev) if self.workspace_bytes else None
@@ -216,7 +218,7 @@ class ResidualNorm:
         if _elsewhere(stream, dev):
             return _on_stream(stream, dev, self.forward, x, residual, weight, h)
         h = self._check_inputs(x, residual, weight, h)
-        y = torch.empty((self.n, self.d), dtype=self._dt, device=dev)
+        y = torch.empty_like(x)
         rstd = torch.empty(self.n, dtype=torch.float32, device=dev)
         _call(lib().rece_norm_forward, dev, (),
               (self.n, self.d, self._code, self.eps, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(rstd)))
@@ -229,7 +231,7 @@ class ResidualNorm:
         if _elsewhere(stream, dev):
             return _on_stream(stream, dev, self.forward_int8, x, residual, weight, h)
         h = self._check_inputs(x, residual, weight, h)
-        y8 = torch.empty((self.n, self.d), dtype=torch.int8, device=dev)
+        y8 = torch.empty_like(x, dtype=torch.int8)
         scale = torch.empty(self.n, dtype=torch.float32, device=dev)
         _call(lib().rece_norm_forward_int8, dev, (),
               (self.n, self.d, self._code, self.eps, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y8), _ptr(scale)))
@@ -249,8 +251,7 @@ class ResidualNorm:
         _want("weight", weight, torch.float32, (self.d,), dev)
         _want("rstd", rstd, torch.float32, (self.n,), dev)
         ws = _workspace(workspace, self.workspace_bytes, dev)
-        dx = torch.empty(shape, dtype=self._dt, device=dev)
-        dw = torch.empty(self.d, dtype=torch.float32, device=dev)
+        dx, dw = torch.empty_like(dy), torch.empty_like(weight)
         _call(lib().rece_norm_backward, dev, (),
               (self.n, self.d, self._code, _ptr(dy), _ptr(h), _ptr(dh), _ptr(weight), _ptr(rstd), _ptr(ws),
                ws.numel() * ws.element_size(), _ptr(dx), _ptr(dw)))
@@ -267,7 +268,7 @@ def quantize_rows(x, stream=None):
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
     _want("x", x, dt, x.shape)
-    x8 = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    x8 = torch.empty_like(x, dtype=torch.int8)
     scale = torch.empty(x.shape[0], dtype=torch.float32, device=dev)
     _call(lib().rece_quantize_rows, dev, (), (x.shape[0], x.shape[1], code, _ptr(x), _ptr(x8), _ptr(scale)))
     return x8, scale
