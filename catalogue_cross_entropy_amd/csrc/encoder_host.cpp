@@ -55,11 +55,11 @@ rece_status check_attention(const rece_attention_config* c) {
   return RECE_OK;
 }
 
-// sizes of a packed call (a cache may have more rows than a grid has workgroups)
+// sizes of a packed call: a grid holds less than 2^32 lanes, 2^24 workgroups of 256
 rece_status check_packed(const rece_attention_config* c) {
   const rece_status v = check_attention(c);
   if (v != RECE_OK) return v;
-  if ((c->n / 32 + c->n_seq) * c->heads > I32_MAX - 1024) return unsupported("(n / 32 + n_seq) * heads must fit in int32");
+  if ((c->n / 32 + c->n_seq) * c->heads > (1 << 24) - 1024) return unsupported("(n / 32 + n_seq) * heads must be below 2^24 - 1024");
   return RECE_OK;
 }
 
@@ -214,7 +214,8 @@ rece_status rece_quantize_rows(void* stream, int64_t n, int32_t d, int32_t dtype
 rece_status rece_int8_scores(void* stream, int64_t s, int64_t C, int32_t d, int32_t dtype, const int8_t* x8,
                              const float* sx, const int8_t* y8, const float* sy, void* out) {
   if (s < 0 || C < 1 || d < 1) return invalid("s must be >= 0, C and d >= 1");
-  if (s > I32_MAX || C > I32_MAX || int8_tiles(s, C) > I32_MAX) return unsupported("s, C and their tiles must fit in int32");
+  if (s > I32_MAX || C > I32_MAX) return unsupported("s and C must fit in int32");
+  if (d > 256 && int8_tiles(s, C) >= 1 << 24) return unsupported("more than 2^24 tiles of 128 x 128 scores with d beyond 256");
   if (d % 16 != 0 || d > 8192) return unsupported("d must be a multiple of 16, at most 8192");
   if (bad_dtype(dtype)) return unsupported("dtype must be RECE_F32 or RECE_BF16");
   if (s == 0) return RECE_OK;

@@ -15,8 +15,10 @@
 // from floor(o_u / T) + u on.  That number grows by at least ceil(length / T) from one sequence to the next, so
 // the slots are distinct, floor(n / T) + n_seq of them are enough, and no list of tiles is made.
 //
-// Scores and sums are float32.  bf16: scores carry the factor log2(e), p and ds are rounded to bf16 for the second
-// products alone.  float32: scores stay in natural units and their difference to the maximum is scaled.
+// Scores and sums are float32.  bf16: scores carry the factor log2(e); p and ds enter the second products rounded to
+// bf16, whose errors add up like those of independent roundings and stay below the results' own (out, dk and dv are off
+// by 1.3 to 1.45 times the rounding of an exact result), and for dq, where the error of D comes on top, ds as two bf16
+// terms (1.06 times; one term: 1.55).  float32: scores stay in natural units and their difference to the maximum is scaled.
 // D comes from the outputs with what their rounding left (k_attn keeps it; from the rounded outputs alone dq would be off
 // by 1.4 times as much).  The rounding of p in the outputs is still in it and would be the bias gradient's error:
 // k_attn_dq adds the sum of p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
@@ -181,8 +183,9 @@ __device__ __forceinline__ f32x16 block_of(const TileReads<E, D>& o, uint32_t ba
   return s;
 }
 
-// acc[nb][32 coordinates][32 owners] += rows^T[coordinates][32 rows] g[32 rows][32 owners]
-template <class E, int D>
+// acc[nb][32 coordinates][32 owners] += rows^T[coordinates][32 rows] g[32 rows][32 owners].  bf16: g rounded to bf16,
+// or (TERMS 2) that and the rounding of what it left: off by 2^-16 of g.
+template <class E, int D, int TERMS = 1>
 __device__ __forceinline__ void add_product(f32x16 (&acc)[D / 32], const f32x16& g, const TileReads<E, D>& o, uint32_t base) {
   if constexpr (sizeof(E) == 2) {
     constexpr int N = D / 32;
@@ -199,6 +202,14 @@ __device__ __forceinline__ void add_product(f32x16 (&acc)[D / 32], const f32x16&
       together(f);
 #pragma unroll
       for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], b[kk], acc[nb]);
+      if constexpr (TERMS == 2) {
+        u32x4 rest;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          rest[e] = pack_bf16(g[8 * kk + 2 * e] - lo_f32(b[kk][e]), g[8 * kk + 2 * e + 1] - hi_f32(b[kk][e]));
+#pragma unroll
+        for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], rest, acc[nb]);
+      }
     }
   } else {
 #pragma unroll
@@ -407,7 +418,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn(AttnArgs a) {
 }
 
 template <class E, int DH, int NW, bool BIAS>
-__global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= 256 ? 2 : 1) void k_attn_dq(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= (NW == 1 ? 128 : 256) ? 2 : 1) void k_attn_dq(AttnArgs a) {
   using S = Shape<E, DH, NW>;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -490,7 +501,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= 256 ? 2 : 1) void k_attn
         part[v & 1] += x[v];
       }
       rest += part[0] + part[1];
-      add_product<E, DH>(acc, x, o, kb + at);
+      add_product<E, DH, 2>(acc, x, o, kb + at);
     }
     if (t + 1 < nt) {
       const uint32_t nb = lds0 + ((t + 1) & 1) * 2 * S::BYTES;

@@ -198,7 +198,7 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm(NormArgs a) {
             *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + r * d + 8 * at) = make_uint2(q[0], q[1]);
           }
         }
-        if (lane == 0) a.rstd[r] = ok ? (float)(m * (double)rstd / 127.0) : __builtin_nanf("");
+        if (lane == 0) a.rstd[r] = !ok ? __builtin_nanf("") : m > 0.0 ? (float)(m * (double)rstd / 127.0) : 0.0f;
       }
       if (LPR == 256) __syncthreads();
     }

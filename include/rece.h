@@ -374,7 +374,8 @@ rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream
  *   bucket(t) = how many of the bounds are <= t
  *   q [n] rows of heads x d elements, k and v [n] rows of kv_heads x d, dtype; a row's elements are
  *   contiguous, rows begin q_stride, k_stride, v_stride elements apart (multiples of 8, at most 2^23: slices
- *   of one projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads.
+ *   of one projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads;
+ *   (n / 32 + n_seq) heads below 2^24 - 1024.
  *   offsets [n_seq + 1] int32 non-decreasing (values outside [0, n] are clamped; a sequence may be empty)
  *   bias [n_bounds + 1][heads] float32, or NULL: none.  bounds: distances >= 1, increasing, at most
  *   RECE_MAX_DISTANCE.  An entry of at most -1e30 leaves its pairs no weight; a row that
@@ -389,7 +390,7 @@ rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream
  *   dbias[b][h] = sum of ds_ij over the pairs of bucket b (NULL with bias NULL)
  *   dout [n][heads][d]; dq, dk, dv dtype, rows dq_stride, dk_stride, dv_stride elements apart; dbias float32
  * Sums are float32 (dbias: float32 within a workgroup, float64 over them).  Of dtype bf16, p and ds enter their
- * products with the gradients and values rounded to bf16. */
+ * products with the gradients and values rounded to bf16 (ds in dq to 2^-16 of it). */
 #define RECE_MAX_BOUNDS 127
 #define RECE_MAX_DISTANCE 4096
 typedef struct {

@@ -119,3 +119,8 @@ def int8_rows(t):
     """(values, scale) of float64 rows: ties to even."""
     m = t.abs().amax(1, keepdim=True)
     return torch.where(m > 0, (127.0 * t / torch.where(m > 0, m, 1.0)).round(), 0.0).to(torch.int8), m[:, 0] / 127.0
+
+
+def moved(tensors):
+    """Tensors (or None) on the GPU."""
+    return tuple(t if t is None else t.cuda() for t in tensors)
