@@ -160,8 +160,8 @@ template <class E, int D> struct Owners {
 
 // The values are taken as loaded here: reads issued together are waited for once (left to itself the compiler waits for
 // each read before its product and issues the next one after it).
-template <int N>
-__device__ __forceinline__ void together(u32x4 (&f)[N]) {
+template <class V, int N>
+__device__ __forceinline__ void together(V (&f)[N]) {
 #pragma unroll
   for (int q = 0; q < N; ++q) asm volatile("" : "+v"(f[q]));
 }
@@ -212,11 +212,20 @@ __device__ __forceinline__ void add_product(f32x16 (&acc)[D / 32], const f32x16&
       }
     }
   } else {
+    constexpr int N = D / 32;
 #pragma unroll
-    for (int v = 0; v < 16; ++v)
+    for (int q = 0; q < 4; ++q) {
+      float f[4 * N];
 #pragma unroll
-      for (int nb = 0; nb < D / 32; ++nb)
-        acc[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(TileReads<E, D>::across1(o, base, nb, v), g[v], acc[nb], 0, 0, 0);
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int nb = 0; nb < N; ++nb) f[e * N + nb] = TileReads<E, D>::across1(o, base, nb, 4 * q + e);
+      together(f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int nb = 0; nb < N; ++nb) acc[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(f[e * N + nb], g[4 * q + e], acc[nb], 0, 0, 0);
+    }
   }
 }
 
@@ -308,7 +317,7 @@ template <class E, int DH, int NW> struct Shape {
 };
 
 template <class E, int DH, int NW, bool BIAS>
-__global__ __launch_bounds__(64 * NW, 2) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 1 && sizeof(E) * DH > 256 ? 1 : 2) void k_attn(AttnArgs a) {
   using S = Shape<E, DH, NW>;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -523,6 +532,7 @@ constexpr int SKEW = 63 * 33 * 4;   // bytes of a block by distance
 template <class E, int DH, int IW, bool BIAS>
 __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn_dkv(AttnArgs a) {
   constexpr int NT = 64 * IW, RB = TileRows<E, DH>::RB, BYTES = 32 * RB;
+  constexpr bool AHEAD = RB <= 256;               // rows on the way during the work (wider ones do not fit in registers)
   constexpr bool REST = BIAS || sizeof(E) == 4;   // what the log-sum-exp's rounding left counts (dbias, float32)
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -581,7 +591,7 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
   for (int h0 = 0; h0 < group; h0 += a.hp) {
     const int nh = min(a.hp, group - h0), head0 = kvh * group + h0;
     int hh = w / nt, t = w - hh * nt;      // the wave's pair: a head of these, a tile
-    if (hh < nh) fetch(head0 + hh, t0 + t);
+    if (AHEAD && hh < nh) fetch(head0 + hh, t0 + t);
     if constexpr (BIAS) {
       if (h0 > 0) __syncthreads();
       for (int x = 0; x < nh; ++x) fill_bias<E, true>(a, lut0 + 4 * words * x, head0 + x, NT, st.len);
@@ -606,6 +616,7 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
           far = lds_at<float>(lut + 4 * (words - 1));
         }
       }
+      if (!AHEAD) fetch(head0 + hh, t0 + t);
       wave_sync();
       cq.stash(qb);
       cg.stash(gb);
@@ -622,7 +633,7 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn
         t -= nt;
         ++hh;
       }
-      if (hh < nh) fetch(head0 + hh, t0 + t);
+      if (AHEAD && hh < nh) fetch(head0 + hh, t0 + t);
       f32x16 x = block_of<E, DH>(o, qb, kk);
       f32x16 dp = block_of<E, DH>(o, gb, vv);
       const uint32_t la = lut + 4 * (i0 - j0 - r + 4 * h + 32), pa = par + 16 * h;
@@ -769,7 +780,7 @@ struct LastArgs {
 // of a block (up to 32), so keys and values are read once.  Every wave goes over blocks of 32 keys by itself, with LDS of
 // its own; the four are joined at the end, and the parts of a sequence by k_last_join.
 template <class E, int DH, bool BIAS>
-__global__ __launch_bounds__(256, 2) void k_last(LastArgs a) {
+__global__ __launch_bounds__(256, sizeof(E) * DH > 256 ? 1 : 2) void k_last(LastArgs a) {
   constexpr int RB = TileRows<E, DH>::RB, BYTES = 32 * RB, P = DH + 4;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
