@@ -18,7 +18,7 @@
 // Scores and sums are float32.  bf16: scores carry the factor log2(e); p and ds enter the second products rounded to
 // bf16, whose errors add up like those of independent roundings and stay below the results' own (out, dk and dv are off
 // by 1.3 to 1.45 times the rounding of an exact result), and for dq, where the error of D comes on top, ds as two bf16
-// terms (1.06 times; one term: 1.55).  float32: scores stay in natural units and their difference to the maximum is scaled.
+// terms (1.1 times; one term: 1.55), as k_last's p, where they cost nothing.  float32: scores stay in natural units and their difference to the maximum is scaled.
 // D comes from the outputs with what their rounding left (k_attn keeps it; from the rounded outputs alone dq would be off
 // by 1.4 times as much).  The rounding of p in the outputs is still in it and would be the bias gradient's error:
 // k_attn_dq adds the sum of p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
@@ -880,7 +880,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DH > 256 ? 1 : 2) void k_last(Last
       x[v] = exp_of<E>(x[v] - ref);
       sum += x[v];
     }
-    add_product<E, DH>(acc, x, o, vb);
+    add_product<E, DH, 2>(acc, x, o, vb);   // (the cache's rows bound it, not the products)
   }
   sum += __shfl_xor(sum, 32);
   // the four waves: [4][group][P] of LDS, elements, then reference and sum
