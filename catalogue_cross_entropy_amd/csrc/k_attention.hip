@@ -18,10 +18,24 @@
 // Scores and sums are float32.  bf16: scores carry the factor log2(e); p and ds enter the second products rounded to
 // bf16, whose errors add up like those of independent roundings and stay below the results' own (out, dk and dv are off
 // by 1.3 to 1.45 times the rounding of an exact result), and for dq, where the error of D comes on top, ds as two bf16
-// terms (1.1 times; one term: 1.55), as k_last's p, where they cost nothing.  float32: scores stay in natural units and their difference to the maximum is scaled.
+// terms (1.1 times; one term: 1.55), as k_last's p, where they cost
+// nothing.  float32: scores stay in natural units and their difference to the maximum is scaled.
 // D comes from the outputs with what their rounding left (k_attn keeps it; from the rounded outputs alone dq would be off
 // by 1.4 times as much).  The rounding of p in the outputs is still in it and would be the bias gradient's error:
 // k_attn_dq adds the sum of p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
+// What bounds it: the time of one block in one wave, a chain of LDS reads, products and exponentials that two to four waves
+// per SIMD hide in part (two for k_attn_dkv at 64 wide: dk, dv, the keys' and values' rows and the next tile are 192
+// registers); with few long sequences the longest one's last tile.  Vector units are busy 20 to 38 %, matrix units 2 to
+// 14 % at 32 and 64 wide (float32 40 to 49 %) and 18 to 35 % at 128.  Measured (bf16 unless said; k_attn, k_attn_dq, k_attn_dkv in us):
+//   256 x 150 tokens, 2 heads of 32, bias, gradients           17, 24, 39 (34 MB of rows, 3.5 GFLOP: startup and latencies)
+//   200 x 200, 4 heads of 64, bias, gradients                  36, 47, 72
+//   2,000 x 20, 4 heads of 64, bias, gradients                 44, 54, 70 (a wave for a sequence)
+//   16 x 1,021, 8 heads on 2 of 64, bias, gradients            70, 95, 169 (80 GFLOP, 240 TFLOP/s); float32 329, 464, 780
+//   8 x 2,000, 8 heads of 128, gradients                       167, 240, 436 (306 GFLOP, 360 TFLOP/s)
+//   3 x 2,731, 16 heads on 4 of 128, forward                   167 (122 GFLOP, 740 TFLOP/s)
+// k_last is bound by the cache's rows where there are many, by its chain of launches and loads where there are few:
+//   2,048 x 500, 4 heads of 64, bias  197 us (1.05 GB at 5.3 TB/s);  1 x 65,536, 8 heads on 2 of 128  18 us and the join 5
+//   (67 MB; 2.9 TB/s in all);  5 x 200, 2 heads of 32  7 us
 #include <algorithm>
 #include <cmath>
 
@@ -975,8 +989,8 @@ __global__ __launch_bounds__(1024) void k_last_join(LastArgs a) {
 int slots_of(int64_t n, int64_t n_seq, int T) { return (int)(n / T + n_seq); }
 
 // Waves of a workgroup of k_attn and k_attn_dq: four that share the tiles, or one by itself where a sequence has few more
-// tokens than one wave's 32.  Measured (bf16, both kernels): 2,000 x 20 tokens, 4 heads of 64: 84 us with one wave, 154 with
-// four; 200 x 200: 92 and 82; 16 x 1,021, 8 heads: 194 and 152.
+// tokens than one wave's 32.  Measured (bf16, both kernels, one wave and four): 2,000 x 20 tokens, 4 heads of 64: 84 and
+// 154 us; 200 x 200: 92 and 82; 16 x 1,021, 8 heads: 194 and 152.
 int query_waves(const rece_attention_config& c) { return c.n <= 64 * c.n_seq ? 1 : 4; }
 
 // Waves of a workgroup of k_attn_dkv: more of them deal one tile's queries among themselves where there are too few tiles
@@ -984,7 +998,7 @@ int query_waves(const rece_attention_config& c) { return c.n <= 64 * c.n_seq ? 1
 // 4,000 tokens, 4 heads on 1: 575, 333, 168 us; 16 x 1,021, 8 heads on 2: 333, 207, 176; 200 x 200, 4 heads: 72, 90, 130.
 int key_waves(const rece_attention_config& c) {
   const int64_t tasks = (c.n / 32 + c.n_seq) * c.kv_heads, items = c.heads / c.kv_heads * (c.n / c.n_seq) / 64;
-  const int most = tasks <= 1536 ? 4 : tasks <= 3072 ? 2 : 1;
+  const int most = tasks <= 1536 ? 4 : tasks <= 3000 ? 2 : 1;
   return items >= 4 ? most : items >= 2 ? std::min(most, 2) : 1;
 }
 
