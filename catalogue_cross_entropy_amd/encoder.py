@@ -6,6 +6,11 @@ their scores.
 
 Argument marshalling only, like the rest of the binding; what ops.py says about streams
 and workspaces holds here too.
+
+Every call can be captured into a graph.  For autograd's backward pass torch asks that no
+eager graph over the same leaves is alive during the capture (their gradients' nodes belong
+to the eager stream, and torch ends the process): drop its results first, or warm up on the
+stream of the capture.
 """
 from __future__ import annotations
 
