@@ -990,15 +990,18 @@ int slots_of(int64_t n, int64_t n_seq, int T) { return (int)(n / T + n_seq); }
 
 // Waves of a workgroup of k_attn and k_attn_dq: four that share the tiles, or one by itself where a sequence has few more
 // tokens than one wave's 32.  Measured (bf16, both kernels, one wave and four): 2,000 x 20 tokens, 4 heads of 64: 84 and
-// 154 us; 200 x 200: 92 and 82; 16 x 1,021, 8 heads: 194 and 152.
+// 154 us; 200 x 200: 92 and 82; 16 x 1,021, 8 heads: 194 and 152;
+// 1 x 4,000: 214 and 177.
 int query_waves(const rece_attention_config& c) { return c.n <= 64 * c.n_seq ? 1 : 4; }
 
 // Waves of a workgroup of k_attn_dkv: more of them deal one tile's queries among themselves where there are too few tiles
 // of keys to fill the card (two waves per SIMD, 2,048) and enough queries to deal.  Measured (bf16, with 1, 2, 4 waves):
 // 4,000 tokens, 4 heads on 1: 575, 333, 168 us; 16 x 1,021, 8 heads on 2: 333, 207, 176; 200 x 200, 4 heads: 72, 90, 130.
+// Eight where a CU has one tile at most, since one such workgroup fills it (4, 8 waves; tiles): 4,000 tokens (126): 174,
+// 115 us; 4 x 600, 4 heads on 1 (79): 49, 36; 2 x 300, 4 heads (80): 14.3, 13.4; 8 x 400, 4 heads (432): 21, 27.
 int key_waves(const rece_attention_config& c) {
   const int64_t tasks = (c.n / 32 + c.n_seq) * c.kv_heads, items = c.heads / c.kv_heads * (c.n / c.n_seq) / 64;
-  const int most = tasks <= 1536 ? 4 : tasks <= 3000 ? 2 : 1;
+  const int most = tasks <= 256 ? 8 : tasks <= 1536 ? 4 : tasks <= 3000 ? 2 : 1;
   return items >= 4 ? most : items >= 2 ? std::min(most, 2) : 1;
 }
 
@@ -1131,18 +1134,20 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
     const auto lds_of = [&](int iw, int hp) {
       return (size_t)(iw * (2 * 32 * TileRows<E, DH>::RB + 3 * 128) + (B ? 4 * hp * (words + iw * (a.dlast + 34)) + iw * SKEW : 0));
     };
-    int waves = key_waves(c);
+    constexpr int MOST = sizeof(E) * DH <= 128 ? 8 : 4;   // eight leave a lane 256 registers
+    int waves = std::min(key_waves(c), MOST);
     while (waves > 1 && lds_of(waves, 1) > MAX_LDS) waves /= 2;
-    // (more heads than this would cost the second workgroup of a CU)
+    // (of up to four waves, more heads than this would cost the second workgroup of a CU)
     a.hp = 1;
-    while (a.hp < group && lds_of(waves, a.hp + 1) <= std::max<size_t>(MAX_LDS / 2, lds_of(waves, 1))) ++a.hp;
+    while (a.hp < group && lds_of(waves, a.hp + 1) <= std::max<size_t>(waves == 8 ? MAX_LDS : MAX_LDS / 2, lds_of(waves, 1))) ++a.hp;
     a.slots = slots_of(c.n, c.n_seq, 32);
     const auto dkv_run = [&](auto iw) {
       constexpr int IW = decltype(iw)::value;
       return launch(k_attn_dkv<E, DH, IW, B>, (int64_t)a.slots * a.hk + CLEAN, 64 * IW, lds_of(IW, a.hp), st, a);
     };
     return waves == 1 ? dkv_run(std::integral_constant<int, 1>())
-                      : waves == 2 ? dkv_run(std::integral_constant<int, 2>()) : dkv_run(std::integral_constant<int, 4>());
+                      : waves == 2 ? dkv_run(std::integral_constant<int, 2>())
+                      : waves == 4 ? dkv_run(std::integral_constant<int, 4>()) : dkv_run(std::integral_constant<int, MOST>());
   });
   if (r != hipSuccess || !bias) return r;
   return launch_join_rows(a.part, a.slots, (a.nbounds + 1) * a.hq, dbias, st);
