@@ -26,8 +26,8 @@
 // What bounds it: the time of one block in one wave, a chain of LDS reads, products and exponentials that two to four waves
 // per SIMD hide in part (two for k_attn_dkv at 64 wide: dk, dv, the keys' and values' rows and the next tile are 192
 // registers); with few long sequences the longest one's last tile.  Vector units are busy 20 to 38 %, matrix units 2 to
-// 14 % at 32 and 64 wide (float32 40 to 49 %) and 18 to 35 % at 128.  Measured (bf16 unless said; k_attn, k_attn_dq, k_attn_dkv in us):
-//   256 x 150 tokens, 2 heads of 32, bias, gradients           17, 24, 39 (34 MB of rows, 3.5 GFLOP: startup and latencies)
+// 21 % at 32 and 64 wide (float32 40 to 52 %) and 18 to 35 % at 128.  Measured (bf16 unless said; k_attn, k_attn_dq, k_attn_dkv in us):
+//   256 x 150 tokens, 2 heads of 32, bias, gradients           17, 24, 37 (39 MB of rows, 3.5 GFLOP: startup and latencies)
 //   200 x 200, 4 heads of 64, bias, gradients                  36, 47, 72
 //   2,000 x 20, 4 heads of 64, bias, gradients                 44, 54, 70 (a wave for a sequence)
 //   16 x 1,021, 8 heads on 2 of 64, bias, gradients            70, 95, 169 (80 GFLOP, 240 TFLOP/s); float32 329, 464, 780
@@ -542,9 +542,10 @@ constexpr int SKEW = 63 * 33 * 4;   // bytes of a block by distance
 
 // One workgroup for 32 keys and a key head.  Its IW waves deal the group's (head, 32 queries) pairs among themselves, each
 // with LDS of its own and no barrier on the way, and add up what they have at the end.  Where the tables of the bias of
-// all heads of a group and its gradients do not fit in LDS, they take `hp` heads at a time.
+// all heads of a group and its gradients do not fit in LDS, they take `hp` heads at a time.  Three waves per SIMD at 32 wide
+// (one register fewer than the two-wave form took: 256 x 150 tokens 38.9 -> 36.7 us).
 template <class E, int DH, int IW, bool BIAS>
-__global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 128 ? 2 : 1) void k_attn_dkv(AttnArgs a) {
+__global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 64 ? 3 : sizeof(E) * DH <= 128 ? 2 : 1) void k_attn_dkv(AttnArgs a) {
   constexpr int NT = 64 * IW, RB = TileRows<E, DH>::RB, BYTES = 32 * RB;
   constexpr bool AHEAD = RB <= 256;               // rows on the way during the work (wider ones do not fit in registers)
   constexpr bool REST = BIAS || sizeof(E) == 4;   // what the log-sum-exp's rounding left counts (dbias, float32)
