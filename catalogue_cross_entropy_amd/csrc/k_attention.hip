@@ -15,14 +15,13 @@
 // from floor(o_u / T) + u on.  That number grows by at least ceil(length / T) from one sequence to the next, so
 // the slots are distinct, floor(n / T) + n_seq of them are enough, and no list of tiles is made.
 //
-// Scores and sums are float32.  bf16: scores carry the factor log2(e); p and ds enter the second products rounded to
-// bf16, whose errors add up like those of independent roundings and stay below the results' own (out, dk and dv are off
-// by 1.3 to 1.45 times the rounding of an exact result), and for dq, where the error of D comes on top, ds as two bf16
-// terms (1.1 times; one term: 1.55), as k_last's p, where they cost
-// nothing.  float32: scores stay in natural units and their difference to the maximum is scaled.
+// Scores and sums are float32.  bf16: scores carry the factor log2(e); p and ds enter the second products as two bf16 terms
+// (off by 2^-16 of them), so that out and the gradients are off by their own rounding alone.  One term's errors are as large
+// as the results' rounding (out off by 1.25, dk and dv by 1.4 times it) for a tenth less time: 16 x 1,021 k_attn 71 us, with
+// two terms 80; k_attn_dkv 168, 189.  float32: scores stay in natural units and their difference to the maximum is scaled.
 // D comes from the outputs with what their rounding left (k_attn keeps it; from the rounded outputs alone dq would be off
-// by 1.4 times as much).  The rounding of p in the outputs is still in it and would be the bias gradient's error:
-// k_attn_dq adds the sum of p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
+// by 1.4 times as much).  What rounding is still in it would be the bias gradient's error: k_attn_dq adds the sum of
+// p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
 // What bounds it: the time of one block in one wave, a chain of LDS reads, products and exponentials that two to four waves
 // per SIMD hide in part (two for k_attn_dkv at 64 wide: dk, dv, the keys' and values' rows and the next tile are 192
 // registers); with few long sequences the longest one's last tile.  Vector units are busy 20 to 38 %, matrix units 2 to
@@ -197,33 +196,28 @@ __device__ __forceinline__ f32x16 block_of(const TileReads<E, D>& o, uint32_t ba
   return s;
 }
 
-// acc[nb][32 coordinates][32 owners] += rows^T[coordinates][32 rows] g[32 rows][32 owners].  bf16: g rounded to bf16,
-// or (TERMS 2) that and the rounding of what it left: off by 2^-16 of g.
-template <class E, int D, int TERMS = 1>
+// acc[nb][32 coordinates][32 owners] += rows^T[coordinates][32 rows] g[32 rows][32 owners].  bf16: g rounded to bf16
+// and the rounding of what that left, off by 2^-16 of g.  The second term takes the first one's registers: formed side by
+// side they cost k_attn_dq at 64 wide its third wave per SIMD (200 x 200: 48 and 59 us).
+template <class E, int D>
 __device__ __forceinline__ void add_product(f32x16 (&acc)[D / 32], const f32x16& g, const TileReads<E, D>& o, uint32_t base) {
   if constexpr (sizeof(E) == 2) {
     constexpr int N = D / 32;
-    u32x4 b[2];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b[kk][e] = pack_bf16(g[8 * kk + 2 * e], g[8 * kk + 2 * e + 1]);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      u32x4 f[N];
+      u32x4 b, f[N];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = pack_bf16(g[8 * kk + 2 * e], g[8 * kk + 2 * e + 1]);
 #pragma unroll
       for (int nb = 0; nb < N; ++nb) f[nb] = TileReads<E, D>::across(o, base, nb, kk);
       together(f);
 #pragma unroll
-      for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], b[kk], acc[nb]);
-      if constexpr (TERMS == 2) {
-        u32x4 rest;
+      for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], b, acc[nb]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          rest[e] = pack_bf16(g[8 * kk + 2 * e] - lo_f32(b[kk][e]), g[8 * kk + 2 * e + 1] - hi_f32(b[kk][e]));
+      for (int e = 0; e < 4; ++e)
+        b[e] = pack_bf16(g[8 * kk + 2 * e] - lo_f32(b[e]), g[8 * kk + 2 * e + 1] - hi_f32(b[e]));
 #pragma unroll
-        for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], rest, acc[nb]);
-      }
+      for (int nb = 0; nb < N; ++nb) acc[nb] = TileMma<E>::run(f[nb], b, acc[nb]);
     }
   } else {
     constexpr int N = D / 32;
@@ -524,7 +518,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= (NW == 1 ? 128 : 256) ? 
         part[v & 1] += x[v];
       }
       rest += part[0] + part[1];
-      add_product<E, DH, 2>(acc, x, o, kb + at);
+      add_product<E, DH>(acc, x, o, kb + at);
     }
     if (t + 1 < nt) {
       const uint32_t nb = lds0 + ((t + 1) & 1) * 2 * S::BYTES;
@@ -543,7 +537,7 @@ constexpr int SKEW = 63 * 33 * 4;   // bytes of a block by distance
 // One workgroup for 32 keys and a key head.  Its IW waves deal the group's (head, 32 queries) pairs among themselves, each
 // with LDS of its own and no barrier on the way, and add up what they have at the end.  Where the tables of the bias of
 // all heads of a group and its gradients do not fit in LDS, they take `hp` heads at a time.  Three waves per SIMD at 32 wide
-// (one register fewer than the two-wave form took: 256 x 150 tokens 38.9 -> 36.7 us).
+// although a few registers go through memory (256 x 150 tokens: two waves 41.6, three 39.1 us).
 template <class E, int DH, int IW, bool BIAS>
 __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 64 ? 3 : sizeof(E) * DH <= 128 ? 2 : 1) void k_attn_dkv(AttnArgs a) {
   constexpr int NT = 64 * IW, RB = TileRows<E, DH>::RB, BYTES = 32 * RB;
@@ -895,7 +889,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DH > 256 ? 1 : 2) void k_last(Last
       x[v] = exp_of<E>(x[v] - ref);
       sum += x[v];
     }
-    add_product<E, DH, 2>(acc, x, o, vb);   // (the cache's rows bound it, not the products)
+    add_product<E, DH>(acc, x, o, vb);
   }
   sum += __shfl_xor(sum, 32);
   // the four waves: [4][group][P] of LDS, elements, then reference and sum

@@ -390,7 +390,8 @@ rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream
  *   dbias[b][h] = sum of ds_ij over the pairs of bucket b (NULL with bias NULL)
  *   dout [n][heads][d]; dq, dk, dv dtype, rows dq_stride, dk_stride, dv_stride elements apart; dbias float32
  * Sums are float32 (dbias: float32 within a workgroup, float64 over them).  Of dtype bf16, p and ds enter their
- * products with the gradients and values rounded to bf16 (ds in dq, and p in rece_last_attention, to 2^-16 of them). */
+ * products with the gradients and values to 2^-16 of them, as two terms each: where q, k, v or dout hold an infinity,
+ * results that it reaches may be NaN instead of infinite. */
 #define RECE_MAX_BOUNDS 127
 #define RECE_MAX_DISTANCE 4096
 typedef struct {
