@@ -7,7 +7,8 @@
 // over the rows with a stride and keep the weight in registers.
 //
 // Sums of squares are float64 (float32 squares pass the range from 1.8e19 on, and the additions
-// hide behind the memory).  Values in 8 bits are rint(127 p / max |p|), p = h w, decided as in
+// hide behind the memory), and so are dweight's over a lane's rows, whose number grows with n (float32: 2.3 U sqrt(sum of the
+// terms' squares) at 61 rows, now 1.1 U, U = 2^-24; 51,200 x 256 backward 17.2 -> 17.7 us).  Values in 8 bits are rint(127 p / max |p|), p = h w, decided as in
 // float64: the float32 quotient decides where it is further from a half than its own error.
 //
 // Measured (bf16): 51,200 x 256 forward 17 us (105 MB, 6.1 TB/s with what the caches keep), backward 17 us and the join of
@@ -215,7 +216,7 @@ struct NormGradArgs {
   const float* weight;
   const float* rstd;
   void* dx;
-  float* part;           // [grid][d] sums of dy h rstd over a workgroup's rows
+  float* part;           // [grid][d] sums of dy h rstd over a workgroup's rows, rounded
   int64_t n;
   int d;
 };
@@ -227,12 +228,16 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_grad(NormGradArgs a) {
   extern __shared__ float sw[];   // [RPB][LPR * NCH * 8] where RPB > 1
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int d = a.d, d8 = d >> 3;
-  F8 w[NCH], dw[NCH];
+  F8 w[NCH];
+  double dw[NCH][8];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int at = lane + c * LPR;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[c].v[e] = dw[c].v[e] = 0.0f;
+    for (int e = 0; e < 8; ++e) {
+      w[c].v[e] = 0.0f;
+      dw[c][e] = 0.0;
+    }
     if (at < d8) w[c] = load8(a.weight + 8 * at);
   }
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.n; r0 += (int64_t)gridDim.x * RPB) {
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_grad(NormGradArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         h[c].v[e] *= rstd;                        // the normalised row
-        dw[c].v[e] = fmaf(g[c].v[e], h[c].v[e], dw[c].v[e]);
+        dw[c][e] = fma((double)g[c].v[e], (double)h[c].v[e], dw[c][e]);
         g[c].v[e] *= w[c].v[e];
         s = fmaf(g[c].v[e], h[c].v[e], s);
       }
@@ -279,22 +284,27 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_grad(NormGradArgs a) {
     if (LPR == 256) __syncthreads();
   }
   float* out = a.part + (int64_t)blockIdx.x * d;
+  F8 sum[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[c].v[e] = (float)dw[c][e];
   if constexpr (RPB == 1) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int at = lane + c * LPR;
-      if (at < d8) store8(out + 8 * at, dw[c]);
+      if (at < d8) store8(out + 8 * at, sum[c]);
     }
   } else {
     constexpr int W = LPR * NCH * 8;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) store8(sw + sub * W + 8 * (lane + c * LPR), dw[c]);
+    for (int c = 0; c < NCH; ++c) store8(sw + sub * W + 8 * (lane + c * LPR), sum[c]);
     __syncthreads();
     for (int t = threadIdx.x; t < d; t += NORM_THREADS) {
-      float v = 0.0f;
+      double v = 0.0;
 #pragma unroll
-      for (int q = 0; q < RPB; ++q) v += sw[q * W + t];
-      out[t] = v;
+      for (int q = 0; q < RPB; ++q) v += (double)sw[q * W + t];
+      out[t] = (float)v;
     }
   }
 }

@@ -438,7 +438,7 @@ rece_status rece_last_attention(const rece_attention_config* cfg, void* stream, 
  *   values 0 and scale NaN.
  * Backward: dy, dh (or NULL: the gradient that reaches h past the norm) [n][d], h and rstd of the forward call:
  *   dx = dh + rstd (dy weight - h rstd^2 mean(dy weight h)): the gradient of x and of the residual alike
- *   dweight [d] float32 = sum over rows of dy h rstd
+ *   dweight [d] float32 = sum over rows of dy h rstd (float64 sums; those of a workgroup's rows are rounded)
  *   workspace  rece_norm_workspace_bytes bytes, temporary */
 rece_status rece_norm_workspace_bytes(int64_t n, int32_t d, size_t* bytes);
 rece_status rece_norm_forward(void* stream, int64_t n, int32_t d, int32_t dtype, float eps, const void* x,
