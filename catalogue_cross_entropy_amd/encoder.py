@@ -131,8 +131,11 @@ class SequenceAttention(_Attention):
         return out, ws
 
     def backward(self, q, k, v, offsets, out, workspace, dout, bias=None, dq=None, dk=None, dv=None, stream=None):
-        """Returns (dq, dk, dv, dbias or None); dq, dk and dv may be given as slices of one gradient."""
+        """Returns (dq, dk, dv, dbias or None); dq, dk and dv may be given as slices of one gradient.  `out` and
+        `workspace` are those of the forward call."""
         import torch
+        if workspace is None:
+            raise ValueError("workspace must be the one that forward returned (with need_grad)")
         dev = q.device
         if _elsewhere(stream, dev):
             return _on_stream(stream, dev, self.backward, q, k, v, offsets, out, workspace, dout, bias, dq, dk, dv)
