@@ -200,8 +200,10 @@ class LogProb:
         return logp, ent, ws
 
     def backward(self, X, Y, ids, workspace, dlogp, dentropy=None, dX=None, dY=None, stream=None):
-        """Returns (dX [s, d], dY [C, d]): float32, or bf16 with bf16_grads."""
+        """Returns (dX [s, d], dY [C, d]): float32, or bf16 with bf16_grads.  `workspace` is the forward call's."""
         import torch
+        if workspace is None:
+            raise ValueError("workspace must be the one that forward returned (with need_grad)")
         dev = X.device
         if _elsewhere(stream, dev):
             return _on_stream(stream, dev, self.backward, X, Y, ids, workspace, dlogp, dentropy, dX, dY)
