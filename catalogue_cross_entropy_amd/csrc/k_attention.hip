@@ -825,7 +825,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DH > 256 ? 1 : 2) void k_last(Last
   const uint32_t kb = lds0 + w * 2 * BYTES, vb = kb + BYTES;
   f32x16 acc[DH / 32] = {};
   float m = NEG_INF, sum = 0.0f;
-  const int nb32 = (len + 31) / 32, step = 4 * a.splits;
+  const int nb32 = len / 32 + (len % 32 != 0), step = 4 * a.splits;   // (lengths up to 2^31 - 1)
   // copies of 64 lanes
   constexpr int PT = 32 * TileRows<E, DH>::CPR / 64;
   u32x4 rk[PT], rv[PT];
@@ -865,7 +865,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DH > 256 ? 1 : 2) void k_last(Last
 #pragma unroll
       for (int v = 0; v < 16; ++v) x[v] = BIAS ? fmaf(x[v], a.c, far) : x[v] * a.c;
     }
-    if (j0 + 32 > len) {
+    if (len - j0 < 32) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) x[v] = back - tile_row(v) < 0 ? NEG_INF : x[v];
     }
@@ -1153,7 +1153,7 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
 // 24.3, of 1,024 33.2; 300 x 1,500: 512 workgroups 48 us, 1,024 53.
 int64_t last_splits(const rece_attention_config& c, int64_t max_len) {
   if (max_len <= 1024) return 1;
-  const int64_t wgs = c.n_seq * c.kv_heads, want = (512 + wgs - 1) / wgs, most = (max_len + 255) / 256;
+  const int64_t wgs = c.n_seq * c.kv_heads, want = (512 + wgs - 1) / wgs, most = max_len / 256 + (max_len % 256 != 0);
   return std::max<int64_t>(1, std::min<int64_t>({want, most, LAST_SPLITS}));
 }
 
