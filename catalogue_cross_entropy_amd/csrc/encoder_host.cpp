@@ -68,7 +68,8 @@ rece_status check_last(const rece_attention_config* c, int64_t max_len) {
   if (v != RECE_OK) return v;
   if (max_len < 1) return invalid("max_len must be >= 1");
   if (c->heads / c->kv_heads > 32) return unsupported("heads / kv_heads must be at most 32");
-  if (c->n_seq * c->heads > I32_MAX / 1024) return unsupported("n_seq * heads must be below 2^21");
+  // (a grid of n_seq * kv_heads workgroups of 256 lanes, and of n_seq * heads joins of 1,024 lanes, below 2^32 lanes)
+  if (c->n_seq * c->heads >= 1 << 22) return unsupported("n_seq * heads must be below 2^22");
   return RECE_OK;
 }
 

@@ -374,7 +374,7 @@ rece_status rece_preference_loss(const rece_preference_config* cfg, void* stream
  *   bucket(t) = how many of the bounds are <= t
  *   q [n] rows of heads x d elements, k and v [n] rows of kv_heads x d, dtype; a row's elements are
  *   contiguous, rows begin q_stride, k_stride, v_stride elements apart (multiples of 8, at most 2^23: slices
- *   of one projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads;
+ *   of one projection will do).  d a multiple of 8, at most 128; heads a multiple of kv_heads, at most 1024;
  *   (n / 32 + n_seq) heads below 2^24 - 1024.
  *   offsets [n_seq + 1] int32 non-decreasing (values outside [0, n] are clamped; a sequence may be empty)
  *   bias [n_bounds + 1][heads] float32, or NULL: none.  bounds: distances >= 1, increasing, at most
@@ -421,8 +421,9 @@ rece_status rece_attention_backward(const rece_attention_config* cfg, void* stre
  * are rows begin[u] .. begin[u] + length[u] - 1 of k and v (n rows in all; begin and length [n_seq] int32,
  * clamped to them; sequences may share rows), its query, row u of q, stands at the last of them:
  *   out_uh = softmax_j(scale q_uh . k_jg + bias[bucket(length[u] - 1 - j)][h]) v_jg      out [n_seq][heads][d]
- * A sequence of length 0 gives 0.  heads / kv_heads at most 32.  max_len >= 1: the lengths to plan for (longer
- * sequences are right too, but slower).  workspace: rece_last_attention_workspace_bytes bytes, temporary (may be 0). */
+ * A sequence of length 0 gives 0.  heads at most 1024, heads / kv_heads at most 32, n_seq heads below 2^22.  max_len >= 1:
+ * the lengths to plan for (longer sequences are right too, but slower).  workspace: rece_last_attention_workspace_bytes
+ * bytes, temporary (may be 0). */
 rece_status rece_last_attention_workspace_bytes(const rece_attention_config* cfg, int64_t max_len, size_t* bytes);
 rece_status rece_last_attention(const rece_attention_config* cfg, void* stream, int64_t max_len, const void* q,
                                 const void* k, const void* v, const int32_t* begin, const int32_t* length,
