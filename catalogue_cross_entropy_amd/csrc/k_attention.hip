@@ -123,8 +123,9 @@ __device__ __forceinline__ void clean_rows(const AttnArgs& a, int which, int nt,
 }
 
 // TI rows of D elements from memory to LDS by NT threads (a workgroup or a wave), PT chunks each.  Rows beyond the end
-// repeat the sequence's last one and chunks beyond the head its last one: their weights and the owners' elements
-// there are 0.  Whole tiles take one lane offset beside scalar ones.
+// repeat the sequence's last one, whose weights there are 0.  Threads of chunks beyond the head copy its last one once more:
+// those chunks stay 0 in LDS (the owners' elements there are 0 too, but 0 times an infinity would be NaN).  Whole tiles
+// take one lane offset beside scalar ones.
 template <class E, int D, int NT, int TI> struct Copy {
   using T = TileRows<E, D>;
   static constexpr int PT = TI * T::CPR / NT, BYTES = TI * T::RB;
@@ -133,11 +134,18 @@ template <class E, int D, int NT, int TI> struct Copy {
   static_assert(TI * T::CPR % NT == 0 && NT % T::CPR == 0, "whole chunks per thread, whole rows per step");
   u32x4 r[PT];
   uint32_t off, to[NV];
+  static __device__ __forceinline__ uint32_t place(int row, int c) { return row * T::RB + ((c ^ (row & T::SWM)) << 4); }
   __device__ __forceinline__ void init(int64_t stride, int cpr) {
-    const int i = (int)threadIdx.x % NT, row = i / T::CPR, c = i % T::CPR;
-    off = (uint32_t)row * (uint32_t)stride + min(c, cpr - 1) * 16;
+    const int i = (int)threadIdx.x % NT, row = i / T::CPR, c = min(i % T::CPR, cpr - 1);
+    off = (uint32_t)row * (uint32_t)stride + c * 16;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) to[v] = row * T::RB + ((c ^ ((row + v * RPQ) & T::SWM)) << 4);
+    for (int v = 0; v < NV; ++v) to[v] = place(row + v * RPQ, c) - v * RPQ * T::RB;
+  }
+  // chunks beyond the head, once for each buffer
+  static __device__ __forceinline__ void clear(uint32_t buf, int cpr) {
+    const int i = (int)threadIdx.x % NT;
+    if (i % T::CPR >= cpr)
+      for (int q = 0; q < PT; ++q) lds_put(buf + place(i / T::CPR + q * RPQ, i % T::CPR), u32x4{0u, 0u, 0u, 0u});
   }
   __device__ __forceinline__ void fetch(const char* head, int64_t stride, int row0, int len) {
     const char* p = head + row0 * stride;
@@ -358,6 +366,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && sizeof(E) * DH > 256 ? 1 : 2) v
   ck.fetch(kh, a.ks, 0, st.len);
   cv.fetch(vh, a.vs, 0, st.len);
   if constexpr (BIAS) fill_bias<E, false>(a, lut, head, S::NT, st.len);
+  for (int x = 0; x < 4; ++x) ck.clear(lds0 + x * S::BYTES, cpr);
   ck.stash(lds0);
   cv.stash(lds0 + S::BYTES);
   __syncthreads();
@@ -490,6 +499,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) * DH <= (NW == 1 ? 128 : 256) ? 
   ck.fetch(kh, a.ks, 0, st.len);
   cv.fetch(vh, a.vs, 0, st.len);
   if constexpr (BIAS) fill_bias<E, false>(a, lut, head, S::NT, st.len);
+  for (int x = 0; x < 4; ++x) ck.clear(lds0 + x * S::BYTES, cpr);
   ck.stash(lds0);
   cv.stash(lds0 + S::BYTES);
   __syncthreads();
@@ -580,6 +590,8 @@ __global__ __launch_bounds__(64 * IW, sizeof(E) * DH <= 64 ? 3 : sizeof(E) * DH 
   Copy<E, DH, 64, 32> cq, cg;
   cq.init(a.qs, cpr);
   cg.init(os, cpr);
+  cq.clear(qb, cpr);
+  cg.clear(gb, cpr);
   float2 nl = make_float2(0.0f, 0.0f);
   float nd = 0.0f;
   auto fetch = [&](int head, int t) {
