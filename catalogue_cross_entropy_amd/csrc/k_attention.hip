@@ -1141,7 +1141,8 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
     const auto lds_of = [&](int iw, int hp) {
       return (size_t)(iw * (2 * 32 * TileRows<E, DH>::RB + 3 * 128) + (B ? 4 * hp * (words + iw * (a.dlast + 34)) + iw * SKEW : 0));
     };
-    constexpr int MOST = sizeof(E) * DH <= 128 ? 8 : 4;   // eight leave a lane 256 registers
+    // eight leave a lane 256 registers; four of float32 at 128 wide with a bias take 162 KB of LDS before its tables
+    constexpr int MOST = sizeof(E) * DH <= 128 ? 8 : B && sizeof(E) * DH > 256 ? 2 : 4;
     int waves = std::min(key_waves(c), MOST);
     while (waves > 1 && lds_of(waves, 1) > MAX_LDS) waves /= 2;
     // (of up to four waves, more heads than this would cost the second workgroup of a CU)
@@ -1154,7 +1155,8 @@ hipError_t attention_backward(const rece_attention_config& c, const void* q, con
     };
     return waves == 1 ? dkv_run(std::integral_constant<int, 1>())
                       : waves == 2 ? dkv_run(std::integral_constant<int, 2>())
-                      : waves == 4 ? dkv_run(std::integral_constant<int, 4>()) : dkv_run(std::integral_constant<int, MOST>());
+                      : waves == 4 ? dkv_run(std::integral_constant<int, std::min(4, MOST)>())
+                                   : dkv_run(std::integral_constant<int, MOST>());
   });
   if (r != hipSuccess || !bias) return r;
   return launch_join_rows(a.part, a.slots, (a.nbounds + 1) * a.hq, dbias, st);
