@@ -65,3 +65,23 @@ def test_weight_gradient_of_many_rows(n, d):
     off = dweight_error(dw, dy, h, exact)
     print(f"  dweight: {off:.2f} U")
     assert off <= MOST
+
+
+def test_weight_gradient_beyond_two_to_the_31_elements():
+    n, d = 290_003, 8192
+    g = torch.Generator(device="cuda").manual_seed(0)
+    h, dy = (torch.randn(n, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = torch.rand(d, generator=g, device="cuda")
+    op = rece.ResidualNorm(n, d)
+    print(f"[gpu] dweight n={n} d={d}", flush=True)
+    _, _, rstd = op.forward(h, None, w)
+    _, dw = op.backward(dy, h, w, rstd)
+    total, squares = torch.zeros(d, dtype=torch.float64, device="cuda"), 0.0
+    for a in range(0, n, 20_000):
+        x = h[a:a + 20_000].double()
+        terms = dy[a:a + 20_000].double() * x / (x.square().mean(1, keepdim=True) + 1e-6).sqrt()
+        total += terms.sum(0)
+        squares += float(terms.square().sum())
+    off = float((dw.double() - total).norm()) / (U * squares ** 0.5)
+    print(f"  dweight: {off:.2f} U")
+    assert off <= MOST
