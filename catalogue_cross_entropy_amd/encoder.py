@@ -58,6 +58,8 @@ class _Attention:
         self._code, self._dt = _dtype(dtype)
         if bounds is not None and len(self.bounds) > MAX_BOUNDS:
             raise ValueError(f"at most {MAX_BOUNDS} bounds")
+        if bounds is not None and any(not 1 <= b <= MAX_DISTANCE for b in self.bounds):
+            raise ValueError(f"bounds must be in [1, {MAX_DISTANCE}]")
         self._rows = rows
         self._cfgs = {}
         self.cfg = self._config(heads * d, kv_heads * d, kv_heads * d)
