@@ -22,18 +22,23 @@
 // D comes from the outputs with what their rounding left (k_attn keeps it; from the rounded outputs alone dq would be off
 // by 1.4 times as much).  What rounding is still in it would be the bias gradient's error: k_attn_dq adds the sum of
 // p (dp - D) over the row to it, which is 0 for the exact D, for k_attn_dkv.
+// float32: D keeps what the outputs' sums rounded, which no other row averages out: dq is off by 3.0e-7 to 6.3e-7 relative,
+// 1.1 to 1.6 times the errors of a float32 form that sums p dp (k_attn_dkv's D has the remainder and does not have it).
 // What bounds it: the time of one block in one wave, a chain of LDS reads, products and exponentials that two to four waves
-// per SIMD hide in part (two for k_attn_dkv at 64 wide: dk, dv, the keys' and values' rows and the next tile are 192
-// registers); with few long sequences the longest one's last tile.  Vector units are busy 20 to 38 %, matrix units 2 to
-// 21 % at 32 and 64 wide (float32 40 to 52 %) and 18 to 35 % at 128.  Measured (bf16 unless said; k_attn, k_attn_dq, k_attn_dkv in us):
-//   256 x 150 tokens, 2 heads of 32, bias, gradients           17, 24, 37 (39 MB of rows, 3.5 GFLOP: startup and latencies)
-//   200 x 200, 4 heads of 64, bias, gradients                  36, 47, 72
-//   2,000 x 20, 4 heads of 64, bias, gradients                 44, 54, 70 (a wave for a sequence)
-//   16 x 1,021, 8 heads on 2 of 64, bias, gradients            70, 95, 169 (80 GFLOP, 240 TFLOP/s); float32 329, 464, 780
-//   8 x 2,000, 8 heads of 128, gradients                       167, 240, 436 (306 GFLOP, 360 TFLOP/s)
-//   3 x 2,731, 16 heads on 4 of 128, forward                   167 (122 GFLOP, 740 TFLOP/s)
+// per SIMD hide in part (two for k_attn_dkv in bf16 at 64 wide: dk and dv are 64 registers, the keys' and values' rows 32, the
+// next tile 32, scores and dp 32; with fragments and offsets 236 to 256); with few long sequences the longest one's last
+// tile.  Vector units are busy 20 to 39 %, matrix units 3 to 22 % at 32 and 64 wide (float32 40 to 49 %) and 25 to 38 % at
+// 128.  Measured (bf16 unless said; k_attn, k_attn_dq, k_attn_dkv in us):
+//   256 x 150 tokens, 2 heads of 32, bias, gradients           19, 23, 40 (39 MB of rows, 3.5 GFLOP: startup and latencies)
+//   200 x 200, 4 heads of 64, bias, gradients                  41, 47, 77
+//   2,000 x 20, 4 heads of 64, bias, gradients                 45, 54, 73 (a wave for a sequence)
+//   the same and one sequence of 10,000                        341, 369, 533 (a wave for each of its tiles, see query_waves)
+//   16 x 1,021, 8 heads on 2 of 64, bias, gradients            79, 93, 190 (80 GFLOP, 220 TFLOP/s); float32 332, 469, 779
+//   1 x 4,000, 4 heads on 1 of 64, bias, gradients             86, 89, 126
+//   8 x 2,000, 8 heads of 128, gradients                       201, 246, 464 (306 GFLOP, 336 TFLOP/s)
+//   3 x 2,731, 16 heads on 4 of 128, forward                   205 (122 GFLOP, 600 TFLOP/s)
 // k_last is bound by the cache's rows where there are many, by its chain of launches and loads where there are few:
-//   2,048 x 500, 4 heads of 64, bias  197 us (1.05 GB at 5.3 TB/s);  1 x 65,536, 8 heads on 2 of 128  18 us and the join 5
+//   2,048 x 500, 4 heads of 64, bias  196 us (1.05 GB at 5.3 TB/s);  1 x 65,536, 8 heads on 2 of 128  18 us and the join 5
 //   (67 MB; 2.9 TB/s in all);  5 x 200, 2 heads of 32  7 us
 #include <algorithm>
 #include <cmath>
@@ -996,16 +1001,16 @@ __global__ __launch_bounds__(1024) void k_last_join(LastArgs a) {
 int slots_of(int64_t n, int64_t n_seq, int T) { return (int)(n / T + n_seq); }
 
 // Waves of a workgroup of k_attn and k_attn_dq: four that share the tiles, or one by itself where a sequence has few more
-// tokens than one wave's 32.  Measured (bf16, both kernels, one wave and four): 2,000 x 20 tokens, 4 heads of 64: 84 and
-// 154 us; 200 x 200: 92 and 82; 16 x 1,021, 8 heads: 194 and 152;
-// 1 x 4,000: 214 and 177.
+// tokens than one wave's 32.  Measured (bf16, both kernels, one wave and four): 2,000 x 20 tokens, 4 heads of 64: 103 and
+// 172 us; 200 x 200: 104 and 92; 16 x 1,021, 8 heads: 224 and 173; 1 x 4,000: 220 and 178.  The mean length decides, here and
+// in key_waves (lengths lie on the device): among many short sequences a long one gets the short ones' form.
 int query_waves(const rece_attention_config& c) { return c.n <= 64 * c.n_seq ? 1 : 4; }
 
 // Waves of a workgroup of k_attn_dkv: more of them deal one tile's queries among themselves where there are too few tiles
 // of keys to fill the card (two waves per SIMD, 2,048) and enough queries to deal.  Measured (bf16, with 1, 2, 4 waves):
-// 4,000 tokens, 4 heads on 1: 575, 333, 168 us; 16 x 1,021, 8 heads on 2: 333, 207, 176; 200 x 200, 4 heads: 72, 90, 130.
-// Eight where a CU has one tile at most, since one such workgroup fills it (4, 8 waves; tiles): 4,000 tokens (126): 174,
-// 115 us; 4 x 600, 4 heads on 1 (79): 49, 36; 2 x 300, 4 heads (80): 14.3, 13.4; 8 x 400, 4 heads (432): 21, 27.
+// 4,000 tokens, 4 heads on 1: 674, 354, 183 us; 16 x 1,021, 8 heads on 2: 391, 272, 195; 200 x 200, 4 heads: 82, 96, 134.
+// Eight where a CU has one tile at most, since one such workgroup fills it (4, 8 waves; tiles): 4,000 tokens (126): 183,
+// 129 us; 4 x 600, 4 heads on 1 (79): 51, 38; 2 x 300, 4 heads (80): 14.9, 13.8; 8 x 400, 4 heads (432): 22, 27.
 int key_waves(const rece_attention_config& c) {
   const int64_t tasks = (c.n / 32 + c.n_seq) * c.kv_heads, items = c.heads / c.kv_heads * (c.n / c.n_seq) / 64;
   const int most = tasks <= 256 ? 8 : tasks <= 1536 ? 4 : tasks <= 3000 ? 2 : 1;

@@ -11,8 +11,10 @@
 // terms' squares) at 61 rows, now 1.1 U, U = 2^-24; 51,200 x 256 backward 17.2 -> 17.7 us).  Values in 8 bits are rint(127 p / max |p|), p = h w, decided as in
 // float64: the float32 quotient decides where it is further from a half than its own error.
 //
-// Measured (bf16): 51,200 x 256 forward 17 us (105 MB, 6.1 TB/s with what the caches keep), backward 17 us and the join of
-// the partial dweights 4; 16,381 x 1,000 in 8 bits 25 us (115 MB, 4.6 TB/s); 5 x 64 in 8 bits 2.9 us, a launch.
+// Measured (bf16): 51,200 x 256 forward 17 us (105 MB, 6.1 TB/s with what the caches keep), backward 18 us and the join of
+// the partial dweights 4 (float32: 40, 34, 5); 16,381 x 1,000 in 8 bits 25 us (115 MB, 4.6 TB/s; float32 40 us, 213 MB, 5.3);
+// 5 x 64 in 8 bits 2.9 us, a launch.  Rows of a table in 8 bits, 1,000,000 x 128: 101 us (388 MB, 3.8 TB/s), where the
+// float64 maximum and the rounding keep the vector unit 80 % busy at 3 bytes an element; float32 131 us (644 MB, 4.9 TB/s).
 #include <algorithm>
 
 #include "rece_device.h"

@@ -286,7 +286,7 @@ def quantize_rows(x, stream=None):
 
 class Int8Scores:
     """Scores of s positions against C items, both as rows of d 8-bit integers with a float32 scale each
-    (quantize_rows, ResidualNorm.forward_int8), in bf16 or float32."""
+    (quantize_rows, ResidualNorm.forward_int8), d a multiple of 16, in bf16 or float32."""
 
     def __init__(self, s: int, C: int, d: int, dtype: str = "bf16"):
         self.s, self.C, self.d, self.dtype = s, C, d, dtype

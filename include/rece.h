@@ -436,7 +436,7 @@ rece_status rece_last_attention(const rece_attention_config* cfg, void* stream, 
  * In 8 bits: with m = max_t |h_t weight_t| of a row,
  *   y8_t = rint(127 h_t weight_t / m) (ties to even),  scale = m rstd / 127     (y = scale y8)
  *   y8 [n][d] int8, scale [n] float32; a row of zeros has scale 0, a row that holds a NaN or an infinity has
- *   values 0 and scale NaN.
+ *   values 0 and scale NaN.  (rece_int8_scores takes rows of a multiple of 16.)
  * Backward: dy, dh (or NULL: the gradient that reaches h past the norm) [n][d], h and rstd of the forward call:
  *   dx = dh + rstd (dy weight - h rstd^2 mean(dy weight h)): the gradient of x and of the residual alike
  *   dweight [d] float32 = sum over rows of dy h rstd (float64 sums; those of a workgroup's rows are rounded)
@@ -451,7 +451,7 @@ rece_status rece_norm_backward(void* stream, int64_t n, int32_t d, int32_t dtype
                                size_t workspace_bytes, void* dx, float* dweight);
 
 /* Rows in 8 bits: x8 = rint(127 x / m), scale = m / 127 with m = max |x| of a row (as above).  An item table is laid
- * out once like this for rece_int8_scores. */
+ * out once like this for rece_int8_scores (d a multiple of 16 there, of 8 here). */
 rece_status rece_quantize_rows(void* stream, int64_t n, int32_t d, int32_t dtype, const void* x, int8_t* x8, float* scale);
 
 /* Scores of positions against items, both in 8 bits with a scale per row:

@@ -43,6 +43,24 @@ def test_bf16_attention_is_off_by_its_results_rounding(lens, hq, hk, d, n_bucket
     assert max(worst.values()) <= MOST, worst
 
 
+@pytest.mark.parametrize("lens,hq,hk,d,n_buckets", [([300, 1, 77, 513], 4, 2, 32, 16), ([300, 1, 77], 4, 2, 64, 16),
+                                                    ([260, 90], 4, 1, 128, 0), ([20] * 60, 2, 2, 64, 16)])
+def test_float32_attention(lens, hq, hk, d, n_buckets):
+    """Scores of d products: sqrt(d) steps and a handful for scale, bias and log-sum-exp, each U / sqrt(3) of scores of some 3:
+    (sqrt(128) + 8) U sqrt(3) = 2e-6 of p at most, and of sums of p."""
+    print(f"[gpu] accuracy f32 lens={lens[:4]} hq={hq} hk={hk} d={d} buckets={n_buckets}", flush=True)
+    op, (q, k, v), offs, bias, bounds, dout, (Q, K, V) = make(lens, hq, hk, d, "f32", n_buckets)
+    o, b = offs.cuda(), None if bias is None else bias.cuda()
+    out, ws = op.forward(Q, K, V, o, bias=b)
+    grads = op.backward(Q, K, V, o, out, ws, dout.cuda(), bias=b)
+    want = attention(q, k, v, offs.tolist(), op.scale, bias=bias, bounds=bounds or (), dout=dout)
+    for name, t in zip(("out", "dq", "dk", "dv", "dbias"), (out, *grads)):
+        if t is not None:
+            off = float((t.double().cpu() - want[name][0]).norm() / want[name][0].norm())
+            print(f"   {name}: {off:.2e}")
+            assert off <= 2e-6, name
+
+
 @pytest.mark.parametrize("hq,hk,d,lens,max_len", [(4, 2, 32, [300, 1, 900, 64], 900), (8, 2, 64, [2000, 1500, 700], 2000),
                                                   (8, 2, 128, [1100, 31, 333], 400)])
 def test_bf16_last_tokens_are_off_by_their_results_rounding(hq, hk, d, lens, max_len):
