@@ -20,7 +20,7 @@
 #include <algorithm>
 
 #include "rece_device.h"
-#include "rece_internal.h"
+#include "rece_ops.h"
 #include "rece_tile.h"
 
 namespace rece {

@@ -47,7 +47,7 @@
 #include <cmath>
 
 #include "rece_device.h"
-#include "rece_internal.h"
+#include "rece_ops.h"
 #include "rece_parts.h"
 #include "rece_tile.h"
 

@@ -18,7 +18,7 @@
 #include <algorithm>
 
 #include "rece_device.h"
-#include "rece_internal.h"
+#include "rece_ops.h"
 
 namespace rece {
 

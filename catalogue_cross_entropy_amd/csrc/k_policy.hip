@@ -19,7 +19,7 @@
 #include <cmath>
 
 #include "rece_device.h"
-#include "rece_internal.h"
+#include "rece_ops.h"
 
 namespace rece {
 

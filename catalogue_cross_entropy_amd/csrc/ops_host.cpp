@@ -5,7 +5,7 @@
 
 #include <cmath>
 
-#include "rece_internal.h"
+#include "rece_ops.h"
 
 using namespace rece;
 
