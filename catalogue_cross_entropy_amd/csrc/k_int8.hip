@@ -50,13 +50,6 @@ struct Int8Args {
   int splits;         // k_int8_march: runs of positions
 };
 
-__device__ __forceinline__ uint32_t pack_bf16_2(float a, float b) {
-  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  const f2 v = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
-}
-
 __device__ __forceinline__ i32x16 mma_i8(u32x4 a, u32x4 b, i32x16 c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
@@ -72,7 +65,7 @@ __device__ __forceinline__ f32x4 load_f4(const float* p) {
 }
 
 __device__ __forceinline__ void put_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put_one(bf16* p, float v) { p->bits = (uint16_t)pack_bf16_2(v, 0.0f); }
+__device__ __forceinline__ void put_one(bf16* p, float v) { p->bits = (uint16_t)pack_bf16(v, 0.0f); }
 
 // 16 bytes to an address of any element.
 template <int ALIGN>
@@ -144,7 +137,7 @@ __global__ __launch_bounds__(256, 2) void k_int8_march(Int8Args a) {
         } o;
 #pragma unroll
         for (int i = 0; i < NI * ES / 4; ++i)
-          o.w[i] = ES == 2 ? pack_bf16_2(f[(2 * i) % NI], f[(2 * i + 1) % NI]) : __float_as_uint(f[i % NI]);
+          o.w[i] = ES == 2 ? pack_bf16(f[(2 * i) % NI], f[(2 * i + 1) % NI]) : __float_as_uint(f[i % NI]);
         *reinterpret_cast<Piece*>(dst) = o;
       } else {
 #pragma unroll
@@ -241,7 +234,7 @@ __global__ __launch_bounds__(256, 2) void k_int8_tile(Int8Args a) {
             for (int e = 0; e < 4; ++e) f[e] = (float)acc[i][p][4 * g + e] * px[p] * py[i][4 * g + e];
             char* at = smem + (32 * p + r) * PITCH + (64 * wi + 32 * i + 8 * g + 4 * hf) * ES;
             if constexpr (ES == 2)
-              *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16_2(f[0], f[1]), pack_bf16_2(f[2], f[3]));
+              *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
             else
               *reinterpret_cast<f32x4*>(at) = f32x4{f[0], f[1], f[2], f[3]};
           }
@@ -319,7 +312,7 @@ __global__ __launch_bounds__(256) void k_int8_few(Int8Args a) {
             u32x2_t v[sizeof(O) / 2];
           } o;
           if constexpr (sizeof(O) == 2) {
-            o.v[0] = u32x2_t{pack_bf16_2(f[0], f[1]), pack_bf16_2(f[2], f[3])};
+            o.v[0] = u32x2_t{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
           } else {
             o.v[0] = u32x2_t{__float_as_uint(f[0]), __float_as_uint(f[1])};
             o.v[1] = u32x2_t{__float_as_uint(f[2]), __float_as_uint(f[3])};

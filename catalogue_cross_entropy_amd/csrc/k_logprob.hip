@@ -125,13 +125,11 @@ __device__ __forceinline__ float lp_weight(float d, float a, float b) {
 // Row of value v of a 32 x 32 block (less 4 h for the lane half h).
 __device__ __forceinline__ constexpr int lp_row(int v) { return tile_row(v); }
 
-template <class E, int D, int NWS> using LpLds = TileReads<E, D>;
-
 // acc[ob][nb] += G[32 owners][32 streamed] . rows[32 streamed][D], lane l holding G[owner l % 32]
 // [streamed lp_row(v) + 4 (l / 32)] in g[ob][v].  bf16: TERMS products, each with the bf16
 // rounding of what the ones before left of G (2: off by at most 2^-16 of a weight, 3: all 24 bits).
 template <class E, int D, int NWS, int OB, int TERMS>
-__device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g)[OB], const LpLds<E, D, NWS>& o,
+__device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g)[OB], const TileReads<E, D>& o,
                                            uint32_t base) {
   using T = LpTile<E, D, NWS>;
   if constexpr (sizeof(E) == 2) {
@@ -210,7 +208,7 @@ __device__ __forceinline__ void lp_product(f32x16 (&acc)[OB][D / 32], f32x16 (&g
 template <class E, int D, int OB, int NWO, int NWS, int MODE, bool ENT, int TERMS, int MINW>
 __global__ __launch_bounds__(64 * NWO * NWS, MINW) void k_lp_sweep(LpArgs a) {
   using T = LpTile<E, D, NWS>;
-  using L = LpLds<E, D, NWS>;
+  using L = TileReads<E, D>;
   constexpr int TI = T::TI, RB = T::RB, CPR = T::CPR, NT = 64 * NWO * NWS;
   constexpr int KC = L::KC;
   constexpr int PT = T::BYTES / 16 / NT;   // chunks a thread copies per tile

@@ -19,6 +19,7 @@
 
 #include "rece_device.h"
 #include "rece_ops.h"
+#include "rece_tile.h"
 
 namespace rece {
 
@@ -52,16 +53,10 @@ __device__ __forceinline__ F8 load8(const float* p) {
   }
   return r;
 }
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const f32x2_t v = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-}
 __device__ __forceinline__ void store8(bf16* p, const F8& r) {
   u32x4 w;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = pack2(r.v[2 * e], r.v[2 * e + 1]);
+  for (int e = 0; e < 4; ++e) w[e] = pack_bf16(r.v[2 * e], r.v[2 * e + 1]);
   *reinterpret_cast<u32x4*>(p) = w;
 }
 __device__ __forceinline__ void store8(float* p, const F8& r) {
@@ -72,7 +67,7 @@ __device__ __forceinline__ void store8(float* p, const F8& r) {
 __device__ __forceinline__ void rounded(F8& r, const bf16*) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const uint32_t w = pack2(r.v[2 * e], r.v[2 * e + 1]);
+    const uint32_t w = pack_bf16(r.v[2 * e], r.v[2 * e + 1]);
     r.v[2 * e] = __uint_as_float(w << 16);
     r.v[2 * e + 1] = __uint_as_float(w & 0xFFFF0000u);
   }
